@@ -61,6 +61,18 @@ typedef enum moe_status {
 #define MOE_MAX_E 1024 /* routed experts per router / route call */
 #define MOE_MAX_K 32   /* experts per token */
 #define MOE_MAX_R 8    /* row-parallel partial buffers */
+#define MOE_MAX_GROUPS 32     /* expert groups of moe_group_topk_route */
+#define MOE_MAX_DIM 65536     /* N and K of the expert and adapter products */
+#define MOE_MAX_RANK 256      /* rank of the low-rank adapters */
+#define MOE_MAX_ADAPTERS 1024 /* adapters of one moe_adapter_linear call */
+
+/* Scores of moe_group_topk_route. */
+#define MOE_SCORE_SOFTMAX 0 /* softmax over all E logits */
+#define MOE_SCORE_SIGMOID 1 /* sigmoid of each logit */
+
+/* Activations of the expert and adapter products. */
+#define MOE_ACT_NONE 0   /* out = y, N outputs */
+#define MOE_ACT_SWIGLU 1 /* out = silu(y[0 .. N/2)) * y[N/2 .. N): gate rows first, N/2 outputs */
 
 /* Bits written (OR-ed) into the optional device error flag. */
 #define MOE_FLAG_BAD_INDEX 1 /* some map[t,j] was outside [0, n_rows) */
@@ -173,6 +185,143 @@ int moe_tail_fused(const float* logits, int64_t E, int32_t k, float routed_scale
                    void* residual_out_bf16, void* normed_out_bf16,
                    int32_t* topk_ids_out, float* topk_w_out,
                    int64_t T, int64_t H, int32_t* err_flag, cudaStream_t stream);
+
+/*
+ * Top-k routing by scores, with groups of experts and a bias for balance.
+ * Per token, over its E logits l:
+ *
+ *   s   = softmax(l) over all E experts, or sigmoid(l)        (score_fn)
+ *   c   = s + bias                                           (choice value)
+ *   the experts form n_group groups of E / n_group neighbours; a group's score
+ *   is the sum of its group_top (1 or 2) largest c; the topk_group best groups
+ *   stay (n_group == 1: all experts)
+ *   ids = the k largest c inside them, in descending order
+ *   w_j = routed_scale * s[ids_j], divided by the sum of the k scores if
+ *         renormalize is 1 (all zero where that sum is zero)
+ *
+ * The bias moves the choice only, never the weights.  Without a bias (NULL)
+ * the experts are ordered by their logits, of which s is a monotone function,
+ * and a group's score is the sum of its group_top largest s.  Equal values go
+ * to the lower group and the lower expert.  Choice values that 32 bits cannot
+ * tell apart are compared in 64: the ids are those of the formula in 64 bits.
+ * The softmax over the k selected logits of moe_topk_route is this call with
+ * score_fn softmax, no bias, one group and renormalize 1.
+ *
+ *   logits   [T, E] FP32; a NaN counts as -inf.  -inf has the score 0 (a row
+ *            of nothing else too), so an expert is taken out of the choice by
+ *            a bias of -inf, not by its logit alone; with softmax, +inf takes
+ *            the whole mass (shared by all that hold it).
+ *   bias     [E] FP32 or NULL; a choice value that is NaN counts as -inf.  An
+ *            expert whose choice value is -inf is taken after all others.
+ *   topk_ids [T, k] int32, written: k distinct experts
+ *   topk_w   [T, k] FP32, written
+ *   T >= 0; 1 <= E <= MOE_MAX_E; E % n_group == 0; 1 <= topk_group <= n_group
+ *   <= MOE_MAX_GROUPS; group_top 1 or 2 (a group of one expert: that one);
+ *   1 <= k <= min(MOE_MAX_K, topk_group * E / n_group); routed_scale finite.
+ */
+int moe_group_topk_route(const float* logits, const float* bias, int32_t* topk_ids, float* topk_w,
+                         int64_t T, int64_t E, int32_t k, int32_t n_group, int32_t topk_group,
+                         int32_t group_top, int32_t score_fn, int32_t renormalize, float routed_scale,
+                         cudaStream_t stream);
+
+/*
+ * Rows that moe_expert_map may need for any ids: T * k + min(E, T * k) *
+ * (block - 1).  Host only; -1 for sizes out of range.
+ */
+int64_t moe_expert_rows(int64_t T, int64_t E, int32_t k, int32_t block);
+
+/*
+ * The expert-sorted row layout of a routed batch: the (token, slot) pairs
+ * grouped by expert, experts ascending, slots in ascending (token, slot)
+ * order in each, every group starting on a multiple of `block` rows.
+ *
+ *   topk_ids  [T, k] int32.  An id outside [0, E) (a padded token, an expert
+ *             of another rank) gets no row: its map entry is -1.  The same
+ *             expert twice in a token gets two rows.
+ *   row_map   [T, k] int32, written: each slot's row, the `map` of
+ *             moe_finalize_add_rmsnorm (which adds nothing for -1 and raises
+ *             MOE_FLAG_BAD_INDEX if it is given a flag)
+ *   row_token [n_rows] int32, written: each row's token; -1 for rows that no
+ *             slot has (padding, and the rows behind the last group)
+ *   offsets   [E + 1] int32, written: first row of each expert, then the end
+ *   counts    [E] int32, written: rows of each expert (without padding)
+ *   n_rows >= moe_expert_rows(T, E, k, block); T * k <= 2^30; n_rows < 2^31;
+ *   1 <= E <= MOE_MAX_E; 1 <= k <= MOE_MAX_K; 1 <= block <= 4096.
+ * T == 0 writes the empty layout (offsets and counts all zero).
+ */
+int moe_expert_map(const int32_t* topk_ids, int32_t* row_map, int32_t* row_token, int32_t* offsets,
+                   int32_t* counts, int64_t n_rows, int64_t T, int64_t E, int32_t k, int32_t block,
+                   cudaStream_t stream);
+
+/* Workspace of moe_expert_linear in bytes (host only); -1 for sizes out of range. */
+int64_t moe_expert_linear_workspace(int64_t n_rows, int64_t E, int64_t N, int64_t K);
+
+/*
+ * The experts' products: for every expert e and every row r of its segment
+ * [offsets[e], offsets[e] + counts[e]),
+ *
+ *   y      = W_e . x[src]      src = row_token[r], or r without row_token
+ *   out[r] = y  or  silu(y[0 .. N/2)) * y[N/2 .. N)          (act)
+ *
+ * FP32 sums of exact products; the activation works on the FP32 sums; one
+ * rounding to BF16 (nearest even).
+ *
+ *   x_bf16    [n_x, K] BF16: the tokens (row_token given) or the rows
+ *   row_token [n_rows] int32 or NULL (then n_x >= n_rows).  A token of a
+ *             segment's row outside [0, n_x) is never dereferenced: the row
+ *             counts as zeros and MOE_FLAG_BAD_INDEX is OR-ed into *err_flag.
+ *   w_bf16    [E, N, K] BF16, each expert's weight row-major
+ *   offsets   [E] or [E + 1] int32, counts [E] int32: the segments, as
+ *             moe_expert_map writes them; no two may overlap.  One that is not inside
+ *             [0, n_rows) is skipped and raises MOE_FLAG_BAD_INDEX.
+ *   out_bf16  [n_rows, N or N/2] BF16; rows that are in no segment are not
+ *             written.  Must not overlap any input.
+ *   workspace device memory of at least moe_expert_linear_workspace() bytes,
+ *             16-byte aligned (NULL if that is 0).  Its contents need no
+ *             preparation and mean nothing afterwards; two calls that may run
+ *             at the same time need one each.
+ *   err_flag  device int32 or NULL (MOE_FLAG_BAD_INDEX, MOE_FLAG_TIMEOUT)
+ *   n_rows >= 0 and < 2^31; 1 <= E <= MOE_MAX_E; 8 <= N, K <= MOE_MAX_DIM;
+ *   K % 8 == 0; N % 8 == 0 (N % 16 == 0 with SwiGLU).
+ */
+int moe_expert_linear(const void* x_bf16, int64_t n_x, const int32_t* row_token, const void* w_bf16,
+                      const int32_t* offsets, const int32_t* counts, void* out_bf16, int64_t n_rows,
+                      int64_t E, int64_t N, int64_t K, int32_t act, void* workspace,
+                      int64_t workspace_bytes, int32_t* err_flag, cudaStream_t stream);
+
+/* Workspace of moe_adapter_linear in bytes (host only); -1 for sizes out of range. */
+int64_t moe_adapter_linear_workspace(int64_t T, int64_t N, int64_t K, int32_t R, int32_t L);
+
+/*
+ * A projection shared by all tokens, with the low-rank adapter of each
+ * token's request beside it:
+ *
+ *   v      = adapter_scale[a] * (A_a . x[t])     a = adapter_ids[t]
+ *   y      = W . x[t] + B_a . v                  (no adapter: y = W . x[t])
+ *   out[t] = y  or  silu(y[0 .. N/2)) * y[N/2 .. N)          (act)
+ *
+ * FP32 sums; v is carried with at least 16 significant bits; one rounding to
+ * BF16 at the end.
+ *
+ *   x_bf16         [T, K] BF16
+ *   w_bf16         [N, K] BF16
+ *   adapter_a_bf16 [L, R, K] BF16, adapter_b_bf16 [L, N, R] BF16 (adapters of
+ *                  a lower rank: padded with zeros)
+ *   adapter_ids    [T] int32, any order.  A negative id means no adapter; one
+ *                  >= L means none too and raises MOE_FLAG_BAD_INDEX.
+ *   adapter_scale  [L] FP32
+ *   out_bf16       [T, N or N/2] BF16, written; must not overlap any input
+ *   workspace      device memory of at least moe_adapter_linear_workspace()
+ *                  bytes, 16-byte aligned; as in moe_expert_linear
+ *   err_flag       device int32 or NULL (MOE_FLAG_BAD_INDEX, MOE_FLAG_TIMEOUT)
+ *   T >= 0; N and K as in moe_expert_linear; R % 8 == 0, 8 <= R <=
+ *   MOE_MAX_RANK; 1 <= L <= MOE_MAX_ADAPTERS; T * R < 2^31.
+ */
+int moe_adapter_linear(const void* x_bf16, const void* w_bf16, const void* adapter_a_bf16,
+                       const void* adapter_b_bf16, const int32_t* adapter_ids,
+                       const float* adapter_scale, void* out_bf16, int64_t T, int64_t N, int64_t K,
+                       int32_t R, int32_t L, int32_t act, void* workspace, int64_t workspace_bytes,
+                       int32_t* err_flag, cudaStream_t stream);
 
 /*
  * Test hook of the bounded waits; no counterpart on the pages.  The next

@@ -10,10 +10,15 @@ allocated with torch when not given.
 * ``moe_topk_route(logits, k, scale)``       -> ids [T, k] int32, weights [T, k] FP32
 * ``moe_finalize_add_rmsnorm(...)``          -> (residual_out, normed) BF16 [T, H]
 * ``moe_tail_fused(logits, k, scale, ...)``  -> (residual_out, normed, ids, weights)
+* ``moe_group_topk_route(logits, k, scale, ...)`` -> ids [T, k] int32, weights [T, k] FP32
+* ``moe_expert_map(ids, E, block)``          -> (row_map, row_token, offsets, counts) int32
+* ``moe_expert_linear(x, w, offsets, counts, ...)`` -> expert rows BF16 [n_rows, N or N/2]
+* ``moe_adapter_linear(x, w, a, b, ids, scale, ...)`` -> BF16 [T, N or N/2]
 """
 
 from __future__ import annotations
 
+import contextlib
 import ctypes
 
 import torch
@@ -30,6 +35,11 @@ __all__ = [
     "moe_topk_route",
     "moe_finalize_add_rmsnorm",
     "moe_tail_fused",
+    "moe_group_topk_route",
+    "moe_expert_rows",
+    "moe_expert_map",
+    "moe_expert_linear",
+    "moe_adapter_linear",
     "MoeTailError",
     "lib",
 ]
@@ -139,6 +149,179 @@ def moe_tail_fused(logits, k, routed_scale, rows, row_map, shared, residual, gam
         T, H, _ptr(err_flag, torch.int32, "err_flag", optional=True), _stream(stream))
     check(st, "moe_tail_fused")
     return residual_out, normed_out, topk_ids, topk_w
+
+
+_SCORES = {"softmax": _lib.MOE_SCORE_SOFTMAX, "sigmoid": _lib.MOE_SCORE_SIGMOID}
+_ACTS = {None: _lib.MOE_ACT_NONE, "none": _lib.MOE_ACT_NONE, "swiglu": _lib.MOE_ACT_SWIGLU}
+
+
+def _choice(table, value, name):
+    if value not in table:
+        raise ValueError(f"{name} must be one of {sorted(str(v) for v in table)}, got {value!r}")
+    return table[value]
+
+
+def _shaped(t, shape, name):
+    if t is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have the shape {list(shape)}, got {list(t.shape)}")
+
+
+@contextlib.contextmanager
+def _launching(device, stream, *tensors):
+    """The device and stream of a launch: every tensor has to be on `device`,
+    which is current inside, and what is allocated inside belongs to the
+    launching stream (so that no other stream's work can still hold it)."""
+    if device.type != "cuda":
+        raise TypeError("the tensors must be CUDA tensors (there is no CPU path)")
+    for t in tensors:
+        if t is not None and t.device != device:
+            raise ValueError(f"all tensors must be on {device}, got {t.device}")
+    with contextlib.ExitStack() as on:
+        if device.index != torch.cuda.current_device():
+            on.enter_context(torch.cuda.device(device))
+        if stream is None:
+            yield torch.cuda.current_stream().cuda_stream
+            return
+        if isinstance(stream, int):
+            stream = torch.cuda.ExternalStream(stream) if stream else torch.cuda.default_stream()
+        if stream.device != device:
+            raise ValueError(f"the stream must be on {device}, got {stream.device}")
+        on.enter_context(torch.cuda.stream(stream))
+        yield stream.cuda_stream
+
+
+def moe_group_topk_route(logits, k, routed_scale, bias=None, n_group=1, topk_group=1, group_top=2, scores="sigmoid",
+                         renormalize=True, topk_ids=None, topk_w=None, stream=None):
+    """Top-k experts per token by sigmoid or softmax scores plus a bias, inside
+    the topk_group best of n_group expert groups (a group counts by the sum of
+    its group_top best); the weights are the scores without the bias, divided
+    by their sum if renormalize, times routed_scale."""
+    if logits.dim() != 2:
+        raise ValueError("logits must have 2 dimensions")
+    T, E = logits.shape
+    k = int(k)
+    _shaped(bias, (E,), "bias")
+    _shaped(topk_ids, (T, k), "topk_ids")
+    _shaped(topk_w, (T, k), "topk_w")
+    with _launching(logits.device, stream, bias, topk_ids, topk_w) as handle:
+        if topk_ids is None:
+            topk_ids = torch.empty((T, max(k, 0)), dtype=torch.int32, device=logits.device)
+        if topk_w is None:
+            topk_w = torch.empty((T, max(k, 0)), dtype=torch.float32, device=logits.device)
+        st = lib().moe_group_topk_route(
+            _ptr(logits, torch.float32, "logits", 2), _ptr(bias, torch.float32, "bias", 1, optional=True),
+            _ptr(topk_ids, torch.int32, "topk_ids"), _ptr(topk_w, torch.float32, "topk_w"), T, E, k, int(n_group),
+            int(topk_group), int(group_top), _choice(_SCORES, scores, "scores"), 1 if renormalize else 0,
+            float(routed_scale), handle)
+    check(st, "moe_group_topk_route")
+    return topk_ids, topk_w
+
+
+def moe_expert_rows(T, E, k, block=1):
+    """Rows moe_expert_map may need for any ids (host only)."""
+    n = lib().moe_expert_rows(int(T), int(E), int(k), int(block))
+    if n < 0:
+        raise ValueError("sizes out of range")
+    return n
+
+
+def moe_expert_map(topk_ids, E, block=1, n_rows=None, row_map=None, row_token=None, offsets=None, counts=None,
+                   stream=None):
+    """The expert-sorted row layout of topk_ids [T, k]: (row_map [T, k],
+    row_token [n_rows], offsets [E + 1], counts [E]), every expert's rows
+    starting on a multiple of block; ids outside [0, E) get no row (-1)."""
+    if topk_ids.dim() != 2:
+        raise ValueError("topk_ids must have 2 dimensions")
+    T, k = topk_ids.shape
+    E, block = int(E), int(block)
+    if n_rows is None:
+        n_rows = moe_expert_rows(T, E, k, block) if row_token is None else row_token.numel()
+    _shaped(row_map, (T, k), "row_map")
+    _shaped(row_token, (n_rows,), "row_token")
+    _shaped(offsets, (E + 1,), "offsets")
+    _shaped(counts, (E,), "counts")
+    with _launching(topk_ids.device, stream, row_map, row_token, offsets, counts) as handle:
+        def out(t, *shape):
+            return torch.empty(shape, dtype=torch.int32, device=topk_ids.device) if t is None else t
+
+        row_map, row_token = out(row_map, T, k), out(row_token, n_rows)
+        offsets, counts = out(offsets, E + 1), out(counts, E)
+        st = lib().moe_expert_map(
+            _ptr(topk_ids, torch.int32, "topk_ids", 2), _ptr(row_map, torch.int32, "row_map"),
+            _ptr(row_token, torch.int32, "row_token"), _ptr(offsets, torch.int32, "offsets"),
+            _ptr(counts, torch.int32, "counts"), n_rows, T, E, k, block, handle)
+    check(st, "moe_expert_map")
+    return row_map, row_token, offsets, counts
+
+
+def _workspace(given, nbytes, device):
+    if nbytes < 0:
+        raise ValueError("sizes out of range")
+    if given is None and nbytes > 0:
+        given = torch.empty(nbytes, dtype=torch.uint8, device=device)
+    return given, 0 if given is None else given.numel()
+
+
+def moe_expert_linear(x, w, offsets, counts, row_token=None, act=None, out=None, workspace=None, err_flag=None,
+                      stream=None):
+    """The experts' products out[r] = act(w[e] @ x[src]) for the rows r of each
+    expert's segment [offsets[e], offsets[e] + counts[e]); src = row_token[r],
+    or r without row_token.  x [n, K], w [E, N, K] BF16; act None or "swiglu"
+    (gate rows of w first; N/2 outputs).  Rows in no segment are not written.
+    workspace: a uint8 tensor to use instead of one allocated by the call."""
+    if x.dim() != 2 or w.dim() != 3 or x.shape[1] != w.shape[2]:
+        raise ValueError("x must be [n, K] and w [E, N, K]")
+    E, N, K = w.shape
+    n_rows = x.shape[0] if row_token is None else row_token.numel()
+    n_out = N // 2 if _choice(_ACTS, act, "act") == _lib.MOE_ACT_SWIGLU else N
+    _shaped(out, (n_rows, n_out), "out")
+    _shaped(counts, (E,), "counts")
+    if offsets.dim() != 1 or offsets.numel() not in (E, E + 1):
+        raise ValueError("offsets must have E or E + 1 entries")
+    with _launching(x.device, stream, w, offsets, counts, row_token, out, workspace, err_flag) as handle:
+        if out is None:
+            out = torch.empty((n_rows, n_out), dtype=torch.bfloat16, device=x.device)
+        workspace, nbytes = _workspace(workspace, lib().moe_expert_linear_workspace(n_rows, E, N, K), x.device)
+        st = lib().moe_expert_linear(
+            _ptr(x, torch.bfloat16, "x", 2), x.shape[0], _ptr(row_token, torch.int32, "row_token", 1, optional=True),
+            _ptr(w, torch.bfloat16, "w", 3), _ptr(offsets, torch.int32, "offsets"), _ptr(counts, torch.int32, "counts"),
+            _ptr(out, torch.bfloat16, "out"), n_rows, E, N, K, _choice(_ACTS, act, "act"),
+            _ptr(workspace, torch.uint8, "workspace", optional=True), nbytes,
+            _ptr(err_flag, torch.int32, "err_flag", optional=True), handle)
+    check(st, "moe_expert_linear")
+    return out
+
+
+def moe_adapter_linear(x, w, adapter_a, adapter_b, adapter_ids, adapter_scale, act=None, out=None, workspace=None,
+                       err_flag=None, stream=None):
+    """One projection for all tokens with each token's low-rank adapter beside
+    it: act(w @ x[t] + scale[a] * b[a] @ (a[a] @ x[t])), a = adapter_ids[t]
+    (negative: none).  x [T, K], w [N, K], adapter_a [L, R, K], adapter_b
+    [L, N, R] BF16, adapter_ids [T] int32, adapter_scale [L] FP32."""
+    if x.dim() != 2 or w.dim() != 2 or adapter_a.dim() != 3 or adapter_b.dim() != 3:
+        raise ValueError("x must be [T, K], w [N, K], adapter_a [L, R, K] and adapter_b [L, N, R]")
+    (T, K), N = x.shape, w.shape[0]
+    L, R = adapter_a.shape[:2]
+    n_out = N // 2 if _choice(_ACTS, act, "act") == _lib.MOE_ACT_SWIGLU else N
+    _shaped(w, (N, K), "w")
+    _shaped(adapter_a, (L, R, K), "adapter_a")
+    _shaped(adapter_b, (L, N, R), "adapter_b")
+    _shaped(adapter_ids, (T,), "adapter_ids")
+    _shaped(adapter_scale, (L,), "adapter_scale")
+    _shaped(out, (T, n_out), "out")
+    with _launching(x.device, stream, w, adapter_a, adapter_b, adapter_ids, adapter_scale, out, workspace,
+                    err_flag) as handle:
+        if out is None:
+            out = torch.empty((T, n_out), dtype=torch.bfloat16, device=x.device)
+        workspace, nbytes = _workspace(workspace, lib().moe_adapter_linear_workspace(T, N, K, R, L), x.device)
+        st = lib().moe_adapter_linear(
+            _ptr(x, torch.bfloat16, "x", 2), _ptr(w, torch.bfloat16, "w"), _ptr(adapter_a, torch.bfloat16, "adapter_a"),
+            _ptr(adapter_b, torch.bfloat16, "adapter_b"), _ptr(adapter_ids, torch.int32, "adapter_ids"),
+            _ptr(adapter_scale, torch.float32, "adapter_scale"), _ptr(out, torch.bfloat16, "out"), T, N, K, R, L,
+            _choice(_ACTS, act, "act"), _ptr(workspace, torch.uint8, "workspace", optional=True), nbytes,
+            _ptr(err_flag, torch.int32, "err_flag", optional=True), handle)
+    check(st, "moe_adapter_linear")
+    return out
 
 
 def moe_debug_withhold_stream_stage(stage):

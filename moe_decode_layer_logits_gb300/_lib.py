@@ -22,6 +22,14 @@ MOE_FLAG_TIMEOUT = 2
 MOE_MAX_E = 1024
 MOE_MAX_K = 32
 MOE_MAX_R = 8
+MOE_MAX_GROUPS = 32
+MOE_MAX_DIM = 65536
+MOE_MAX_RANK = 256
+MOE_MAX_ADAPTERS = 1024
+MOE_SCORE_SOFTMAX = 0
+MOE_SCORE_SIGMOID = 1
+MOE_ACT_NONE = 0
+MOE_ACT_SWIGLU = 1
 
 _vp = ctypes.c_void_p
 _i64 = ctypes.c_int64
@@ -36,6 +44,16 @@ SIGNATURES = {
                                                 _vp, _vp, _i64, _i64, _vp, _vp]),
     "moe_tail_fused": (ctypes.c_int, [_vp, _i64, _i32, _f32, _vp, _i64, _vp, _vp, _vp, _vp, _f32, _vp, _vp,
                                       _vp, _vp, _i64, _i64, _vp, _vp]),
+    "moe_group_topk_route": (ctypes.c_int, [_vp, _vp, _vp, _vp, _i64, _i64, _i32, _i32, _i32, _i32, _i32, _i32, _f32,
+                                            _vp]),
+    "moe_expert_rows": (_i64, [_i64, _i64, _i32, _i32]),
+    "moe_expert_map": (ctypes.c_int, [_vp, _vp, _vp, _vp, _vp, _i64, _i64, _i64, _i32, _i32, _vp]),
+    "moe_expert_linear_workspace": (_i64, [_i64, _i64, _i64, _i64]),
+    "moe_expert_linear": (ctypes.c_int, [_vp, _i64, _vp, _vp, _vp, _vp, _vp, _i64, _i64, _i64, _i64, _i32, _vp, _i64,
+                                         _vp, _vp]),
+    "moe_adapter_linear_workspace": (_i64, [_i64, _i64, _i64, _i32, _i32]),
+    "moe_adapter_linear": (ctypes.c_int, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _i64, _i64, _i64, _i32, _i32, _i32, _vp,
+                                          _i64, _vp, _vp]),
     "moe_debug_withhold_stream_stage": (ctypes.c_int, [_i32]),
     "moe_debug_withhold_router_stage": (ctypes.c_int, [_i32]),
     "moe_debug_fail_next_launch": (ctypes.c_int, [_i32]),
