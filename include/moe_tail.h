@@ -349,6 +349,17 @@ int moe_debug_withhold_stream_stage(int32_t stage);
 int moe_debug_withhold_router_stage(int32_t kb);
 
 /*
+ * Test hook of the bounded waits of the expert products; no counterpart on
+ * the pages.  The next launch of the product kernel issues no loads for K
+ * block `stage` (counted over all tiles of that thread block) in its first thread block, so
+ * that block gives up after its bounded wait: MOE_FLAG_TIMEOUT is set, the
+ * launch completes, its outputs are invalid, and the next launch is
+ * unaffected.  stage -1 cancels the request.  Returns MOE_OK, or
+ * MOE_ERR_INVALID_ARG for stage < -1.  Not for production use.
+ */
+int moe_debug_withhold_expert_stage(int32_t stage);
+
+/*
  * Test hook of the launch-error path; no counterpart on the pages.  With
  * on = 1 the next kernel launch made by any entry point asks the CUDA
  * runtime for more dynamic shared memory than a thread block may have; the

@@ -29,6 +29,7 @@ from ._lib import MoeTailError, check, lib
 __all__ = [
     "moe_debug_withhold_stream_stage",
     "moe_debug_withhold_router_stage",
+    "moe_debug_withhold_expert_stage",
     "moe_debug_fail_next_launch",
     "moe_debug_router_tc_shape",
     "moe_router_logits_fp32",
@@ -337,6 +338,13 @@ def moe_debug_withhold_router_stage(kb):
     wait runs out, its tile is written as NaN and MOE_FLAG_TIMEOUT is set;
     -1 cancels the request."""
     check(lib().moe_debug_withhold_router_stage(int(kb)), "moe_debug_withhold_router_stage")
+
+
+def moe_debug_withhold_expert_stage(stage):
+    """Test hook of the bounded waits: the next launch of the product kernel
+    issues no loads for K block `stage` of its first thread block, so that its
+    wait runs out and MOE_FLAG_TIMEOUT is set; -1 cancels the request."""
+    check(lib().moe_debug_withhold_expert_stage(int(stage)), "moe_debug_withhold_expert_stage")
 
 
 def moe_debug_fail_next_launch(on=True):

@@ -56,6 +56,7 @@ SIGNATURES = {
                                           _i64, _vp, _vp]),
     "moe_debug_withhold_stream_stage": (ctypes.c_int, [_i32]),
     "moe_debug_withhold_router_stage": (ctypes.c_int, [_i32]),
+    "moe_debug_withhold_expert_stage": (ctypes.c_int, [_i32]),
     "moe_debug_fail_next_launch": (ctypes.c_int, [_i32]),
     "moe_debug_router_tc_shape": (ctypes.c_int, [_i64, _i64, _i64, _i32, _i32, _i32, _i32, _vp, _vp]),
 }

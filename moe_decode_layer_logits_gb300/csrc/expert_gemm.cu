@@ -1,0 +1,601 @@
+// Products of row segments with their experts' weights on the 5th-generation
+// tensor cores: out[r, :] = act(W_e x[src(r)]) for the rows r of segment e.
+//
+// The weights are the M side (UMMA M = 128 weight rows) and the rows the N
+// side with an N of the segment's own size (16 .. 256 in steps of 16), so a
+// batch of few rows an expert streams each weight once at the HBM's rate, and
+// a large one wastes less than 16 columns a tile.  One persistent CTA per SM:
+//  - warp 0 streams 64-wide K blocks of the weights (tiled TMA) and of the
+//    rows (TMA gather by the row's token, or tiled) into a ring of stages of
+//    128-byte swizzled rows;
+//  - warp 1 owns the tensor memory, two accumulators of 256 columns, and one
+//    lane issues the MMAs;
+//  - warps 2..5 read the finished accumulator while the next tile's MMAs run,
+//    apply the activation to the FP32 sums and store BF16 once.
+// With SwiGLU a tile holds 64 gate and the 64 matching up rows, interleaved by
+// 16, so that a gate and its up sit 16 tensor-memory lanes apart, in one warp.
+//
+// The tile list (segments x row tiles x weight tiles) is made on the device
+// from the counts: every CTA scans them.  Row tiles are as wide as the mean
+// segment asks for (fewer columns leave room for more stages in flight).
+// Whole rounds of the list go round-robin over the CTAs, so that the weight
+// tiles of a segment run at the same time and share its rows in the L2; the
+// last, partial round is split over all CTAs along K, the pieces are left as
+// FP32 partial tiles, and a second small kernel adds them in order (no
+// atomics: the same inputs give the same bits).
+#include <atomic>
+
+#include "expert_gemm.h"
+#include "host_util.h"
+#include "umma.cuh"
+
+namespace moe {
+
+namespace {
+
+constexpr int kThreads = 192;
+constexpr int kMaxStages = 12;
+constexpr int kRingBytes = 200 * 1024;
+constexpr int kMaxRows = 256;  // rows of a tile (UMMA N)
+constexpr int kAccCols = 256;
+
+struct GemmParams {
+  const int32_t* row_token;
+  const int32_t* offsets;
+  const int32_t* counts;
+  uint16_t* out;
+  float* partial;
+  int32_t* err_flag;
+  int64_t n_rows;
+  int n_x;
+  int E, n_out, K;
+  int slot_rows;  // rows of a partial tile's slot
+  int split;      // the last round is split along K
+  int withhold;   // test hook: the K block CTA 0 never loads, or -1
+};
+
+struct Barriers {
+  uint64_t full[kMaxStages], empty[kMaxStages];
+  uint64_t acc_full[2], acc_empty[2];
+  uint64_t drained;
+  uint32_t tmem_base;
+  int abort_flag;
+  int bn;
+};
+
+__host__ __device__ inline int round_up(int v, int m) { return (v + m - 1) / m * m; }
+
+// The tile list in shared memory: per segment its first row, its rows, and the
+// row tiles before it.
+struct Tiles {
+  int* start;
+  int* count;
+  int* before;  // E + 1
+};
+
+// Rows per tile from the mean rows of the segments that have any: the
+// smallest of 32, 64, 128, 256 that leaves room for a segment a half larger.
+__device__ __forceinline__ int tile_rows(int total, int active) {
+  const int mean = active > 0 ? (total + active - 1) / active : 0;
+  const int want = mean + (mean + 1) / 2;
+  return want <= 32 ? 32 : want <= 64 ? 64 : want <= 128 ? 128 : 256;
+}
+
+// Fills the tile list; every thread of the block calls it.  *bn_out holds the
+// rows per tile afterwards.
+__device__ void list_tiles(const GemmParams& p, Tiles t, int* bn_out, bool report) {
+  for (int e = threadIdx.x; e < p.E; e += blockDim.x) {
+    int64_t beg = 0, cnt = p.n_rows;
+    if (p.offsets) {
+      beg = p.offsets[e];
+      cnt = p.counts[e];
+      if (beg < 0 || cnt < 0 || beg + cnt > p.n_rows) {  // not inside the rows: skipped
+        if (report && p.err_flag) atomicOr(p.err_flag, MOE_FLAG_BAD_INDEX);
+        beg = 0;
+        cnt = 0;
+      }
+    }
+    t.start[e] = static_cast<int>(beg);
+    t.count[e] = static_cast<int>(cnt);
+  }
+  __syncthreads();
+  if (threadIdx.x < 32) {
+    const int lane = threadIdx.x;
+    const int per = (p.E + 31) / 32, b = min(p.E, lane * per), e = min(p.E, b + per);
+    long long total = 0;
+    int active = 0;
+    for (int i = b; i < e; ++i) {
+      total += t.count[i];
+      active += t.count[i] > 0 ? 1 : 0;
+    }
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) {
+      total += __shfl_xor_sync(0xFFFFFFFFu, total, off);
+      active += __shfl_xor_sync(0xFFFFFFFFu, active, off);
+    }
+    if (total > p.n_rows) {  // overlapping segments: none is taken
+      if (lane == 0 && report && p.err_flag) atomicOr(p.err_flag, MOE_FLAG_BAD_INDEX);
+      for (int i = b; i < e; ++i) t.count[i] = 0;
+      total = 0;
+    }
+    const int bn = tile_rows(static_cast<int>(total), active);
+    int mine = 0;
+    for (int i = b; i < e; ++i) mine += (t.count[i] + bn - 1) / bn;
+    int upto = mine;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const int v = __shfl_up_sync(0xFFFFFFFFu, upto, off);
+      if (lane >= off) upto += v;
+    }
+    int at = upto - mine;
+    for (int i = b; i < e; ++i) {
+      t.before[i] = at;
+      at += (t.count[i] + bn - 1) / bn;
+    }
+    if (lane == 31) {
+      t.before[p.E] = upto;
+      *bn_out = bn;
+    }
+  }
+  __syncthreads();
+}
+
+// One piece of work: weight tile m and nr rows from r0 of segment e, K blocks
+// [kb0, kb1).  slot >= 0: an incomplete sum, left in that slot of this CTA.
+struct Piece {
+  int e, m, r0, nr, kb0, kb1, slot, alone;
+};
+
+struct Schedule {
+  int64_t tiles, whole;  // tiles in the list, tiles given out whole
+  int64_t rest_units;    // K blocks of the split round
+  int mt, nkb, G;
+  __device__ Schedule(const GemmParams& p, const Tiles& t, int rows_out) {
+    mt = (p.n_out + rows_out - 1) / rows_out;
+    nkb = (p.K + umma::kBK - 1) / umma::kBK;
+    G = gridDim.x;
+    tiles = static_cast<int64_t>(t.before[p.E]) * mt;
+    whole = p.split ? tiles / G * G : tiles;
+    rest_units = (tiles - whole) * nkb;
+  }
+  // Start of CTA b's share of the split round.
+  __device__ int64_t share(int b) const { return rest_units * b / G; }
+};
+
+// Tile `tile` of the list.
+__device__ __forceinline__ void locate(const Tiles& t, int E, int mt, int64_t tile, Piece& w) {
+  const int at = static_cast<int>(tile / mt);
+  int lo = 0, hi = E;  // before[lo] <= at < before[hi]
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (t.before[mid] <= at) lo = mid;
+    else hi = mid;
+  }
+  const int ntt = t.before[lo + 1] - t.before[lo];
+  const int local = static_cast<int>(tile - static_cast<int64_t>(t.before[lo]) * mt);
+  const int tt = local % ntt;
+  const int64_t cnt = t.count[lo];
+  const int a = static_cast<int>(cnt * tt / ntt), b = static_cast<int>(cnt * (tt + 1) / ntt);
+  w.e = lo;
+  w.m = local / ntt;
+  w.r0 = t.start[lo] + a;
+  w.nr = b - a;
+  w.alone = ntt == 1;
+}
+
+// The pieces of one CTA, in the order in which all its warps walk them.
+struct Walk {
+  int64_t next, u, uend;
+  __device__ Walk(const Schedule& s) : next(blockIdx.x), u(s.share(blockIdx.x)), uend(s.share(blockIdx.x + 1)) {}
+  __device__ bool get(const Schedule& s, const Tiles& t, int E, Piece& w) {
+    if (next < s.whole) {
+      locate(t, E, s.mt, next, w);
+      w.kb0 = 0;
+      w.kb1 = s.nkb;
+      w.slot = -1;
+      next += s.G;
+      return true;
+    }
+    if (u >= uend) return false;
+    locate(t, E, s.mt, s.whole + u / s.nkb, w);
+    w.kb0 = static_cast<int>(u % s.nkb);
+    w.kb1 = static_cast<int>(min(static_cast<int64_t>(s.nkb), w.kb0 + (uend - u)));
+    w.slot = w.kb0 == 0 ? (w.kb1 == s.nkb ? -1 : 1) : 0;
+    u += w.kb1 - w.kb0;
+    return true;
+  }
+};
+
+__device__ __forceinline__ float* slot_tile(const GemmParams& p, int cta, int slot) {
+  return p.partial + (static_cast<int64_t>(cta) * 2 + slot) * p.slot_rows * umma::kBM;
+}
+
+__device__ __forceinline__ float silu_mul(float g, float u) { return g / (1.f + expf(-g)) * u; }
+
+// Whether row r's token names a row of x.
+__device__ __forceinline__ bool token_ok(const GemmParams& p, int r) {
+  if (!p.row_token) return true;
+  const int s = p.row_token[r];
+  return s >= 0 && s < p.n_x;
+}
+
+// Stores 32 columns (rows r0 + c ..) of one weight tile; v[i] is this lane's
+// weight row for row i.  Neighbouring lanes swap halves of two rows so that
+// each store covers a whole row piece of the warp.
+template <bool SWIGLU>
+__device__ __forceinline__ void store32(const GemmParams& p, const Piece& w, int c, int q, const float (&v)[32],
+                                        unsigned bad) {
+  const int lane = threadIdx.x & 31;
+  const int left = w.nr - c;
+  if constexpr (SWIGLU) {
+    // lanes 0..15 hold gates, lanes 16..31 their ups: after the swap the lower
+    // half finishes row i, the upper half row i + 1
+    const bool up = lane >= 16;
+    const int o = w.m * 64 + q * 16 + (lane & 15);
+#pragma unroll
+    for (int i = 0; i < 32; i += 2) {
+      const float other = __shfl_xor_sync(0xFFFFFFFFu, up ? v[i] : v[i + 1], 16);
+      const float g = up ? other : v[i], u = up ? v[i + 1] : other;
+      const int r = up ? i + 1 : i;
+      float y = silu_mul(g, u);
+      if ((bad >> r) & 1u) y = 0.f;
+      if (r < left && o < p.n_out)
+        p.out[static_cast<int64_t>(w.r0 + c + r) * p.n_out + o] = static_cast<uint16_t>(pack_bf16x2(y, 0.f));
+    }
+  } else {
+    const bool odd = lane & 1;
+    const int o = w.m * 128 + q * 32 + (lane & ~1);
+#pragma unroll
+    for (int i = 0; i < 32; i += 2) {
+      const float other = __shfl_xor_sync(0xFFFFFFFFu, odd ? v[i] : v[i + 1], 1);
+      const float a = odd ? other : v[i], b = odd ? v[i + 1] : other;
+      const int r = odd ? i + 1 : i;
+      uint32_t y = pack_bf16x2(a, b);
+      if ((bad >> r) & 1u) y = 0u;
+      if (r < left && o < p.n_out)
+        *reinterpret_cast<uint32_t*>(p.out + static_cast<int64_t>(w.r0 + c + r) * p.n_out + o) = y;
+    }
+  }
+}
+
+template <bool SWIGLU>
+__global__ void __launch_bounds__(kThreads, 1)
+expert_gemm_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constant__ CUtensorMap tmap_w,
+                   const GemmParams p) {
+  using namespace umma;
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ Barriers sb;
+  uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  int* list = reinterpret_cast<int*>(ring + kRingBytes);
+  const Tiles t{list, list + p.E, list + 2 * p.E};
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  volatile int* abort_v = &sb.abort_flag;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kMaxStages; ++s) {
+      mbar_init(&sb.full[s], 1);
+      mbar_init(&sb.empty[s], 1);
+    }
+    for (int a = 0; a < 2; ++a) {
+      mbar_init(&sb.acc_full[a], 1);
+      mbar_init(&sb.acc_empty[a], 4);
+    }
+    mbar_init(&sb.drained, 1);
+    sb.abort_flag = 0;
+    mbar_init_fence();
+  }
+  if (warp == 1) tmem_alloc(&sb.tmem_base, 2 * kAccCols);
+  fence_before_sync();
+  __syncthreads();
+  fence_after_sync();
+  const uint32_t tmem = sb.tmem_base;
+  allow_dependent_launch();
+  grid_dependency_wait();
+  list_tiles(p, t, &sb.bn, blockIdx.x == 0);
+  const int stage_bytes = kBM * kRowBytes + sb.bn * kRowBytes;
+  const int nstages = min(kMaxStages, kRingBytes / stage_bytes);
+  const Schedule s(p, t, SWIGLU ? 64 : 128);
+
+  if (warp == 0) {
+    // -------------------------------------------------------------- loads
+    const uint64_t once = l2_evict_first_policy(), keep = l2_evict_normal_policy();
+    const int withheld = blockIdx.x == 0 ? p.withhold : -1;
+    Walk walk(s);
+    Piece w;
+    int n = 0;  // stages armed so far
+    bool stop = false;
+    while (!stop && walk.get(s, t, p.E, w)) {
+      const int groups = (w.nr + 3) >> 2, boxes = (w.nr + 15) >> 4;
+      int4 tok[2];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        int i4[4] = {0, 0, 0, 0};
+        if (p.row_token) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const int r = (lane + 32 * h) * 4 + j;
+            if (r < w.nr) {
+              const int v = p.row_token[w.r0 + r];
+              if (v >= 0 && v < p.n_x) i4[j] = v;
+              else if (p.err_flag) atomicOr(p.err_flag, MOE_FLAG_BAD_INDEX);  // loads token 0, stored as zeros
+            }
+          }
+        }
+        tok[h] = make_int4(i4[0], i4[1], i4[2], i4[3]);
+      }
+      const uint32_t bytes =
+          static_cast<uint32_t>(kBM + (p.row_token ? groups * 4 : boxes * 16)) * kRowBytes;
+      const uint64_t pol = w.alone ? once : keep;
+      for (int kb = w.kb0; kb < w.kb1; ++kb, ++n) {
+        const int st = n % nstages, use = n / nstages;
+        if ((use > 0 && !wait(&sb.empty[st], (use - 1) & 1, abort_v)) || *abort_v) {
+          stop = true;
+          break;
+        }
+        __syncwarp();
+        if (n == withheld) continue;  // neither armed nor loaded: the MMA warp's wait runs out
+        const uint32_t a = smem_addr(ring) + static_cast<uint32_t>(st * stage_bytes);
+        const uint32_t b = a + kBM * kRowBytes;
+        if (lane == 0) mbar_arrive_expect_tx(&sb.full[st], bytes);
+        __syncwarp();
+        if (SWIGLU) {
+          if (lane < 4)  // 16 gate rows and their 16 up rows
+            tma_load_4d(a + lane * 32 * kRowBytes, &tmap_w, kb * kBK, w.m * 64 + lane * 16, 0, w.e, &sb.full[st], pol);
+        } else if (lane == 0) {
+          tma_load_4d(a, &tmap_w, kb * kBK, w.m * 128, 0, w.e, &sb.full[st], pol);
+        }
+        if (p.row_token) {
+          if (lane < groups) tma_gather4(b + lane * 4 * kRowBytes, &tmap_x, kb * kBK, tok[0], &sb.full[st]);
+          if (lane + 32 < groups)
+            tma_gather4(b + (lane + 32) * 4 * kRowBytes, &tmap_x, kb * kBK, tok[1], &sb.full[st]);
+        } else if (lane < boxes) {
+          tma_load_2d(b + lane * 16 * kRowBytes, &tmap_x, kb * kBK, w.r0 + lane * 16, &sb.full[st]);
+        }
+      }
+    }
+    __syncwarp();
+    // drain: no copy may land after this CTA exits
+    if (lane == 0) {
+      for (int i = n > nstages ? n - nstages : 0; i < n; ++i)
+        if (i != withheld) wait(&sb.full[i % nstages], (i / nstages) & 1, abort_v, true);
+    }
+  } else if (warp == 1) {
+    // ---------------------------------------------------------------- MMA
+    if (lane == 0) {
+      Walk walk(s);
+      Piece w;
+      int n = 0, seq = 0;
+      bool stop = false;
+      while (!stop && walk.get(s, t, p.E, w)) {
+        const int acc = seq & 1, use = seq >> 1;
+        if (use > 0 && !wait(&sb.acc_empty[acc], (use - 1) & 1, abort_v)) break;
+        fence_after_sync();
+        const uint32_t d = tmem + acc * kAccCols;
+        const uint32_t idesc = idesc_bf16(kBM, round_up(w.nr, 16));
+        for (int kb = w.kb0; kb < w.kb1; ++kb, ++n) {
+          const int st = n % nstages;
+          if (!wait(&sb.full[st], (n / nstages) & 1, abort_v)) {
+            stop = true;
+            break;
+          }
+          fence_after_sync();
+          const uint32_t a = smem_addr(ring) + static_cast<uint32_t>(st * stage_bytes);
+          const uint32_t b = a + kBM * kRowBytes;
+#pragma unroll
+          for (int kk = 0; kk < kBK / 16; ++kk)
+            mma_bf16(d, desc_sw128(a + kk * 32), desc_sw128(b + kk * 32), idesc, kb != w.kb0 || kk != 0);
+          mma_commit(&sb.empty[st]);
+        }
+        mma_commit(&sb.acc_full[acc]);
+        ++seq;
+      }
+      mma_commit(&sb.drained);  // also after an abort: fires once the issued MMAs are done
+      wait(&sb.drained, 0, abort_v, true);
+    }
+    __syncwarp();
+  } else {
+    // ----------------------------------------------------------- epilogue
+    const int q = warp & 3;  // this warp's quarter of the tensor-memory lanes
+    Walk walk(s);
+    Piece w;
+    int seq = 0;
+    while (walk.get(s, t, p.E, w)) {
+      const int acc = seq & 1, use = seq >> 1;
+      ++seq;
+      const bool ok = wait(&sb.acc_full[acc], use & 1, abort_v) && !*abort_v;
+      __syncwarp();
+      if (!ok) break;
+      fence_after_sync();
+      const uint32_t d = tmem + acc * kAccCols + (static_cast<uint32_t>(q * 32) << 16);
+      float* part = w.slot >= 0 ? slot_tile(p, blockIdx.x, w.slot) + q * 32 + lane : nullptr;
+#pragma unroll 1
+      for (int c = 0; c < w.nr; c += 32) {
+        uint32_t raw[32];
+        tmem_ld32(d + static_cast<uint32_t>(c), raw);
+        if (part) {
+#pragma unroll
+          for (int i = 0; i < 32; ++i)
+            if (c + i < w.nr) part[(c + i) * kBM] = __uint_as_float(raw[i]);
+        } else {
+          const unsigned bad =
+              p.row_token ? __ballot_sync(0xFFFFFFFFu, c + lane < w.nr && !token_ok(p, w.r0 + c + lane)) : 0u;
+          float v[32];
+#pragma unroll
+          for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(raw[i]);
+          store32<SWIGLU>(p, w, c, q, v, bad);
+        }
+      }
+      fence_before_sync();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sb.acc_empty[acc]);
+    }
+  }
+  __syncwarp();
+  fence_before_sync();
+  __syncthreads();
+  if (threadIdx.x == 0 && p.err_flag && *abort_v) atomicOr(p.err_flag, MOE_FLAG_TIMEOUT);
+  if (warp == 1) {
+    fence_after_sync();
+    tmem_dealloc(tmem, 2 * kAccCols);
+  }
+}
+
+// Adds the partial tiles of the split round.  CTA (b, y) takes the tile at the
+// end of share b if that end lies inside it and no earlier share ends there,
+// and of its rows those with row / 16 % gridDim.y == y.
+template <bool SWIGLU>
+__global__ void __launch_bounds__(128) expert_join_kernel(const GemmParams p, int G) {
+  extern __shared__ int join_list[];
+  __shared__ int bn;
+  const Tiles t{join_list, join_list + p.E, join_list + 2 * p.E};
+  allow_dependent_launch();
+  grid_dependency_wait();
+  list_tiles(p, t, &bn, false);
+  Schedule s(p, t, SWIGLU ? 64 : 128);
+  s.G = G;
+  s.whole = s.tiles / G * G;
+  s.rest_units = (s.tiles - s.whole) * s.nkb;
+  const int b = blockIdx.x;
+  const int64_t end = s.share(b + 1), tile0 = end / s.nkb * s.nkb;
+  if (end == tile0 || end >= s.rest_units) return;  // the share ends between two tiles
+  if (s.share(b) > tile0) return;                   // an earlier share ends in this tile
+  Piece w;
+  locate(t, p.E, s.mt, s.whole + end / s.nkb, w);
+  int last = b + 1;
+  while (s.share(last + 1) < tile0 + s.nkb) ++last;
+  const int l = threadIdx.x, q = l >> 5, lane = l & 31;
+  for (int c = blockIdx.y * 16; c < w.nr; c += gridDim.y * 16) {
+    float v[32];
+#pragma unroll
+    for (int i = 0; i < 32; ++i) v[i] = 0.f;
+    for (int j = b; j <= last; ++j) {
+      if (s.share(j) == s.share(j + 1)) continue;
+      const float* part = slot_tile(p, j, j == b ? 1 : 0) + l;
+#pragma unroll
+      for (int i = 0; i < 16; ++i)
+        if (c + i < w.nr) v[i] += part[(c + i) * umma::kBM];
+    }
+    const unsigned bad =
+        p.row_token ? __ballot_sync(0xFFFFFFFFu, lane < 16 && c + lane < w.nr && !token_ok(p, w.r0 + c + lane)) : 0u;
+    Piece sub = w;
+    sub.nr = min(w.nr, c + 16);
+    store32<SWIGLU>(p, sub, c, q, v, bad);
+  }
+}
+
+// ---------------------------------------------------------------- host side
+
+PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
+  static std::atomic<PFN_cuTensorMapEncodeTiled_v12000> fn{nullptr};
+  PFN_cuTensorMapEncodeTiled_v12000 f = fn.load();
+  if (!f) {
+    void* ptr = nullptr;
+    cudaDriverEntryPointQueryResult r;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000, cudaEnableDefault, &r) == cudaSuccess &&
+        r == cudaDriverEntryPointSuccess) {
+      f = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(ptr);
+      fn.store(f);
+    }
+  }
+  return f;
+}
+
+// Row-major BF16 tensor of `rank` dimensions (innermost first), 128-byte swizzle.
+bool make_map(CUtensorMap* map, const void* base, int rank, const cuuint64_t* dims, const cuuint64_t* strides,
+              const cuuint32_t* box) {
+  const PFN_cuTensorMapEncodeTiled_v12000 fn = encode_fn();
+  const cuuint32_t one[5] = {1, 1, 1, 1, 1};
+  return fn && fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank, const_cast<void*>(base), dims, strides, box, one,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+size_t gemm_smem(int64_t E) { return 1024 + kRingBytes + static_cast<size_t>(3 * E + 1) * sizeof(int); }
+
+template <bool SWIGLU>
+cudaError_t opt_in(int dev) {
+  static std::atomic<bool> done[64];
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  if (!done[dev].load()) {
+    const cudaError_t e =
+        cudaFuncSetAttribute(expert_gemm_kernel<SWIGLU>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             static_cast<int>(gemm_smem(MOE_MAX_E)));
+    if (e != cudaSuccess) return e;
+    done[dev].store(true);
+  }
+  return cudaSuccess;
+}
+
+std::atomic<int> g_withheld{-1};
+
+template <bool SWIGLU>
+cudaError_t launch(const ExpertGemm& g, cudaStream_t stream) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = opt_in<SWIGLU>(dev);
+  if (e != cudaSuccess) return e;
+  GemmParams p{};
+  p.row_token = g.row_token;
+  p.offsets = g.offsets;
+  p.counts = g.counts;
+  p.out = static_cast<uint16_t*>(g.out);
+  p.partial = g.partial;
+  p.err_flag = g.err_flag;
+  p.n_rows = g.n_rows;
+  p.n_x = static_cast<int>(g.n_x);
+  p.E = static_cast<int>(g.E);
+  p.n_out = static_cast<int>(SWIGLU ? g.N / 2 : g.N);
+  p.K = static_cast<int>(g.K);
+  p.slot_rows = static_cast<int>(g.n_rows < kMaxRows ? round_up(static_cast<int>(g.n_rows), 16) : kMaxRows);
+  p.split = 1;
+  p.withhold = g_withheld.exchange(-1);
+
+  // weights as [E][gate, up][n_out][K]; rows of x.  Without any token to read
+  // (n_x == 0) the map names the weights' first row, and every row is stored
+  // as zeros.
+  CUtensorMap mx, mw;
+  const cuuint64_t K = static_cast<cuuint64_t>(g.K), kb = K * 2;
+  const cuuint64_t wd[4] = {K, static_cast<cuuint64_t>(p.n_out), SWIGLU ? 2u : 1u, static_cast<cuuint64_t>(g.E)};
+  const cuuint64_t ws[3] = {kb, kb * p.n_out, kb * static_cast<cuuint64_t>(g.N)};
+  const cuuint32_t wb[4] = {umma::kBK, SWIGLU ? 16u : 128u, SWIGLU ? 2u : 1u, 1u};
+  const cuuint64_t xd[2] = {K, static_cast<cuuint64_t>(g.n_x > 0 ? g.n_x : 1)};
+  const cuuint32_t xb[2] = {umma::kBK, g.row_token ? 1u : 16u};
+  if (!make_map(&mw, g.w, 4, wd, ws, wb) || !make_map(&mx, g.n_x > 0 ? g.x : g.w, 2, xd, &kb, xb))
+    return cudaErrorInvalidValue;
+
+  const int G = sm_count();
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(G), 1, 1);
+  cfg.blockDim = dim3(kThreads, 1, 1);
+  cfg.dynamicSmemBytes = launch_smem(gemm_smem(g.E));
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1] = {pdl_attribute()};
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  e = cudaLaunchKernelEx(&cfg, expert_gemm_kernel<SWIGLU>, mx, mw, p);
+  if (e != cudaSuccess || !p.split) return e;
+  cfg.gridDim = dim3(static_cast<unsigned>(G - 1), static_cast<unsigned>((p.slot_rows + 15) / 16 < 8 ? (p.slot_rows + 15) / 16 : 8), 1);
+  cfg.blockDim = dim3(128, 1, 1);
+  cfg.dynamicSmemBytes = launch_smem(static_cast<size_t>(3 * p.E + 1) * sizeof(int));
+  return cudaLaunchKernelEx(&cfg, expert_join_kernel<SWIGLU>, p, G);
+}
+
+}  // namespace
+
+int64_t expert_gemm_workspace(int64_t n_rows) {
+  if (n_rows <= 0) return 0;
+  const int64_t rows = n_rows < kMaxRows ? round_up(static_cast<int>(n_rows), 16) : kMaxRows;
+  return static_cast<int64_t>(sm_count()) * 2 * rows * umma::kBM * 4;
+}
+
+cudaError_t launch_expert_gemm(const ExpertGemm& g, cudaStream_t stream) {
+  return g.swiglu ? launch<true>(g, stream) : launch<false>(g, stream);
+}
+
+}  // namespace moe
+
+extern "C" int moe_debug_withhold_expert_stage(int32_t stage) {
+  if (stage < -1) return MOE_ERR_INVALID_ARG;
+  moe::g_withheld.store(stage);
+  return MOE_OK;
+}

@@ -5,6 +5,7 @@
 //
 // FP32 sums of exact BF16 products; the activation works on the FP32 sums and
 // the result is rounded to BF16 once.
+#include "expert_gemm.h"
 #include "host_util.h"
 #include "common.cuh"
 
@@ -152,7 +153,7 @@ static int check_linear(int64_t N, int64_t K, int32_t act) {
 
 extern "C" int64_t moe_expert_linear_workspace(int64_t n_rows, int64_t E, int64_t N, int64_t K) {
   if (n_rows < 0 || E < 1 || N < 1 || K < 1) return -1;
-  return 0;
+  return moe::expert_gemm_workspace(n_rows);
 }
 
 extern "C" int moe_expert_linear(const void* x_bf16, int64_t n_x, const int32_t* row_token, const void* w_bf16,
@@ -172,19 +173,9 @@ extern "C" int moe_expert_linear(const void* x_bf16, int64_t n_x, const int32_t*
   if (!aligned(x_bf16, 16) || !aligned(w_bf16, 16) || !aligned(out_bf16, 16) || !aligned(workspace, 16) ||
       !aligned(row_token, 4) || !aligned(offsets, 4) || !aligned(counts, 4) || !aligned(err_flag, 4))
     return MOE_ERR_MISALIGNED;
-  LinearParams p{};
-  p.x = static_cast<const uint16_t*>(x_bf16);
-  p.row_token = row_token;
-  p.w = static_cast<const uint16_t*>(w_bf16);
-  p.offsets = offsets;
-  p.counts = counts;
-  p.out = static_cast<uint16_t*>(out_bf16);
-  p.n_x = n_x;
-  p.n_rows = n_rows;
-  p.N = N;
-  p.K = K;
-  p.err_flag = err_flag;
-  if (launch_linear(p, E, act, stream) != cudaSuccess) {
+  const ExpertGemm g{x_bf16, row_token, w_bf16, offsets, counts, out_bf16, n_x, n_rows, E, N, K,
+                     act == MOE_ACT_SWIGLU, static_cast<float*>(workspace), err_flag};
+  if (launch_expert_gemm(g, stream) != cudaSuccess) {
     (void)cudaGetLastError();
     return MOE_ERR_CUDA;
   }

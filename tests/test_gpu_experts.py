@@ -345,6 +345,20 @@ def test_expert_linear_same_bits_again_and_in_any_company(M):
     assert torch.equal(a, b)
 
 
+@pytest.mark.parametrize("T,gather", [(2, True), (300, False)])
+def test_expert_linear_wait_runs_out_and_the_next_launch_is_clean(M, T, gather):
+    c = draw_layer(6, T, 4, 2, 1024, 4096, gather=gather)
+    want, flag = run_expert(M, c, None, gather)
+    assert flag == 0
+    M.moe_debug_withhold_expert_stage(2)
+    _, flag = run_expert(M, c, None, gather)
+    assert flag & L.MOE_FLAG_TIMEOUT
+    again, flag = run_expert(M, c, None, gather)
+    assert flag == 0 and torch.equal(again, want)
+    with pytest.raises(M.MoeTailError):
+        M.moe_debug_withhold_expert_stage(-2)
+
+
 # ---------------------------------------------------------------------------
 # the projection with adapters
 # ---------------------------------------------------------------------------
