@@ -12,12 +12,14 @@
 //    lane issues the MMAs;
 //  - warps 2..5 read the finished accumulator while the next tile's MMAs run,
 //    apply the activation to the FP32 sums and store BF16 once;
-//  - with a token list, warps 6..9 gather the rows with 16-byte asynchronous
-//    copies (eight lanes a row of the stage) that arrive on the stage's own
-//    barrier as they land, and warp 10 passes that on behind a proxy fence.
-//    (The fence waits for its thread's copies in flight: in the copying warps
-//    it left one stage in flight, 10.4 ms at T = 8192.  A TMA gather of four
-//    rows costs the copy engine about 50 cycles whatever its size: 13.8 ms.)
+//  - with a token list, tiles of up to 32 rows are gathered by warp 0 (TMA, four
+//    rows a copy), larger ones by warps 6..9 with 16-byte asynchronous copies
+//    (eight lanes a row of the stage) that arrive on the stage's own barrier as
+//    they land, and warp 10 passes that on behind a proxy fence.  (The fence
+//    waits for its thread's copies in flight: in the copying warps it left one
+//    stage in flight.  A TMA gather costs the copy engine about 50 cycles
+//    whatever its size, so 64 a K block took 13.8 ms at T = 8192 against 3.0;
+//    at T = 64 the relay's latency costs 2053 us against @G4@.)
 // With SwiGLU a tile holds 64 gate and the 64 matching up rows, interleaved by
 // 16, so that a gate and its up sit 16 tensor-memory lanes apart, in one warp.
 //
@@ -227,12 +229,25 @@ __device__ __forceinline__ float* slot_tile(const GemmParams& p, int cta, int sl
 
 __device__ __forceinline__ float silu_mul(float g, float u) { return g / (1.f + expf(-g)) * u; }
 
+// Whether row r's token names a row of x.
+__device__ __forceinline__ bool token_ok(const GemmParams& p, int r) {
+  const int s = p.row_token[r];
+  return s >= 0 && s < p.n_x;
+}
+
+// Rows c .. c + 31 of the tile whose token names no row (one bit a row): they
+// are stored as zeros.
+__device__ __forceinline__ unsigned bad_rows(const GemmParams& p, const Piece& w, int c) {
+  const int r = c + (threadIdx.x & 31);
+  return p.row_token ? __ballot_sync(0xFFFFFFFFu, r < w.nr && !token_ok(p, w.r0 + r)) : 0u;
+}
+
 // Stores 32 columns (rows r0 + c ..) of one weight tile; v[i] is this lane's
 // weight row for row i.  Neighbouring lanes swap halves of two rows so that
 // each store covers a whole row piece of the warp.  m: the 128-row weight tile.
 template <bool SWIGLU>
 __device__ __forceinline__ void store32(const GemmParams& p, const Piece& w, int m, int c, int q,
-                                        const float (&v)[32]) {
+                                        const float (&v)[32], unsigned bad) {
   const int lane = threadIdx.x & 31;
   const int left = w.nr - c;
   if constexpr (SWIGLU) {
@@ -245,7 +260,7 @@ __device__ __forceinline__ void store32(const GemmParams& p, const Piece& w, int
       const float other = __shfl_xor_sync(0xFFFFFFFFu, up ? v[i] : v[i + 1], 16);
       const float g = up ? other : v[i], u = up ? v[i + 1] : other;
       const int r = up ? i + 1 : i;
-      const float y = silu_mul(g, u);
+      const float y = (bad >> r) & 1u ? 0.f : silu_mul(g, u);
       if (r < left && o < p.n_out)
         p.out[static_cast<int64_t>(w.r0 + c + r) * p.n_out + o] = static_cast<uint16_t>(pack_bf16x2(y, 0.f));
     }
@@ -258,7 +273,8 @@ __device__ __forceinline__ void store32(const GemmParams& p, const Piece& w, int
       const float a = odd ? other : v[i], b = odd ? v[i + 1] : other;
       const int r = odd ? i + 1 : i;
       if (r < left && o < p.n_out)
-        *reinterpret_cast<uint32_t*>(p.out + static_cast<int64_t>(w.r0 + c + r) * p.n_out + o) = pack_bf16x2(a, b);
+        *reinterpret_cast<uint32_t*>(p.out + static_cast<int64_t>(w.r0 + c + r) * p.n_out + o) =
+            (bad >> r) & 1u ? 0u : pack_bf16x2(a, b);
     }
   }
 }
@@ -278,9 +294,14 @@ expert_gemm_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_cons
   const int who = PAIR ? blockIdx.x >> 1 : blockIdx.x;
   volatile int* abort_v = &sb.abort_flag;
 
+  if (warp == 1) tmem_alloc<PAIR>(&sb.tmem_base, 2 * kAccCols);
+  allow_dependent_launch();
+  grid_dependency_wait();
+  list_tiles<PAIR>(p, t, &sb.bn, blockIdx.x == 0);
+  const bool few = GATHER && !PAIR && sb.bn == 32;  // rows gathered by TMA
   if (threadIdx.x == 0) {
     for (int s = 0; s < kMaxStages; ++s) {
-      mbar_init(&sb.full[s], 1 + (GATHER ? (PAIR ? 2 : 1) : 0));
+      mbar_init(&sb.full[s], 1 + (GATHER && !few ? (PAIR ? 2 : 1) : 0));
       mbar_init(&sb.landed[s], 32 * kLoaders);
       mbar_init(&sb.empty[s], 1);
     }
@@ -292,7 +313,6 @@ expert_gemm_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_cons
     sb.abort_flag = 0;
     mbar_init_fence();
   }
-  if (warp == 1) tmem_alloc<PAIR>(&sb.tmem_base, 2 * kAccCols);
   fence_before_sync();
   __syncthreads();
   if (PAIR) {  // the peer's barriers are ready before anything signals them
@@ -301,9 +321,6 @@ expert_gemm_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_cons
   }
   fence_after_sync();
   const uint32_t tmem = sb.tmem_base;
-  allow_dependent_launch();
-  grid_dependency_wait();
-  list_tiles<PAIR>(p, t, &sb.bn, blockIdx.x == 0);
   // a stage: 128 weight rows, then this CTA's rows (a pair's CTA holds half of the tile's)
   const int stage_bytes = (kBM + (PAIR ? kPairRows / 2 : sb.bn)) * kRowBytes;
   const int nstages = min(kMaxStages, kRingBytes / stage_bytes);
@@ -322,8 +339,21 @@ expert_gemm_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_cons
     bool stop = false;
     while (!stop && walk.get(s, t, p.E, w)) {
       const int mine = PAIR ? round_up(w.nr, 16) / 2 : w.nr;  // rows in this CTA
-      const int boxes = GATHER ? 0 : (mine + 31) >> 5;
-      const uint32_t bytes = static_cast<uint32_t>((PAIR ? 2 : 1) * (kBM + boxes * 32)) * kRowBytes;
+      const int boxes = GATHER ? 0 : (mine + 31) >> 5, quads = few ? (mine + 3) >> 2 : 0;
+      const uint32_t bytes = static_cast<uint32_t>((PAIR ? 2 : 1) * (kBM + boxes * 32 + quads * 4)) * kRowBytes;
+      int4 tok = make_int4(0, 0, 0, 0);  // lane l: rows 4 l .. 4 l + 3
+      if (lane < quads) {
+        int v[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          v[i] = lane * 4 + i < w.nr ? p.row_token[w.r0 + lane * 4 + i] : 0;
+          if (v[i] < 0 || v[i] >= p.n_x) {  // loads token 0, stored as zeros
+            if (p.err_flag) atomicOr(p.err_flag, MOE_FLAG_BAD_INDEX);
+            v[i] = 0;
+          }
+        }
+        tok = make_int4(v[0], v[1], v[2], v[3]);
+      }
       const int m = PAIR ? w.m * 2 + rank : w.m, r0 = w.r0 + rank * mine;
       const uint64_t pol = w.alone ? once : keep;
       for (int kb = w.kb0; kb < w.kb1; ++kb, ++n) {
@@ -345,6 +375,7 @@ expert_gemm_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_cons
         } else if (lane < 4) {  // 16 gate rows and their 16 up rows
           tma_load_5d<PAIR>(a + lane * 32 * kRowBytes, &tmap_w, kb * kBK, m * 64 + lane * 16, 0, 0, w.e, bar, pol);
         }
+        if (lane < quads) tma_gather4(b + lane * 4 * kRowBytes, &tmap_x, kb * kBK, tok, bar);
         if (!GATHER && lane < boxes)
           tma_load_2d<PAIR>(b + lane * 32 * kRowBytes, &tmap_x, kb * kBK, r0 + lane * 32, bar);
       }
@@ -415,7 +446,7 @@ expert_gemm_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_cons
           float v[32];
 #pragma unroll
           for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(raw[i]);
-          store32<SWIGLU>(p, w, PAIR ? w.m * 2 + rank : w.m, c, q, v);
+          store32<SWIGLU>(p, w, PAIR ? w.m * 2 + rank : w.m, c, q, v, GATHER ? bad_rows(p, w, c) : 0u);
         }
       }
       fence_before_sync();
@@ -425,7 +456,7 @@ expert_gemm_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_cons
         else mbar_arrive(&sb.acc_empty[acc]);
       }
     }
-  } else if (GATHER && warp < 6 + kLoaders) {
+  } else if (GATHER && !few && warp < 6 + kLoaders) {
     // ------------------------------------------------------------- gather
     // Warp j takes rows 16 i + 4 j .. + 3 of this CTA's rows, eight lanes a
     // row, 16 bytes a lane, at their place in the 128-byte swizzle.
@@ -470,7 +501,7 @@ expert_gemm_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_cons
       }
     }
     copy_drain();
-  } else if (GATHER) {
+  } else if (GATHER && !few) {
     // -------------------------------------------------- gathered rows are in
     if (lane == 0) {
       Walk walk(s, who);
@@ -541,7 +572,7 @@ __global__ void __launch_bounds__(128) expert_join_kernel(const GemmParams p, in
     }
     Piece sub = w;
     sub.nr = min(w.nr, c + 16);
-    store32<SWIGLU>(p, sub, w.m, c, q, v);
+    store32<SWIGLU>(p, sub, w.m, c, q, v, bad_rows(p, w, c));
   }
 }
 
@@ -658,11 +689,12 @@ cudaError_t prepare_and_launch(const ExpertGemm& g, cudaStream_t stream) {
   const cuuint64_t wd[5] = {K, p.weave ? 16 : n, SWIGLU ? 2u : 1u, p.weave ? n / 16 : 1, static_cast<cuuint64_t>(g.E)};
   const cuuint64_t ws[4] = {row, row * n, row * 16, row * static_cast<cuuint64_t>(g.N)};
   const cuuint32_t wb[5] = {umma::kBK, SWIGLU ? 16u : 128u, SWIGLU ? 2u : 1u, p.weave ? 4u : 1u, 1u};
-  const cuuint64_t xd[2] = {K, static_cast<cuuint64_t>(g.n_x)};
-  const cuuint32_t xb[2] = {umma::kBK, 32u};
-  if (!make_map(&mw, g.w, 5, wd, ws, wb)) return cudaErrorInvalidValue;
-  if (g.row_token) mx = mw;  // not used: the rows are gathered
-  else if (!make_map(&mx, g.x, 2, xd, &row, xb)) return cudaErrorInvalidValue;
+  // rows: boxes of 32, or of one for the gather.  Without any token to read
+  // (n_x == 0) the map names the first weight row, and every row is stored as zeros.
+  const cuuint64_t xd[2] = {K, static_cast<cuuint64_t>(g.n_x > 0 ? g.n_x : 1)};
+  const cuuint32_t xb[2] = {umma::kBK, g.row_token ? 1u : 32u};
+  if (!make_map(&mw, g.w, 5, wd, ws, wb) || !make_map(&mx, g.n_x > 0 ? g.x : g.w, 2, xd, &row, xb))
+    return cudaErrorInvalidValue;
 
   const bool pair = g.n_rows / g.E >= kPairMeanRows;
   if (g.row_token)
