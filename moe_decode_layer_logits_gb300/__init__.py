@@ -162,33 +162,59 @@ def _choice(table, value, name):
     return table[value]
 
 
-def _shaped(t, shape, name):
-    if t is not None and tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name} must have the shape {list(shape)}, got {list(t.shape)}")
+class _Launch:
+    """The device and stream of a launch, as a context: `device` is current
+    inside, and what is allocated inside belongs to the launching stream (so
+    that no other stream's work can still hold it).  Yields the stream's
+    handle.  A launch on the current device and stream, the usual case, costs
+    nothing beyond looking the stream up."""
 
+    __slots__ = ("device", "stream", "on")
 
-@contextlib.contextmanager
-def _launching(device, stream, *tensors):
-    """The device and stream of a launch: every tensor has to be on `device`,
-    which is current inside, and what is allocated inside belongs to the
-    launching stream (so that no other stream's work can still hold it)."""
-    if device.type != "cuda":
-        raise TypeError("the tensors must be CUDA tensors (there is no CPU path)")
-    for t in tensors:
-        if t is not None and t.device != device:
-            raise ValueError(f"all tensors must be on {device}, got {t.device}")
-    with contextlib.ExitStack() as on:
-        if device.index != torch.cuda.current_device():
+    def __init__(self, device, stream):
+        self.device, self.stream, self.on = device, stream, None
+
+    def __enter__(self):
+        device, stream = self.device, self.stream
+        if device.type != "cuda":
+            raise TypeError("the tensors must be CUDA tensors (there is no CPU path)")
+        if stream is None and device.index == torch.cuda.current_device():
+            return torch.cuda.current_stream(device).cuda_stream
+        with contextlib.ExitStack() as on:
             on.enter_context(torch.cuda.device(device))
-        if stream is None:
-            yield torch.cuda.current_stream().cuda_stream
-            return
-        if isinstance(stream, int):
-            stream = torch.cuda.ExternalStream(stream) if stream else torch.cuda.default_stream()
-        if stream.device != device:
-            raise ValueError(f"the stream must be on {device}, got {stream.device}")
-        on.enter_context(torch.cuda.stream(stream))
-        yield stream.cuda_stream
+            if stream is None:
+                stream = torch.cuda.current_stream(device)
+            elif isinstance(stream, int):
+                stream = torch.cuda.ExternalStream(stream) if stream else torch.cuda.default_stream(device)
+            if stream.device != device:
+                raise ValueError(f"the stream must be on {device}, got {stream.device}")
+            on.enter_context(torch.cuda.stream(stream))
+            self.on = on.pop_all()
+        return stream.cuda_stream
+
+    def __exit__(self, *exc):
+        return self.on.__exit__(*exc) if self.on is not None else None
+
+
+def _arg(t, dtype, name, shape, device):
+    """Pointer of a tensor of this type, shape and device."""
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must have the shape {list(shape)}, got {list(t.shape)}")
+    if t.device != device:
+        raise ValueError(f"{name} must be on {device}, got {t.device}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+def _opt(t, dtype, name, shape, device):
+    return None if t is None else _arg(t, dtype, name, shape, device)
+
+
+def _flag(t, device):
+    return None if t is None else _arg(t, torch.int32, "err_flag", t.shape, device)
 
 
 def moe_group_topk_route(logits, k, routed_scale, bias=None, n_group=1, topk_group=1, group_top=2, scores="sigmoid",
@@ -199,21 +225,18 @@ def moe_group_topk_route(logits, k, routed_scale, bias=None, n_group=1, topk_gro
     by their sum if renormalize, times routed_scale."""
     if logits.dim() != 2:
         raise ValueError("logits must have 2 dimensions")
-    T, E = logits.shape
-    k = int(k)
-    _shaped(bias, (E,), "bias")
-    _shaped(topk_ids, (T, k), "topk_ids")
-    _shaped(topk_w, (T, k), "topk_w")
-    with _launching(logits.device, stream, bias, topk_ids, topk_w) as handle:
+    (T, E), k, device = logits.shape, int(k), logits.device
+    scores = _choice(_SCORES, scores, "scores")
+    args = _arg(logits, torch.float32, "logits", (T, E), device), _opt(bias, torch.float32, "bias", (E,), device)
+    with _Launch(device, stream) as handle:
         if topk_ids is None:
-            topk_ids = torch.empty((T, max(k, 0)), dtype=torch.int32, device=logits.device)
+            topk_ids = torch.empty((T, max(k, 0)), dtype=torch.int32, device=device)
         if topk_w is None:
-            topk_w = torch.empty((T, max(k, 0)), dtype=torch.float32, device=logits.device)
-        st = lib().moe_group_topk_route(
-            _ptr(logits, torch.float32, "logits", 2), _ptr(bias, torch.float32, "bias", 1, optional=True),
-            _ptr(topk_ids, torch.int32, "topk_ids"), _ptr(topk_w, torch.float32, "topk_w"), T, E, k, int(n_group),
-            int(topk_group), int(group_top), _choice(_SCORES, scores, "scores"), 1 if renormalize else 0,
-            float(routed_scale), handle)
+            topk_w = torch.empty((T, max(k, 0)), dtype=torch.float32, device=device)
+        st = lib().moe_group_topk_route(*args, _arg(topk_ids, torch.int32, "topk_ids", (T, k), device),
+                                        _arg(topk_w, torch.float32, "topk_w", (T, k), device), T, E, k, int(n_group),
+                                        int(topk_group), int(group_top), scores, 1 if renormalize else 0,
+                                        float(routed_scale), handle)
     check(st, "moe_group_topk_route")
     return topk_ids, topk_w
 
@@ -233,34 +256,34 @@ def moe_expert_map(topk_ids, E, block=1, n_rows=None, row_map=None, row_token=No
     starting on a multiple of block; ids outside [0, E) get no row (-1)."""
     if topk_ids.dim() != 2:
         raise ValueError("topk_ids must have 2 dimensions")
-    T, k = topk_ids.shape
-    E, block = int(E), int(block)
+    (T, k), E, block, device = topk_ids.shape, int(E), int(block), topk_ids.device
     if n_rows is None:
         n_rows = moe_expert_rows(T, E, k, block) if row_token is None else row_token.numel()
-    _shaped(row_map, (T, k), "row_map")
-    _shaped(row_token, (n_rows,), "row_token")
-    _shaped(offsets, (E + 1,), "offsets")
-    _shaped(counts, (E,), "counts")
-    with _launching(topk_ids.device, stream, row_map, row_token, offsets, counts) as handle:
-        def out(t, *shape):
-            return torch.empty(shape, dtype=torch.int32, device=topk_ids.device) if t is None else t
+    ids = _arg(topk_ids, torch.int32, "topk_ids", (T, k), device)
+    with _Launch(device, stream) as handle:
+        def out(t, shape):
+            return torch.empty(shape, dtype=torch.int32, device=device) if t is None else t
 
-        row_map, row_token = out(row_map, T, k), out(row_token, n_rows)
-        offsets, counts = out(offsets, E + 1), out(counts, E)
+        row_map, row_token = out(row_map, (T, k)), out(row_token, (n_rows,))
+        offsets, counts = out(offsets, (E + 1,)), out(counts, (E,))
         st = lib().moe_expert_map(
-            _ptr(topk_ids, torch.int32, "topk_ids", 2), _ptr(row_map, torch.int32, "row_map"),
-            _ptr(row_token, torch.int32, "row_token"), _ptr(offsets, torch.int32, "offsets"),
-            _ptr(counts, torch.int32, "counts"), n_rows, T, E, k, block, handle)
+            ids, _arg(row_map, torch.int32, "row_map", (T, k), device),
+            _arg(row_token, torch.int32, "row_token", (n_rows,), device),
+            _arg(offsets, torch.int32, "offsets", (E + 1,), device),
+            _arg(counts, torch.int32, "counts", (E,), device), n_rows, T, E, k, block, handle)
     check(st, "moe_expert_map")
     return row_map, row_token, offsets, counts
 
 
 def _workspace(given, nbytes, device):
+    """(tensor, pointer, bytes) of a call's workspace."""
     if nbytes < 0:
         raise ValueError("sizes out of range")
-    if given is None and nbytes > 0:
+    if given is None:
+        if nbytes == 0:
+            return None, None, 0
         given = torch.empty(nbytes, dtype=torch.uint8, device=device)
-    return given, 0 if given is None else given.numel()
+    return given, _arg(given, torch.uint8, "workspace", given.shape, device), given.numel()
 
 
 def moe_expert_linear(x, w, offsets, counts, row_token=None, act=None, out=None, workspace=None, err_flag=None,
@@ -272,23 +295,23 @@ def moe_expert_linear(x, w, offsets, counts, row_token=None, act=None, out=None,
     workspace: a uint8 tensor to use instead of one allocated by the call."""
     if x.dim() != 2 or w.dim() != 3 or x.shape[1] != w.shape[2]:
         raise ValueError("x must be [n, K] and w [E, N, K]")
-    E, N, K = w.shape
-    n_rows = x.shape[0] if row_token is None else row_token.numel()
-    n_out = N // 2 if _choice(_ACTS, act, "act") == _lib.MOE_ACT_SWIGLU else N
-    _shaped(out, (n_rows, n_out), "out")
-    _shaped(counts, (E,), "counts")
-    if offsets.dim() != 1 or offsets.numel() not in (E, E + 1):
+    (E, N, K), (n_x, _), device = w.shape, x.shape, x.device
+    n_rows = n_x if row_token is None else row_token.numel()
+    act = _choice(_ACTS, act, "act")
+    n_out = N // 2 if act == _lib.MOE_ACT_SWIGLU else N
+    if offsets.dim() != 1 or offsets.shape[0] not in (E, E + 1):
         raise ValueError("offsets must have E or E + 1 entries")
-    with _launching(x.device, stream, w, offsets, counts, row_token, out, workspace, err_flag) as handle:
+    args = (_arg(x, torch.bfloat16, "x", (n_x, K), device), n_x,
+            _opt(row_token, torch.int32, "row_token", (n_rows,), device), _arg(w, torch.bfloat16, "w", (E, N, K), device),
+            _arg(offsets, torch.int32, "offsets", offsets.shape, device),
+            _arg(counts, torch.int32, "counts", (E,), device))
+    L = lib()
+    with _Launch(device, stream) as handle:
         if out is None:
-            out = torch.empty((n_rows, n_out), dtype=torch.bfloat16, device=x.device)
-        workspace, nbytes = _workspace(workspace, lib().moe_expert_linear_workspace(n_rows, E, N, K), x.device)
-        st = lib().moe_expert_linear(
-            _ptr(x, torch.bfloat16, "x", 2), x.shape[0], _ptr(row_token, torch.int32, "row_token", 1, optional=True),
-            _ptr(w, torch.bfloat16, "w", 3), _ptr(offsets, torch.int32, "offsets"), _ptr(counts, torch.int32, "counts"),
-            _ptr(out, torch.bfloat16, "out"), n_rows, E, N, K, _choice(_ACTS, act, "act"),
-            _ptr(workspace, torch.uint8, "workspace", optional=True), nbytes,
-            _ptr(err_flag, torch.int32, "err_flag", optional=True), handle)
+            out = torch.empty((n_rows, n_out), dtype=torch.bfloat16, device=device)
+        ws, ws_ptr, nbytes = _workspace(workspace, L.moe_expert_linear_workspace(n_rows, E, N, K), device)
+        st = L.moe_expert_linear(*args, _arg(out, torch.bfloat16, "out", (n_rows, n_out), device), n_rows, E, N, K, act,
+                                 ws_ptr, nbytes, _flag(err_flag, device), handle)
     check(st, "moe_expert_linear")
     return out
 
@@ -301,26 +324,21 @@ def moe_adapter_linear(x, w, adapter_a, adapter_b, adapter_ids, adapter_scale, a
     [L, N, R] BF16, adapter_ids [T] int32, adapter_scale [L] FP32."""
     if x.dim() != 2 or w.dim() != 2 or adapter_a.dim() != 3 or adapter_b.dim() != 3:
         raise ValueError("x must be [T, K], w [N, K], adapter_a [L, R, K] and adapter_b [L, N, R]")
-    (T, K), N = x.shape, w.shape[0]
-    L, R = adapter_a.shape[:2]
-    n_out = N // 2 if _choice(_ACTS, act, "act") == _lib.MOE_ACT_SWIGLU else N
-    _shaped(w, (N, K), "w")
-    _shaped(adapter_a, (L, R, K), "adapter_a")
-    _shaped(adapter_b, (L, N, R), "adapter_b")
-    _shaped(adapter_ids, (T,), "adapter_ids")
-    _shaped(adapter_scale, (L,), "adapter_scale")
-    _shaped(out, (T, n_out), "out")
-    with _launching(x.device, stream, w, adapter_a, adapter_b, adapter_ids, adapter_scale, out, workspace,
-                    err_flag) as handle:
+    (T, K), N, (L, R, _), device = x.shape, w.shape[0], adapter_a.shape, x.device
+    act = _choice(_ACTS, act, "act")
+    n_out = N // 2 if act == _lib.MOE_ACT_SWIGLU else N
+    args = (_arg(x, torch.bfloat16, "x", (T, K), device), _arg(w, torch.bfloat16, "w", (N, K), device),
+            _arg(adapter_a, torch.bfloat16, "adapter_a", (L, R, K), device),
+            _arg(adapter_b, torch.bfloat16, "adapter_b", (L, N, R), device),
+            _arg(adapter_ids, torch.int32, "adapter_ids", (T,), device),
+            _arg(adapter_scale, torch.float32, "adapter_scale", (L,), device))
+    so = lib()
+    with _Launch(device, stream) as handle:
         if out is None:
-            out = torch.empty((T, n_out), dtype=torch.bfloat16, device=x.device)
-        workspace, nbytes = _workspace(workspace, lib().moe_adapter_linear_workspace(T, N, K, R, L), x.device)
-        st = lib().moe_adapter_linear(
-            _ptr(x, torch.bfloat16, "x", 2), _ptr(w, torch.bfloat16, "w"), _ptr(adapter_a, torch.bfloat16, "adapter_a"),
-            _ptr(adapter_b, torch.bfloat16, "adapter_b"), _ptr(adapter_ids, torch.int32, "adapter_ids"),
-            _ptr(adapter_scale, torch.float32, "adapter_scale"), _ptr(out, torch.bfloat16, "out"), T, N, K, R, L,
-            _choice(_ACTS, act, "act"), _ptr(workspace, torch.uint8, "workspace", optional=True), nbytes,
-            _ptr(err_flag, torch.int32, "err_flag", optional=True), handle)
+            out = torch.empty((T, n_out), dtype=torch.bfloat16, device=device)
+        ws, ws_ptr, nbytes = _workspace(workspace, so.moe_adapter_linear_workspace(T, N, K, R, L), device)
+        st = so.moe_adapter_linear(*args, _arg(out, torch.bfloat16, "out", (T, n_out), device), T, N, K, R, L, act, ws_ptr,
+                                   nbytes, _flag(err_flag, device), handle)
     check(st, "moe_adapter_linear")
     return out
 

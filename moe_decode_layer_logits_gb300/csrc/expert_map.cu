@@ -1,5 +1,16 @@
-// moe_expert_map: the expert-sorted row layout of a routed batch (stable
-// counting sort of the T * k slots by expert, tokens ascending in each).
+// moe_expert_map: the expert-sorted row layout of a routed batch, a stable
+// counting sort of the T * k slots by expert (tokens ascending in each).
+//
+// One launch of one thread-block cluster (a single CTA for small batches), no
+// global scratch: CTA r takes the r-th stretch of the slots, each of its warps
+// a stretch of that.  Every warp counts its slots per expert in shared memory;
+// the counts are added up over the warps and, through distributed shared
+// memory, over the cluster, and scanned over the experts; then each warp walks
+// its slots once more, 32 at a time and in order, and gives every slot its
+// place (equal experts within the 32 by a warp match).  Integer counts only:
+// the layout does not depend on the order of the atomics.  Bound by latency:
+// two passes over a warp's slots and two cluster barriers; more warps shorten
+// the walks until adding up their counts costs as much.
 #include "host_util.h"
 #include "common.cuh"
 
@@ -16,52 +27,120 @@ struct ExpertMapParams {
   int E, k, block;
 };
 
-constexpr int kMapThreads = 1024;
+constexpr int kMapMaxWarps = 32;
+constexpr int kMapMaxCluster = 8;
 
-// One CTA: counts, offsets, then one warp per expert places its slots in
-// ascending order.
-__global__ void __launch_bounds__(kMapThreads) expert_map_kernel(const ExpertMapParams p) {
-  __shared__ int count_s[MOE_MAX_E];
-  __shared__ int start_s[MOE_MAX_E + 1];
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+// Shared memory: [warps][E] counts, then places; [E] each: this CTA's counts,
+// the cluster's, the expert's first row, this CTA's first row.
+static size_t map_smem(int warps, int E) { return static_cast<size_t>(warps + 4) * E * sizeof(int); }
+
+__global__ void __launch_bounds__(kMapMaxWarps * 32) expert_map_kernel(const ExpertMapParams p) {
+  extern __shared__ int map_mem[];
+  __shared__ int warp_rows[kMapMaxWarps];
+  __shared__ int all_rows;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, W = blockDim.x >> 5, E = p.E;
+  int* hist = map_mem;
+  int* mine = map_mem + W * E;
+  int* total = mine + E;
+  int* start = total + E;
+  int* first = start + E;
+  cg::cluster_group cluster = cg::this_cluster();
+  const int C = static_cast<int>(cluster.num_blocks()), rank = static_cast<int>(cluster.block_rank());
   allow_dependent_launch();
+  for (int i = tid; i < W * E; i += blockDim.x) hist[i] = 0;
+  __syncthreads();
   grid_dependency_wait();
-  for (int e = tid; e < p.E; e += kMapThreads) count_s[e] = 0;
-  __syncthreads();
-  for (int64_t i = tid; i < p.slots; i += kMapThreads) {
+
+  // this warp's slots, whole groups of 32
+  const int64_t groups = (p.slots + 31) / 32, walkers = static_cast<int64_t>(C) * W;
+  const int64_t me = static_cast<int64_t>(rank) * W + warp;
+  const int64_t beg = groups * me / walkers * 32, end = min(p.slots, groups * (me + 1) / walkers * 32);
+  int* count = hist + warp * E;
+  for (int64_t i = beg + lane; i < end; i += 32) {
     const int e = p.ids[i];
-    if (e >= 0 && e < p.E) atomicAdd(&count_s[e], 1);
-    else p.row_map[i] = -1;
+    if (e >= 0 && e < E) atomicAdd(&count[e], 1);
   }
-  for (int64_t i = tid; i < p.n_rows; i += kMapThreads) p.row_token[i] = -1;
   __syncthreads();
-  if (tid == 0) {
+  // over the warps: places before each warp, and this CTA's counts
+  for (int e = tid; e < E; e += blockDim.x) {
     int at = 0;
-    for (int e = 0; e < p.E; ++e) {
-      start_s[e] = at;
-      at += (count_s[e] + p.block - 1) / p.block * p.block;
+    for (int w = 0; w < W; ++w) {
+      const int c = hist[w * E + e];
+      hist[w * E + e] = at;
+      at += c;
     }
-    start_s[p.E] = at;
+    mine[e] = at;
+  }
+  cluster_arrive_release();
+  cluster_wait_acquire();
+  // over the cluster, then over the experts (thread i: `per` neighbours)
+  const int per = (E + blockDim.x - 1) / blockDim.x;
+  const int eb = min(E, tid * per), ee = min(E, eb + per);
+  int rows = 0;
+  for (int e = eb; e < ee; ++e) {
+    int before = 0, all = 0;
+    for (int r = 0; r < C; ++r) {
+      const int c = *cluster.map_shared_rank(&mine[e], r);
+      if (r < rank) before += c;
+      all += c;
+    }
+    first[e] = before;
+    total[e] = all;
+    rows += (all + p.block - 1) / p.block * p.block;
+    if (rank == 0) p.counts[e] = all;
+  }
+  int upto = rows;
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1) {
+    const int v = __shfl_up_sync(0xFFFFFFFFu, upto, off);
+    if (lane >= off) upto += v;
+  }
+  if (lane == 31) warp_rows[warp] = upto;
+  cluster_arrive_release();  // this CTA has read its peers' counts
+  __syncthreads();
+  int base = 0;
+  for (int w = 0; w < warp; ++w) base += warp_rows[w];
+  base += upto - rows;
+  for (int e = eb; e < ee; ++e) {
+    start[e] = base;
+    first[e] += base;
+    if (rank == 0) p.offsets[e] = base;
+    base += (total[e] + p.block - 1) / p.block * p.block;
+  }
+  if (tid == static_cast<int>(blockDim.x) - 1) {
+    all_rows = base;
+    if (rank == 0) p.offsets[E] = base;
   }
   __syncthreads();
-  for (int e = tid; e <= p.E; e += kMapThreads) {
-    p.offsets[e] = start_s[e];
-    if (e < p.E) p.counts[e] = count_s[e];
+  // places
+  for (int64_t g = beg; g < end; g += 32) {
+    const int64_t i = g + lane;
+    const int e = i < end ? p.ids[i] : -1;
+    const bool ok = e >= 0 && e < E;
+    const unsigned same = __match_any_sync(0xFFFFFFFFu, ok ? e : -1);
+    const int before = __popc(same & ((1u << lane) - 1u));
+    int row = -1;
+    if (ok) row = count[e] + before;
+    __syncwarp();
+    if (ok && before == 0) count[e] = row + __popc(same);
+    __syncwarp();
+    if (ok) {
+      row += first[e];
+      p.row_token[row] = static_cast<int>(i) / p.k;
+    }
+    if (i < end) p.row_map[i] = row;
   }
-  for (int e = warp; e < p.E; e += kMapThreads / 32) {
-    int at = start_s[e];
-    for (int64_t b = 0; b < p.slots; b += 32) {
-      const int64_t i = b + lane;
-      const bool mine = i < p.slots && p.ids[i] == e;
-      const unsigned m = __ballot_sync(0xFFFFFFFFu, mine);
-      if (mine) {
-        const int row = at + __popc(m & ((1u << lane) - 1u));
-        p.row_map[i] = row;
-        p.row_token[row] = static_cast<int>(i / p.k);
-      }
-      at += __popc(m);
+  // rows that no slot has
+  if (p.block > 1) {
+    for (int e = static_cast<int>(me); e < E; e += static_cast<int>(walkers)) {
+      const int n = (total[e] + p.block - 1) / p.block * p.block;
+      for (int r = total[e] + lane; r < n; r += 32) p.row_token[start[e] + r] = -1;
     }
   }
+  for (int64_t r = all_rows + static_cast<int64_t>(rank) * blockDim.x + tid; r < p.n_rows;
+       r += static_cast<int64_t>(C) * blockDim.x)
+    p.row_token[r] = -1;
+  cluster_wait_acquire();  // no CTA leaves while a peer may read its counts
 }
 
 }  // namespace moe
@@ -86,14 +165,29 @@ extern "C" int moe_expert_map(const int32_t* topk_ids, int32_t* row_map, int32_t
       !aligned(counts, 4))
     return MOE_ERR_MISALIGNED;
   ExpertMapParams p{topk_ids, row_map, row_token, offsets, counts, n_rows, T * k, static_cast<int>(E), k, block};
+  // warps for about 64 slots each, up to 32 in a CTA, then more CTAs
+  const int64_t want = (p.slots + 63) / 64;
+  const int warps = want < 4 ? 4 : want > kMapMaxWarps ? kMapMaxWarps : static_cast<int>(want);
+  int C = 1;
+  while (C < kMapMaxCluster && static_cast<int64_t>(C) * kMapMaxWarps < want) C *= 2;
+  const size_t smem = map_smem(warps, p.E);
+  if (smem > 48 * 1024 && cudaFuncSetAttribute(expert_map_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               static_cast<int>(map_smem(kMapMaxWarps, MOE_MAX_E))) != cudaSuccess) {
+    (void)cudaGetLastError();
+    return MOE_ERR_CUDA;
+  }
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(1, 1, 1);
-  cfg.blockDim = dim3(kMapThreads, 1, 1);
-  cfg.dynamicSmemBytes = launch_smem(0);
+  cfg.gridDim = dim3(static_cast<unsigned>(C), 1, 1);
+  cfg.blockDim = dim3(static_cast<unsigned>(warps * 32), 1, 1);
+  cfg.dynamicSmemBytes = launch_smem(smem);
   cfg.stream = stream;
-  cudaLaunchAttribute attr[1] = {pdl_attribute()};
+  cudaLaunchAttribute attr[2] = {pdl_attribute(), {}};
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = static_cast<unsigned>(C);
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = C > 1 ? 2 : 1;
   if (cudaLaunchKernelEx(&cfg, expert_map_kernel, p) != cudaSuccess) {
     (void)cudaGetLastError();
     return MOE_ERR_CUDA;

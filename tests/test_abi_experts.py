@@ -153,7 +153,12 @@ def test_binding_refuses_before_anything_is_launched(lib):
         M.moe_expert_linear(z(4, 16), z(2, 8, 16), z(2), z(2), act="relu")
     with pytest.raises(ValueError, match="offsets"):
         M.moe_expert_linear(z(4, 16), z(2, 8, 16), z(5), z(2))
+    b = torch.bfloat16
     with pytest.raises(ValueError, match="adapter_b"):
-        M.moe_adapter_linear(z(4, 16), z(8, 16), z(2, 8, 16), z(2, 9, 8), z(4), z(2))
+        M.moe_adapter_linear(z(4, 16, dtype=b), z(8, 16, dtype=b), z(2, 8, 16, dtype=b), z(2, 9, 8, dtype=b), z(4), z(2))
+    with pytest.raises(TypeError, match="w must be"):
+        M.moe_adapter_linear(z(4, 16, dtype=b), z(8, 16), z(2, 8, 16, dtype=b), z(2, 8, 8, dtype=b), z(4), z(2))
+    with pytest.raises(ValueError, match="contiguous"):
+        M.moe_group_topk_route(z(16, 4).t(), 2, 1.0)
     with pytest.raises(ValueError, match="range"):
         M.moe_expert_rows(1, 8, 0)
