@@ -162,51 +162,42 @@ def _choice(table, value, name):
     return table[value]
 
 
-class _Launch:
-    """The device and stream of a launch, as a context: `device` is current
-    inside, and what is allocated inside belongs to the launching stream (so
-    that no other stream's work can still hold it).  Yields the stream's
-    handle.  A launch on the current device and stream, the usual case, costs
-    nothing beyond looking the stream up."""
+_raw_stream = torch._C._cuda_getCurrentRawStream  # the current stream's handle, without a Stream object
 
-    __slots__ = ("device", "stream", "on")
 
-    def __init__(self, device, stream):
-        self.device, self.stream, self.on = device, stream, None
-
-    def __enter__(self):
-        device, stream = self.device, self.stream
-        if device.type != "cuda":
-            raise TypeError("the tensors must be CUDA tensors (there is no CPU path)")
-        if stream is None and device.index == torch.cuda.current_device():
-            return torch.cuda.current_stream(device).cuda_stream
-        with contextlib.ExitStack() as on:
-            on.enter_context(torch.cuda.device(device))
-            if stream is None:
-                stream = torch.cuda.current_stream(device)
-            elif isinstance(stream, int):
-                stream = torch.cuda.ExternalStream(stream) if stream else torch.cuda.default_stream(device)
-            if stream.device != device:
-                raise ValueError(f"the stream must be on {device}, got {stream.device}")
-            on.enter_context(torch.cuda.stream(stream))
-            self.on = on.pop_all()
-        return stream.cuda_stream
-
-    def __exit__(self, *exc):
-        return self.on.__exit__(*exc) if self.on is not None else None
+def _enter(device, stream):
+    """(stream handle, context to close or None) of a launch on `device`:
+    until the context is closed the device is current and what is allocated
+    belongs to the launching stream (so that no other stream's work can still
+    hold it).  A launch on the current device and stream, the usual case, needs
+    no context."""
+    if device.type != "cuda":
+        raise TypeError("the tensors must be CUDA tensors (there is no CPU path)")
+    if stream is None and device.index == torch.cuda.current_device():
+        return _raw_stream(device.index), None
+    with contextlib.ExitStack() as on:
+        on.enter_context(torch.cuda.device(device))
+        if stream is None:
+            stream = torch.cuda.current_stream(device)
+        elif isinstance(stream, int):
+            stream = torch.cuda.ExternalStream(stream) if stream else torch.cuda.default_stream(device)
+        if stream.device != device:
+            raise ValueError(f"the stream must be on {device}, got {stream.device}")
+        on.enter_context(torch.cuda.stream(stream))
+        return stream.cuda_stream, on.pop_all()
 
 
 def _arg(t, dtype, name, shape, device):
     """Pointer of a tensor of this type, shape and device."""
+    if t.dtype is dtype and t.shape == shape and t.device == device and t.is_contiguous():
+        return t.data_ptr()
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if t.shape != shape:
         raise ValueError(f"{name} must have the shape {list(shape)}, got {list(t.shape)}")
     if t.device != device:
         raise ValueError(f"{name} must be on {device}, got {t.device}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    return t.data_ptr()
+    raise ValueError(f"{name} must be contiguous")
 
 
 def _opt(t, dtype, name, shape, device):
@@ -226,17 +217,21 @@ def moe_group_topk_route(logits, k, routed_scale, bias=None, n_group=1, topk_gro
     if logits.dim() != 2:
         raise ValueError("logits must have 2 dimensions")
     (T, E), k, device = logits.shape, int(k), logits.device
-    scores = _choice(_SCORES, scores, "scores")
-    args = _arg(logits, torch.float32, "logits", (T, E), device), _opt(bias, torch.float32, "bias", (E,), device)
-    with _Launch(device, stream) as handle:
+    lg, bs = _arg(logits, torch.float32, "logits", (T, E), device), _opt(bias, torch.float32, "bias", (E,), device)
+    score_fn = _choice(_SCORES, scores, "scores")
+    handle, on = _enter(device, stream)
+    try:
         if topk_ids is None:
             topk_ids = torch.empty((T, max(k, 0)), dtype=torch.int32, device=device)
         if topk_w is None:
             topk_w = torch.empty((T, max(k, 0)), dtype=torch.float32, device=device)
-        st = lib().moe_group_topk_route(*args, _arg(topk_ids, torch.int32, "topk_ids", (T, k), device),
+        st = lib().moe_group_topk_route(lg, bs, _arg(topk_ids, torch.int32, "topk_ids", (T, k), device),
                                         _arg(topk_w, torch.float32, "topk_w", (T, k), device), T, E, k, int(n_group),
-                                        int(topk_group), int(group_top), scores, 1 if renormalize else 0,
+                                        int(topk_group), int(group_top), score_fn, 1 if renormalize else 0,
                                         float(routed_scale), handle)
+    finally:
+        if on is not None:
+            on.close()
     check(st, "moe_group_topk_route")
     return topk_ids, topk_w
 
@@ -260,17 +255,24 @@ def moe_expert_map(topk_ids, E, block=1, n_rows=None, row_map=None, row_token=No
     if n_rows is None:
         n_rows = moe_expert_rows(T, E, k, block) if row_token is None else row_token.numel()
     ids = _arg(topk_ids, torch.int32, "topk_ids", (T, k), device)
-    with _Launch(device, stream) as handle:
-        def out(t, shape):
-            return torch.empty(shape, dtype=torch.int32, device=device) if t is None else t
-
-        row_map, row_token = out(row_map, (T, k)), out(row_token, (n_rows,))
-        offsets, counts = out(offsets, (E + 1,)), out(counts, (E,))
+    handle, on = _enter(device, stream)
+    try:
+        if row_map is None:
+            row_map = torch.empty((T, k), dtype=torch.int32, device=device)
+        if row_token is None:
+            row_token = torch.empty(n_rows, dtype=torch.int32, device=device)
+        if offsets is None:
+            offsets = torch.empty(E + 1, dtype=torch.int32, device=device)
+        if counts is None:
+            counts = torch.empty(E, dtype=torch.int32, device=device)
         st = lib().moe_expert_map(
             ids, _arg(row_map, torch.int32, "row_map", (T, k), device),
             _arg(row_token, torch.int32, "row_token", (n_rows,), device),
             _arg(offsets, torch.int32, "offsets", (E + 1,), device),
             _arg(counts, torch.int32, "counts", (E,), device), n_rows, T, E, k, block, handle)
+    finally:
+        if on is not None:
+            on.close()
     check(st, "moe_expert_map")
     return row_map, row_token, offsets, counts
 
@@ -306,12 +308,16 @@ def moe_expert_linear(x, w, offsets, counts, row_token=None, act=None, out=None,
             _arg(offsets, torch.int32, "offsets", offsets.shape, device),
             _arg(counts, torch.int32, "counts", (E,), device))
     L = lib()
-    with _Launch(device, stream) as handle:
+    handle, on = _enter(device, stream)
+    try:
         if out is None:
             out = torch.empty((n_rows, n_out), dtype=torch.bfloat16, device=device)
         ws, ws_ptr, nbytes = _workspace(workspace, L.moe_expert_linear_workspace(n_rows, E, N, K), device)
         st = L.moe_expert_linear(*args, _arg(out, torch.bfloat16, "out", (n_rows, n_out), device), n_rows, E, N, K, act,
                                  ws_ptr, nbytes, _flag(err_flag, device), handle)
+    finally:
+        if on is not None:
+            on.close()
     check(st, "moe_expert_linear")
     return out
 
@@ -333,12 +339,16 @@ def moe_adapter_linear(x, w, adapter_a, adapter_b, adapter_ids, adapter_scale, a
             _arg(adapter_ids, torch.int32, "adapter_ids", (T,), device),
             _arg(adapter_scale, torch.float32, "adapter_scale", (L,), device))
     so = lib()
-    with _Launch(device, stream) as handle:
+    handle, on = _enter(device, stream)
+    try:
         if out is None:
             out = torch.empty((T, n_out), dtype=torch.bfloat16, device=device)
         ws, ws_ptr, nbytes = _workspace(workspace, so.moe_adapter_linear_workspace(T, N, K, R, L), device)
         st = so.moe_adapter_linear(*args, _arg(out, torch.bfloat16, "out", (T, n_out), device), T, N, K, R, L, act, ws_ptr,
                                    nbytes, _flag(err_flag, device), handle)
+    finally:
+        if on is not None:
+            on.close()
     check(st, "moe_adapter_linear")
     return out
 

@@ -28,22 +28,21 @@ struct ExpertMapParams {
 };
 
 constexpr int kMapMaxWarps = 32;
+constexpr int kMapBatch = 8;  // groups of 32 slots whose ids a warp loads at once
 constexpr int kMapMaxCluster = 8;
 
 // Shared memory: [warps][E] counts, then places; [E] each: this CTA's counts,
-// the cluster's, the expert's first row, this CTA's first row.
-static size_t map_smem(int warps, int E) { return static_cast<size_t>(warps + 4) * E * sizeof(int); }
+// the cluster's, this CTA's first row.
+static size_t map_smem(int warps, int E) { return static_cast<size_t>(warps + 3) * E * sizeof(int); }
 
 __global__ void __launch_bounds__(kMapMaxWarps * 32) expert_map_kernel(const ExpertMapParams p) {
   extern __shared__ int map_mem[];
   __shared__ int warp_rows[kMapMaxWarps];
-  __shared__ int all_rows;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, W = blockDim.x >> 5, E = p.E;
   int* hist = map_mem;
   int* mine = map_mem + W * E;
   int* total = mine + E;
-  int* start = total + E;
-  int* first = start + E;
+  int* first = total + E;
   cg::cluster_group cluster = cg::this_cluster();
   const int C = static_cast<int>(cluster.num_blocks()), rank = static_cast<int>(cluster.block_rank());
   allow_dependent_launch();
@@ -51,25 +50,59 @@ __global__ void __launch_bounds__(kMapMaxWarps * 32) expert_map_kernel(const Exp
   __syncthreads();
   grid_dependency_wait();
 
+  // rows that no slot has stay -1: every row is filled before the cluster
+  // barrier, and the places are written after it
+  {
+    const int64_t threads = static_cast<int64_t>(C) * blockDim.x, at = static_cast<int64_t>(rank) * blockDim.x + tid;
+    const int64_t quads = (reinterpret_cast<uintptr_t>(p.row_token) & 15) == 0 ? p.n_rows / 4 : 0;
+    for (int64_t i = at; i < quads; i += threads) reinterpret_cast<int4*>(p.row_token)[i] = make_int4(-1, -1, -1, -1);
+    for (int64_t i = quads * 4 + at; i < p.n_rows; i += threads) p.row_token[i] = -1;
+  }
   // this warp's slots, whole groups of 32
   const int64_t groups = (p.slots + 31) / 32, walkers = static_cast<int64_t>(C) * W;
   const int64_t me = static_cast<int64_t>(rank) * W + warp;
   const int64_t beg = groups * me / walkers * 32, end = min(p.slots, groups * (me + 1) / walkers * 32);
   int* count = hist + warp * E;
-  for (int64_t i = beg + lane; i < end; i += 32) {
-    const int e = p.ids[i];
-    if (e >= 0 && e < E) atomicAdd(&count[e], 1);
+  int id[kMapBatch];
+  auto load = [&](int64_t g) {  // ids of the groups from slot g; E where there is none
+#pragma unroll
+    for (int b = 0; b < kMapBatch; ++b) {
+      const int64_t i = g + b * 32 + lane;
+      const unsigned e = i < end ? static_cast<unsigned>(p.ids[i]) : 0xFFFFFFFFu;
+      id[b] = e < static_cast<unsigned>(E) ? static_cast<int>(e) : E;
+    }
+  };
+  for (int64_t g = beg; g < end; g += 32 * kMapBatch) {
+    load(g);
+#pragma unroll
+    for (int b = 0; b < kMapBatch; ++b)
+      if (id[b] < E) atomicAdd(&count[id[b]], 1);
   }
   __syncthreads();
-  // over the warps: places before each warp, and this CTA's counts
-  for (int e = tid; e < E; e += blockDim.x) {
-    int at = 0;
-    for (int w = 0; w < W; ++w) {
-      const int c = hist[w * E + e];
-      hist[w * E + e] = at;
-      at += c;
+  // over the warps: places before each warp, and this CTA's counts; `parts`
+  // neighbouring threads share an expert
+  int parts = 1;
+  while (parts * 2 * E <= static_cast<int>(blockDim.x) && parts * 2 <= W) parts *= 2;
+  const int q = tid & (parts - 1), span = (W + parts - 1) / parts, w0 = min(W, q * span), w1 = min(W, w0 + span);
+  for (int e0 = 0; e0 < E; e0 += blockDim.x / parts) {
+    const int e = e0 + tid / parts;
+    int sum = 0;
+    if (e < E)
+      for (int w = w0; w < w1; ++w) sum += hist[w * E + e];
+    int at = sum;
+    for (int off = 1; off < parts; off <<= 1) {
+      const int v = __shfl_up_sync(0xFFFFFFFFu, at, off, parts);
+      if (q >= off) at += v;
     }
-    mine[e] = at;
+    if (e < E) {
+      if (q == parts - 1) mine[e] = at;
+      at -= sum;
+      for (int w = w0; w < w1; ++w) {
+        const int c = hist[w * E + e];
+        hist[w * E + e] = at;
+        at += c;
+      }
+    }
   }
   cluster_arrive_release();
   cluster_wait_acquire();
@@ -79,10 +112,13 @@ __global__ void __launch_bounds__(kMapMaxWarps * 32) expert_map_kernel(const Exp
   int rows = 0;
   for (int e = eb; e < ee; ++e) {
     int before = 0, all = 0;
-    for (int r = 0; r < C; ++r) {
-      const int c = *cluster.map_shared_rank(&mine[e], r);
-      if (r < rank) before += c;
-      all += c;
+    int c[kMapMaxCluster];
+#pragma unroll
+    for (int r = 0; r < kMapMaxCluster; ++r) c[r] = r < C ? *cluster.map_shared_rank(&mine[e], r) : 0;
+#pragma unroll
+    for (int r = 0; r < kMapMaxCluster; ++r) {
+      if (r < rank) before += c[r];
+      all += c[r];
     }
     first[e] = before;
     total[e] = all;
@@ -102,44 +138,39 @@ __global__ void __launch_bounds__(kMapMaxWarps * 32) expert_map_kernel(const Exp
   for (int w = 0; w < warp; ++w) base += warp_rows[w];
   base += upto - rows;
   for (int e = eb; e < ee; ++e) {
-    start[e] = base;
     first[e] += base;
     if (rank == 0) p.offsets[e] = base;
     base += (total[e] + p.block - 1) / p.block * p.block;
   }
-  if (tid == static_cast<int>(blockDim.x) - 1) {
-    all_rows = base;
-    if (rank == 0) p.offsets[E] = base;
-  }
+  if (tid == static_cast<int>(blockDim.x) - 1 && rank == 0) p.offsets[E] = base;
   __syncthreads();
   // places
-  for (int64_t g = beg; g < end; g += 32) {
-    const int64_t i = g + lane;
-    const int e = i < end ? p.ids[i] : -1;
-    const bool ok = e >= 0 && e < E;
-    const unsigned same = __match_any_sync(0xFFFFFFFFu, ok ? e : -1);
-    const int before = __popc(same & ((1u << lane) - 1u));
-    int row = -1;
-    if (ok) row = count[e] + before;
-    __syncwarp();
-    if (ok && before == 0) count[e] = row + __popc(same);
-    __syncwarp();
-    if (ok) {
-      row += first[e];
-      p.row_token[row] = static_cast<int>(i) / p.k;
+  const int bits = 32 - __clz(E);
+  for (int64_t g = beg; g < end; g += 32 * kMapBatch) {
+    if (end - beg > 32 * kMapBatch) load(g);  // otherwise they are still there
+#pragma unroll
+    for (int b = 0; b < kMapBatch; ++b) {
+      if (g + b * 32 >= end) break;
+      const int64_t i = g + b * 32 + lane;
+      const int e = id[b];
+      unsigned same = 0xFFFFFFFFu;  // lanes with this lane's expert
+      for (int bit = 0; bit < bits; ++bit) {
+        const unsigned set = __ballot_sync(0xFFFFFFFFu, (e >> bit) & 1);
+        same &= (e >> bit) & 1 ? set : ~set;
+      }
+      const int before = __popc(same & ((1u << lane) - 1u));
+      int row = -1;
+      if (e < E) row = count[e] + before;
+      __syncwarp();
+      if (e < E && before == 0) count[e] = row + __popc(same);
+      __syncwarp();
+      if (e < E) {
+        row += first[e];
+        p.row_token[row] = static_cast<int>(i) / p.k;
+      }
+      if (i < end) p.row_map[i] = row;
     }
-    if (i < end) p.row_map[i] = row;
   }
-  // rows that no slot has
-  if (p.block > 1) {
-    for (int e = static_cast<int>(me); e < E; e += static_cast<int>(walkers)) {
-      const int n = (total[e] + p.block - 1) / p.block * p.block;
-      for (int r = total[e] + lane; r < n; r += 32) p.row_token[start[e] + r] = -1;
-    }
-  }
-  for (int64_t r = all_rows + static_cast<int64_t>(rank) * blockDim.x + tid; r < p.n_rows;
-       r += static_cast<int64_t>(C) * blockDim.x)
-    p.row_token[r] = -1;
   cluster_wait_acquire();  // no CTA leaves while a peer may read its counts
 }
 
@@ -165,11 +196,17 @@ extern "C" int moe_expert_map(const int32_t* topk_ids, int32_t* row_map, int32_t
       !aligned(counts, 4))
     return MOE_ERR_MISALIGNED;
   ExpertMapParams p{topk_ids, row_map, row_token, offsets, counts, n_rows, T * k, static_cast<int>(E), k, block};
-  // warps for about 64 slots each, up to 32 in a CTA, then more CTAs
-  const int64_t want = (p.slots + 63) / 64;
-  const int warps = want < 4 ? 4 : want > kMapMaxWarps ? kMapMaxWarps : static_cast<int>(want);
+  // A warp for about 128 slots or 1024 rows.  Small CTAs have the shorter
+  // barriers, so the cluster grows first (8 warps each up to 8 CTAs), then the
+  // CTAs, up to 32 warps.  With 8 / 16 / 32 warps a CTA at E = 256, k = 8:
+  // T = 512 5.1 / 6.0 / 8.7 us, T = 4096 10.4 / 8.2 / 9.6 us, T = 32768
+  // 59 / 39 / 33 us.
+  int64_t want = (p.slots + 127) / 128;
+  if (want < (p.n_rows + 1023) / 1024) want = (p.n_rows + 1023) / 1024;
   int C = 1;
-  while (C < kMapMaxCluster && static_cast<int64_t>(C) * kMapMaxWarps < want) C *= 2;
+  while (C < kMapMaxCluster && static_cast<int64_t>(C) * 8 < want) C *= 2;
+  const int64_t per_cta = (want + C - 1) / C;
+  const int warps = per_cta < 8 ? 8 : per_cta > kMapMaxWarps ? kMapMaxWarps : static_cast<int>(per_cta);
   const size_t smem = map_smem(warps, p.E);
   if (smem > 48 * 1024 && cudaFuncSetAttribute(expert_map_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                static_cast<int>(map_smem(kMapMaxWarps, MOE_MAX_E))) != cudaSuccess) {

@@ -51,91 +51,8 @@ __device__ __forceinline__ double warp_sum_f64(double v) {
   return v;
 }
 
-// The choice of one token in 64 bits.  `sc` and `key` are E values each of this
-// warp's shared memory.  Lane j < k gets the j-th id and its score.
-__device__ __noinline__ void group_select_f64(const GroupRouteParams& p, const float* __restrict__ row, double* sc,
-                                              double* key, int& id, double& score) {
-  const int lane = threadIdx.x & 31;
-  const double inf = __longlong_as_double(0x7FF0000000000000ll);
-  // scores
-  double m = -inf;
-  for (int i = lane; i < p.E; i += 32) {
-    const float l = row[i];
-    const double z = isnan(l) ? -inf : static_cast<double>(l);
-    key[i] = z;
-    m = fmax(m, z);
-  }
-  double sum = 1.0;
-  if (p.softmax) {
-    m = warp_max_f64(m);
-    double part = 0.0;
-    for (int i = lane; i < p.E; i += 32) {
-      const double z = key[i];
-      const double e = m == -inf ? 0.0 : z == m ? 1.0 : exp(z - m);
-      sc[i] = e;
-      part += e;
-    }
-    sum = warp_sum_f64(part);
-    if (sum == 0.0) sum = 1.0;
-  }
-  for (int i = lane; i < p.E; i += 32) {
-    const double s = p.softmax ? sc[i] / sum : 1.0 / (1.0 + exp(-key[i]));
-    sc[i] = s;
-    if (p.bias) {
-      const double c = s + static_cast<double>(p.bias[i]);
-      key[i] = isnan(c) ? -inf : c;
-    }
-  }
-  __syncwarp();
-  // groups: the worst ones are taken out (their keys become NaN)
-  const int size = p.E / p.n_group;
-  if (p.topk_group < p.n_group) {
-    double gs = -inf;
-    if (lane < p.n_group) {
-      const bool by_key = p.bias != nullptr || p.group_top == 1;
-      double b1 = -inf, b2 = -inf;
-      for (int i = lane * size; i < (lane + 1) * size; ++i) {
-        const double v = by_key ? key[i] : sc[i];
-        if (v > b1) { b2 = b1; b1 = v; }
-        else if (v > b2) b2 = v;
-      }
-      gs = p.group_top == 2 && size > 1 ? b1 + b2 : b1;
-      if (isnan(gs)) gs = -inf;
-    }
-    int rank = 0;
-    for (int g = 0; g < p.n_group; ++g) {
-      const double o = __shfl_sync(0xFFFFFFFFu, gs, g);
-      rank += (o > gs || (o == gs && g < lane)) ? 1 : 0;
-    }
-    const unsigned in = __ballot_sync(0xFFFFFFFFu, lane < p.n_group && rank < p.topk_group);
-    for (int i = lane; i < p.E; i += 32)
-      if (!((in >> (i / size)) & 1u)) key[i] = __longlong_as_double(0x7FF8000000000000ll);
-    __syncwarp();
-  }
-  // k rounds: the largest key, the lowest expert among equals
-  id = 0;
-  score = 0.0;
-  for (int r = 0; r < p.k; ++r) {
-    double b = -inf;
-    int at = 0x7FFFFFFF;
-    for (int i = lane; i < p.E; i += 32) {
-      const double v = key[i];
-      if (v > b || (v == b && i < at)) { b = v; at = i; }
-    }
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) {
-      const double ob = __shfl_xor_sync(0xFFFFFFFFu, b, off);
-      const int oa = __shfl_xor_sync(0xFFFFFFFFu, at, off);
-      if (oa != 0x7FFFFFFF && (at == 0x7FFFFFFF || ob > b || (ob == b && oa < at))) { b = ob; at = oa; }
-    }
-    if (lane == r) { id = at; score = sc[at]; }
-    __syncwarp();
-    if (lane == 0) key[at] = __longlong_as_double(0x7FF8000000000000ll);
-    __syncwarp();
-  }
-}
-
-// Order-preserving key of a float without NaN; -0 and +0 share one.
+// Order-preserving keys of numbers (NaN counts as -inf; -0 and +0 share one).
+// Every key is above 0.
 __device__ __forceinline__ uint32_t order_key(float f) {
   uint32_t u = __float_as_uint(f);
   if ((u << 1) == 0u) u = 0u;
@@ -144,6 +61,101 @@ __device__ __forceinline__ uint32_t order_key(float f) {
 __device__ __forceinline__ float order_value(uint32_t k) {
   return __uint_as_float((k & 0x80000000u) ? (k & 0x7FFFFFFFu) : ~k);
 }
+__device__ __forceinline__ uint64_t order_key64(double d) {
+  uint64_t u = static_cast<uint64_t>(__double_as_longlong(d));
+  if ((u << 1) > 0xFFE0000000000000ull) u = 0xFFF0000000000000ull;
+  if ((u << 1) == 0u) u = 0u;
+  return (u >> 63) ? ~u : (u | 0x8000000000000000ull);
+}
+
+// A logit with NaN as -inf.
+__device__ __forceinline__ float logit(float l) { return isnan(l) ? __int_as_float(0xFF800000) : l; }
+
+__device__ __forceinline__ double sigmoid_f64(float l) { return 1.0 / (1.0 + exp(-static_cast<double>(l))); }
+
+// The choice of one token in 64 bits.  `sc` and `key` are E values each of
+// this warp's shared memory.  Lane j < k gets the j-th id and its score.  The
+// 64-bit pipe is narrow, so it computes the values, and their integer keys are
+// compared.
+__device__ __noinline__ void group_select_f64(const GroupRouteParams& p, const float* __restrict__ row, double* sc,
+                                              uint64_t* key, int& id, double& score) {
+  const int lane = threadIdx.x & 31;
+  const double inf = __longlong_as_double(0x7FF0000000000000ll);
+  double m = -inf, sum = 1.0;
+  if (p.softmax) {
+    for (int i = lane; i < p.E; i += 32) m = fmax(m, static_cast<double>(logit(row[i])));
+    m = warp_max_f64(m);
+    double part = 0.0;
+    for (int i = lane; i < p.E; i += 32) {
+      const double z = logit(row[i]);
+      const double e = m == -inf ? 0.0 : z == m ? 1.0 : exp(z - m);
+      sc[i] = e;
+      part += e;
+    }
+    sum = warp_sum_f64(part);
+    if (sum == 0.0) sum = 1.0;
+  }
+  const int size = p.E / p.n_group;
+  const bool grouped = p.topk_group < p.n_group;
+  for (int i = lane; i < p.E; i += 32) {
+    const float l = logit(row[i]);
+    const double s = p.softmax ? sc[i] / sum : sigmoid_f64(l);
+    sc[i] = s;
+    key[i] = order_key64(p.bias ? s + static_cast<double>(p.bias[i]) : static_cast<double>(l));
+  }
+  __syncwarp();
+  if (grouped) {
+    // group scores; the keys of the groups that do not stay become 0
+    double gs = -inf;
+    if (lane < p.n_group) {
+      uint64_t k1 = 0, k2 = 0;
+      int i1 = -1, i2 = -1;
+      for (int i = lane * size; i < (lane + 1) * size; ++i) {
+        // without a bias the scores order like the logits, whose keys these are
+        const uint64_t v = key[i];
+        if (v > k1) { k2 = k1; i2 = i1; k1 = v; i1 = i; }
+        else if (v > k2) { k2 = v; i2 = i; }
+      }
+      const bool by_logit = !p.bias && p.group_top == 1;
+      auto value = [&](int i) {
+        return by_logit ? static_cast<double>(logit(row[i])) : sc[i] + (p.bias ? static_cast<double>(p.bias[i]) : 0.0);
+      };
+      gs = value(i1);
+      if (p.group_top == 2 && size > 1) gs += value(i2);
+    }
+    const uint64_t gk = lane < p.n_group ? order_key64(gs) : 0ull;
+    int rank = 0;
+    for (int g = 0; g < p.n_group; ++g) {
+      const uint64_t o = __shfl_sync(0xFFFFFFFFu, gk, g);
+      rank += (o > gk || (o == gk && g < lane)) ? 1 : 0;
+    }
+    const unsigned in = __ballot_sync(0xFFFFFFFFu, lane < p.n_group && rank < p.topk_group);
+    for (int i = lane; i < p.E; i += 32)
+      if (!((in >> (i / size)) & 1u)) key[i] = 0ull;
+    __syncwarp();
+  }
+  // k rounds: the largest key, the lowest expert among equals
+  id = 0;
+  score = 0.0;
+  for (int r = 0; r < p.k; ++r) {
+    uint64_t b = 0ull;
+    int at = 0x7FFFFFFF;
+    for (int i = lane; i < p.E; i += 32) {
+      const uint64_t v = key[i];
+      if (v > b) { b = v; at = i; }
+    }
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) {
+      const uint64_t ob = __shfl_xor_sync(0xFFFFFFFFu, b, off);
+      const int oa = __shfl_xor_sync(0xFFFFFFFFu, at, off);
+      if (ob > b || (ob == b && oa < at)) { b = ob; at = oa; }
+    }
+    if (lane == r) { id = at; score = sc[at]; }
+    __syncwarp();
+    if (lane == 0) key[at] = 0ull;
+    __syncwarp();
+  }
+}
 
 // Adds v to the two largest values b1 >= b2 so far.
 __device__ __forceinline__ void top_two(float& b1, float& b2, float v) {
@@ -151,43 +163,52 @@ __device__ __forceinline__ void top_two(float& b1, float& b2, float v) {
   b1 = fmaxf(b1, v);
 }
 
-// The two halves of a candidate: a larger value is the better choice (larger
-// key, then lower expert).
+// A candidate: a larger value is the better choice (larger key, then lower
+// expert).
 __device__ __forceinline__ uint64_t candidate(float v, int expert) {
   return (static_cast<uint64_t>(order_key(v)) << 32) | static_cast<uint32_t>(0xFFFFFFFFu - static_cast<uint32_t>(expert));
 }
-__device__ __forceinline__ int candidate_expert(uint64_t c) { return static_cast<int>(0xFFFFFFFFu - static_cast<uint32_t>(c)); }
+__device__ __forceinline__ int candidate_expert(uint64_t c) {
+  return static_cast<int>(0xFFFFFFFFu - static_cast<uint32_t>(c));
+}
+
+// Whether a >= b may be in the wrong order.  The error of a choice value is
+// `doubt` / 2 and one rounding of its size.
+__device__ __forceinline__ bool too_close(float a, float b, float doubt) {
+  const float inf = __int_as_float(0x7F800000);
+  return !(a - b > doubt + 4.7683716e-7f * fmaxf(fabsf(a), fabsf(b))) && !(b == -inf && a > -inf);
+}
 
 // Shared memory of one warp, in bytes: the larger of the 32-bit selection's
 // arrays and the 64-bit one's.
 __host__ __device__ constexpr int route_list_at(int E) { return (E * 4 + (E + E / 32 + 1) * 4 + 15) / 16 * 16; }
 __host__ __device__ constexpr int route_smem(int E) {
-  const int fast = route_list_at(E) + (kCandidates + 40) * 8 + 128, slow = E * 16;
+  const int fast = route_list_at(E) + (kCandidates + 8 + 40) * 8 + 128 + kCandidates * 4, slow = E * 16;
   return (fast > slow ? fast : slow) / 16 * 16 + 16;
 }
 
-template <int EPL>
+// SOFTMAX, BIAS, GROUPS: which steps the call needs.
+template <int EPL, bool SOFTMAX, bool BIAS, bool GROUPS>
 __global__ void __launch_bounds__(kGroupRouteWarps * 32) group_route_kernel(const GroupRouteParams p) {
   extern __shared__ __align__(16) uint8_t route_mem[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int64_t t = static_cast<int64_t>(blockIdx.x) * kGroupRouteWarps + warp;
   const float inf = __int_as_float(0x7F800000);
+  uint8_t* mem = route_mem + static_cast<size_t>(warp) * route_smem(p.E);
+  float* lv = reinterpret_cast<float*>(mem);         // [E] logits
+  float* kv = lv + p.E;                              // [E + E / 32] choice values, one word of padding per 32
+  uint64_t* list = reinterpret_cast<uint64_t*>(mem + route_list_at(p.E));
+  uint64_t* best = list + kCandidates + 8;           // [k + 1]
+  int* chosen = reinterpret_cast<int*>(best + 40);   // [32] groups that stay
+  int* who = chosen + 32;                            // [kCandidates] experts compared in 64 bits
+  const float* row = p.logits + t * p.E;
   allow_dependent_launch();
   // the bias is a parameter, but it too is read after the wait: a balancing
   // step may just have written it
   grid_dependency_wait();
   if (t >= p.T) return;
-  uint8_t* mem = route_mem + static_cast<size_t>(warp) * route_smem(p.E);
-  float* sv = reinterpret_cast<float*>(mem);         // [E] scores
-  float* kv = sv + p.E;                              // [E + E / 32] choice values, one word of padding per 32
-  uint64_t* list = reinterpret_cast<uint64_t*>(mem + route_list_at(p.E));
-  uint64_t* best = list + kCandidates;               // [k + 1]
-  int* chosen = reinterpret_cast<int*>(best + 40);   // [32] groups that stay
-  const float* row = p.logits + t * p.E;
 
-  // scores and choice values; `doubt`: how far apart two choice values of
-  // this row must lie, beside 2^-22 of their size, to be in the right order
-  float key[EPL];
+  float key[EPL], bias[BIAS ? EPL : 1];
   int num[EPL];  // the expert of each key; -1: none
   float m = -inf;
 #pragma unroll
@@ -195,42 +216,54 @@ __global__ void __launch_bounds__(kGroupRouteWarps * 32) group_route_kernel(cons
     const int i = lane + 32 * s;
     num[s] = i < p.E ? i : -1;
     key[s] = i < p.E ? row[i] : -inf;
-    if (isnan(key[s])) key[s] = -inf;
-    m = fmaxf(m, key[s]);
+    if (BIAS) bias[s] = i < p.E ? p.bias[i] : 0.f;
   }
+#pragma unroll
+  for (int s = 0; s < EPL; ++s) {
+    key[s] = logit(key[s]);
+    if (SOFTMAX) m = fmaxf(m, key[s]);
+    if (num[s] >= 0) lv[num[s]] = key[s];
+  }
+  // Choice values from the short exponential and quotient.  A sigmoid: the
+  // exponential within 2^-21 + 2^-24 |l| of itself, which moves s by s (1 - s)
+  // of that (s (1 - s) <= 1/4, times |l| <= 0.23), and the sum and quotient
+  // 5 * 2^-24: together under 2^-21.  A softmax term: 2^-21 + 2^-23 |l - m| of
+  // itself, s |l - m| < 1/2, the sum of E terms and the quotient (E / 32 + 12)
+  // 2^-24.  Two values: twice that.
+  const float doubt = SOFTMAX ? 2.f * (8.f + 1.f + EPL + 12.f) * 5.9604645e-8f : 9.536743e-7f;
   float inv = 1.f;
-  if (p.softmax) {
+  if (SOFTMAX) {
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, off));
+  }
+  // Softmax terms, for the choice and for the weights' sum: expf where the
+  // weights depend on them.
+  float e[SOFTMAX ? EPL : 1];
+  if (SOFTMAX) {
     float z = 0.f;
 #pragma unroll
-    for (int s = 0; s < EPL; ++s)
-      if (num[s] >= 0 && m > -inf) z += key[s] == m ? 1.f : expf(key[s] - m);
+    for (int s = 0; s < EPL; ++s) {
+      e[s] = m == -inf || num[s] < 0 ? 0.f : key[s] == m ? 1.f : expf(key[s] - m);
+      z += e[s];
+    }
     z = warp_sum(z);
     inv = z > 0.f ? 1.f / z : 0.f;
   }
-  // Sigmoid: expf 2 ulp, sum, quotient: within 2^-22 of a value below 1.  A
-  // softmax term: 2^-24 (|l - m| + E / 32 + 12) of itself, and s |l - m| < 1.
-  // Two values: twice that.
-  const float doubt = p.softmax ? 2.f * (1.f + EPL + 12.f) * 5.9604645e-8f : 4.7683716e-7f;
+  if (BIAS) {
 #pragma unroll
-  for (int s = 0; s < EPL; ++s) {
-    if (num[s] < 0) continue;
-    const float l = key[s];
-    const float sc = p.softmax ? (m == -inf ? 0.f : (l == m ? 1.f : expf(l - m)) * inv) : 1.f / (1.f + expf(-l));
-    sv[num[s]] = sc;
-    if (p.bias) {
-      key[s] = sc + p.bias[num[s]];
+    for (int s = 0; s < EPL; ++s) {
+      const float sc = SOFTMAX ? e[s] * inv : __fdividef(1.f, 1.f + __expf(fminf(-key[s], 80.f)));
+      key[s] = sc + bias[s];
       if (isnan(key[s])) key[s] = -inf;
     }
   }
 
   bool exactly = false;  // the whole row again in 64 bits
   int live = p.E;        // keys in the choice
-  if (p.topk_group < p.n_group) {
+  if (GROUPS) {
     // group scores: P lanes a group
     const int size = p.E / p.n_group;
-    const bool by_key = p.bias != nullptr || p.group_top == 1;
+    const bool by_key = BIAS || p.group_top == 1;
 #pragma unroll
     for (int s = 0; s < EPL; ++s)
       if (num[s] >= 0) kv[num[s] + (num[s] >> 5)] = key[s];
@@ -240,9 +273,10 @@ __global__ void __launch_bounds__(kGroupRouteWarps * 32) group_route_kernel(cons
     const int g = lane / P, sub = lane & (P - 1);
     float b1 = -inf, b2 = -inf;
     if (g < p.n_group) {
+#pragma unroll 4
       for (int j = sub; j < size; j += P) {
         const int i = g * size + j;
-        top_two(b1, b2, by_key ? kv[i + (i >> 5)] : sv[i]);
+        top_two(b1, b2, kv[i + (i >> 5)]);
       }
     }
     for (int d = 1; d < P; d <<= 1) {
@@ -250,22 +284,67 @@ __global__ void __launch_bounds__(kGroupRouteWarps * 32) group_route_kernel(cons
       top_two(b1, b2, o1);
       top_two(b1, b2, o2);
     }
-    float gs = p.group_top == 2 && size > 1 ? b1 + b2 : b1;
+    const bool two = p.group_top == 2 && size > 1;
+    if (!by_key) {  // without a bias the best logits have the best scores
+      b1 = SOFTMAX ? (m == -inf ? 0.f : (b1 == m ? 1.f : expf(b1 - m)) * inv) : 1.f / (1.f + expf(-b1));
+      b2 = SOFTMAX ? (m == -inf ? 0.f : (b2 == m ? 1.f : expf(b2 - m)) * inv) : 1.f / (1.f + expf(-b2));
+    }
+    float gs = two ? b1 + b2 : b1;
     if (isnan(gs)) gs = -inf;
     int rank = 0;
+#pragma unroll 4
     for (int o = 0; o < p.n_group; ++o) {
       const float v = __shfl_sync(0xFFFFFFFFu, gs, o * P);
       rank += (v > gs || (v == gs && o < g)) ? 1 : 0;
     }
-    const bool in = g < p.n_group && rank < p.topk_group;
-    if (p.bias != nullptr || p.group_top == 2) {  // otherwise the scores are logits, and exact
-      float lo = in ? gs : inf, hi = in || g >= p.n_group ? -inf : gs;
-#pragma unroll
-      for (int off = 16; off > 0; off >>= 1) {
-        lo = fminf(lo, __shfl_xor_sync(0xFFFFFFFFu, lo, off));
-        hi = fmaxf(hi, __shfl_xor_sync(0xFFFFFFFFu, hi, off));
+    bool in = g < p.n_group && rank < p.topk_group;
+    if (BIAS || p.group_top == 2) {  // otherwise the scores are logits, and exact
+      const unsigned last = __ballot_sync(0xFFFFFFFFu, g < p.n_group && rank == p.topk_group - 1);
+      const unsigned next = __ballot_sync(0xFFFFFFFFu, g < p.n_group && rank == p.topk_group);
+      const float lo = __shfl_sync(0xFFFFFFFFu, gs, __ffs(last) - 1), hi = __shfl_sync(0xFFFFFFFFu, gs, __ffs(next) - 1);
+      if (too_close(lo, hi, 2.f * doubt)) {
+        if (SOFTMAX || !BIAS) {
+          exactly = true;
+        } else {
+          // the values that may be among a group's best, again in 64 bits
+          const float need = two ? b2 : b1;
+          const float lim = need > -inf ? need - (doubt + 4.7683716e-7f * fabsf(need)) : need;
+          int n = 0;
+          for (int j = 0; j < (size + P - 1) / P; ++j) {
+            const int i = g * size + j * P + sub;
+            const bool take = g < p.n_group && j * P + sub < size && kv[i + (i >> 5)] >= lim;
+            const unsigned bal = __ballot_sync(0xFFFFFFFFu, take);
+            const int at = n + __popc(bal & ((1u << lane) - 1u));
+            if (take && at < kCandidates) who[at] = i;
+            n += __popc(bal);
+          }
+          exactly = n > kCandidates;
+          if (!exactly) {
+            __syncwarp();
+            double* val = reinterpret_cast<double*>(list);
+            for (int at = lane; at < n; at += 32) val[at] = sigmoid_f64(lv[who[at]]) + static_cast<double>(p.bias[who[at]]);
+            __syncwarp();
+            uint64_t k1 = 0, k2 = 0;
+            double v1 = 0.0, v2 = 0.0;
+            for (int at = 0; at < n; ++at) {
+              const unsigned d = static_cast<unsigned>(who[at] - g * size);
+              if (d < static_cast<unsigned>(size)) {
+                const double v = val[at];
+                const uint64_t k = order_key64(v);
+                if (k > k1) { k2 = k1; v2 = v1; k1 = k; v1 = v; }
+                else if (k > k2) { k2 = k; v2 = v; }
+              }
+            }
+            const uint64_t gk = g < p.n_group ? order_key64(two ? v1 + v2 : v1) : 0ull;
+            rank = 0;
+            for (int o = 0; o < p.n_group; ++o) {
+              const uint64_t v = __shfl_sync(0xFFFFFFFFu, gk, o * P);
+              rank += (v > gk || (v == gk && o < g)) ? 1 : 0;
+            }
+            in = g < p.n_group && rank < p.topk_group;
+          }
+        }
       }
-      exactly = !(lo - hi > 2.f * doubt + 4.7683716e-7f * fmaxf(fabsf(lo), fabsf(hi))) && !(hi == -inf && lo > -inf);
     }
     const unsigned heads = __ballot_sync(0xFFFFFFFFu, in && sub == 0);
     if (in && sub == 0) chosen[__popc(heads & ((1u << lane) - 1u))] = g;
@@ -287,7 +366,6 @@ __global__ void __launch_bounds__(kGroupRouteWarps * 32) group_route_kernel(cons
   }
 
   int id = 0;
-  float score = 0.f;
   int n = 0;
   if (!exactly) {
     // tau: the smallest of G >= k maxima over G groups of lanes is met by at
@@ -297,30 +375,38 @@ __global__ void __launch_bounds__(kGroupRouteWarps * 32) group_route_kernel(cons
 #pragma unroll
     for (int s = 1; s < EPL; ++s) tau = fmaxf(tau, key[s]);
     for (int d = 1; d < 32 && 32 / (2 * d) >= p.k; d <<= 1) tau = fmaxf(tau, __shfl_xor_sync(0xFFFFFFFFu, tau, d));
+    tau = order_value(__reduce_min_sync(0xFFFFFFFFu, order_key(tau)));
+    const float lim = BIAS && tau > -inf ? tau - (doubt + 4.7683716e-7f * fabsf(tau)) : tau;
+    unsigned bal[EPL];
 #pragma unroll
-    for (int off = 16; off > 0; off >>= 1) tau = fminf(tau, __shfl_xor_sync(0xFFFFFFFFu, tau, off));
-    const float lim = p.bias && tau > -inf ? tau - (doubt + 4.7683716e-7f * fabsf(tau)) : tau;
+    for (int s = 0; s < EPL; ++s) bal[s] = __ballot_sync(0xFFFFFFFFu, num[s] >= 0 && key[s] >= lim);
 #pragma unroll
     for (int s = 0; s < EPL; ++s) {
-      const bool take = num[s] >= 0 && key[s] >= lim;
-      const unsigned bal = __ballot_sync(0xFFFFFFFFu, take);
-      const int at = n + __popc(bal & ((1u << lane) - 1u));
-      if (take && at < kCandidates) list[at] = candidate(key[s], num[s]);
-      n += __popc(bal);
+      const int at = n + __popc(bal[s] & ((1u << lane) - 1u));
+      if (((bal[s] >> lane) & 1u) && at < kCandidates) list[at] = candidate(key[s], num[s]);
+      n += __popc(bal[s]);
     }
     exactly = n > kCandidates;
   }
   if (!exactly) {
-    // rank = how many candidates beat this one (they are all different)
+    // rank = how many candidates beat this one (they are all different); the
+    // list is padded with 0, below every candidate, to whole blocks of 8
+    const int blocks = (n + 7) >> 3;
+    if (lane < 8 * blocks - n) list[n + lane] = 0ull;
     __syncwarp();
+    const ulonglong2* pairs = reinterpret_cast<const ulonglong2*>(list);
     for (int b = 0; b < n; b += 64) {
       const uint64_t v0 = b + lane < n ? list[b + lane] : ~0ull, v1 = b + lane + 32 < n ? list[b + lane + 32] : ~0ull;
       int r0 = 0, r1 = 0;
-#pragma unroll 4
-      for (int c = 0; c < n; ++c) {
-        const uint64_t o = list[c];
-        r0 += o > v0 ? 1 : 0;
-        r1 += o > v1 ? 1 : 0;
+      for (int c = 0; c < blocks; ++c) {
+        ulonglong2 o[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) o[i] = pairs[4 * c + i];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          r0 += (o[i].x > v0 ? 1 : 0) + (o[i].y > v0 ? 1 : 0);
+          r1 += (o[i].x > v1 ? 1 : 0) + (o[i].y > v1 ? 1 : 0);
+        }
       }
       if (b + lane < n && r0 <= p.k) best[r0] = v0;
       if (b + lane + 32 < n && r1 <= p.k) best[r1] = v1;
@@ -328,68 +414,54 @@ __global__ void __launch_bounds__(kGroupRouteWarps * 32) group_route_kernel(cons
     __syncwarp();
     const uint64_t mine = lane < p.k ? best[lane] : 0ull;
     id = lane < p.k ? candidate_expert(mine) : 0;
-    if (p.bias) {
+    if (BIAS) {
       bool close = false;
       if (lane < p.k && lane + 1 < n) {
         const uint64_t next = best[lane + 1];
-        const float a = order_value(static_cast<uint32_t>(mine >> 32)), b = order_value(static_cast<uint32_t>(next >> 32));
-        close = !(a - b > doubt + 4.7683716e-7f * fmaxf(fabsf(a), fabsf(b))) && !(b == -inf && a > -inf);
+        close = too_close(order_value(static_cast<uint32_t>(mine >> 32)),
+                          order_value(static_cast<uint32_t>(next >> 32)), doubt);
         if (close) {  // the same logit and bias are a tie in any precision
           const int o = candidate_expert(next);
-          close = row[id] != row[o] || p.bias[id] != p.bias[o];
+          close = lv[id] != lv[o] || p.bias[id] != p.bias[o];
         }
       }
       if (__any_sync(0xFFFFFFFFu, close)) {
-        if (p.softmax) {
+        if (SOFTMAX) {
           exactly = true;
         } else {
-          // the candidates again in 64 bits: value v, ties to the lower expert
-          double* exact = reinterpret_cast<double*>(list);
-          const int per = (n + 31) / 32;
-          for (int c = 0; c < per; ++c) {
-            const int at = c * 32 + lane;
-            int e = -1;
-            double v = 0.0;
-            if (at < n) {
-              e = candidate_expert(list[at]);
-              const double z = isnan(row[e]) ? -__longlong_as_double(0x7FF0000000000000ll) : static_cast<double>(row[e]);
-              v = 1.0 / (1.0 + exp(-z)) + static_cast<double>(p.bias[e]);
-              if (isnan(v)) v = __longlong_as_double(0xFFF0000000000000ll);
-            }
-            __syncwarp();
-            if (at < n) {
-              exact[at] = v;
-              reinterpret_cast<int*>(kv)[at] = e;
-            }
+          // the candidates again in 64 bits
+          for (int at = lane; at < n; at += 32) {
+            const int x = candidate_expert(list[at]);
+            who[at] = x;
+            list[at] = order_key64(sigmoid_f64(lv[x]) + static_cast<double>(p.bias[x]));
           }
           __syncwarp();
-          for (int c = 0; c < per; ++c) {
-            const int at = c * 32 + lane;
-            if (at >= n) continue;
-            const double v = exact[at];
-            const int e = reinterpret_cast<int*>(kv)[at];
+          for (int at = lane; at < n; at += 32) {
+            const uint64_t v = list[at];
+            const int x = who[at];
             int r = 0;
             for (int o = 0; o < n; ++o) {
-              const double u = exact[o];
-              r += (u > v || (u == v && reinterpret_cast<int*>(kv)[o] < e)) ? 1 : 0;
+              const uint64_t u = list[o];
+              r += (u > v || (u == v && who[o] < x)) ? 1 : 0;
             }
-            if (r < p.k) chosen[r] = e;
+            if (r < p.k) best[r] = static_cast<uint64_t>(x);
           }
           __syncwarp();
-          if (lane < p.k) id = chosen[lane];
+          if (lane < p.k) id = static_cast<int>(best[lane]);
         }
       }
     }
   }
+  float w = 0.f;
   if (exactly) {
     double s64;
     __syncwarp();
-    group_select_f64(p, row, reinterpret_cast<double*>(mem), reinterpret_cast<double*>(mem) + p.E, id, s64);
-    score = static_cast<float>(s64);
-  } else {
-    score = lane < p.k ? sv[id] : 0.f;
+    group_select_f64(p, row, reinterpret_cast<double*>(mem), reinterpret_cast<uint64_t*>(mem) + p.E, id, s64);
+    if (lane < p.k) w = static_cast<float>(s64);
+  } else if (lane < p.k) {
+    const float l = lv[id];
+    w = SOFTMAX ? (m == -inf ? 0.f : (l == m ? 1.f : expf(l - m)) * inv) : 1.f / (1.f + expf(-l));
   }
-  float w = lane < p.k ? score : 0.f;
   if (p.renorm) {
     const float sum = warp_sum(w);
     w = sum > 0.f ? w / sum : 0.f;
@@ -400,11 +472,12 @@ __global__ void __launch_bounds__(kGroupRouteWarps * 32) group_route_kernel(cons
   }
 }
 
-template <int EPL>
+template <int EPL, bool SOFTMAX, bool BIAS, bool GROUPS>
 static cudaError_t launch_group_route(const GroupRouteParams& p, cudaStream_t stream) {
   const int smem = kGroupRouteWarps * route_smem(p.E);
+  const auto kernel = group_route_kernel<EPL, SOFTMAX, BIAS, GROUPS>;
   if (smem > 48 * 1024) {
-    const cudaError_t e = cudaFuncSetAttribute(group_route_kernel<EPL>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
   }
   cudaLaunchConfig_t cfg = {};
@@ -415,7 +488,18 @@ static cudaError_t launch_group_route(const GroupRouteParams& p, cudaStream_t st
   cudaLaunchAttribute attr[1] = {pdl_attribute()};
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, group_route_kernel<EPL>, p);
+  return cudaLaunchKernelEx(&cfg, kernel, p);
+}
+
+template <int EPL>
+static cudaError_t launch_group_route(const GroupRouteParams& p, cudaStream_t stream) {
+  const bool g = p.topk_group < p.n_group;
+  if (p.softmax) {
+    if (p.bias) return g ? launch_group_route<EPL, true, true, true>(p, stream) : launch_group_route<EPL, true, true, false>(p, stream);
+    return g ? launch_group_route<EPL, true, false, true>(p, stream) : launch_group_route<EPL, true, false, false>(p, stream);
+  }
+  if (p.bias) return g ? launch_group_route<EPL, false, true, true>(p, stream) : launch_group_route<EPL, false, true, false>(p, stream);
+  return g ? launch_group_route<EPL, false, false, true>(p, stream) : launch_group_route<EPL, false, false, false>(p, stream);
 }
 
 }  // namespace moe
@@ -438,11 +522,9 @@ extern "C" int moe_group_topk_route(const float* logits, const float* bias, int3
   GroupRouteParams p{logits, bias, topk_ids, topk_w, static_cast<int>(T), static_cast<int>(E), k, n_group,
                      topk_group, group_top, score_fn == MOE_SCORE_SOFTMAX, renormalize, routed_scale};
   cudaError_t e;
-  if (E <= 32) e = launch_group_route<1>(p, stream);
-  else if (E <= 64) e = launch_group_route<2>(p, stream);
+  if (E <= 64) e = launch_group_route<2>(p, stream);
   else if (E <= 128) e = launch_group_route<4>(p, stream);
   else if (E <= 256) e = launch_group_route<8>(p, stream);
-  else if (E <= 512) e = launch_group_route<16>(p, stream);
   else e = launch_group_route<32>(p, stream);
   if (e != cudaSuccess) {
     (void)cudaGetLastError();
