@@ -1,0 +1,859 @@
+// Products of row segments with their experts' weights on the 5th-generation
+// tensor cores: out[r, :] = act(W_e x[src(r)]) for the rows r of segment e
+// (device code and launch helpers; expert_gemm.cu and adapter_gemm.cu hold the
+// calls).
+//
+// The weights are the M side (UMMA M = 128 weight rows) and the rows the N
+// side with an N of the segment's own size (16 .. 256 in steps of 16), so a
+// batch of few rows an expert streams each weight once at the HBM's rate, and
+// a large one wastes less than 16 columns a tile.  Persistent CTAs, one per SM:
+//  - warp 0 streams 64-wide K blocks of the weights (one TMA copy a stage) and,
+//    without a token list, of the rows into a ring of stages of 128-byte
+//    swizzled rows;
+//  - warp 1 owns the tensor memory, two accumulators of 256 columns, and one
+//    lane issues the MMAs;
+//  - warps 2..5 read the finished accumulator while the next tile's MMAs run,
+//    apply the activation to the FP32 sums and store BF16 once;
+//  - with a token list, tiles of up to 32 rows are gathered by warp 0 (TMA, four
+//    rows a copy), larger ones by warps 6..9 with 16-byte asynchronous copies
+//    (eight lanes a row of the stage) that arrive on the stage's own barrier as
+//    they land, and warp 10 passes that on behind a proxy fence.  (The fence
+//    waits for its thread's copies in flight: in the copying warps it left one
+//    stage in flight.  A TMA gather costs the copy engine about 50 cycles
+//    whatever its size, so 64 a K block took 13.8 ms at T = 8192 against 3.0;
+//    at T = 64 the relay's latency costs 2053 us against @G4@.)
+// With SwiGLU a tile holds 64 gate and the 64 matching up rows, interleaved by
+// 16, so that a gate and its up sit 16 tensor-memory lanes apart, in one warp.
+//
+// Large segments run in pairs of CTAs (cta_group::2): 256 weight rows and up
+// to 256 rows a tile, each CTA loading its 128 weight rows and half of the
+// rows, so that every operand byte is read once per pair.
+//
+// The tile list (segments x row tiles x weight tiles) is made on the device
+// from the counts: every CTA scans them.  Single CTAs take row tiles as wide
+// as the mean segment asks for (fewer columns leave room for more stages in
+// flight).  Whole rounds of the list go round-robin over the CTAs, so that the
+// weight tiles of a segment run at the same time and share its rows in the L2;
+// the last, partial round is split over all CTAs along K, the pieces are left
+// as FP32 partial tiles, and a second small kernel adds them in order (no
+// atomics: the same inputs give the same bits).  Pairs take whole tiles.
+//
+// What becomes of the sums is the kernel's Out:
+//  - kRows    act, one rounding, row r of the output;
+//  - kLow     scaled by the segment, left as two BF16 parts (value and rest): the
+//             low-rank product of an adapter, 16 significant bits;
+//  - kParts   every piece left as an FP32 partial tile, for the caller's own
+//             last kernel;
+//  - kScatter rows sorted by adapter, every segment starting on a multiple of
+//             16 rows: behind a tile's K blocks come, for each adapter that has
+//             rows in the tile, its B against the two parts of its low-rank
+//             product, added to that adapter's columns only (so no other token
+//             can see it); act, one rounding, the row's token of the output.
+#pragma once
+
+#include <atomic>
+
+#include "expert_gemm.h"
+#include "host_util.h"
+#include "umma.cuh"
+
+namespace moe {
+
+namespace {
+
+constexpr int kMaxStages = 12;
+constexpr int kRingBytes = 200 * 1024;
+constexpr int kSoloRows = 128;  // most rows of a single CTA's tile
+constexpr int kPairRows = 256;  // rows of a pair's tile
+constexpr int kAccCols = 256;
+constexpr int kLoaders = 4;     // gathering warps
+
+constexpr int threads_of(bool gather) { return 192 + (gather ? 32 * (kLoaders + 1) : 0); }
+
+enum Out { kRows, kLow, kParts, kScatter };
+
+struct GemmParams {
+  const uint16_t* x;
+  const int32_t* row_token;
+  const int32_t* offsets;
+  const int32_t* counts;
+  uint16_t* out;
+  float* partial;
+  int32_t* err_flag;
+  int64_t n_rows;
+  int n_x;
+  int E, n_out, K;
+  int slot_rows;  // rows of a partial tile's slot
+  int weave;      // SwiGLU: one copy brings the whole weight tile (n_out a multiple of 16)
+  int withhold;   // test hook: the K block CTA 0 never loads, or -1
+  int wait_late;  // the inputs are ready at the start: wait for the previous kernel at the end
+  // adapters
+  const float* scale;     // kLow: [E] factors
+  uint16_t* low[2];       // kLow, kScatter: [n_rows, R] value and rest
+  const int32_t* seg;     // kScatter: [segs + 1] first rows by adapter, then the end
+  int segs, R;            // kScatter: the last segment's rows have no adapter
+};
+
+struct Barriers {
+  uint64_t full[kMaxStages], empty[kMaxStages];
+  uint64_t landed[kMaxStages];  // gathered rows
+  uint64_t acc_full[2], acc_empty[2];
+  uint64_t drained;
+  uint32_t tmem_base;
+  int abort_flag;
+  int bn, few;
+};
+
+__host__ __device__ inline int round_up(int v, int m) { return (v + m - 1) / m * m; }
+
+// The tile list in shared memory: per segment its first row, its rows, and the
+// row tiles before it.
+struct Tiles {
+  int* start;
+  int* count;
+  int* before;  // E + 1
+};
+
+// Rows per tile of single CTAs, from the mean rows of the segments that have
+// any: the smallest of 32, 64, 128 that leaves room for a segment a half larger.
+__device__ __forceinline__ int tile_rows(int mean) {
+  const int want = mean + (mean + 1) / 2;
+  return want <= 32 ? 32 : want <= 64 ? 64 : kSoloRows;
+}
+
+// A gather of up to this mean of rows is TMA's.
+constexpr int kFewRows = 4;
+
+// Fills the tile list; every thread of the block calls it.  Afterwards *bn_out
+// holds the rows per tile and *few_out whether the segments have few rows.
+template <bool PAIR>
+__device__ void list_tiles(const GemmParams& p, Tiles t, int* bn_out, int* few_out, bool report) {
+  for (int e = threadIdx.x; e < p.E; e += blockDim.x) {
+    int64_t beg = 0, cnt = p.seg ? p.seg[p.segs] : p.n_rows;
+    if (p.offsets) {
+      beg = p.offsets[e];
+      cnt = p.counts[e];
+      if (beg < 0 || cnt < 0 || beg + cnt > p.n_rows) {  // not inside the rows: skipped
+        if (report && p.err_flag) atomicOr(p.err_flag, MOE_FLAG_BAD_INDEX);
+        beg = 0;
+        cnt = 0;
+      }
+    }
+    t.start[e] = static_cast<int>(beg);
+    t.count[e] = static_cast<int>(cnt);
+  }
+  __syncthreads();
+  if (threadIdx.x < 32) {
+    const int lane = threadIdx.x;
+    const int per = (p.E + 31) / 32, b = min(p.E, lane * per), e = min(p.E, b + per);
+    long long total = 0;
+    int active = 0;
+    for (int i = b; i < e; ++i) {
+      total += t.count[i];
+      active += t.count[i] > 0 ? 1 : 0;
+    }
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) {
+      total += __shfl_xor_sync(0xFFFFFFFFu, total, off);
+      active += __shfl_xor_sync(0xFFFFFFFFu, active, off);
+    }
+    if (total > p.n_rows) {  // overlapping segments: none is taken
+      if (lane == 0 && report && p.err_flag) atomicOr(p.err_flag, MOE_FLAG_BAD_INDEX);
+      for (int i = b; i < e; ++i) t.count[i] = 0;
+      total = 0;
+    }
+    const int mean = active > 0 ? static_cast<int>((total + active - 1) / active) : 0;
+    const int bn = PAIR ? kPairRows : tile_rows(mean);
+    int mine = 0;
+    for (int i = b; i < e; ++i) mine += (t.count[i] + bn - 1) / bn;
+    int upto = mine;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const int v = __shfl_up_sync(0xFFFFFFFFu, upto, off);
+      if (lane >= off) upto += v;
+    }
+    int at = upto - mine;
+    for (int i = b; i < e; ++i) {
+      t.before[i] = at;
+      at += (t.count[i] + bn - 1) / bn;
+    }
+    if (lane == 31) {
+      t.before[p.E] = upto;
+      *bn_out = bn;
+      *few_out = mean <= kFewRows;
+    }
+  }
+  __syncthreads();
+}
+
+// One piece of work: weight tile m and nr rows from r0 of segment e, K blocks
+// [kb0, kb1).  slot >= 0: an incomplete sum, left in that slot of this CTA.
+struct Piece {
+  int e, m, r0, nr, kb0, kb1, slot, alone;
+  int64_t tile;
+};
+
+struct Schedule {
+  int64_t tiles, whole;  // tiles in the list, tiles given out whole
+  int64_t rest_units;    // K blocks of the split round
+  int mt, nkb, G;        // weight tiles, K blocks, walkers (CTAs or pairs)
+  __device__ Schedule(const GemmParams& p, const Tiles& t, int rows_out, int walkers, bool split) : G(walkers) {
+    mt = (p.n_out + rows_out - 1) / rows_out;
+    nkb = (p.K + umma::kBK - 1) / umma::kBK;
+    tiles = static_cast<int64_t>(t.before[p.E]) * mt;
+    whole = split ? tiles / G * G : tiles;
+    rest_units = (tiles - whole) * nkb;
+  }
+  // Start of walker b's share of the split round.
+  __device__ int64_t share(int b) const { return rest_units * b / G; }
+};
+
+// Tile `tile` of the list.
+__device__ __forceinline__ void locate(const Tiles& t, int E, int mt, int64_t tile, Piece& w) {
+  const int at = static_cast<int>(tile / mt);
+  int lo = 0, hi = E;  // before[lo] <= at < before[hi]
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (t.before[mid] <= at) lo = mid;
+    else hi = mid;
+  }
+  const int ntt = t.before[lo + 1] - t.before[lo];
+  const int local = static_cast<int>(tile - static_cast<int64_t>(t.before[lo]) * mt);
+  const int tt = local % ntt;
+  // row tiles of nearly the same size, in whole sixteens
+  const int cnt = t.count[lo];
+  const int64_t sixteens = (static_cast<int64_t>(cnt) + 15) / 16;
+  const int a = static_cast<int>(sixteens * tt / ntt * 16);
+  const int b = static_cast<int>(min(static_cast<int64_t>(cnt), sixteens * (tt + 1) / ntt * 16));
+  w.e = lo;
+  w.m = local / ntt;
+  w.r0 = t.start[lo] + a;
+  w.nr = b - a;
+  w.alone = ntt == 1;
+  w.tile = tile;
+}
+
+// The pieces of one walker, in the order in which all its warps walk them.
+struct Walk {
+  int64_t next, u, uend;
+  __device__ Walk(const Schedule& s, int who) : next(who), u(s.share(who)), uend(s.share(who + 1)) {}
+  __device__ bool get(const Schedule& s, const Tiles& t, int E, Piece& w) {
+    if (next < s.whole) {
+      locate(t, E, s.mt, next, w);
+      w.kb0 = 0;
+      w.kb1 = s.nkb;
+      w.slot = -1;
+      next += s.G;
+      return true;
+    }
+    if (u >= uend) return false;
+    locate(t, E, s.mt, s.whole + u / s.nkb, w);
+    w.kb0 = static_cast<int>(u % s.nkb);
+    w.kb1 = static_cast<int>(min(static_cast<int64_t>(s.nkb), w.kb0 + (uend - u)));
+    w.slot = w.kb0 == 0 ? (w.kb1 == s.nkb ? -1 : 1) : 0;
+    u += w.kb1 - w.kb0;
+    return true;
+  }
+};
+
+__device__ __forceinline__ float* slot_tile(const GemmParams& p, int cta, int slot) {
+  return p.partial + (static_cast<int64_t>(cta) * 2 + slot) * p.slot_rows * umma::kBM;
+}
+
+// kParts: the place of any piece of the list.  A CTA has at most one piece of
+// the split round that starts a tile, and one that does not; whole tiles follow.
+__host__ __device__ inline int64_t parts_index(int64_t whole_tile, int G, int cta, int kb0) {
+  return whole_tile >= 0 ? 2 * static_cast<int64_t>(G) + whole_tile : 2 * static_cast<int64_t>(cta) + (kb0 == 0 ? 1 : 0);
+}
+__device__ __forceinline__ float* parts_tile(const GemmParams& p, const Schedule& s, int cta, const Piece& w) {
+  return p.partial + parts_index(w.tile < s.whole ? w.tile : -1, s.G, cta, w.kb0) * p.slot_rows * umma::kBM;
+}
+
+__device__ __forceinline__ float silu_mul(float g, float u) { return g / (1.f + expf(-g)) * u; }
+
+// Whether row r's token names a row of x.
+__device__ __forceinline__ bool token_ok(const GemmParams& p, int r) {
+  const int s = p.row_token[r];
+  return s >= 0 && s < p.n_x;
+}
+
+// Rows c .. c + 31 of the tile whose token names no row (one bit a row): they
+// are stored as zeros.
+__device__ __forceinline__ unsigned bad_rows(const GemmParams& p, const Piece& w, int c) {
+  const int r = c + (threadIdx.x & 31);
+  return p.row_token ? __ballot_sync(0xFFFFFFFFu, r < w.nr && !token_ok(p, w.r0 + r)) : 0u;
+}
+
+// Stores NC columns (rows r0 + c ..) of one weight tile; v[i] is this lane's
+// weight row for row i.  Neighbouring lanes swap halves of two rows so that
+// each store covers a whole row piece of the warp.  m: the 128-row weight tile.
+// aux: kRows the bad rows' bits, kScatter the token of row c + lane, kLow the
+// factor's bits.
+template <bool SWIGLU, Out OUT, int NC>
+__device__ __forceinline__ void store_cols(const GemmParams& p, const Piece& w, int m, int c, int q,
+                                           const float (&v)[NC], unsigned aux) {
+  const int lane = threadIdx.x & 31;
+  const int left = w.nr - c;
+  // lanes of a row: 0..15 hold gates and 16..31 their ups (after the swap the
+  // lower half finishes row i, the upper half row i + 1); without SwiGLU even
+  // and odd lanes share out the two rows
+  const bool second = SWIGLU ? lane >= 16 : lane & 1;
+  const int o = SWIGLU ? m * 64 + q * 16 + (lane & 15) : m * 128 + q * 32 + (lane & ~1);
+#pragma unroll
+  for (int i = 0; i < NC; i += 2) {
+    const float other = __shfl_xor_sync(0xFFFFFFFFu, second ? v[i] : v[i + 1], SWIGLU ? 16 : 1);
+    const float a = second ? other : v[i], b = second ? v[i + 1] : other;
+    const int r = second ? i + 1 : i;
+    int64_t row = w.r0 + c + r;
+    bool live = r < left && o < p.n_out;
+    if (OUT == kScatter) {
+      const int t0 = __shfl_sync(0xFFFFFFFFu, static_cast<int>(aux), i);
+      const int t1 = __shfl_sync(0xFFFFFFFFu, static_cast<int>(aux), i + 1);
+      row = second ? t1 : t0;
+      live = live && row >= 0;
+    }
+    if (OUT == kLow) {
+      const float f = __uint_as_float(aux), x = f * a, y = f * b;
+      const uint32_t hi = pack_bf16x2(x, y);
+      // the rest of an infinite value is none
+      const float rx = x - bf16lo(hi), ry = y - bf16hi(hi);
+      const uint32_t rest = pack_bf16x2(isfinite(x) ? rx : 0.f, isfinite(y) ? ry : 0.f);
+      if (live) {
+        *reinterpret_cast<uint32_t*>(p.low[0] + row * p.n_out + o) = hi;
+        *reinterpret_cast<uint32_t*>(p.low[1] + row * p.n_out + o) = rest;
+      }
+    } else {
+      const bool bad = OUT == kRows && ((aux >> r) & 1u);
+      if (SWIGLU) {
+        const float y = bad ? 0.f : silu_mul(a, b);
+        if (live) p.out[row * p.n_out + o] = static_cast<uint16_t>(pack_bf16x2(y, 0.f));
+      } else if (live) {
+        *reinterpret_cast<uint32_t*>(p.out + row * p.n_out + o) = bad ? 0u : pack_bf16x2(a, b);
+      }
+    }
+  }
+}
+
+// store_cols' aux for rows c .. of a tile.
+template <Out OUT>
+__device__ __forceinline__ unsigned store_aux(const GemmParams& p, const Piece& w, int c) {
+  if (OUT == kLow) return __float_as_uint(p.scale[w.e]);
+  if (OUT == kScatter) {
+    const int r = c + (threadIdx.x & 31);
+    return static_cast<unsigned>(r < w.nr ? p.row_token[w.r0 + r] : -1);
+  }
+  return bad_rows(p, w, c);
+}
+
+// The adapters of a tile, in the order in which all warps walk them: columns
+// [c0, c0 + n) of the tile against adapter a.
+struct Adapters {
+  int a, r0, r1, c0, n;
+  __device__ Adapters(const GemmParams& p, const int* seg, const Piece& w) : r0(w.r0), r1(w.r0 + w.nr) {
+    int lo = 0, hi = p.segs;  // the last segment that starts at or before r0
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (seg[mid] <= r0) lo = mid;
+      else hi = mid;
+    }
+    a = lo - 1;
+  }
+  __device__ bool get(const GemmParams& p, const int* seg) {
+    while (++a < p.segs - 1) {
+      const int b = max(seg[a], r0), e = min(seg[a + 1], r1);
+      if (seg[a] >= r1) return false;
+      if (e > b) {
+        c0 = b - r0;
+        n = e - b;
+        return true;
+      }
+    }
+    return false;
+  }
+};
+
+template <bool SWIGLU, bool GATHER, bool PAIR, Out OUT>
+__global__ void __launch_bounds__(threads_of(GATHER), 1)
+expert_gemm_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constant__ CUtensorMap tmap_w,
+                   const __grid_constant__ CUtensorMap tmap_b, const GemmParams p) {
+  static_assert(OUT != kScatter || (PAIR && GATHER), "sorted rows run in pairs");
+  using namespace umma;
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ Barriers sb;
+  uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  int* list = reinterpret_cast<int*>(ring + kRingBytes);
+  const Tiles t{list, list + p.E, list + 2 * p.E};
+  int* seg = list + 3 * p.E + 1;  // kScatter: the adapters' first rows
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = PAIR ? static_cast<int>(cg::this_cluster().block_rank()) : 0;
+  const int who = PAIR ? blockIdx.x >> 1 : blockIdx.x;
+  volatile int* abort_v = &sb.abort_flag;
+
+  if (warp == 1) tmem_alloc<PAIR>(&sb.tmem_base, 2 * kAccCols);
+  allow_dependent_launch();
+  if (!p.wait_late) grid_dependency_wait();
+  if (OUT == kScatter)
+    for (int i = threadIdx.x; i <= p.segs; i += blockDim.x) seg[i] = p.seg[i];
+  list_tiles<PAIR>(p, t, &sb.bn, &sb.few, blockIdx.x == 0);
+  const bool few = GATHER && !PAIR && sb.few;  // rows gathered by TMA
+  const int depth = OUT == kScatter ? (p.R + kBK - 1) / kBK : 0;  // K blocks of an adapter's B
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kMaxStages; ++s) {
+      mbar_init(&sb.full[s], 1 + (GATHER && !few ? (PAIR ? 2 : 1) : 0));
+      mbar_init(&sb.landed[s], 32 * kLoaders);
+      mbar_init(&sb.empty[s], 1);
+    }
+    for (int a = 0; a < 2; ++a) {
+      mbar_init(&sb.acc_full[a], 1);
+      mbar_init(&sb.acc_empty[a], PAIR ? 8 : 4);
+    }
+    mbar_init(&sb.drained, 1);
+    sb.abort_flag = 0;
+    mbar_init_fence();
+  }
+  fence_before_sync();
+  __syncthreads();
+  if (PAIR) {  // the peer's barriers are ready before anything signals them
+    cluster_arrive_release();
+    cluster_wait_acquire();
+  }
+  fence_after_sync();
+  const uint32_t tmem = sb.tmem_base;
+  // a stage: 128 weight rows, then this CTA's rows (a pair's CTA holds half of the tile's)
+  const int stage_bytes = (kBM + (PAIR ? kPairRows / 2 : sb.bn)) * kRowBytes;
+  const int nstages = min(kMaxStages, kRingBytes / stage_bytes);
+  const Schedule s(p, t, (SWIGLU ? 64 : 128) * (PAIR ? 2 : 1), PAIR ? gridDim.x >> 1 : gridDim.x, !PAIR);
+  // barriers that the first CTA of a pair keeps for both
+  const uint32_t full0 = PAIR ? cluster_addr(&sb.full[0], 0) : smem_addr(&sb.full[0]);
+  const uint32_t acc_empty0 = PAIR ? cluster_addr(&sb.acc_empty[0], 0) : smem_addr(&sb.acc_empty[0]);
+
+  if (warp == 0) {
+    // -------------------------------------------------------------- loads
+    const uint64_t once = l2_evict_first_policy(), keep = l2_evict_normal_policy();
+    const int withheld = who == 0 ? p.withhold : -1;
+    Walk walk(s, who);
+    Piece w;
+    int n = 0;  // stages so far
+    bool stop = false;
+    while (!stop && walk.get(s, t, p.E, w)) {
+      const int mine = PAIR ? round_up(w.nr, 16) / 2 : w.nr;  // rows in this CTA
+      const int boxes = GATHER ? 0 : (mine + 31) >> 5, quads = few ? (mine + 3) >> 2 : 0;
+      const uint32_t bytes = static_cast<uint32_t>((PAIR ? 2 : 1) * (kBM + boxes * 32 + quads * 4)) * kRowBytes;
+      int4 tok = make_int4(0, 0, 0, 0);  // lane l: rows 4 l .. 4 l + 3
+      if (lane < quads) {
+        int v[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          v[i] = lane * 4 + i < w.nr ? p.row_token[w.r0 + lane * 4 + i] : 0;
+          if (v[i] < 0 || v[i] >= p.n_x) {  // loads token 0, stored as zeros
+            if (p.err_flag) atomicOr(p.err_flag, MOE_FLAG_BAD_INDEX);
+            v[i] = 0;
+          }
+        }
+        tok = make_int4(v[0], v[1], v[2], v[3]);
+      }
+      const int m = PAIR ? w.m * 2 + rank : w.m, r0 = w.r0 + rank * mine;
+      const uint64_t pol = w.alone ? once : keep;
+      for (int kb = w.kb0; kb < w.kb1; ++kb, ++n) {
+        const int st = n % nstages, use = n / nstages;
+        const bool go = (use == 0 || wait(&sb.empty[st], (use - 1) & 1, abort_v)) && !*abort_v;
+        if (!__all_sync(0xFFFFFFFFu, go)) {
+          stop = true;
+          break;
+        }
+        if (n == withheld) continue;  // neither armed nor loaded: the MMA warp's wait runs out
+        const uint32_t a = smem_addr(ring) + static_cast<uint32_t>(st * stage_bytes);
+        const uint32_t b = a + kBM * kRowBytes, bar = full0 + st * 8;
+        if (lane == 0 && rank == 0) mbar_arrive_expect_tx(&sb.full[st], bytes);
+        __syncwarp();
+        if (!SWIGLU) {
+          if (lane == 0) tma_load_5d<PAIR>(a, &tmap_w, kb * kBK, m * 128, 0, 0, w.e, bar, pol);
+        } else if (p.weave) {
+          if (lane == 0) tma_load_5d<PAIR>(a, &tmap_w, kb * kBK, 0, 0, m * 4, w.e, bar, pol);
+        } else if (lane < 4) {  // 16 gate rows and their 16 up rows
+          tma_load_5d<PAIR>(a + lane * 32 * kRowBytes, &tmap_w, kb * kBK, m * 64 + lane * 16, 0, 0, w.e, bar, pol);
+        }
+        if (lane < quads) tma_gather4(b + lane * 4 * kRowBytes, &tmap_x, kb * kBK, tok, bar);
+        if (!GATHER && lane < boxes)
+          tma_load_2d<PAIR>(b + lane * 32 * kRowBytes, &tmap_x, kb * kBK, r0 + lane * 32, bar);
+      }
+      if (OUT == kScatter && !stop) {
+        Adapters ad(p, seg, w);
+        while (!stop && ad.get(p, seg)) {
+          for (int i = 0; i < 2 * depth; ++i, ++n) {
+            const int st = n % nstages, use = n / nstages;
+            const bool go = (use == 0 || wait(&sb.empty[st], (use - 1) & 1, abort_v)) && !*abort_v;
+            if (!__all_sync(0xFFFFFFFFu, go)) {
+              stop = true;
+              break;
+            }
+            const uint32_t a = smem_addr(ring) + static_cast<uint32_t>(st * stage_bytes), bar = full0 + st * 8;
+            const int kb = i >> 1;
+            if (lane == 0 && rank == 0) mbar_arrive_expect_tx(&sb.full[st], 2 * kBM * kRowBytes);
+            __syncwarp();
+            if (!SWIGLU) {
+              if (lane == 0) tma_load_5d<PAIR>(a, &tmap_b, kb * kBK, m * 128, 0, 0, ad.a, bar, keep);
+            } else if (p.weave) {
+              if (lane == 0) tma_load_5d<PAIR>(a, &tmap_b, kb * kBK, 0, 0, m * 4, ad.a, bar, keep);
+            } else if (lane < 4) {
+              tma_load_5d<PAIR>(a + lane * 32 * kRowBytes, &tmap_b, kb * kBK, m * 64 + lane * 16, 0, 0, ad.a, bar, keep);
+            }
+          }
+        }
+      }
+    }
+    __syncwarp();
+    // drain: no copy may land after this CTA exits (a pair's copies are counted
+    // by its first CTA, and neither leaves before the other)
+    if (lane == 0 && rank == 0) {
+      for (int i = n > nstages ? n - nstages : 0; i < n; ++i)
+        if (i != withheld) wait(&sb.full[i % nstages], (i / nstages) & 1, abort_v, true);
+    }
+  } else if (warp == 1) {
+    // ---------------------------------------------------------------- MMA
+    if (lane == 0 && rank == 0) {
+      Walk walk(s, who);
+      Piece w;
+      int n = 0, seq = 0;
+      bool stop = false;
+      while (!stop && walk.get(s, t, p.E, w)) {
+        const int acc = seq & 1, use = seq >> 1;
+        if (use > 0 && !wait(&sb.acc_empty[acc], (use - 1) & 1, abort_v)) break;
+        fence_after_sync();
+        const uint32_t d = tmem + acc * kAccCols;
+        const uint32_t idesc = idesc_bf16(PAIR ? 2 * kBM : kBM, round_up(w.nr, 16));
+        for (int kb = w.kb0; kb < w.kb1; ++kb, ++n) {
+          const int st = n % nstages;
+          if (!wait(&sb.full[st], (n / nstages) & 1, abort_v)) {
+            stop = true;
+            break;
+          }
+          fence_after_sync();
+          const uint32_t a = smem_addr(ring) + static_cast<uint32_t>(st * stage_bytes);
+          const uint32_t b = a + kBM * kRowBytes;
+#pragma unroll
+          for (int kk = 0; kk < kBK / 16; ++kk)
+            mma_bf16<PAIR>(d, desc_sw128(a + kk * 32), desc_sw128(b + kk * 32), idesc, kb != w.kb0 || kk != 0);
+          mma_commit<PAIR>(&sb.empty[st]);
+        }
+        if (OUT == kScatter && !stop) {
+          Adapters ad(p, seg, w);
+          while (!stop && ad.get(p, seg)) {
+            const uint32_t sub = idesc_bf16(2 * kBM, ad.n);
+            for (int i = 0; i < 2 * depth; ++i, ++n) {
+              const int st = n % nstages;
+              if (!wait(&sb.full[st], (n / nstages) & 1, abort_v)) {
+                stop = true;
+                break;
+              }
+              fence_after_sync();
+              const uint32_t a = smem_addr(ring) + static_cast<uint32_t>(st * stage_bytes);
+              const uint32_t b = a + kBM * kRowBytes;
+              const int ks = (min(kBK, p.R - (i >> 1) * kBK) + 15) >> 4;
+              for (int kk = 0; kk < ks; ++kk)
+                mma_bf16<PAIR>(d + ad.c0, desc_sw128(a + kk * 32), desc_sw128(b + kk * 32), sub, 1);
+              mma_commit<PAIR>(&sb.empty[st]);
+            }
+          }
+        }
+        mma_commit<PAIR>(&sb.acc_full[acc]);
+        ++seq;
+      }
+      mma_commit<PAIR>(&sb.drained);  // also after an abort: fires once the issued MMAs are done
+    }
+    __syncwarp();
+  } else if (warp < 6) {
+    // ----------------------------------------------------------- epilogue
+    const int q = warp & 3;  // this warp's quarter of the tensor-memory lanes
+    Walk walk(s, who);
+    Piece w;
+    int seq = 0;
+    while (walk.get(s, t, p.E, w)) {
+      const int acc = seq & 1, use = seq >> 1;
+      ++seq;
+      const bool ok = wait(&sb.acc_full[acc], use & 1, abort_v) && !*abort_v;
+      if (!__all_sync(0xFFFFFFFFu, ok)) break;
+      fence_after_sync();
+      const uint32_t d = tmem + acc * kAccCols + (static_cast<uint32_t>(q * 32) << 16);
+      float* part = nullptr;
+      if (OUT == kParts) part = parts_tile(p, s, who, w) + q * 32 + lane;
+      else if (w.slot >= 0) part = slot_tile(p, who, w.slot) + q * 32 + lane;
+#pragma unroll 1
+      for (int c = 0; c < w.nr; c += 32) {
+        uint32_t raw[32];
+        tmem_ld32(d + static_cast<uint32_t>(c), raw);
+        if (OUT == kParts || part) {
+#pragma unroll
+          for (int i = 0; i < 32; ++i)
+            if (c + i < w.nr) part[(c + i) * kBM] = __uint_as_float(raw[i]);
+        } else {
+          float v[32];
+#pragma unroll
+          for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(raw[i]);
+          store_cols<SWIGLU, OUT, 32>(p, w, PAIR ? w.m * 2 + rank : w.m, c, q, v, store_aux<OUT>(p, w, c));
+        }
+      }
+      fence_before_sync();
+      __syncwarp();
+      if (lane == 0) {
+        if (PAIR) arrive_cluster(acc_empty0 + acc * 8);
+        else mbar_arrive(&sb.acc_empty[acc]);
+      }
+    }
+  } else if (GATHER && !few && warp < 6 + kLoaders) {
+    // ------------------------------------------------------------- gather
+    // Warp j takes rows 16 i + 4 j .. + 3 of this CTA's rows, eight lanes a
+    // row, 16 bytes a lane, at their place in the 128-byte swizzle.
+    const int j = warp - 6, sub = lane >> 3, chunk = lane & 7;
+    Walk walk(s, who);
+    Piece w;
+    int n = 0;
+    bool stop = false;
+    while (!stop && walk.get(s, t, p.E, w)) {
+      const int mine = PAIR ? round_up(w.nr, 16) / 2 : w.nr;
+      const int rounds = (mine - 4 * j + 15) >> 4;  // <= 8; none for the last warps of a small tile
+      int tok[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int r = 16 * i + 4 * j + sub, rr = rank * mine + r;
+        tok[i] = -1;
+        if (r < mine && rr < w.nr) {
+          const int v = p.row_token[w.r0 + rr];
+          if (v >= 0 && v < p.n_x) tok[i] = v;
+          else if (OUT != kScatter && p.err_flag) atomicOr(p.err_flag, MOE_FLAG_BAD_INDEX);  // a row of zeros
+        }
+      }
+      for (int kb = w.kb0; kb < w.kb1; ++kb, ++n) {
+        const int st = n % nstages, use = n / nstages;
+        const bool go = (use == 0 || wait(&sb.empty[st], (use - 1) & 1, abort_v)) && !*abort_v;
+        if (!__all_sync(0xFFFFFFFFu, go)) {
+          stop = true;
+          break;
+        }
+        const uint32_t b = smem_addr(ring) + static_cast<uint32_t>(st * stage_bytes + kBM * kRowBytes);
+        const int col = kb * kBK + chunk * 8;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          if (i < rounds) {
+            const int r = 16 * i + 4 * j + sub;
+            const bool live = tok[i] >= 0 && col < p.K;
+            copy16_async(b + r * kRowBytes + ((chunk ^ (r & 7)) << 4),
+                         p.x + (live ? static_cast<int64_t>(tok[i]) * p.K + col : 0), live);
+          }
+        }
+        copy_arrive(&sb.landed[st]);
+      }
+      if (OUT == kScatter && !stop) {
+        Adapters ad(p, seg, w);
+        while (!stop && ad.get(p, seg)) {
+          const int half = ad.n / 2;
+          const int64_t first = w.r0 + ad.c0 + rank * half;
+          for (int i = 0; i < 2 * depth; ++i, ++n) {
+            const int st = n % nstages, use = n / nstages;
+            const bool go = (use == 0 || wait(&sb.empty[st], (use - 1) & 1, abort_v)) && !*abort_v;
+            if (!__all_sync(0xFFFFFFFFu, go)) {
+              stop = true;
+              break;
+            }
+            const uint32_t b = smem_addr(ring) + static_cast<uint32_t>(st * stage_bytes + kBM * kRowBytes);
+            const int col = (i >> 1) * kBK + chunk * 8;
+            const uint16_t* low = p.low[i & 1];
+#pragma unroll
+            for (int h = 0; h < 8; ++h) {
+              const int r = 16 * h + 4 * j + sub;
+              if (r < half) {
+                const bool live = col < p.R;
+                copy16_async(b + r * kRowBytes + ((chunk ^ (r & 7)) << 4), low + (live ? (first + r) * p.R + col : 0),
+                             live);
+              }
+            }
+            copy_arrive(&sb.landed[st]);
+          }
+        }
+      }
+    }
+    copy_drain();
+  } else if (GATHER && !few) {
+    // -------------------------------------------------- gathered rows are in
+    if (lane == 0) {
+      Walk walk(s, who);
+      Piece w;
+      int n = 0;
+      bool stop = false;
+      while (!stop && walk.get(s, t, p.E, w)) {
+        int stages = w.kb1 - w.kb0;
+        if (OUT == kScatter) {
+          Adapters ad(p, seg, w);
+          while (ad.get(p, seg)) stages += 2 * depth;
+        }
+        for (int i = 0; i < stages; ++i, ++n) {
+          const int st = n % nstages;
+          if (!wait(&sb.landed[st], (n / nstages) & 1, abort_v)) {
+            stop = true;
+            break;
+          }
+          proxy_fence();
+          if (PAIR) arrive_cluster(full0 + st * 8);
+          else mbar_arrive(&sb.full[st]);
+        }
+      }
+    }
+  }
+  __syncwarp();
+  fence_before_sync();
+  __syncthreads();
+  if (threadIdx.x == 32) wait(&sb.drained, 0, abort_v, true);  // no MMA is in flight any more
+  __syncwarp();
+  if (PAIR) {  // the peer's copies and arrivals are over too
+    cluster_arrive_release();
+    cluster_wait_acquire();
+  }
+  if (p.wait_late) grid_dependency_wait();
+  if (threadIdx.x == 0 && p.err_flag && *abort_v) atomicOr(p.err_flag, MOE_FLAG_TIMEOUT);
+  if (warp == 1) {
+    fence_after_sync();
+    tmem_dealloc<PAIR>(tmem, 2 * kAccCols);
+  }
+}
+
+// Adds the partial tiles of the split round.  CTA (b, y) takes the tile at the
+// end of share b if that end lies inside it and no earlier share ends there,
+// and of its rows those with row / 16 % gridDim.y == y.
+template <bool SWIGLU, Out OUT>
+__global__ void __launch_bounds__(128) expert_join_kernel(const GemmParams p, int G) {
+  extern __shared__ int join_list[];
+  __shared__ int bn, few;
+  const Tiles t{join_list, join_list + p.E, join_list + 2 * p.E};
+  allow_dependent_launch();
+  grid_dependency_wait();
+  list_tiles<false>(p, t, &bn, &few, false);
+  const Schedule s(p, t, SWIGLU ? 64 : 128, G, true);
+  const int b = blockIdx.x;
+  const int64_t end = s.share(b + 1), tile0 = end / s.nkb * s.nkb;
+  if (end == tile0 || end >= s.rest_units) return;  // the share ends between two tiles
+  if (s.share(b) > tile0) return;                   // an earlier share ends in this tile
+  Piece w;
+  locate(t, p.E, s.mt, s.whole + end / s.nkb, w);
+  int last = b + 1;
+  while (s.share(last + 1) < tile0 + s.nkb) ++last;
+  const int l = threadIdx.x, q = l >> 5;
+  for (int c = blockIdx.y * 16; c < w.nr; c += gridDim.y * 16) {
+    float v[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) v[i] = 0.f;
+    for (int j = b; j <= last; ++j) {
+      if (s.share(j) == s.share(j + 1)) continue;
+      const float* part = slot_tile(p, j, j == b ? 1 : 0) + l;
+#pragma unroll
+      for (int i = 0; i < 16; ++i)
+        if (c + i < w.nr) v[i] += part[(c + i) * umma::kBM];
+    }
+    store_cols<SWIGLU, OUT, 16>(p, w, w.m, c, q, v, store_aux<OUT>(p, w, c));
+  }
+}
+
+// ---------------------------------------------------------------- host side
+
+inline PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
+  static std::atomic<PFN_cuTensorMapEncodeTiled_v12000> fn{nullptr};
+  PFN_cuTensorMapEncodeTiled_v12000 f = fn.load();
+  if (!f) {
+    void* ptr = nullptr;
+    cudaDriverEntryPointQueryResult r;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000, cudaEnableDefault, &r) == cudaSuccess &&
+        r == cudaDriverEntryPointSuccess) {
+      f = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(ptr);
+      fn.store(f);
+    }
+  }
+  return f;
+}
+
+// Row-major BF16 tensor of `rank` dimensions (innermost first), 128-byte swizzle.
+inline bool make_map(CUtensorMap* map, const void* base, int rank, const cuuint64_t* dims, const cuuint64_t* strides,
+              const cuuint32_t* box) {
+  const PFN_cuTensorMapEncodeTiled_v12000 fn = encode_fn();
+  const cuuint32_t one[5] = {1, 1, 1, 1, 1};
+  return fn && fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank, const_cast<void*>(base), dims, strides, box, one,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Dynamic shared memory: the ring, the tile list, the adapters' first rows.
+inline size_t gemm_smem(int64_t E, int segs) {
+  return 1024 + kRingBytes + static_cast<size_t>(3 * E + 1 + segs + 1) * sizeof(int);
+}
+
+// Opt the kernel into its dynamic shared memory, once per device.
+template <bool SWIGLU, bool GATHER, bool PAIR, Out OUT>
+cudaError_t opt_in(int dev) {
+  static std::atomic<bool> done[64];
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  if (!done[dev].load()) {
+    const cudaError_t e =
+        cudaFuncSetAttribute(expert_gemm_kernel<SWIGLU, GATHER, PAIR, OUT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             static_cast<int>(gemm_smem(OUT == kScatter ? 1 : MOE_MAX_E, OUT == kScatter ? MOE_MAX_ADAPTERS + 1 : 0)));
+    if (e != cudaSuccess) return e;
+    done[dev].store(true);
+  }
+  return cudaSuccess;
+}
+
+template <bool SWIGLU, bool GATHER, bool PAIR, Out OUT>
+cudaError_t launch(const CUtensorMap& mx, const CUtensorMap& mw, const CUtensorMap& mb, const GemmParams& p,
+                   cudaStream_t stream) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = opt_in<SWIGLU, GATHER, PAIR, OUT>(dev);
+  if (e != cudaSuccess) return e;
+  const int G = PAIR ? sm_count() / 2 * 2 : sm_count();
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(G), 1, 1);
+  cfg.blockDim = dim3(threads_of(GATHER), 1, 1);
+  cfg.dynamicSmemBytes = launch_smem(gemm_smem(p.E, p.segs));
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2] = {pdl_attribute(), {}};
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (PAIR) {
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = 2;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.numAttrs = 2;
+  }
+  e = cudaLaunchKernelEx(&cfg, expert_gemm_kernel<SWIGLU, GATHER, PAIR, OUT>, mx, mw, mb, p);
+  if (e != cudaSuccess || PAIR || OUT == kParts) return e;
+  const int rows16 = (p.slot_rows + 15) / 16;
+  cfg.gridDim = dim3(static_cast<unsigned>(G - 1), static_cast<unsigned>(rows16), 1);
+  cfg.blockDim = dim3(128, 1, 1);
+  cfg.dynamicSmemBytes = launch_smem(static_cast<size_t>(3 * p.E + 1) * sizeof(int));
+  return cudaLaunchKernelEx(&cfg, expert_join_kernel<SWIGLU, OUT>, p, G);
+}
+
+// Rows of a partial tile's slot.
+inline int slot_rows_of(int64_t n_rows) {
+  return static_cast<int>(n_rows < kSoloRows ? round_up(static_cast<int>(n_rows), 16) : kSoloRows);
+}
+
+// Weights as (K, N, 1, 1, E); SwiGLU: (K, n_out, gate / up, 1, E), or (K, 16,
+// gate / up, n_out / 16, E) where n_out divides (`weave`), so that one box is a
+// whole interleaved tile.
+inline bool weight_map(CUtensorMap* map, const void* w, int64_t E, int64_t N, int64_t K, bool swiglu, bool weave) {
+  const cuuint64_t row = static_cast<cuuint64_t>(K) * 2, n = static_cast<cuuint64_t>(swiglu ? N / 2 : N);
+  const cuuint64_t dims[5] = {static_cast<cuuint64_t>(K), weave ? 16 : n, swiglu ? 2u : 1u, weave ? n / 16 : 1,
+                              static_cast<cuuint64_t>(E)};
+  const cuuint64_t strides[4] = {row, row * n, row * 16, row * static_cast<cuuint64_t>(N)};
+  const cuuint32_t box[5] = {umma::kBK, swiglu ? 16u : 128u, swiglu ? 2u : 1u, weave ? 4u : 1u, 1u};
+  return make_map(map, w, 5, dims, strides, box);
+}
+
+// Rows of x in boxes of 32, or of one for the gather.
+inline bool row_map_of(CUtensorMap* map, const void* x, int64_t n_x, int64_t K, bool gather) {
+  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(K), static_cast<cuuint64_t>(n_x)}, row = static_cast<cuuint64_t>(K) * 2;
+  const cuuint32_t box[2] = {umma::kBK, gather ? 1u : 32u};
+  return make_map(map, x, 2, dims, &row, box);
+}
+
+}  // namespace
+}  // namespace moe

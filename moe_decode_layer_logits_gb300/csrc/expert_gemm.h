@@ -24,4 +24,26 @@ int64_t expert_gemm_workspace(int64_t n_rows);
 
 cudaError_t launch_expert_gemm(const ExpertGemm& g, cudaStream_t stream);
 
+// MOE_OK if N, K and act are sizes that the products take.
+int check_linear(int64_t N, int64_t K, int32_t act);
+
+struct AdapterLinear {
+  const uint16_t* x;    // [T, K]
+  const uint16_t* w;    // [N, K]
+  const uint16_t* a;    // [L, R, K]
+  const uint16_t* b;    // [L, N, R]
+  const int32_t* ids;   // [T]
+  const float* scale;   // [L]
+  uint16_t* out;        // [T, N or N/2]
+  int64_t T, N, K;
+  int R, L;
+  bool swiglu;
+  uint8_t* workspace;  // adapter_workspace() bytes
+  int32_t* err_flag;
+};
+
+int64_t adapter_workspace(int64_t T, int64_t N, int64_t K, int R, int L);
+
+cudaError_t launch_adapter_linear(const AdapterLinear& g, cudaStream_t stream);
+
 }  // namespace moe

@@ -11,21 +11,11 @@
 // the layout does not depend on the order of the atomics.  Bound by latency:
 // two passes over a warp's slots and two cluster barriers; more warps shorten
 // the walks until adding up their counts costs as much.
+#include "expert_map.h"
 #include "host_util.h"
 #include "common.cuh"
 
 namespace moe {
-
-struct ExpertMapParams {
-  const int32_t* ids;
-  int32_t* row_map;
-  int32_t* row_token;
-  int32_t* offsets;
-  int32_t* counts;
-  int64_t n_rows;
-  int64_t slots;  // T * k
-  int E, k, block;
-};
 
 constexpr int kMapMaxWarps = 32;
 constexpr int kMapBatch = 8;  // groups of 32 slots whose ids a warp loads at once
@@ -68,8 +58,12 @@ __global__ void __launch_bounds__(kMapMaxWarps * 32) expert_map_kernel(const Exp
 #pragma unroll
     for (int b = 0; b < kMapBatch; ++b) {
       const int64_t i = g + b * 32 + lane;
-      const unsigned e = i < end ? static_cast<unsigned>(p.ids[i]) : 0xFFFFFFFFu;
-      id[b] = e < static_cast<unsigned>(E) ? static_cast<int>(e) : E;
+      const int e = i < end ? p.ids[i] : -1;
+      id[b] = e >= 0 && e < E - p.rest ? e : E;
+      if (p.rest && i < end && id[b] == E) {
+        if (e >= 0 && p.err_flag) atomicOr(p.err_flag, MOE_FLAG_BAD_INDEX);
+        id[b] = E - 1;
+      }
     }
   };
   for (int64_t g = beg; g < end; g += 32 * kMapBatch) {
@@ -168,10 +162,43 @@ __global__ void __launch_bounds__(kMapMaxWarps * 32) expert_map_kernel(const Exp
         row += first[e];
         p.row_token[row] = static_cast<int>(i) / p.k;
       }
-      if (i < end) p.row_map[i] = row;
+      if (i < end && p.row_map) p.row_map[i] = row;
     }
   }
   cluster_wait_acquire();  // no CTA leaves while a peer may read its counts
+}
+
+cudaError_t launch_expert_map(const ExpertMapParams& p, cudaStream_t stream) {
+  // A warp for about 128 slots or 1024 rows.  Small CTAs have the shorter
+  // barriers, so the cluster grows first (8 warps each up to 8 CTAs), then the
+  // CTAs, up to 32 warps.  With 8 / 16 / 32 warps a CTA at E = 256, k = 8:
+  // T = 512 5.1 / 6.0 / 8.7 us, T = 4096 10.4 / 8.2 / 9.6 us, T = 32768
+  // 59 / 39 / 33 us.
+  int64_t want = (p.slots + 127) / 128;
+  if (want < (p.n_rows + 1023) / 1024) want = (p.n_rows + 1023) / 1024;
+  int C = 1;
+  while (C < kMapMaxCluster && static_cast<int64_t>(C) * 8 < want) C *= 2;
+  const int64_t per_cta = (want + C - 1) / C;
+  const int warps = per_cta < 8 ? 8 : per_cta > kMapMaxWarps ? kMapMaxWarps : static_cast<int>(per_cta);
+  const size_t smem = map_smem(warps, p.E);
+  if (smem > 48 * 1024) {
+    const cudaError_t e = cudaFuncSetAttribute(expert_map_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               static_cast<int>(map_smem(kMapMaxWarps, MOE_MAX_E + 1)));
+    if (e != cudaSuccess) return e;
+  }
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(C), 1, 1);
+  cfg.blockDim = dim3(static_cast<unsigned>(warps * 32), 1, 1);
+  cfg.dynamicSmemBytes = launch_smem(smem);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2] = {pdl_attribute(), {}};
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = static_cast<unsigned>(C);
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = C > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, expert_map_kernel, p);
 }
 
 }  // namespace moe
@@ -195,37 +222,9 @@ extern "C" int moe_expert_map(const int32_t* topk_ids, int32_t* row_map, int32_t
   if (!aligned(topk_ids, 4) || !aligned(row_map, 4) || !aligned(row_token, 4) || !aligned(offsets, 4) ||
       !aligned(counts, 4))
     return MOE_ERR_MISALIGNED;
-  ExpertMapParams p{topk_ids, row_map, row_token, offsets, counts, n_rows, T * k, static_cast<int>(E), k, block};
-  // A warp for about 128 slots or 1024 rows.  Small CTAs have the shorter
-  // barriers, so the cluster grows first (8 warps each up to 8 CTAs), then the
-  // CTAs, up to 32 warps.  With 8 / 16 / 32 warps a CTA at E = 256, k = 8:
-  // T = 512 5.1 / 6.0 / 8.7 us, T = 4096 10.4 / 8.2 / 9.6 us, T = 32768
-  // 59 / 39 / 33 us.
-  int64_t want = (p.slots + 127) / 128;
-  if (want < (p.n_rows + 1023) / 1024) want = (p.n_rows + 1023) / 1024;
-  int C = 1;
-  while (C < kMapMaxCluster && static_cast<int64_t>(C) * 8 < want) C *= 2;
-  const int64_t per_cta = (want + C - 1) / C;
-  const int warps = per_cta < 8 ? 8 : per_cta > kMapMaxWarps ? kMapMaxWarps : static_cast<int>(per_cta);
-  const size_t smem = map_smem(warps, p.E);
-  if (smem > 48 * 1024 && cudaFuncSetAttribute(expert_map_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               static_cast<int>(map_smem(kMapMaxWarps, MOE_MAX_E))) != cudaSuccess) {
-    (void)cudaGetLastError();
-    return MOE_ERR_CUDA;
-  }
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(C), 1, 1);
-  cfg.blockDim = dim3(static_cast<unsigned>(warps * 32), 1, 1);
-  cfg.dynamicSmemBytes = launch_smem(smem);
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[2] = {pdl_attribute(), {}};
-  attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = static_cast<unsigned>(C);
-  attr[1].val.clusterDim.y = 1;
-  attr[1].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = C > 1 ? 2 : 1;
-  if (cudaLaunchKernelEx(&cfg, expert_map_kernel, p) != cudaSuccess) {
+  const ExpertMapParams p{topk_ids, row_map, row_token, offsets, counts, n_rows, T * k, static_cast<int>(E), k, block,
+                          0, nullptr};
+  if (launch_expert_map(p, stream) != cudaSuccess) {
     (void)cudaGetLastError();
     return MOE_ERR_CUDA;
   }
