@@ -2,12 +2,13 @@
 // low-rank adapter beside it, out[t] = act(W x[t] + s_a B_a (A_a x[t])).
 //
 // Two forms:
-//  - up to kFewTokens tokens (decode): the low-rank products by one warp per
-//    (token, rank row); at the same time the shared projection, every tile's
-//    K split evenly over all SMs (kParts); then one kernel adds the pieces in
-//    order, expands each token's low-rank product against its own B in FP32,
-//    applies the activation and rounds once.  Bound by the weights' bytes and,
-//    at this size, by three launches' latency.
+//  - few tokens (decode): one kernel streams the shared weights, every tile's K
+//    split evenly over all SMs (kParts), while further warps of the same CTAs
+//    compute the low-rank products, one warp per (token, rank row); a second one
+//    adds the pieces in order, expands each token's low-rank product against its
+//    own B in FP32, applies the activation and rounds once.  It starts while the
+//    first runs and requests the B rows into the L2 meanwhile.  Bound by the
+//    weights' bytes and, at this size, by the latency of two launches.
 //  - more tokens: the tokens are sorted by adapter (segments start on multiples
 //    of 16 rows), the low-rank products are the expert products of A (kLow),
 //    and the shared projection runs in CTA pairs over the sorted rows with the
@@ -21,40 +22,9 @@ namespace moe {
 
 namespace {
 
-constexpr int64_t kFewTokens = kSoloRows;  // one row tile
-
-// low[t, r] = scale[a] * A_a[r] . x[t], one warp per (t, r).
-__global__ void __launch_bounds__(256)
-adapter_low_kernel(const uint16_t* __restrict__ x, const uint16_t* __restrict__ a, const int32_t* __restrict__ ids,
-                      const float* __restrict__ scale, float* __restrict__ low, int64_t T, int64_t K, int R, int L,
-                      int32_t* err_flag) {
-  const int lane = threadIdx.x & 31;
-  const int64_t job = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
-  // The product that follows starts as soon as this kernel's blocks have
-  // waited for the previous one: it reads the same inputs, and this kernel's
-  // result only behind its own wait.
-  grid_dependency_wait();
-  allow_dependent_launch();
-  if (job >= T * R) return;
-  const int64_t t = job / R;
-  const int r = static_cast<int>(job % R);
-  const int id = ids[t];
-  if (id < 0 || id >= L) {
-    if (id >= L && lane == 0 && err_flag) atomicOr(err_flag, MOE_FLAG_BAD_INDEX);
-    return;
-  }
-  const uint16_t* ar = a + (static_cast<int64_t>(id) * R + r) * K;
-  float s = 0.f;
-  for (int64_t k = lane * 8; k < K; k += 256) {
-    float f[8], g[8];
-    unpack8(ld_keep16(x + t * K + k), f);
-    unpack8(ld_keep16(ar + k), g);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) s = fmaf(f[i], g[i], s);
-  }
-  s = warp_sum(s);
-  if (lane == 0) low[t * R + r] = s * scale[id];
-}
+// Few tokens: one row tile, or as many as keep the low-rank products (a warp
+// each) behind the weights' stream.
+bool few_form(int64_t T, int R) { return T <= kSoloRows || (T <= 512 && T * R <= 8192); }
 
 struct FinishParams {
   const float* partial;
@@ -63,44 +33,88 @@ struct FinishParams {
   const int32_t* ids;
   uint16_t* out;
   int T, N, n_out, R, L, slot_rows;
-  int tiles, whole, nkb, G;  // the product's schedule
+  int row_tiles, whole, nkb, G;  // the product's schedule
 };
 
 constexpr int kFinishTokens = 8;
+constexpr int kFinishPieces = kMaxCtas;  // pieces of one tile: at most one a CTA
+constexpr int kFinishBatch = 2;          // pieces loaded at once
 
-// One CTA: 128 weight rows of the product (one of its tiles) and 8 tokens.
+// One CTA: 128 weight rows of the product and 8 tokens of one of its tiles.
+// What follows from the sizes and ids comes before the wait for the product;
+// behind it are two rounds of loads (pieces; low-rank products and B).  64
+// registers, so that the next product's CTA fits beside the SM's last of these.
 template <bool SWIGLU>
-__global__ void __launch_bounds__(128) adapter_finish_kernel(const FinishParams p) {
+__global__ void __launch_bounds__(128, 8) adapter_finish_kernel(const FinishParams p) {
   extern __shared__ float low_s[];  // [kFinishTokens][R]
   __shared__ int id_s[kFinishTokens];
+  __shared__ int piece_s[kFinishPieces];
+  __shared__ int pieces;
   const int l = threadIdx.x, q = l >> 5, m = blockIdx.x, t0 = blockIdx.y * kFinishTokens;
   allow_dependent_launch();
-  grid_dependency_wait();
   const int nt = min(kFinishTokens, p.T - t0);
-  for (int i = l; i < kFinishTokens; i += 128) {
-    const int a = i < nt ? p.ids[t0 + i] : -1;
-    id_s[i] = a < p.L ? a : -1;
+  if (l < kFinishTokens) {
+    const int a = l < nt ? p.ids[t0 + l] : -1;
+    id_s[l] = a < p.L ? a : -1;
   }
+  // this tile of the list: the row tile that holds t0 (eight tokens lie in one)
+  const int sixteens = (p.T + 15) / 16;
+  int tt = 0, r0 = 0;
+  while (tt + 1 < p.row_tiles && sixteens * (tt + 1) / p.row_tiles * 16 <= t0) {
+    ++tt;
+    r0 = sixteens * tt / p.row_tiles * 16;
+  }
+  // its pieces, in the order of K (sizes within 32 bits: fewer tiles than SMs
+  // are split, of at most 1024 K blocks each)
+  const int tile = m * p.row_tiles + tt;
+  if (l < 32) {
+    if (tile < p.whole) {
+      if (l == 0) {
+        piece_s[0] = static_cast<int>(parts_index(tile, p.G, 0, 0));
+        pieces = 1;
+      }
+    } else {
+      const unsigned units = (gridDim.x * p.row_tiles - p.whole) * p.nkb, G = p.G;
+      const unsigned beg = static_cast<unsigned>(tile - p.whole) * p.nkb, end = beg + p.nkb;
+      int n = 0;
+      const unsigned from = beg * G / units;
+      for (unsigned j0 = from; j0 < G; j0 += 32) {
+        const unsigned j = j0 + l, u0 = units * j / G, u1 = units * (j + 1) / G;
+        const bool in = j < G && u0 < u1 && u1 > beg && u0 < end;
+        const unsigned bal = __ballot_sync(0xFFFFFFFFu, in);
+        if (in) piece_s[n + __popc(bal & ((1u << l) - 1u))] = static_cast<int>(parts_index(-1, p.G, j, u0 <= beg ? 0 : 1));
+        n += __popc(bal);
+        if (units * (j0 + 32) / G >= end) break;
+      }
+      if (l == 0) pieces = n;
+    }
+  }
+  __syncthreads();
+  if (l < 2 * kFinishTokens) {
+    const int a = id_s[l >> 1];
+    const int per = SWIGLU ? 64 : 128, first = m * per, n = min(per, p.n_out - first);
+    if (a >= 0 && (SWIGLU || !(l & 1)))
+      prefetch_l2(p.b + (static_cast<int64_t>(a) * p.N + ((l & 1) ? p.n_out : 0) + first) * p.R,
+                  static_cast<uint32_t>(n) * p.R * 2);
+  }
+  grid_dependency_wait();
   for (int i = l; i < nt * p.R; i += 128) low_s[i] = p.low[static_cast<int64_t>(t0) * p.R + i];
   float v[kFinishTokens];
 #pragma unroll
   for (int i = 0; i < kFinishTokens; ++i) v[i] = 0.f;
-  auto add = [&](int64_t index) {
-    const float* part = p.partial + (index * p.slot_rows + t0) * umma::kBM + l;
+  const float* part = p.partial + static_cast<int64_t>(t0 - r0) * umma::kBM + l;
+  const int64_t step = static_cast<int64_t>(p.slot_rows) * umma::kBM;
+  for (int c = 0; c < pieces; c += kFinishBatch) {
+    float f[kFinishBatch][kFinishTokens];
 #pragma unroll
-    for (int i = 0; i < kFinishTokens; ++i)
-      if (i < nt) v[i] += part[i * umma::kBM];
-  };
-  if (m < p.whole) {
-    add(parts_index(m, p.G, 0, 0));
-  } else {
-    const int64_t units = static_cast<int64_t>(p.tiles - p.whole) * p.nkb;
-    const int64_t beg = static_cast<int64_t>(m - p.whole) * p.nkb, end = beg + p.nkb;
-    auto share = [&](int64_t j) { return units * j / p.G; };
-    int j = static_cast<int>(beg * p.G / units);
-    while (share(j + 1) <= beg) ++j;
-    for (; j < p.G && share(j) < end; ++j)
-      if (share(j) < share(j + 1)) add(parts_index(-1, p.G, j, share(j) <= beg ? 0 : 1));
+    for (int j = 0; j < kFinishBatch; ++j)
+#pragma unroll
+      for (int i = 0; i < kFinishTokens; ++i)
+        f[j][i] = c + j < pieces && i < nt ? part[piece_s[c + j] * step + i * umma::kBM] : 0.f;
+#pragma unroll
+    for (int j = 0; j < kFinishBatch; ++j)
+#pragma unroll
+      for (int i = 0; i < kFinishTokens; ++i) v[i] += f[j][i];
   }
   __syncthreads();
   // this lane's weight row
@@ -136,13 +150,14 @@ size_t up256(size_t v) { return (v + 255) / 256 * 256; }
 
 // Places in the workspace.
 struct Few {
-  int tiles, whole, G, slot_rows;
+  int tiles, row_tiles, whole, G, slot_rows;
   size_t low, parts, bytes;
   Few(int64_t T, int64_t N, int R) {
-    G = sm_count();
+    G = gemm_ctas();
     slot_rows = slot_rows_of(T);
-    tiles = static_cast<int>((N + umma::kBM - 1) / umma::kBM);  // gate and up: 64 + 64 rows a tile
-    whole = tiles / G * G;
+    row_tiles = static_cast<int>((T + kSoloRows - 1) / kSoloRows);
+    tiles = static_cast<int>((N + umma::kBM - 1) / umma::kBM);  // with SwiGLU 64 gate and 64 up rows each
+    whole = tiles * row_tiles / G * G;
     low = 0;
     parts = up256(static_cast<size_t>(T) * R * 4);
     bytes = parts + (2 * static_cast<size_t>(G) + whole) * slot_rows * umma::kBM * 4;
@@ -168,18 +183,6 @@ template <bool SWIGLU>
 cudaError_t few_tokens(const AdapterLinear& g, cudaStream_t stream) {
   const Few f(g.T, g.N, g.R);
   float* low = reinterpret_cast<float*>(g.workspace + f.low);
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>((g.T * g.R + 7) / 8), 1, 1);
-  cfg.blockDim = dim3(256, 1, 1);
-  cfg.dynamicSmemBytes = launch_smem(0);
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1] = {pdl_attribute()};
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  cudaError_t e = cudaLaunchKernelEx(&cfg, adapter_low_kernel, g.x, g.a, g.ids, g.scale, low, g.T, g.K, g.R, g.L,
-                                     g.err_flag);
-  if (e != cudaSuccess) return e;
-
   GemmParams p{};
   p.x = g.x;
   p.partial = reinterpret_cast<float*>(g.workspace + f.parts);
@@ -192,20 +195,28 @@ cudaError_t few_tokens(const AdapterLinear& g, cudaStream_t stream) {
   p.slot_rows = f.slot_rows;
   p.weave = SWIGLU && p.n_out % 16 == 0;
   p.withhold = -1;
-  p.wait_late = 1;
+  p.scale = g.scale;
+  p.a = g.a;
+  p.ids = g.ids;
+  p.low32 = low;
+  p.R = g.R;
+  p.L = g.L;
   CUtensorMap mx, mw;
   if (!weight_map(&mw, g.w, 1, g.N, g.K, SWIGLU, p.weave) || !row_map_of(&mx, g.x, g.T, g.K, false))
     return cudaErrorInvalidValue;
-  e = launch<SWIGLU, false, false, kParts>(mx, mw, mw, p, stream);
+  const cudaError_t e = launch<SWIGLU, false, false, kParts>(mx, mw, mw, p, stream);
   if (e != cudaSuccess) return e;
 
-  const int rows_out = SWIGLU ? 64 : 128;
   const FinishParams fp{p.partial, low, g.b, g.ids, g.out, static_cast<int>(g.T), static_cast<int>(g.N), p.n_out, g.R, g.L,
-                        f.slot_rows, (p.n_out + rows_out - 1) / rows_out, f.whole,
-                        (p.K + umma::kBK - 1) / umma::kBK, f.G};
-  cfg.gridDim = dim3(static_cast<unsigned>(fp.tiles), static_cast<unsigned>((g.T + kFinishTokens - 1) / kFinishTokens), 1);
+                        f.slot_rows, f.row_tiles, f.whole, (p.K + umma::kBK - 1) / umma::kBK, f.G};
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(f.tiles), static_cast<unsigned>((g.T + kFinishTokens - 1) / kFinishTokens), 1);
   cfg.blockDim = dim3(128, 1, 1);
   cfg.dynamicSmemBytes = launch_smem(static_cast<size_t>(kFinishTokens) * g.R * 4);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1] = {pdl_attribute()};
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, adapter_finish_kernel<SWIGLU>, fp);
 }
 
@@ -260,11 +271,11 @@ cudaError_t many_tokens(const AdapterLinear& g, cudaStream_t stream) {
 
 int64_t adapter_workspace(int64_t T, int64_t N, int64_t K, int R, int L) {
   (void)K;
-  return static_cast<int64_t>(T <= kFewTokens ? Few(T, N, R).bytes : Many(T, R, L).bytes);
+  return static_cast<int64_t>(few_form(T, R) ? Few(T, N, R).bytes : Many(T, R, L).bytes);
 }
 
 cudaError_t launch_adapter_linear(const AdapterLinear& g, cudaStream_t stream) {
-  if (g.T <= kFewTokens) return g.swiglu ? few_tokens<true>(g, stream) : few_tokens<false>(g, stream);
+  if (few_form(g.T, g.R)) return g.swiglu ? few_tokens<true>(g, stream) : few_tokens<false>(g, stream);
   return g.swiglu ? many_tokens<true>(g, stream) : many_tokens<false>(g, stream);
 }
 

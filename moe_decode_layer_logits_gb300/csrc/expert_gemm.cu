@@ -45,7 +45,7 @@ cudaError_t prepare_and_launch(const ExpertGemm& g, cudaStream_t stream) {
 }  // namespace
 
 int64_t expert_gemm_workspace(int64_t n_rows) {
-  return n_rows <= 0 ? 0 : static_cast<int64_t>(sm_count()) * 2 * slot_rows_of(n_rows) * umma::kBM * 4;
+  return n_rows <= 0 ? 0 : static_cast<int64_t>(gemm_ctas()) * 2 * slot_rows_of(n_rows) * umma::kBM * 4;
 }
 
 cudaError_t launch_expert_gemm(const ExpertGemm& g, cudaStream_t stream) {

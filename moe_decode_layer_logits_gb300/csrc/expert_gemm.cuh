@@ -42,8 +42,11 @@
 //  - kRows    act, one rounding, row r of the output;
 //  - kLow     scaled by the segment, left as two BF16 parts (value and rest): the
 //             low-rank product of an adapter, 16 significant bits;
-//  - kParts   every piece left as an FP32 partial tile, for the caller's own
-//             last kernel;
+//  - kParts   one segment: every piece left as an FP32 partial tile, for the
+//             caller's own last kernel, and the adapters' low-rank products of
+//             the rows computed by further warps beside it.  The weights are a
+//             parameter, so the first stages are requested before the wait for
+//             the previous kernel;
 //  - kScatter rows sorted by adapter, every segment starting on a multiple of
 //             16 rows: behind a tile's K blocks come, for each adapter that has
 //             rows in the tile, its B against the two parts of its low-rank
@@ -63,14 +66,20 @@ namespace {
 
 constexpr int kMaxStages = 12;
 constexpr int kRingBytes = 200 * 1024;
-constexpr int kSoloRows = 128;  // most rows of a single CTA's tile
-constexpr int kPairRows = 256;  // rows of a pair's tile
+constexpr int kSoloRows = 128;  // most rows of a single CTA's tile (1 << 7)
+constexpr int kPairRows = 256;  // rows of a pair's tile (1 << 8)
 constexpr int kAccCols = 256;
+constexpr int kMaxCtas = 256;   // of a launch
 constexpr int kLoaders = 4;     // gathering warps
 
-constexpr int threads_of(bool gather) { return 192 + (gather ? 32 * (kLoaders + 1) : 0); }
+constexpr int kLowWarps = 8;    // kParts: warps that compute low-rank products
+
 
 enum Out { kRows, kLow, kParts, kScatter };
+
+constexpr int threads_of(bool gather, Out out) {
+  return 192 + (gather ? 32 * (kLoaders + 1) : 0) + (out == kParts ? 32 * kLowWarps : 0);
+}
 
 struct GemmParams {
   const uint16_t* x;
@@ -86,9 +95,12 @@ struct GemmParams {
   int slot_rows;  // rows of a partial tile's slot
   int weave;      // SwiGLU: one copy brings the whole weight tile (n_out a multiple of 16)
   int withhold;   // test hook: the K block CTA 0 never loads, or -1
-  int wait_late;  // the inputs are ready at the start: wait for the previous kernel at the end
   // adapters
-  const float* scale;     // kLow: [E] factors
+  const float* scale;     // kLow, kParts: factor of each
+  const uint16_t* a;      // kParts: [L, R, K]
+  const int32_t* ids;     // kParts: [n_rows]
+  float* low32;           // kParts: [n_rows, R] low-rank products
+  int L;
   uint16_t* low[2];       // kLow, kScatter: [n_rows, R] value and rest
   const int32_t* seg;     // kScatter: [segs + 1] first rows by adapter, then the end
   int segs, R;            // kScatter: the last segment's rows have no adapter
@@ -102,9 +114,15 @@ struct Barriers {
   uint32_t tmem_base;
   int abort_flag;
   int bn, few;
+  int pieces;
 };
 
 __host__ __device__ inline int round_up(int v, int m) { return (v + m - 1) / m * m; }
+
+// a / b for a >= 0, b > 0; in 32 bits where a fits.
+__device__ __forceinline__ int64_t quotient(int64_t a, int b) {
+  return a >> 32 ? a / b : static_cast<int64_t>(static_cast<uint32_t>(a) / static_cast<uint32_t>(b));
+}
 
 // The tile list in shared memory: per segment its first row, its rows, and the
 // row tiles before it.
@@ -114,43 +132,74 @@ struct Tiles {
   int* before;  // E + 1
 };
 
-// Rows per tile of single CTAs, from the mean rows of the segments that have
-// any: the smallest of 32, 64, 128 that leaves room for a segment a half larger.
-__device__ __forceinline__ int tile_rows(int mean) {
+// Rows per tile of single CTAs (a power of two), from the mean rows of the
+// segments that have any: the smallest of 32, 64, 128 that leaves room for a
+// segment a half larger.
+__device__ __forceinline__ int tile_shift(int mean) {
   const int want = mean + (mean + 1) / 2;
-  return want <= 32 ? 32 : want <= 64 ? 64 : kSoloRows;
+  return want <= 32 ? 5 : want <= 64 ? 6 : 7;
 }
 
 // A gather of up to this mean of rows is TMA's.
 constexpr int kFewRows = 4;
 
+// Row tiles of the one segment of kScatter: of the few numbers that hold it,
+// the one whose rounds over the pairs take the fewest rows.
+__device__ __forceinline__ int scatter_tiles(int total, int mt, int G) {
+  const int least = (total + kPairRows - 1) / kPairRows;
+  int best = least;
+  long long cost = -1;
+  for (int n = least; n < least + 8 && n > 0; ++n) {
+    const long long c = ((static_cast<long long>(n) * mt + G - 1) / G) * round_up((total + n - 1) / n, 16);
+    if (cost < 0 || c < cost) {
+      cost = c;
+      best = n;
+    }
+  }
+  return best;
+}
+
 // Fills the tile list; every thread of the block calls it.  Afterwards *bn_out
 // holds the rows per tile and *few_out whether the segments have few rows.
-template <bool PAIR>
-__device__ void list_tiles(const GemmParams& p, Tiles t, int* bn_out, int* few_out, bool report) {
-  for (int e = threadIdx.x; e < p.E; e += blockDim.x) {
-    int64_t beg = 0, cnt = p.seg ? p.seg[p.segs] : p.n_rows;
-    if (p.offsets) {
-      beg = p.offsets[e];
-      cnt = p.counts[e];
-      if (beg < 0 || cnt < 0 || beg + cnt > p.n_rows) {  // not inside the rows: skipped
-        if (report && p.err_flag) atomicOr(p.err_flag, MOE_FLAG_BAD_INDEX);
-        beg = 0;
-        cnt = 0;
-      }
+template <bool PAIR, Out OUT>
+__device__ void list_tiles(const GemmParams& p, Tiles t, int mt, int* bn_out, int* few_out, bool report) {
+  if (OUT == kParts || OUT == kScatter) {  // one segment, not the caller's
+    if (threadIdx.x == 0) {
+      const int n = OUT == kScatter ? p.seg[p.segs] : static_cast<int>(p.n_rows);
+      const int bn = PAIR ? kPairRows : n <= 32 ? 32 : n <= 64 ? 64 : kSoloRows;
+      t.start[0] = 0;
+      t.count[0] = n;
+      t.before[0] = 0;
+      t.before[1] = OUT == kScatter ? scatter_tiles(n, mt, gridDim.x >> 1) : (n + bn - 1) / bn;
+      *bn_out = bn;
+      *few_out = 0;
     }
-    t.start[e] = static_cast<int>(beg);
-    t.count[e] = static_cast<int>(cnt);
-  }
-  __syncthreads();
-  if (threadIdx.x < 32) {
+  } else if (threadIdx.x < 32) {
+    // lane l takes `per` neighbouring segments, eight loaded at once
     const int lane = threadIdx.x;
     const int per = (p.E + 31) / 32, b = min(p.E, lane * per), e = min(p.E, b + per);
     long long total = 0;
     int active = 0;
-    for (int i = b; i < e; ++i) {
-      total += t.count[i];
-      active += t.count[i] > 0 ? 1 : 0;
+    for (int i0 = b; i0 < e; i0 += 8) {
+      int beg[8], cnt[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        beg[i] = i0 + i < e ? p.offsets[i0 + i] : 0;
+        cnt[i] = i0 + i < e ? p.counts[i0 + i] : 0;
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        if (i0 + i >= e) break;
+        if (beg[i] < 0 || cnt[i] < 0 || static_cast<int64_t>(beg[i]) + cnt[i] > p.n_rows) {  // not inside the rows: skipped
+          if (report && p.err_flag) atomicOr(p.err_flag, MOE_FLAG_BAD_INDEX);
+          beg[i] = 0;
+          cnt[i] = 0;
+        }
+        t.start[i0 + i] = beg[i];
+        t.count[i0 + i] = cnt[i];
+        total += cnt[i];
+        active += cnt[i] > 0 ? 1 : 0;
+      }
     }
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) {
@@ -163,9 +212,18 @@ __device__ void list_tiles(const GemmParams& p, Tiles t, int* bn_out, int* few_o
       total = 0;
     }
     const int mean = active > 0 ? static_cast<int>((total + active - 1) / active) : 0;
-    const int bn = PAIR ? kPairRows : tile_rows(mean);
+    int shift = PAIR ? 8 : tile_shift(mean);  // rows per tile, as a power of two
+    if (OUT == kLow) {
+      // narrow weights, so few tiles: the widest rows per tile that still give
+      // every CTA one
+      for (shift = 7; shift > 5; --shift) {
+        int tiles = 0;
+        for (int i = b; i < e; ++i) tiles += (t.count[i] + (1 << shift) - 1) >> shift;
+        if (__reduce_add_sync(0xFFFFFFFFu, tiles) >= static_cast<int>(gridDim.x)) break;
+      }
+    }
     int mine = 0;
-    for (int i = b; i < e; ++i) mine += (t.count[i] + bn - 1) / bn;
+    for (int i = b; i < e; ++i) mine += (t.count[i] + (1 << shift) - 1) >> shift;
     int upto = mine;
 #pragma unroll
     for (int off = 1; off < 32; off <<= 1) {
@@ -175,11 +233,11 @@ __device__ void list_tiles(const GemmParams& p, Tiles t, int* bn_out, int* few_o
     int at = upto - mine;
     for (int i = b; i < e; ++i) {
       t.before[i] = at;
-      at += (t.count[i] + bn - 1) / bn;
+      at += (t.count[i] + (1 << shift) - 1) >> shift;
     }
     if (lane == 31) {
       t.before[p.E] = upto;
-      *bn_out = bn;
+      *bn_out = 1 << shift;
       *few_out = mean <= kFewRows;
     }
   }
@@ -187,30 +245,40 @@ __device__ void list_tiles(const GemmParams& p, Tiles t, int* bn_out, int* few_o
 }
 
 // One piece of work: weight tile m and nr rows from r0 of segment e, K blocks
-// [kb0, kb1).  slot >= 0: an incomplete sum, left in that slot of this CTA.
-struct Piece {
-  int e, m, r0, nr, kb0, kb1, slot, alone;
-  int64_t tile;
+// [kb0, kb1).  part >= 0: left as an FP32 partial tile at that place.
+struct __align__(16) Piece {
+  int e, m, r0, nr, kb0, kb1, part, alone;
 };
 
+constexpr int kPieces = 256;  // of a walker that are kept in shared memory
+
+// How the tile list is given out to G walkers (CTAs or pairs).
 struct Schedule {
   int64_t tiles, whole;  // tiles in the list, tiles given out whole
   int64_t rest_units;    // K blocks of the split round
-  int mt, nkb, G;        // weight tiles, K blocks, walkers (CTAs or pairs)
-  __device__ Schedule(const GemmParams& p, const Tiles& t, int rows_out, int walkers, bool split) : G(walkers) {
-    mt = (p.n_out + rows_out - 1) / rows_out;
+  int mt, nkb, G;        // weight tiles, K blocks, walkers
+  __device__ Schedule(const GemmParams& p, const Tiles& t, int weight_tiles, int walkers, bool split)
+      : mt(weight_tiles), G(walkers) {
     nkb = (p.K + umma::kBK - 1) / umma::kBK;
     tiles = static_cast<int64_t>(t.before[p.E]) * mt;
-    whole = split ? tiles / G * G : tiles;
+    whole = split ? quotient(tiles, G) * G : tiles;
     rest_units = (tiles - whole) * nkb;
   }
   // Start of walker b's share of the split round.
-  __device__ int64_t share(int b) const { return rest_units * b / G; }
+  __device__ int64_t share(int b) const { return quotient(rest_units * b, G); }
+  // Pieces of walker b: its whole tiles b, b + G, ..., then its share, which is
+  // no longer than a tile and so lies in at most two.
+  __device__ int pieces(int b) const {
+    int n = whole > b ? static_cast<int>(quotient(whole - b + G - 1, G)) : 0;
+    const int64_t u = share(b), left = share(b + 1) - u;
+    if (left > 0) n += u - quotient(u, nkb) * nkb + left > nkb ? 2 : 1;
+    return n;
+  }
 };
 
 // Tile `tile` of the list.
 __device__ __forceinline__ void locate(const Tiles& t, int E, int mt, int64_t tile, Piece& w) {
-  const int at = static_cast<int>(tile / mt);
+  const int at = static_cast<int>(quotient(tile, mt));
   int lo = 0, hi = E;  // before[lo] <= at < before[hi]
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
@@ -223,50 +291,42 @@ __device__ __forceinline__ void locate(const Tiles& t, int E, int mt, int64_t ti
   // row tiles of nearly the same size, in whole sixteens
   const int cnt = t.count[lo];
   const int64_t sixteens = (static_cast<int64_t>(cnt) + 15) / 16;
-  const int a = static_cast<int>(sixteens * tt / ntt * 16);
-  const int b = static_cast<int>(min(static_cast<int64_t>(cnt), sixteens * (tt + 1) / ntt * 16));
+  const int a = static_cast<int>(quotient(sixteens * tt, ntt) * 16);
+  const int b = static_cast<int>(min(static_cast<int64_t>(cnt), quotient(sixteens * (tt + 1), ntt) * 16));
   w.e = lo;
   w.m = local / ntt;
   w.r0 = t.start[lo] + a;
   w.nr = b - a;
   w.alone = ntt == 1;
-  w.tile = tile;
 }
 
-// The pieces of one walker, in the order in which all its warps walk them.
-struct Walk {
-  int64_t next, u, uend;
-  __device__ Walk(const Schedule& s, int who) : next(who), u(s.share(who)), uend(s.share(who + 1)) {}
-  __device__ bool get(const Schedule& s, const Tiles& t, int E, Piece& w) {
-    if (next < s.whole) {
-      locate(t, E, s.mt, next, w);
-      w.kb0 = 0;
-      w.kb1 = s.nkb;
-      w.slot = -1;
-      next += s.G;
-      return true;
-    }
-    if (u >= uend) return false;
-    locate(t, E, s.mt, s.whole + u / s.nkb, w);
-    w.kb0 = static_cast<int>(u % s.nkb);
-    w.kb1 = static_cast<int>(min(static_cast<int64_t>(s.nkb), w.kb0 + (uend - u)));
-    w.slot = w.kb0 == 0 ? (w.kb1 == s.nkb ? -1 : 1) : 0;
-    u += w.kb1 - w.kb0;
-    return true;
-  }
-};
-
-__device__ __forceinline__ float* slot_tile(const GemmParams& p, int cta, int slot) {
-  return p.partial + (static_cast<int64_t>(cta) * 2 + slot) * p.slot_rows * umma::kBM;
-}
-
-// kParts: the place of any piece of the list.  A CTA has at most one piece of
-// the split round that starts a tile, and one that does not; whole tiles follow.
+// Places of the partial tiles.  A walker has at most one piece of the split
+// round that starts a tile (kb0 == 0), and one that does not; kParts leaves its
+// whole tiles too, behind them.
 __host__ __device__ inline int64_t parts_index(int64_t whole_tile, int G, int cta, int kb0) {
   return whole_tile >= 0 ? 2 * static_cast<int64_t>(G) + whole_tile : 2 * static_cast<int64_t>(cta) + (kb0 == 0 ? 1 : 0);
 }
-__device__ __forceinline__ float* parts_tile(const GemmParams& p, const Schedule& s, int cta, const Piece& w) {
-  return p.partial + parts_index(w.tile < s.whole ? w.tile : -1, s.G, cta, w.kb0) * p.slot_rows * umma::kBM;
+
+// Piece i of a walker.  (One copy of the code: its divisions are long, and every
+// warp of the block would fetch its own.)
+__device__ __noinline__ void make_piece(const Schedule& s, const Tiles& t, int E, int who, int i, bool parts, Piece& w) {
+  const int whole = s.whole > who ? static_cast<int>(quotient(s.whole - who + s.G - 1, s.G)) : 0;
+  if (i < whole) {
+    const int64_t tile = who + static_cast<int64_t>(i) * s.G;
+    locate(t, E, s.mt, tile, w);
+    w.kb0 = 0;
+    w.kb1 = s.nkb;
+    w.part = parts ? static_cast<int>(parts_index(tile, s.G, 0, 0)) : -1;
+    return;
+  }
+  int64_t u = s.share(who);
+  const int64_t end = s.share(who + 1);
+  if (i > whole) u = (quotient(u, s.nkb) + 1) * s.nkb;
+  const int64_t nth = quotient(u, s.nkb);
+  locate(t, E, s.mt, s.whole + nth, w);
+  w.kb0 = static_cast<int>(u - nth * s.nkb);
+  w.kb1 = static_cast<int>(min(static_cast<int64_t>(s.nkb), w.kb0 + (end - u)));
+  w.part = !parts && w.kb0 == 0 && w.kb1 == s.nkb ? -1 : static_cast<int>(parts_index(-1, s.G, who, w.kb0));
 }
 
 __device__ __forceinline__ float silu_mul(float g, float u) { return g / (1.f + expf(-g)) * u; }
@@ -373,15 +433,16 @@ struct Adapters {
 };
 
 template <bool SWIGLU, bool GATHER, bool PAIR, Out OUT>
-__global__ void __launch_bounds__(threads_of(GATHER), 1)
+__global__ void __launch_bounds__(threads_of(GATHER, OUT), 1)
 expert_gemm_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constant__ CUtensorMap tmap_w,
-                   const __grid_constant__ CUtensorMap tmap_b, const GemmParams p) {
+                   const __grid_constant__ CUtensorMap tmap_b, const __grid_constant__ GemmParams p) {
   static_assert(OUT != kScatter || (PAIR && GATHER), "sorted rows run in pairs");
   using namespace umma;
   extern __shared__ uint8_t smem_raw[];
   __shared__ Barriers sb;
   uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
-  int* list = reinterpret_cast<int*>(ring + kRingBytes);
+  Piece* piece_s = reinterpret_cast<Piece*>(ring + kRingBytes);
+  int* list = reinterpret_cast<int*>(piece_s + kPieces);
   const Tiles t{list, list + p.E, list + 2 * p.E};
   int* seg = list + 3 * p.E + 1;  // kScatter: the adapters' first rows
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -389,27 +450,47 @@ expert_gemm_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_cons
   const int who = PAIR ? blockIdx.x >> 1 : blockIdx.x;
   volatile int* abort_v = &sb.abort_flag;
 
-  if (warp == 1) tmem_alloc<PAIR>(&sb.tmem_base, 2 * kAccCols);
-  allow_dependent_launch();
-  if (!p.wait_late) grid_dependency_wait();
-  if (OUT == kScatter)
-    for (int i = threadIdx.x; i <= p.segs; i += blockDim.x) seg[i] = p.seg[i];
-  list_tiles<PAIR>(p, t, &sb.bn, &sb.few, blockIdx.x == 0);
-  const bool few = GATHER && !PAIR && sb.few;  // rows gathered by TMA
-  const int depth = OUT == kScatter ? (p.R + kBK - 1) / kBK : 0;  // K blocks of an adapter's B
-  if (threadIdx.x == 0) {
-    for (int s = 0; s < kMaxStages; ++s) {
-      mbar_init(&sb.full[s], 1 + (GATHER && !few ? (PAIR ? 2 : 1) : 0));
-      mbar_init(&sb.landed[s], 32 * kLoaders);
-      mbar_init(&sb.empty[s], 1);
-    }
-    for (int a = 0; a < 2; ++a) {
-      mbar_init(&sb.acc_full[a], 1);
-      mbar_init(&sb.acc_empty[a], PAIR ? 8 : 4);
-    }
+  if (threadIdx.x < kMaxStages) {
+    mbar_init(&sb.landed[threadIdx.x], 32 * kLoaders);
+    mbar_init(&sb.empty[threadIdx.x], 1);
+    mbar_init_fence();
+  } else if (threadIdx.x < kMaxStages + 2) {
+    mbar_init(&sb.acc_full[threadIdx.x - kMaxStages], 1);
+    mbar_init(&sb.acc_empty[threadIdx.x - kMaxStages], PAIR ? 8 : 4);
+    mbar_init_fence();
+  } else if (threadIdx.x == kMaxStages + 2) {
     mbar_init(&sb.drained, 1);
     sb.abort_flag = 0;
     mbar_init_fence();
+  } else if (threadIdx.x == kMaxStages + 3) {
+    prefetch_map(&tmap_w);
+    prefetch_map(&tmap_x);
+  }
+  if (warp == 1) tmem_alloc<PAIR>(&sb.tmem_base, 2 * kAccCols);
+  if (OUT != kParts) {
+    // the trigger comes behind the wait, so that what is launched next finds
+    // this kernel's own inputs ready
+    grid_dependency_wait();
+    allow_dependent_launch();
+  }
+  const int rows_out = (SWIGLU ? 64 : 128) * (PAIR ? 2 : 1), mt = (p.n_out + rows_out - 1) / rows_out;
+  if (OUT == kScatter)
+    for (int i = threadIdx.x; i <= p.segs; i += blockDim.x) seg[i] = p.seg[i];
+  list_tiles<PAIR, OUT>(p, t, mt, &sb.bn, &sb.few, blockIdx.x == 0);  // kParts: reads no global memory
+  const bool few = GATHER && !PAIR && sb.few;  // rows gathered by TMA
+  const int depth = OUT == kScatter ? (p.R + kBK - 1) / kBK : 0;  // K blocks of an adapter's B
+  if (threadIdx.x < kMaxStages) {
+    // a stage is full when its copies have landed and, where other warps gather
+    // the rows, they have been reported (by each CTA of a pair)
+    mbar_init(&sb.full[threadIdx.x], 1 + (GATHER && !few ? (PAIR ? 2 : 1) : 0));
+    mbar_init_fence();
+  }
+  // this walker's pieces, one a thread
+  const Schedule s(p, t, mt, PAIR ? gridDim.x >> 1 : gridDim.x, !PAIR && OUT != kLow);
+  {
+    const int n = s.pieces(who);
+    if (threadIdx.x == 0) sb.pieces = n;
+    for (int i = threadIdx.x; i < min(n, kPieces); i += blockDim.x) make_piece(s, t, p.E, who, i, OUT == kParts, piece_s[i]);
   }
   fence_before_sync();
   __syncthreads();
@@ -422,7 +503,20 @@ expert_gemm_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_cons
   // a stage: 128 weight rows, then this CTA's rows (a pair's CTA holds half of the tile's)
   const int stage_bytes = (kBM + (PAIR ? kPairRows / 2 : sb.bn)) * kRowBytes;
   const int nstages = min(kMaxStages, kRingBytes / stage_bytes);
-  const Schedule s(p, t, (SWIGLU ? 64 : 128) * (PAIR ? 2 : 1), PAIR ? gridDim.x >> 1 : gridDim.x, !PAIR);
+  const int pieces = sb.pieces;
+  // all warps walk the pieces in the same order
+  auto next = [&](int& at, Piece& w) {
+    if (at >= pieces) return false;
+    if (at < kPieces) {
+      w = piece_s[at];
+    } else {
+      Piece made;  // (a reference to w itself would keep it out of the registers)
+      make_piece(s, t, p.E, who, at, OUT == kParts, made);
+      w = made;
+    }
+    ++at;
+    return true;
+  };
   // barriers that the first CTA of a pair keeps for both
   const uint32_t full0 = PAIR ? cluster_addr(&sb.full[0], 0) : smem_addr(&sb.full[0]);
   const uint32_t acc_empty0 = PAIR ? cluster_addr(&sb.acc_empty[0], 0) : smem_addr(&sb.acc_empty[0]);
@@ -431,26 +525,70 @@ expert_gemm_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_cons
     // -------------------------------------------------------------- loads
     const uint64_t once = l2_evict_first_policy(), keep = l2_evict_normal_policy();
     const int withheld = who == 0 ? p.withhold : -1;
-    Walk walk(s, who);
+    auto load_weights = [&](const CUtensorMap* map, uint32_t dst, int kb, int m, int e, uint32_t bar, uint64_t pol) {
+      if (!SWIGLU) {
+        if (lane == 0) tma_load_5d<PAIR>(dst, map, kb * kBK, m * 128, 0, 0, e, bar, pol);
+      } else if (p.weave) {
+        if (lane == 0) tma_load_5d<PAIR>(dst, map, kb * kBK, 0, 0, m * 4, e, bar, pol);
+      } else if (lane < 4) {  // 16 gate rows and their 16 up rows
+        tma_load_5d<PAIR>(dst + lane * 32 * kRowBytes, map, kb * kBK, m * 64 + lane * 16, 0, 0, e, bar, pol);
+      }
+    };
+    // bytes of a stage's copies, and (few) the tokens of lane l's rows 4 l .. + 3
+    auto stage_copies = [&](const Piece& w) {
+      const int mine = PAIR ? round_up(w.nr, 16) / 2 : w.nr;  // rows in this CTA
+      const int rows = GATHER ? (few ? round_up(mine, 4) : 0) : round_up(mine, 32);
+      return static_cast<uint32_t>((PAIR ? 2 : 1) * (kBM + rows)) * kRowBytes;
+    };
+    auto raw_tokens = [&](const Piece& w) {
+      int v[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[i] = few && lane * 4 + i < w.nr ? p.row_token[w.r0 + lane * 4 + i] : 0;
+      return make_int4(v[0], v[1], v[2], v[3]);
+    };
+    int at = 0;
     Piece w;
     int n = 0;  // stages so far
+    int early = 0;
+    if (OUT == kParts) {
+      // a ring of weights before the wait; their rows follow behind it.  (With
+      // more than one stage of weights in the copy engine's queue the rows wait
+      // for them, so the other forms do not run ahead.)
+      int ahead = 0;
+      while (early < nstages && next(ahead, w)) {
+        const uint32_t bytes = stage_copies(w);
+        for (int kb = w.kb0; kb < w.kb1 && early < nstages; ++kb, ++early) {
+          if (lane == 0) mbar_arrive_expect_tx(&sb.full[early], bytes);
+          __syncwarp();
+          load_weights(&tmap_w, smem_addr(ring) + static_cast<uint32_t>(early * stage_bytes), kb, w.m, w.e,
+                       full0 + early * 8, w.alone ? once : keep);
+        }
+      }
+      grid_dependency_wait();
+      // behind the wait, so that what is launched next finds the inputs ready
+      allow_dependent_launch();
+    }
+    // the tokens of a piece are loaded a piece ahead
+    int peek = 0;
+    Piece coming;
+    int4 raw = make_int4(0, 0, 0, 0);
+    if (few && next(peek, coming)) raw = raw_tokens(coming);
     bool stop = false;
-    while (!stop && walk.get(s, t, p.E, w)) {
+    while (!stop && next(at, w)) {
       const int mine = PAIR ? round_up(w.nr, 16) / 2 : w.nr;  // rows in this CTA
       const int boxes = GATHER ? 0 : (mine + 31) >> 5, quads = few ? (mine + 3) >> 2 : 0;
-      const uint32_t bytes = static_cast<uint32_t>((PAIR ? 2 : 1) * (kBM + boxes * 32 + quads * 4)) * kRowBytes;
-      int4 tok = make_int4(0, 0, 0, 0);  // lane l: rows 4 l .. 4 l + 3
-      if (lane < quads) {
-        int v[4];
+      const uint32_t bytes = stage_copies(w);
+      int4 tok = raw;
+      if (few) {
+        if (next(peek, coming)) raw = raw_tokens(coming);
+        int* v = &tok.x;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          v[i] = lane * 4 + i < w.nr ? p.row_token[w.r0 + lane * 4 + i] : 0;
           if (v[i] < 0 || v[i] >= p.n_x) {  // loads token 0, stored as zeros
             if (p.err_flag) atomicOr(p.err_flag, MOE_FLAG_BAD_INDEX);
             v[i] = 0;
           }
         }
-        tok = make_int4(v[0], v[1], v[2], v[3]);
       }
       const int m = PAIR ? w.m * 2 + rank : w.m, r0 = w.r0 + rank * mine;
       const uint64_t pol = w.alone ? once : keep;
@@ -464,14 +602,10 @@ expert_gemm_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_cons
         if (n == withheld) continue;  // neither armed nor loaded: the MMA warp's wait runs out
         const uint32_t a = smem_addr(ring) + static_cast<uint32_t>(st * stage_bytes);
         const uint32_t b = a + kBM * kRowBytes, bar = full0 + st * 8;
-        if (lane == 0 && rank == 0) mbar_arrive_expect_tx(&sb.full[st], bytes);
-        __syncwarp();
-        if (!SWIGLU) {
-          if (lane == 0) tma_load_5d<PAIR>(a, &tmap_w, kb * kBK, m * 128, 0, 0, w.e, bar, pol);
-        } else if (p.weave) {
-          if (lane == 0) tma_load_5d<PAIR>(a, &tmap_w, kb * kBK, 0, 0, m * 4, w.e, bar, pol);
-        } else if (lane < 4) {  // 16 gate rows and their 16 up rows
-          tma_load_5d<PAIR>(a + lane * 32 * kRowBytes, &tmap_w, kb * kBK, m * 64 + lane * 16, 0, 0, w.e, bar, pol);
+        if (OUT != kParts || n >= early) {
+          if (lane == 0 && rank == 0) mbar_arrive_expect_tx(&sb.full[st], bytes);
+          __syncwarp();
+          load_weights(&tmap_w, a, kb, m, w.e, bar, pol);
         }
         if (lane < quads) tma_gather4(b + lane * 4 * kRowBytes, &tmap_x, kb * kBK, tok, bar);
         if (!GATHER && lane < boxes)
@@ -488,16 +622,9 @@ expert_gemm_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_cons
               break;
             }
             const uint32_t a = smem_addr(ring) + static_cast<uint32_t>(st * stage_bytes), bar = full0 + st * 8;
-            const int kb = i >> 1;
             if (lane == 0 && rank == 0) mbar_arrive_expect_tx(&sb.full[st], 2 * kBM * kRowBytes);
             __syncwarp();
-            if (!SWIGLU) {
-              if (lane == 0) tma_load_5d<PAIR>(a, &tmap_b, kb * kBK, m * 128, 0, 0, ad.a, bar, keep);
-            } else if (p.weave) {
-              if (lane == 0) tma_load_5d<PAIR>(a, &tmap_b, kb * kBK, 0, 0, m * 4, ad.a, bar, keep);
-            } else if (lane < 4) {
-              tma_load_5d<PAIR>(a + lane * 32 * kRowBytes, &tmap_b, kb * kBK, m * 64 + lane * 16, 0, 0, ad.a, bar, keep);
-            }
+            load_weights(&tmap_b, a, i >> 1, m, ad.a, bar, keep);
           }
         }
       }
@@ -512,11 +639,11 @@ expert_gemm_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_cons
   } else if (warp == 1) {
     // ---------------------------------------------------------------- MMA
     if (lane == 0 && rank == 0) {
-      Walk walk(s, who);
+      int at = 0;
       Piece w;
       int n = 0, seq = 0;
       bool stop = false;
-      while (!stop && walk.get(s, t, p.E, w)) {
+      while (!stop && next(at, w)) {
         const int acc = seq & 1, use = seq >> 1;
         if (use > 0 && !wait(&sb.acc_empty[acc], (use - 1) & 1, abort_v)) break;
         fence_after_sync();
@@ -565,24 +692,23 @@ expert_gemm_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_cons
   } else if (warp < 6) {
     // ----------------------------------------------------------- epilogue
     const int q = warp & 3;  // this warp's quarter of the tensor-memory lanes
-    Walk walk(s, who);
+    if (OUT == kParts) grid_dependency_wait();
+    int at = 0;
     Piece w;
     int seq = 0;
-    while (walk.get(s, t, p.E, w)) {
+    while (next(at, w)) {
       const int acc = seq & 1, use = seq >> 1;
       ++seq;
       const bool ok = wait(&sb.acc_full[acc], use & 1, abort_v) && !*abort_v;
       if (!__all_sync(0xFFFFFFFFu, ok)) break;
       fence_after_sync();
       const uint32_t d = tmem + acc * kAccCols + (static_cast<uint32_t>(q * 32) << 16);
-      float* part = nullptr;
-      if (OUT == kParts) part = parts_tile(p, s, who, w) + q * 32 + lane;
-      else if (w.slot >= 0) part = slot_tile(p, who, w.slot) + q * 32 + lane;
+      float* part = p.partial + static_cast<int64_t>(w.part) * p.slot_rows * kBM + q * 32 + lane;
 #pragma unroll 1
       for (int c = 0; c < w.nr; c += 32) {
         uint32_t raw[32];
         tmem_ld32(d + static_cast<uint32_t>(c), raw);
-        if (OUT == kParts || part) {
+        if (OUT == kParts || w.part >= 0) {
 #pragma unroll
           for (int i = 0; i < 32; ++i)
             if (c + i < w.nr) part[(c + i) * kBM] = __uint_as_float(raw[i]);
@@ -600,16 +726,42 @@ expert_gemm_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_cons
         else mbar_arrive(&sb.acc_empty[acc]);
       }
     }
+  } else if (OUT == kParts) {
+    // -------------------------------------------------- low-rank products
+    // low32[t, r] = scale[a] * A_a[r] . x[t], one warp per (t, r)
+    grid_dependency_wait();
+    for (int64_t job = static_cast<int64_t>(blockIdx.x) * kLowWarps + warp - 6; job < p.n_rows * p.R;
+         job += static_cast<int64_t>(gridDim.x) * kLowWarps) {
+      const int64_t row = job / p.R;
+      const int r = static_cast<int>(job - row * p.R), id = p.ids[row];
+      if (id < 0 || id >= p.L) {
+        if (id >= p.L && lane == 0 && p.err_flag) atomicOr(p.err_flag, MOE_FLAG_BAD_INDEX);
+        continue;
+      }
+      const uint16_t* ar = p.a + (static_cast<int64_t>(id) * p.R + r) * p.K;
+      const uint16_t* xr = p.x + row * p.K;
+      float sum = 0.f;
+#pragma unroll 6
+      for (int k = lane * 8; k < p.K; k += 256) {
+        float f[8], g[8];
+        unpack8(ld_keep16(xr + k), f);
+        unpack8(ld_stream16(ar + k), g);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) sum = fmaf(f[i], g[i], sum);
+      }
+      sum = warp_sum(sum);
+      if (lane == 0) p.low32[job] = sum * p.scale[id];
+    }
   } else if (GATHER && !few && warp < 6 + kLoaders) {
     // ------------------------------------------------------------- gather
     // Warp j takes rows 16 i + 4 j .. + 3 of this CTA's rows, eight lanes a
     // row, 16 bytes a lane, at their place in the 128-byte swizzle.
     const int j = warp - 6, sub = lane >> 3, chunk = lane & 7;
-    Walk walk(s, who);
+    int at = 0;
     Piece w;
     int n = 0;
     bool stop = false;
-    while (!stop && walk.get(s, t, p.E, w)) {
+    while (!stop && next(at, w)) {
       const int mine = PAIR ? round_up(w.nr, 16) / 2 : w.nr;
       const int rounds = (mine - 4 * j + 15) >> 4;  // <= 8; none for the last warps of a small tile
       int tok[8];
@@ -676,11 +828,11 @@ expert_gemm_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_cons
   } else if (GATHER && !few) {
     // -------------------------------------------------- gathered rows are in
     if (lane == 0) {
-      Walk walk(s, who);
+      int at = 0;
       Piece w;
       int n = 0;
       bool stop = false;
-      while (!stop && walk.get(s, t, p.E, w)) {
+      while (!stop && next(at, w)) {
         int stages = w.kb1 - w.kb0;
         if (OUT == kScatter) {
           Adapters ad(p, seg, w);
@@ -708,7 +860,6 @@ expert_gemm_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_cons
     cluster_arrive_release();
     cluster_wait_acquire();
   }
-  if (p.wait_late) grid_dependency_wait();
   if (threadIdx.x == 0 && p.err_flag && *abort_v) atomicOr(p.err_flag, MOE_FLAG_TIMEOUT);
   if (warp == 1) {
     fence_after_sync();
@@ -718,35 +869,63 @@ expert_gemm_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_cons
 
 // Adds the partial tiles of the split round.  CTA (b, y) takes the tile at the
 // end of share b if that end lies inside it and no earlier share ends there,
-// and of its rows those with row / 16 % gridDim.y == y.
+// and of its rows those with row / 16 % gridDim.y == y.  What follows from the
+// segments comes before the wait for the products, which start this kernel
+// behind their own wait.  64 registers: it fits on an SM beside the products.
+constexpr int kJoinBatch = 2;  // pieces loaded at once
+
 template <bool SWIGLU, Out OUT>
-__global__ void __launch_bounds__(128) expert_join_kernel(const GemmParams p, int G) {
+__global__ void __launch_bounds__(128, 8) expert_join_kernel(const GemmParams p, int G) {
   extern __shared__ int join_list[];
-  __shared__ int bn, few;
+  __shared__ int bn, few, pieces;
+  __shared__ int piece_s[kMaxCtas];
   const Tiles t{join_list, join_list + p.E, join_list + 2 * p.E};
   allow_dependent_launch();
+  const int rows_out = SWIGLU ? 64 : 128, mt = (p.n_out + rows_out - 1) / rows_out;
+  list_tiles<false, OUT>(p, t, mt, &bn, &few, false);
+  const Schedule s(p, t, mt, G, true);
+  const int b = blockIdx.x, l = threadIdx.x, q = l >> 5;
+  const int64_t end = s.share(b + 1), tile0 = quotient(end, s.nkb) * s.nkb;
+  // the share ends between two tiles, or an earlier share ends in this tile
+  const bool none = end == tile0 || end >= s.rest_units || s.share(b) > tile0;
+  Piece w{};
+  if (!none) {
+    locate(t, p.E, s.mt, s.whole + quotient(end, s.nkb), w);
+    if (l < 32) {  // the tile's pieces in the order of K: this share's start of it, then the next shares'
+      int n = 1;
+      if (l == 0) piece_s[0] = static_cast<int>(parts_index(-1, G, b, 0));
+      for (int j0 = b + 1; j0 < G; j0 += 32) {
+        const int j = j0 + l;
+        const int64_t u0 = s.share(min(j, G)), u1 = s.share(min(j + 1, G));
+        const bool in = u0 < u1 && u0 < tile0 + s.nkb;
+        const unsigned bal = __ballot_sync(0xFFFFFFFFu, in);
+        if (in) piece_s[n + __popc(bal & ((1u << l) - 1u))] = static_cast<int>(parts_index(-1, G, j, 1));
+        n += __popc(bal);
+        if (s.share(min(j0 + 32, G)) >= tile0 + s.nkb) break;
+      }
+      if (l == 0) pieces = n;
+    }
+  }
+  __syncthreads();
   grid_dependency_wait();
-  list_tiles<false>(p, t, &bn, &few, false);
-  const Schedule s(p, t, SWIGLU ? 64 : 128, G, true);
-  const int b = blockIdx.x;
-  const int64_t end = s.share(b + 1), tile0 = end / s.nkb * s.nkb;
-  if (end == tile0 || end >= s.rest_units) return;  // the share ends between two tiles
-  if (s.share(b) > tile0) return;                   // an earlier share ends in this tile
-  Piece w;
-  locate(t, p.E, s.mt, s.whole + end / s.nkb, w);
-  int last = b + 1;
-  while (s.share(last + 1) < tile0 + s.nkb) ++last;
-  const int l = threadIdx.x, q = l >> 5;
+  if (none) return;
+  const int64_t step = static_cast<int64_t>(p.slot_rows) * umma::kBM;
   for (int c = blockIdx.y * 16; c < w.nr; c += gridDim.y * 16) {
     float v[16];
 #pragma unroll
     for (int i = 0; i < 16; ++i) v[i] = 0.f;
-    for (int j = b; j <= last; ++j) {
-      if (s.share(j) == s.share(j + 1)) continue;
-      const float* part = slot_tile(p, j, j == b ? 1 : 0) + l;
+    const float* part = p.partial + static_cast<int64_t>(c) * umma::kBM + l;
+    for (int j = 0; j < pieces; j += kJoinBatch) {
+      float f[kJoinBatch][16];
 #pragma unroll
-      for (int i = 0; i < 16; ++i)
-        if (c + i < w.nr) v[i] += part[(c + i) * umma::kBM];
+      for (int k = 0; k < kJoinBatch; ++k)
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+          f[k][i] = j + k < pieces && c + i < w.nr ? part[piece_s[j + k] * step + i * umma::kBM] : 0.f;
+#pragma unroll
+      for (int k = 0; k < kJoinBatch; ++k)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) v[i] += f[k][i];
     }
     store_cols<SWIGLU, OUT, 16>(p, w, w.m, c, q, v, store_aux<OUT>(p, w, c));
   }
@@ -779,9 +958,12 @@ inline bool make_map(CUtensorMap* map, const void* base, int rank, const cuuint6
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Dynamic shared memory: the ring, the tile list, the adapters' first rows.
+// CTAs of a launch: one per SM.
+inline int gemm_ctas() { return sm_count() < kMaxCtas ? sm_count() : kMaxCtas; }
+
+// Dynamic shared memory: the ring, the walker's pieces, the tile list, the adapters' first rows.
 inline size_t gemm_smem(int64_t E, int segs) {
-  return 1024 + kRingBytes + static_cast<size_t>(3 * E + 1 + segs + 1) * sizeof(int);
+  return 1024 + kRingBytes + kPieces * sizeof(Piece) + static_cast<size_t>(3 * E + 1 + segs + 1) * sizeof(int);
 }
 
 // Opt the kernel into its dynamic shared memory, once per device.
@@ -806,10 +988,10 @@ cudaError_t launch(const CUtensorMap& mx, const CUtensorMap& mw, const CUtensorM
   cudaError_t e = cudaGetDevice(&dev);
   if (e == cudaSuccess) e = opt_in<SWIGLU, GATHER, PAIR, OUT>(dev);
   if (e != cudaSuccess) return e;
-  const int G = PAIR ? sm_count() / 2 * 2 : sm_count();
+  const int G = PAIR ? gemm_ctas() / 2 * 2 : gemm_ctas();
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(G), 1, 1);
-  cfg.blockDim = dim3(threads_of(GATHER), 1, 1);
+  cfg.blockDim = dim3(threads_of(GATHER, OUT), 1, 1);
   cfg.dynamicSmemBytes = launch_smem(gemm_smem(p.E, p.segs));
   cfg.stream = stream;
   cudaLaunchAttribute attr[2] = {pdl_attribute(), {}};
@@ -823,12 +1005,14 @@ cudaError_t launch(const CUtensorMap& mx, const CUtensorMap& mw, const CUtensorM
     cfg.numAttrs = 2;
   }
   e = cudaLaunchKernelEx(&cfg, expert_gemm_kernel<SWIGLU, GATHER, PAIR, OUT>, mx, mw, mb, p);
-  if (e != cudaSuccess || PAIR || OUT == kParts) return e;
-  const int rows16 = (p.slot_rows + 15) / 16;
-  cfg.gridDim = dim3(static_cast<unsigned>(G - 1), static_cast<unsigned>(rows16), 1);
-  cfg.blockDim = dim3(128, 1, 1);
-  cfg.dynamicSmemBytes = launch_smem(static_cast<size_t>(3 * p.E + 1) * sizeof(int));
-  return cudaLaunchKernelEx(&cfg, expert_join_kernel<SWIGLU, OUT>, p, G);
+  if constexpr (!PAIR && OUT == kRows) {
+    if (e != cudaSuccess) return e;
+    cfg.gridDim = dim3(static_cast<unsigned>(G - 1), static_cast<unsigned>((p.slot_rows + 15) / 16), 1);
+    cfg.blockDim = dim3(128, 1, 1);
+    cfg.dynamicSmemBytes = launch_smem(static_cast<size_t>(3 * p.E + 1) * sizeof(int));
+    e = cudaLaunchKernelEx(&cfg, expert_join_kernel<SWIGLU, OUT>, p, G);
+  }
+  return e;
 }
 
 // Rows of a partial tile's slot.
