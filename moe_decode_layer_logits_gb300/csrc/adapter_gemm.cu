@@ -58,12 +58,9 @@ __global__ void __launch_bounds__(128, 8) adapter_finish_kernel(const FinishPara
     id_s[l] = a < p.L ? a : -1;
   }
   // this tile of the list: the row tile that holds t0 (eight tokens lie in one)
-  const int sixteens = (p.T + 15) / 16;
-  int tt = 0, r0 = 0;
-  while (tt + 1 < p.row_tiles && sixteens * (tt + 1) / p.row_tiles * 16 <= t0) {
-    ++tt;
-    r0 = sixteens * tt / p.row_tiles * 16;
-  }
+  int tt = 0;
+  while (tt + 1 < p.row_tiles && tile_begin(p.T, p.row_tiles, tt + 1) <= t0) ++tt;
+  const int r0 = tile_begin(p.T, p.row_tiles, tt);
   // its pieces, in the order of K (sizes within 32 bits: fewer tiles than SMs
   // are split, of at most 1024 K blocks each)
   const int tile = m * p.row_tiles + tt;
@@ -97,13 +94,18 @@ __global__ void __launch_bounds__(128, 8) adapter_finish_kernel(const FinishPara
       prefetch_l2(p.b + (static_cast<int64_t>(a) * p.N + ((l & 1) ? p.n_out : 0) + first) * p.R,
                   static_cast<uint32_t>(n) * p.R * 2);
   }
+  const float* part = p.partial + static_cast<int64_t>(t0 - r0) * umma::kBM + l;
+  const int64_t step = static_cast<int64_t>(p.slot_rows) * umma::kBM;
+  const int o = SWIGLU ? m * 64 + q * 16 + (l & 15) : m * 128 + l;
+  const int64_t row = SWIGLU && (l & 16) ? static_cast<int64_t>(p.n_out) + o : o;  // this lane's weight row
+  GemmParams g{};
+  g.out = p.out;
+  g.n_out = p.n_out;
   grid_dependency_wait();
   for (int i = l; i < nt * p.R; i += 128) low_s[i] = p.low[static_cast<int64_t>(t0) * p.R + i];
   float v[kFinishTokens];
 #pragma unroll
   for (int i = 0; i < kFinishTokens; ++i) v[i] = 0.f;
-  const float* part = p.partial + static_cast<int64_t>(t0 - r0) * umma::kBM + l;
-  const int64_t step = static_cast<int64_t>(p.slot_rows) * umma::kBM;
   for (int c = 0; c < pieces; c += kFinishBatch) {
     float f[kFinishBatch][kFinishTokens];
 #pragma unroll
@@ -117,10 +119,7 @@ __global__ void __launch_bounds__(128, 8) adapter_finish_kernel(const FinishPara
       for (int i = 0; i < kFinishTokens; ++i) v[i] += f[j][i];
   }
   __syncthreads();
-  // this lane's weight row
-  const int o = SWIGLU ? m * 64 + q * 16 + (l & 15) : m * 128 + l;
   if (o < p.n_out) {
-    const int64_t row = SWIGLU && (l & 16) ? static_cast<int64_t>(p.n_out) + o : o;
     for (int r = 0; r < p.R; r += 8) {
       uint4 b[kFinishTokens];
 #pragma unroll
@@ -137,9 +136,6 @@ __global__ void __launch_bounds__(128, 8) adapter_finish_kernel(const FinishPara
       }
     }
   }
-  GemmParams g{};
-  g.out = p.out;
-  g.n_out = p.n_out;
   Piece w{};
   w.r0 = t0;
   w.nr = nt;

@@ -119,11 +119,6 @@ struct Barriers {
 
 __host__ __device__ inline int round_up(int v, int m) { return (v + m - 1) / m * m; }
 
-// a / b for a >= 0, b > 0; in 32 bits where a fits.
-__device__ __forceinline__ int64_t quotient(int64_t a, int b) {
-  return a >> 32 ? a / b : static_cast<int64_t>(static_cast<uint32_t>(a) / static_cast<uint32_t>(b));
-}
-
 // The tile list in shared memory: per segment its first row, its rows, and the
 // row tiles before it.
 struct Tiles {
@@ -252,52 +247,66 @@ struct __align__(16) Piece {
 
 constexpr int kPieces = 256;  // of a walker that are kept in shared memory
 
-// How the tile list is given out to G walkers (CTAs or pairs).
+// How the tile list is given out to G walkers.  The calls refuse sizes of more
+// than 2^31 tiles (an output of that many would not fit any memory), and the
+// split round has fewer than kMaxCtas tiles of at most 1024 K blocks, so 32 bits
+// hold every number.
 struct Schedule {
-  int64_t tiles, whole;  // tiles in the list, tiles given out whole
-  int64_t rest_units;    // K blocks of the split round
-  int mt, nkb, G;        // weight tiles, K blocks, walkers
+  unsigned tiles, whole;  // tiles in the list, tiles given out whole
+  unsigned rest_units;    // K blocks of the split round
+  unsigned mt, nkb, G;    // weight tiles, K blocks, walkers
   __device__ Schedule(const GemmParams& p, const Tiles& t, int weight_tiles, int walkers, bool split)
       : mt(weight_tiles), G(walkers) {
     nkb = (p.K + umma::kBK - 1) / umma::kBK;
-    tiles = static_cast<int64_t>(t.before[p.E]) * mt;
-    whole = split ? quotient(tiles, G) * G : tiles;
+    tiles = static_cast<unsigned>(t.before[p.E]) * mt;
+    whole = split ? tiles / G * G : tiles;
     rest_units = (tiles - whole) * nkb;
   }
   // Start of walker b's share of the split round.
-  __device__ int64_t share(int b) const { return quotient(rest_units * b, G); }
-  // Pieces of walker b: its whole tiles b, b + G, ..., then its share, which is
+  __device__ unsigned share(unsigned b) const { return rest_units * b / G; }
+  // Whole tiles of walker b (b, b + G, ...), and all its pieces: its share is
   // no longer than a tile and so lies in at most two.
-  __device__ int pieces(int b) const {
-    int n = whole > b ? static_cast<int>(quotient(whole - b + G - 1, G)) : 0;
-    const int64_t u = share(b), left = share(b + 1) - u;
-    if (left > 0) n += u - quotient(u, nkb) * nkb + left > nkb ? 2 : 1;
-    return n;
+  __device__ unsigned whole_of(unsigned b) const { return whole > b ? (whole - b + G - 1) / G : 0; }
+  __device__ int pieces(unsigned b) const {
+    unsigned n = whole_of(b);
+    if (rest_units > 0) {
+      const unsigned u = share(b), left = share(b + 1) - u;
+      if (left > 0) n += u % nkb + left > nkb ? 2 : 1;
+    }
+    return static_cast<int>(n);
   }
 };
 
+// Rows of row tile tt of ntt of a segment: nearly the same number of sixteens
+// each.
+__host__ __device__ inline int tile_begin(int cnt, int ntt, int tt) {
+  const int sixteens = cnt / 16 + (cnt % 16 != 0 ? 1 : 0), each = sixteens / ntt, more = sixteens % ntt;
+  const int at = (each * tt + (tt < more ? tt : more));
+  return at >= sixteens ? cnt : at * 16;
+}
+
 // Tile `tile` of the list.
-__device__ __forceinline__ void locate(const Tiles& t, int E, int mt, int64_t tile, Piece& w) {
-  const int at = static_cast<int>(quotient(tile, mt));
+__device__ __forceinline__ void locate(const Tiles& t, int E, unsigned mt, unsigned tile, Piece& w) {
+  const int at = static_cast<int>(tile / mt);
   int lo = 0, hi = E;  // before[lo] <= at < before[hi]
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
     if (t.before[mid] <= at) lo = mid;
     else hi = mid;
   }
-  const int ntt = t.before[lo + 1] - t.before[lo];
-  const int local = static_cast<int>(tile - static_cast<int64_t>(t.before[lo]) * mt);
-  const int tt = local % ntt;
-  // row tiles of nearly the same size, in whole sixteens
-  const int cnt = t.count[lo];
-  const int64_t sixteens = (static_cast<int64_t>(cnt) + 15) / 16;
-  const int a = static_cast<int>(quotient(sixteens * tt, ntt) * 16);
-  const int b = static_cast<int>(min(static_cast<int64_t>(cnt), quotient(sixteens * (tt + 1), ntt) * 16));
+  const unsigned ntt = t.before[lo + 1] - t.before[lo], local = tile - t.before[lo] * mt;
   w.e = lo;
-  w.m = local / ntt;
-  w.r0 = t.start[lo] + a;
-  w.nr = b - a;
   w.alone = ntt == 1;
+  w.r0 = t.start[lo];
+  w.nr = t.count[lo];
+  w.m = static_cast<int>(local);
+  if (ntt > 1) {
+    w.m = static_cast<int>(local / ntt);
+    const int tt = static_cast<int>(local % ntt);
+    const int a = tile_begin(w.nr, static_cast<int>(ntt), tt), b = tile_begin(w.nr, static_cast<int>(ntt), tt + 1);
+    w.r0 += a;
+    w.nr = b - a;
+  }
 }
 
 // Places of the partial tiles.  A walker has at most one piece of the split
@@ -307,26 +316,34 @@ __host__ __device__ inline int64_t parts_index(int64_t whole_tile, int G, int ct
   return whole_tile >= 0 ? 2 * static_cast<int64_t>(G) + whole_tile : 2 * static_cast<int64_t>(cta) + (kb0 == 0 ? 1 : 0);
 }
 
-// Piece i of a walker.  (One copy of the code: its divisions are long, and every
-// warp of the block would fetch its own.)
-__device__ __noinline__ void make_piece(const Schedule& s, const Tiles& t, int E, int who, int i, bool parts, Piece& w) {
-  const int whole = s.whole > who ? static_cast<int>(quotient(s.whole - who + s.G - 1, s.G)) : 0;
+// Piece i of a walker.
+__device__ __forceinline__ Piece make_piece(const Schedule& s, const Tiles& t, int E, unsigned who, unsigned i, bool parts) {
+  Piece w;
+  const unsigned whole = s.whole_of(who);
   if (i < whole) {
-    const int64_t tile = who + static_cast<int64_t>(i) * s.G;
+    const unsigned tile = who + i * s.G;
     locate(t, E, s.mt, tile, w);
     w.kb0 = 0;
-    w.kb1 = s.nkb;
+    w.kb1 = static_cast<int>(s.nkb);
     w.part = parts ? static_cast<int>(parts_index(tile, s.G, 0, 0)) : -1;
-    return;
+    return w;
   }
-  int64_t u = s.share(who);
-  const int64_t end = s.share(who + 1);
-  if (i > whole) u = (quotient(u, s.nkb) + 1) * s.nkb;
-  const int64_t nth = quotient(u, s.nkb);
+  unsigned u = s.share(who);
+  const unsigned end = s.share(who + 1);
+  unsigned nth = u / s.nkb;
+  if (i > whole) u = ++nth * s.nkb;
   locate(t, E, s.mt, s.whole + nth, w);
   w.kb0 = static_cast<int>(u - nth * s.nkb);
-  w.kb1 = static_cast<int>(min(static_cast<int64_t>(s.nkb), w.kb0 + (end - u)));
-  w.part = !parts && w.kb0 == 0 && w.kb1 == s.nkb ? -1 : static_cast<int>(parts_index(-1, s.G, who, w.kb0));
+  w.kb1 = static_cast<int>(min(s.nkb, w.kb0 + (end - u)));
+  w.part = !parts && w.kb0 == 0 && w.kb1 == static_cast<int>(s.nkb) ? -1 : static_cast<int>(parts_index(-1, s.G, who, w.kb0));
+  return w;
+}
+
+// The same for the warps of a walker with more than kPieces pieces, as one copy
+// of the code.
+__device__ __noinline__ void make_far_piece(const Schedule& s, const Tiles& t, int E, unsigned who, unsigned i, bool parts,
+                                            Piece* w) {
+  *w = make_piece(s, t, E, who, i, parts);
 }
 
 __device__ __forceinline__ float silu_mul(float g, float u) { return g / (1.f + expf(-g)) * u; }
@@ -490,7 +507,7 @@ expert_gemm_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_cons
   {
     const int n = s.pieces(who);
     if (threadIdx.x == 0) sb.pieces = n;
-    for (int i = threadIdx.x; i < min(n, kPieces); i += blockDim.x) make_piece(s, t, p.E, who, i, OUT == kParts, piece_s[i]);
+    for (int i = threadIdx.x; i < min(n, kPieces); i += blockDim.x) piece_s[i] = make_piece(s, t, p.E, who, i, OUT == kParts);
   }
   fence_before_sync();
   __syncthreads();
@@ -511,7 +528,7 @@ expert_gemm_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_cons
       w = piece_s[at];
     } else {
       Piece made;  // (a reference to w itself would keep it out of the registers)
-      make_piece(s, t, p.E, who, at, OUT == kParts, made);
+      make_far_piece(s, t, p.E, who, at, OUT == kParts, &made);
       w = made;
     }
     ++at;
@@ -871,11 +888,11 @@ expert_gemm_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_cons
 // end of share b if that end lies inside it and no earlier share ends there,
 // and of its rows those with row / 16 % gridDim.y == y.  What follows from the
 // segments comes before the wait for the products, which start this kernel
-// behind their own wait.  64 registers: it fits on an SM beside the products.
+// behind their own wait.  (At most 85 registers: it fits on an SM beside them.)
 constexpr int kJoinBatch = 2;  // pieces loaded at once
 
 template <bool SWIGLU, Out OUT>
-__global__ void __launch_bounds__(128, 8) expert_join_kernel(const GemmParams p, int G) {
+__global__ void __launch_bounds__(128, 6) expert_join_kernel(const GemmParams p, int G) {
   extern __shared__ int join_list[];
   __shared__ int bn, few, pieces;
   __shared__ int piece_s[kMaxCtas];
@@ -885,18 +902,18 @@ __global__ void __launch_bounds__(128, 8) expert_join_kernel(const GemmParams p,
   list_tiles<false, OUT>(p, t, mt, &bn, &few, false);
   const Schedule s(p, t, mt, G, true);
   const int b = blockIdx.x, l = threadIdx.x, q = l >> 5;
-  const int64_t end = s.share(b + 1), tile0 = quotient(end, s.nkb) * s.nkb;
+  const unsigned end = s.share(b + 1), tile0 = end / s.nkb * s.nkb;
   // the share ends between two tiles, or an earlier share ends in this tile
   const bool none = end == tile0 || end >= s.rest_units || s.share(b) > tile0;
   Piece w{};
   if (!none) {
-    locate(t, p.E, s.mt, s.whole + quotient(end, s.nkb), w);
+    locate(t, p.E, s.mt, s.whole + end / s.nkb, w);
     if (l < 32) {  // the tile's pieces in the order of K: this share's start of it, then the next shares'
       int n = 1;
       if (l == 0) piece_s[0] = static_cast<int>(parts_index(-1, G, b, 0));
       for (int j0 = b + 1; j0 < G; j0 += 32) {
         const int j = j0 + l;
-        const int64_t u0 = s.share(min(j, G)), u1 = s.share(min(j + 1, G));
+        const unsigned u0 = s.share(min(j, G)), u1 = s.share(min(j + 1, G));
         const bool in = u0 < u1 && u0 < tile0 + s.nkb;
         const unsigned bal = __ballot_sync(0xFFFFFFFFu, in);
         if (in) piece_s[n + __popc(bal & ((1u << l) - 1u))] = static_cast<int>(parts_index(-1, G, j, 1));
@@ -907,27 +924,34 @@ __global__ void __launch_bounds__(128, 8) expert_join_kernel(const GemmParams p,
     }
   }
   __syncthreads();
-  grid_dependency_wait();
-  if (none) return;
   const int64_t step = static_cast<int64_t>(p.slot_rows) * umma::kBM;
-  for (int c = blockIdx.y * 16; c < w.nr; c += gridDim.y * 16) {
-    float v[16];
+  // The first pass, before the wait, has no rows: it only brings the
+  // instructions into the caches (3.4 us behind the wait without it).
+  for (int pass = 0; pass < 2; ++pass) {
+    if (pass == 1) grid_dependency_wait();
+    if (none) continue;
+    const int nr = pass == 1 ? w.nr : 0;
+    for (int c = blockIdx.y * 16; c < max(nr, static_cast<int>(blockIdx.y) * 16 + 1); c += gridDim.y * 16) {
+      float v[16];
 #pragma unroll
-    for (int i = 0; i < 16; ++i) v[i] = 0.f;
-    const float* part = p.partial + static_cast<int64_t>(c) * umma::kBM + l;
-    for (int j = 0; j < pieces; j += kJoinBatch) {
-      float f[kJoinBatch][16];
+      for (int i = 0; i < 16; ++i) v[i] = 0.f;
+      const float* part = p.partial + static_cast<int64_t>(c) * umma::kBM + l;
+      for (int j = 0; j < pieces; j += kJoinBatch) {
+        float f[kJoinBatch][16];
 #pragma unroll
-      for (int k = 0; k < kJoinBatch; ++k)
+        for (int k = 0; k < kJoinBatch; ++k)
 #pragma unroll
-        for (int i = 0; i < 16; ++i)
-          f[k][i] = j + k < pieces && c + i < w.nr ? part[piece_s[j + k] * step + i * umma::kBM] : 0.f;
+          for (int i = 0; i < 16; ++i)
+            f[k][i] = j + k < pieces && c + i < nr ? part[piece_s[j + k] * step + i * umma::kBM] : 0.f;
 #pragma unroll
-      for (int k = 0; k < kJoinBatch; ++k)
+        for (int k = 0; k < kJoinBatch; ++k)
 #pragma unroll
-        for (int i = 0; i < 16; ++i) v[i] += f[k][i];
+          for (int i = 0; i < 16; ++i) v[i] += f[k][i];
+      }
+      Piece rows = w;
+      rows.nr = nr;
+      store_cols<SWIGLU, OUT, 16>(p, rows, w.m, c, q, v, store_aux<OUT>(p, rows, c));
     }
-    store_cols<SWIGLU, OUT, 16>(p, w, w.m, c, q, v, store_aux<OUT>(p, w, c));
   }
 }
 

@@ -30,6 +30,8 @@ extern "C" int moe_expert_linear(const void* x_bf16, int64_t n_x, const int32_t*
   const int st = check_linear(N, K, act);
   if (st != MOE_OK) return st;
   if (E > MOE_MAX_E || n_x > 0x7FFFFFFFll || n_rows > 0x7FFFFFFFll) return MOE_ERR_UNSUPPORTED;
+  // more tiles than the kernel counts (such an output fits no memory)
+  if ((n_rows / 32 + E) * ((N + 63) / 64) > 0x7FFFFFFFll) return MOE_ERR_UNSUPPORTED;
   if (!row_token && n_x < n_rows) return MOE_ERR_INVALID_ARG;
   if (n_rows == 0) return MOE_OK;
   if ((n_x > 0 && !x_bf16) || !w_bf16 || !offsets || !counts || !out_bf16) return MOE_ERR_INVALID_ARG;

@@ -82,7 +82,7 @@ LIN = dict(x=P, n_x=4, tok=P, w=P, offsets=P, counts=P, out=P, n_rows=32, E=16, 
     (dict(K=0), INVALID), (dict(act=2), INVALID), (dict(nb=-1), INVALID),
     (dict(N=60), UNSUPPORTED), (dict(N=72, act=1), UNSUPPORTED), (dict(K=68), UNSUPPORTED), (dict(E=1025), UNSUPPORTED),
     (dict(N=65544), UNSUPPORTED), (dict(K=65544), UNSUPPORTED), (dict(n_rows=1 << 31), UNSUPPORTED),
-    (dict(n_x=1 << 31), UNSUPPORTED),
+    (dict(n_x=1 << 31), UNSUPPORTED), (dict(n_rows=(1 << 31) - 1, N=65536), UNSUPPORTED),
     (dict(tok=NULL, n_x=31), INVALID),                    # fewer rows than the segments may name
     (dict(x=NULL), INVALID), (dict(w=NULL), INVALID), (dict(offsets=NULL), INVALID), (dict(counts=NULL), INVALID),
     (dict(out=NULL), INVALID),
