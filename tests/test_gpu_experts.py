@@ -265,6 +265,7 @@ EXPERT = [  # T, E, k, K, N, block, gather, hot
     (700, 6, 2, 128, 256, 1, True, 3), (513, 3, 3, 320, 272, 8, False, None), (300, 1, 1, 136, 384, 1, True, None),
     (40, 1024, 8, 64, 32, 1, True, None), (2000, 16, 4, 256, 512, 1, True, None), (2500, 2, 1, 1024, 128, 1, True, 1),
     (257, 1, 1, 4096, 1024, 1, False, None), (600, 5, 2, 136, 336, 1, True, 4), (600, 5, 2, 136, 336, 8, False, 4),
+    (820, 3, 1, 136, 528, 1, True, 1), (820, 3, 1, 264, 272, 1, False, 1), (1400, 8, 2, 520, 272, 1, True, 5), (1024, 2, 1, 64, 512, 1, True, 0),
     (1500, 4, 2, 1032, 528, 1, True, None), (1500, 4, 2, 1032, 512, 1, False, 0), (9, 200, 4, 2048, 64, 1, False, None),
 ]
 
