@@ -65,11 +65,9 @@ namespace moe {
 namespace {
 
 constexpr int kMaxStages = 12;
-constexpr int kSoloRing = 200 * 1024;  // a single CTA leaves room beside it for the next kernel's
-constexpr int kMaxSmem = 231 * 1000;   // dynamic shared memory a CTA may ask for, with room for the static part
+constexpr int kRingBytes = 200 * 1024;
 constexpr int kSoloRows = 128;  // most rows of a single CTA's tile (1 << 7)
-constexpr int kPairRows = 256;  // rows of a pair's tile in one accumulator (UMMA N)
-constexpr int kPairMost = 512;  // in both
+constexpr int kPairRows = 256;  // rows of a pair's tile (1 << 8)
 constexpr int kAccCols = 256;
 constexpr int kMaxCtas = 256;   // of a launch
 constexpr int kLoaders = 4;     // gathering warps
@@ -79,8 +77,8 @@ constexpr int kLowWarps = 8;    // kParts: warps that compute low-rank products
 
 enum Out { kRows, kLow, kParts, kScatter };
 
-constexpr int threads_of(bool gather, bool pair, Out out) {
-  return 192 + (gather ? 32 * (kLoaders + 1) : 0) + (out == kParts ? 32 * kLowWarps : 0) + (pair ? 128 : 0);
+constexpr int threads_of(bool gather, Out out) {
+  return 192 + (gather ? 32 * (kLoaders + 1) : 0) + (out == kParts ? 32 * kLowWarps : 0);
 }
 
 struct GemmParams {
@@ -95,7 +93,6 @@ struct GemmParams {
   int n_x;
   int E, n_out, K;
   int slot_rows;  // rows of a partial tile's slot
-  int ring_bytes;
   int weave;      // SwiGLU: one copy brings the whole weight tile (n_out a multiple of 16)
   int withhold;   // test hook: the K block CTA 0 never loads, or -1
   // adapters
@@ -157,61 +154,9 @@ __device__ __forceinline__ int scatter_tiles(int total, int mt, int G) {
   return best;
 }
 
-// Shared-memory rows of a stage for a pair's tile of `rows` rows (a multiple
-// of 16): half of each accumulator's, in boxes of 32 where TMA loads them.
-__device__ __forceinline__ int pair_stage_rows(int rows, bool gather) {
-  const int a = min(rows, kPairRows) / 2, b = max(rows - kPairRows, 0) / 2;
-  return gather ? a + b : round_up(a, 32) + round_up(b, 32);
-}
-
-// Rows of a tile of the pairs at most `cap` (a multiple of 16) for a segment.
-__device__ __forceinline__ int even_rows(int cnt, int cap) {
-  const int sixteens = (cnt + 15) >> 4, ntt = (cnt + cap - 1) / cap;
-  return ntt > 0 ? (sixteens + ntt - 1) / ntt * 16 : 0;
-}
-
-// The most rows of a pair's tile.  A segment of a few rows more than 256 in two
-// tiles reads its weights twice through half-empty MMAs; in one tile of both
-// accumulators it reads them once, but every stage grows, fewer fit, and the
-// epilogue runs alone.  Weighed by the measured costs: a ring turns around in
-// about 2.3 us however many stages it has, an MMA takes 1.2 ns a row and stage,
-// the epilogue 6 ns a row.  At T = 8192, E = 256 (mean 256 rows) @CAP@.
-template <bool GATHER>
-__device__ int pair_cap(const Tiles& t, int b, int e, int nkb, int ring_bytes) {
-  int most = 0;
-  for (int i = b; i < e; ++i) most = max(most, t.count[i]);
-  if (static_cast<int>(__reduce_max_sync(0xFFFFFFFFu, static_cast<unsigned>(most))) <= kPairRows) return kPairRows;
-  int best = kPairRows;
-  float least = 0.f;
-#pragma unroll
-  for (int k = 0; k < 6; ++k) {
-    const int cap = k == 0 ? 256 : k == 1 ? 288 : k == 2 ? 320 : k == 3 ? 384 : k == 4 ? 448 : 512;
-    unsigned rows = 0;
-    for (int i = b; i < e; ++i) rows = max(rows, static_cast<unsigned>(even_rows(t.count[i], cap)));
-    rows = __reduce_max_sync(0xFFFFFFFFu, rows);
-    const int stages = ring_bytes / ((umma::kBM + pair_stage_rows(static_cast<int>(rows), GATHER)) * umma::kRowBytes);
-    const float turn = 2.3f / static_cast<float>(min(stages, kMaxStages));
-    float cost = 0.f;
-    for (int i = b; i < e; ++i) {
-      const int ntt = (t.count[i] + cap - 1) / cap;
-      const float r = static_cast<float>(even_rows(t.count[i], cap));
-      float stage = fmaxf(turn, 1.2e-3f * r);
-      if (r > kPairRows) stage += 6e-3f * r / static_cast<float>(nkb);
-      cost += static_cast<float>(ntt) * stage;
-    }
-    cost = warp_sum(cost);
-    if (k == 0 || cost < least) {
-      least = cost;
-      best = cap;
-    }
-  }
-  return best;
-}
-
 // Fills the tile list; every thread of the block calls it.  Afterwards *bn_out
-// holds the shared-memory rows of a stage and *few_out whether the segments
-// have few rows.
-template <bool GATHER, bool PAIR, Out OUT>
+// holds the rows per tile and *few_out whether the segments have few rows.
+template <bool PAIR, Out OUT>
 __device__ void list_tiles(const GemmParams& p, Tiles t, int mt, int* bn_out, int* few_out, bool report) {
   if (OUT == kParts || OUT == kScatter) {  // one segment, not the caller's
     if (threadIdx.x == 0) {
@@ -221,7 +166,7 @@ __device__ void list_tiles(const GemmParams& p, Tiles t, int mt, int* bn_out, in
       t.count[0] = n;
       t.before[0] = 0;
       t.before[1] = OUT == kScatter ? scatter_tiles(n, mt, gridDim.x >> 1) : (n + bn - 1) / bn;
-      *bn_out = PAIR ? pair_stage_rows(kPairRows, GATHER) : bn;
+      *bn_out = bn;
       *few_out = 0;
     }
   } else if (threadIdx.x < 32) {
@@ -262,26 +207,18 @@ __device__ void list_tiles(const GemmParams& p, Tiles t, int mt, int* bn_out, in
       total = 0;
     }
     const int mean = active > 0 ? static_cast<int>((total + active - 1) / active) : 0;
-    int shift = tile_shift(mean);  // rows per tile of single CTAs, as a power of two
-    int cap = kPairRows;
-    if (PAIR) cap = pair_cap<GATHER>(t, b, e, (p.K + umma::kBK - 1) / umma::kBK, p.ring_bytes);
-    auto tiles_of = [&](int cnt) { return PAIR ? (cnt + cap - 1) / cap : (cnt + (1 << shift) - 1) >> shift; };
+    int shift = PAIR ? 8 : tile_shift(mean);  // rows per tile, as a power of two
     if (OUT == kLow) {
       // narrow weights, so few tiles: the widest rows per tile that still give
       // every CTA one
       for (shift = 7; shift > 5; --shift) {
         int tiles = 0;
-        for (int i = b; i < e; ++i) tiles += tiles_of(t.count[i]);
+        for (int i = b; i < e; ++i) tiles += (t.count[i] + (1 << shift) - 1) >> shift;
         if (__reduce_add_sync(0xFFFFFFFFu, tiles) >= static_cast<int>(gridDim.x)) break;
       }
     }
     int mine = 0;
-    unsigned rows = 16;
-    for (int i = b; i < e; ++i) {
-      mine += tiles_of(t.count[i]);
-      if (PAIR) rows = max(rows, static_cast<unsigned>(even_rows(t.count[i], cap)));
-    }
-    if (PAIR) rows = __reduce_max_sync(0xFFFFFFFFu, rows);
+    for (int i = b; i < e; ++i) mine += (t.count[i] + (1 << shift) - 1) >> shift;
     int upto = mine;
 #pragma unroll
     for (int off = 1; off < 32; off <<= 1) {
@@ -291,11 +228,11 @@ __device__ void list_tiles(const GemmParams& p, Tiles t, int mt, int* bn_out, in
     int at = upto - mine;
     for (int i = b; i < e; ++i) {
       t.before[i] = at;
-      at += tiles_of(t.count[i]);
+      at += (t.count[i] + (1 << shift) - 1) >> shift;
     }
     if (lane == 31) {
       t.before[p.E] = upto;
-      *bn_out = PAIR ? pair_stage_rows(static_cast<int>(rows), GATHER) : 1 << shift;
+      *bn_out = 1 << shift;
       *few_out = mean <= kFewRows;
     }
   }
@@ -512,31 +449,6 @@ struct Adapters {
   }
 };
 
-// The two accumulators: small tiles take them in turn, a large one takes both.
-// The MMA warp and the epilogue warps follow the same sequence.
-struct Halves {
-  int used[2] = {0, 0};
-  int turn = 0;
-  struct Use {
-    int first, parity_first, parity_second;
-    bool both, wait_first, wait_second;  // (waits: the accumulator was in use before)
-  };
-  __device__ __forceinline__ Use take(bool both) {
-    Use u;
-    u.both = both;
-    u.first = both ? 0 : turn;
-    const int a = u.first == 0 ? used[0] : used[1];
-    u.parity_first = a & 1;
-    u.parity_second = used[1] & 1;
-    u.wait_first = a > 0;
-    u.wait_second = used[1] > 0;
-    if (both || u.first == 0) ++used[0];
-    if (both || u.first == 1) ++used[1];
-    if (!both) turn ^= 1;
-    return u;
-  }
-};
-
 template <bool SWIGLU, bool GATHER, bool PAIR, Out OUT>
 __global__ void __launch_bounds__(512, 1)  // 128 registers: room for the next kernel's blocks beside it
 expert_gemm_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constant__ CUtensorMap tmap_w,
@@ -546,7 +458,7 @@ expert_gemm_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_cons
   extern __shared__ uint8_t smem_raw[];
   __shared__ Barriers sb;
   uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
-  Piece* piece_s = reinterpret_cast<Piece*>(ring + p.ring_bytes);
+  Piece* piece_s = reinterpret_cast<Piece*>(ring + kRingBytes);
   int* list = reinterpret_cast<int*>(piece_s + kPieces);
   const Tiles t{list, list + p.E, list + 2 * p.E};
   int* seg = list + 3 * p.E + 1;  // kScatter: the adapters' first rows
@@ -561,7 +473,7 @@ expert_gemm_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_cons
     mbar_init_fence();
   } else if (threadIdx.x < kMaxStages + 2) {
     mbar_init(&sb.acc_full[threadIdx.x - kMaxStages], 1);
-    mbar_init(&sb.acc_empty[threadIdx.x - kMaxStages], PAIR ? 16 : 4);  // epilogue warps
+    mbar_init(&sb.acc_empty[threadIdx.x - kMaxStages], PAIR ? 8 : 4);
     mbar_init_fence();
   } else if (threadIdx.x == kMaxStages + 2) {
     mbar_init(&sb.drained, 1);
@@ -581,7 +493,7 @@ expert_gemm_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_cons
   const int rows_out = (SWIGLU ? 64 : 128) * (PAIR ? 2 : 1), mt = (p.n_out + rows_out - 1) / rows_out;
   if (OUT == kScatter)
     for (int i = threadIdx.x; i <= p.segs; i += blockDim.x) seg[i] = p.seg[i];
-  list_tiles<GATHER, PAIR, OUT>(p, t, mt, &sb.bn, &sb.few, blockIdx.x == 0);  // kParts: reads no global memory
+  list_tiles<PAIR, OUT>(p, t, mt, &sb.bn, &sb.few, blockIdx.x == 0);  // kParts: reads no global memory
   const bool few = GATHER && !PAIR && sb.few;  // rows gathered by TMA
   const int depth = OUT == kScatter ? (p.R + kBK - 1) / kBK : 0;  // K blocks of an adapter's B
   if (threadIdx.x < kMaxStages) {
@@ -605,20 +517,11 @@ expert_gemm_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_cons
   }
   fence_after_sync();
   const uint32_t tmem = sb.tmem_base;
-  // A stage: 128 weight rows, then this CTA's rows.  A pair's CTA holds half of
-  // the rows of each accumulator: of a tile of N <= 256 rows those from rank *
-  // N / 2; of a larger one the same of its first 256, then of the others.
-  const int stage_bytes = (kBM + sb.bn) * kRowBytes;
-  const int nstages = min(kMaxStages, p.ring_bytes / stage_bytes);
-  // rows of this CTA, rows of them in the first accumulator, the tile's row of its row r
-  auto my_rows = [&](const Piece& w) { return PAIR ? round_up(w.nr, 16) / 2 : w.nr; };
-  auto my_first = [&](const Piece& w) { return PAIR ? min(round_up(w.nr, 16), kPairRows) / 2 : w.nr; };
-  auto tile_row = [&](const Piece& w, int r) {
-    if (!PAIR) return r;
-    const int a = my_first(w), b = my_rows(w) - a;
-    return r < a ? rank * a + r : kPairRows + rank * b + (r - a);
-  };
-  // a ring position and its parity
+  // a stage: 128 weight rows, then this CTA's rows (a pair's CTA holds half of the tile's)
+  const int stage_bytes = (kBM + (PAIR ? kPairRows / 2 : sb.bn)) * kRowBytes;
+  const int nstages = min(kMaxStages, kRingBytes / stage_bytes);
+  // A ring position and its parity; no division in the stage loops (with one
+  // each, every warp's turn took a tenth of the HBM's rate at T = 64).
   struct Stage {
     int st, ph;
   };
@@ -661,8 +564,8 @@ expert_gemm_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_cons
     };
     // bytes of a stage's copies, and (few) the tokens of lane l's rows 4 l .. + 3
     auto stage_copies = [&](const Piece& w) {
-      const int a = my_first(w), b = my_rows(w) - a;
-      const int rows = GATHER ? (few ? round_up(a, 4) : 0) : round_up(a, 32) + round_up(b, 32);
+      const int mine = PAIR ? round_up(w.nr, 16) / 2 : w.nr;  // rows in this CTA
+      const int rows = GATHER ? (few ? round_up(mine, 4) : 0) : round_up(mine, 32);
       return static_cast<uint32_t>((PAIR ? 2 : 1) * (kBM + rows)) * kRowBytes;
     };
     auto raw_tokens = [&](const Piece& w) {
@@ -701,8 +604,8 @@ expert_gemm_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_cons
     if (few && next(peek, coming)) raw = raw_tokens(coming);
     bool stop = false;
     while (!stop && next(at, w)) {
-      const int first = my_first(w), boxes_a = (first + 31) >> 5;
-      const int boxes = GATHER ? 0 : boxes_a + ((my_rows(w) - first + 31) >> 5), quads = few ? (w.nr + 3) >> 2 : 0;
+      const int mine = PAIR ? round_up(w.nr, 16) / 2 : w.nr;  // rows in this CTA
+      const int boxes = GATHER ? 0 : (mine + 31) >> 5, quads = few ? (mine + 3) >> 2 : 0;
       const uint32_t bytes = stage_copies(w);
       int4 tok = raw;
       if (few) {
@@ -716,9 +619,7 @@ expert_gemm_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_cons
           }
         }
       }
-      const int m = PAIR ? w.m * 2 + rank : w.m;
-      // lane l's box of rows: its first row
-      const int box_row = w.r0 + tile_row(w, lane < boxes_a ? lane * 32 : first + (lane - boxes_a) * 32);
+      const int m = PAIR ? w.m * 2 + rank : w.m, r0 = w.r0 + rank * mine;
       const uint64_t pol = w.alone ? once : keep;
       for (int kb = w.kb0; kb < w.kb1; ++kb, ++n, advance(x)) {
         const int st = x.st;
@@ -737,7 +638,7 @@ expert_gemm_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_cons
         }
         if (lane < quads) tma_gather4(b + lane * 4 * kRowBytes, &tmap_x, kb * kBK, tok, bar);
         if (!GATHER && lane < boxes)
-          tma_load_2d<PAIR>(b + lane * 32 * kRowBytes, &tmap_x, kb * kBK, box_row, bar);
+          tma_load_2d<PAIR>(b + lane * 32 * kRowBytes, &tmap_x, kb * kBK, r0 + lane * 32, bar);
       }
       if (OUT == kScatter && !stop) {
         Adapters ad(p, seg, w);
@@ -761,8 +662,9 @@ expert_gemm_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_cons
     // drain: no copy may land after this CTA exits (a pair's copies are counted
     // by its first CTA, and neither leaves before the other)
     if (lane == 0 && rank == 0) {
-      Stage y{n > nstages ? (n - nstages) % nstages : 0, n > nstages ? ((n - nstages) / nstages) & 1 : 0};
-      for (int i = n > nstages ? n - nstages : 0; i < n; ++i, advance(y))
+      const int from = n > nstages ? n - nstages : 0;
+      Stage y{from % nstages, (from / nstages) & 1};
+      for (int i = from; i < n; ++i, advance(y))
         if (i != withheld) wait(&sb.full[y.st], y.ph, abort_v, true);
     }
   } else if (warp == 1) {
@@ -771,18 +673,14 @@ expert_gemm_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_cons
       int at = 0;
       Piece w;
       Stage x{0, 0};
-      Halves h;
+      int seq = 0;
       bool stop = false;
       while (!stop && next(at, w)) {
-        const int rows = round_up(w.nr, 16);
-        const Halves::Use u = h.take(rows > kPairRows);
-        if ((u.wait_first && !wait(&sb.acc_empty[u.first], u.parity_first ^ 1, abort_v)) ||
-            (u.both && u.wait_second && !wait(&sb.acc_empty[1], u.parity_second ^ 1, abort_v)))
-          break;
+        const int acc = seq & 1, use = seq >> 1;
+        if (use > 0 && !wait(&sb.acc_empty[acc], (use - 1) & 1, abort_v)) break;
         fence_after_sync();
-        const uint32_t d = tmem + u.first * kAccCols;
-        const uint32_t idesc = idesc_bf16(PAIR ? 2 * kBM : kBM, u.both ? kPairRows : rows);
-        const uint32_t idesc2 = idesc_bf16(2 * kBM, u.both ? rows - kPairRows : 16);
+        const uint32_t d = tmem + acc * kAccCols;
+        const uint32_t idesc = idesc_bf16(PAIR ? 2 * kBM : kBM, round_up(w.nr, 16));
         for (int kb = w.kb0; kb < w.kb1; ++kb, advance(x)) {
           const int st = x.st;
           if (!wait(&sb.full[st], x.ph, abort_v)) {
@@ -795,12 +693,6 @@ expert_gemm_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_cons
 #pragma unroll
           for (int kk = 0; kk < kBK / 16; ++kk)
             mma_bf16<PAIR>(d, desc_sw128(a + kk * 32), desc_sw128(b + kk * 32), idesc, kb != w.kb0 || kk != 0);
-          if (PAIR && u.both) {
-#pragma unroll
-            for (int kk = 0; kk < kBK / 16; ++kk)
-              mma_bf16<PAIR>(d + kAccCols, desc_sw128(a + kk * 32), desc_sw128(b + kPairRows / 2 * kRowBytes + kk * 32),
-                             idesc2, kb != w.kb0 || kk != 0);
-          }
           mma_commit<PAIR>(&sb.empty[st]);
         }
         if (OUT == kScatter && !stop) {
@@ -823,45 +715,29 @@ expert_gemm_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_cons
             }
           }
         }
-        mma_commit<PAIR>(&sb.acc_full[u.first]);
-        if (u.both) mma_commit<PAIR>(&sb.acc_full[1]);
+        mma_commit<PAIR>(&sb.acc_full[acc]);
+        ++seq;
       }
       mma_commit<PAIR>(&sb.drained);  // also after an abort: fires once the issued MMAs are done
     }
     __syncwarp();
-  } else if (warp < 6 || (PAIR && warp >= (GATHER ? 7 + kLoaders : 6))) {
+  } else if (warp < 6) {
     // ----------------------------------------------------------- epilogue
-    // four warps read a quarter of the tensor-memory lanes each; a pair's CTA
-    // has two such groups, which take every other 32 columns
-    const int q = warp & 3, group = warp < 6 ? 0 : 1;
-    constexpr int kStep = PAIR ? 64 : 32;
+    const int q = warp & 3;  // this warp's quarter of the tensor-memory lanes
     if (OUT == kParts) grid_dependency_wait();
     int at = 0;
     Piece w;
-    Halves h;
+    int seq = 0;
     while (next(at, w)) {
-      const Halves::Use u = h.take(round_up(w.nr, 16) > kPairRows);
-      bool ok = wait(&sb.acc_full[u.first], u.parity_first, abort_v) && !*abort_v;
-      if (u.both) ok = wait(&sb.acc_full[1], u.parity_second, abort_v) && ok;
+      const int acc = seq & 1, use = seq >> 1;
+      ++seq;
+      const bool ok = wait(&sb.acc_full[acc], use & 1, abort_v) && !*abort_v;
       if (!__all_sync(0xFFFFFFFFu, ok)) break;
       fence_after_sync();
-      const uint32_t d = tmem + u.first * kAccCols + (static_cast<uint32_t>(q * 32) << 16);
+      const uint32_t d = tmem + acc * kAccCols + (static_cast<uint32_t>(q * 32) << 16);
       float* part = p.partial + static_cast<int64_t>(w.part) * p.slot_rows * kBM + q * 32 + lane;
-      auto release = [&](int half) {
-        fence_before_sync();
-        __syncwarp();
-        if (lane == 0) {
-          if (PAIR) arrive_cluster(acc_empty0 + half * 8);
-          else mbar_arrive(&sb.acc_empty[half]);
-        }
-      };
-      bool second = false;  // in the second accumulator of a large tile
 #pragma unroll 1
-      for (int c = group * 32; c < w.nr; c += kStep) {
-        if (u.both && !second && c >= kPairRows) {
-          release(0);
-          second = true;
-        }
+      for (int c = 0; c < w.nr; c += 32) {
         uint32_t raw[32];
         tmem_ld32(d + static_cast<uint32_t>(c), raw);
         if (OUT == kParts || w.part >= 0) {
@@ -875,8 +751,12 @@ expert_gemm_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_cons
           store_cols<SWIGLU, OUT, 32>(p, w, PAIR ? w.m * 2 + rank : w.m, c, q, v, store_aux<OUT>(p, w, c));
         }
       }
-      if (u.both && !second) release(0);
-      release(u.both ? 1 : u.first);
+      fence_before_sync();
+      __syncwarp();
+      if (lane == 0) {
+        if (PAIR) arrive_cluster(acc_empty0 + acc * 8);
+        else mbar_arrive(&sb.acc_empty[acc]);
+      }
     }
   } else if (OUT == kParts) {
     // -------------------------------------------------- low-rank products
@@ -909,25 +789,31 @@ expert_gemm_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_cons
     // Warp j takes rows 16 i + 4 j .. + 3 of this CTA's rows, eight lanes a
     // row, 16 bytes a lane, at their place in the 128-byte swizzle.
     const int j = warp - 6, sub = lane >> 3, chunk = lane & 7;
-    constexpr int kRounds = PAIR ? kPairMost / 32 : kSoloRows / 16;
+    const uint32_t place = static_cast<uint32_t>((kBM + 4 * j + sub) * kRowBytes + ((chunk ^ ((4 * j + sub) & 7)) << 4));
     int at = 0;
     Piece w;
     int n = 0;
     Stage x{0, 0};
     bool stop = false;
     while (!stop && next(at, w)) {
-      const int mine = my_rows(w);
-      const int rounds = (mine - 4 * j + 15) >> 4;  // none for the last warps of a small tile
-      int tok[kRounds];
+      const int mine = PAIR ? round_up(w.nr, 16) / 2 : w.nr;  // rows in this CTA, at most 128
+      // Rows without a token of their own are not copied: what the stage holds
+      // there reaches only columns that are not stored, or stored as zeros.
+      const uint16_t* src[8];
+      unsigned live = 0;
 #pragma unroll
-      for (int i = 0; i < kRounds; ++i) {
-        const int r = 16 * i + 4 * j + sub, rr = tile_row(w, r);
-        tok[i] = -1;
+      for (int i = 0; i < 8; ++i) {
+        const int r = 16 * i + 4 * j + sub, rr = rank * mine + r;
+        int tok = -1;
         if (r < mine && rr < w.nr) {
-          const int v = p.row_token[w.r0 + rr];
-          if (v >= 0 && v < p.n_x) tok[i] = v;
-          else if (OUT != kScatter && p.err_flag) atomicOr(p.err_flag, MOE_FLAG_BAD_INDEX);  // a row of zeros
+          tok = p.row_token[w.r0 + rr];
+          if (tok < 0 || tok >= p.n_x) {
+            tok = -1;
+            if (OUT != kScatter && p.err_flag) atomicOr(p.err_flag, MOE_FLAG_BAD_INDEX);
+          }
         }
+        live |= tok >= 0 ? 1u << i : 0u;
+        src[i] = p.x + static_cast<int64_t>(max(tok, 0)) * p.K + chunk * 8 + w.kb0 * kBK;
       }
       for (int kb = w.kb0; kb < w.kb1; ++kb, ++n, advance(x)) {
         const int st = x.st;
@@ -936,16 +822,12 @@ expert_gemm_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_cons
           stop = true;
           break;
         }
-        const uint32_t b = smem_addr(ring) + static_cast<uint32_t>(st * stage_bytes + kBM * kRowBytes);
-        const int col = kb * kBK + chunk * 8;
+        const uint32_t b = smem_addr(ring) + static_cast<uint32_t>(st * stage_bytes) + place;
+        const bool inside = kb * kBK + chunk * 8 < p.K;  // zeros behind the end of K
 #pragma unroll
-        for (int i = 0; i < kRounds; ++i) {
-          if (i < rounds) {
-            const int r = 16 * i + 4 * j + sub;
-            const bool live = tok[i] >= 0 && col < p.K;
-            copy16_async(b + r * kRowBytes + ((chunk ^ (r & 7)) << 4),
-                         p.x + (live ? static_cast<int64_t>(tok[i]) * p.K + col : 0), live);
-          }
+        for (int i = 0; i < 8; ++i) {
+          if ((live >> i) & 1u) copy16_async(b + i * 16 * kRowBytes, src[i], inside);
+          src[i] += kBK;
         }
         copy_arrive(&sb.landed[st]);
       }
@@ -1036,7 +918,7 @@ __global__ void __launch_bounds__(128, 6) expert_join_kernel(const GemmParams p,
   const Tiles t{join_list, join_list + p.E, join_list + 2 * p.E};
   allow_dependent_launch();
   const int rows_out = SWIGLU ? 64 : 128, mt = (p.n_out + rows_out - 1) / rows_out;
-  list_tiles<false, false, OUT>(p, t, mt, &bn, &few, false);
+  list_tiles<false, OUT>(p, t, mt, &bn, &few, false);
   const Schedule s(p, t, mt, G, true);
   const int b = blockIdx.x, l = threadIdx.x, q = l >> 5;
   const unsigned end = s.share(b + 1), tile0 = end / s.nkb * s.nkb;
@@ -1122,16 +1004,9 @@ inline bool make_map(CUtensorMap* map, const void* base, int rank, const cuuint6
 // CTAs of a launch: one per SM.
 inline int gemm_ctas() { return sm_count() < kMaxCtas ? sm_count() : kMaxCtas; }
 
-// Dynamic shared memory beside the ring: alignment, the walker's pieces, the
-// tile list, the adapters' first rows.
-inline int beside_ring(int64_t E, int segs) {
-  return 1024 + kPieces * static_cast<int>(sizeof(Piece)) + static_cast<int>(3 * E + 1 + segs + 1) * static_cast<int>(sizeof(int));
-}
-
-// The ring: pairs take all that is left.
-inline int ring_bytes_of(bool pair, int64_t E, int segs) {
-  const int left = (kMaxSmem - beside_ring(E, segs)) / 1024 * 1024;
-  return pair || left < kSoloRing ? left : kSoloRing;
+// Dynamic shared memory: the ring, the walker's pieces, the tile list, the adapters' first rows.
+inline size_t gemm_smem(int64_t E, int segs) {
+  return 1024 + kRingBytes + kPieces * sizeof(Piece) + static_cast<size_t>(3 * E + 1 + segs + 1) * sizeof(int);
 }
 
 // Opt the kernel into its dynamic shared memory, once per device.
@@ -1142,7 +1017,7 @@ cudaError_t opt_in(int dev) {
   if (!done[dev].load()) {
     const cudaError_t e =
         cudaFuncSetAttribute(expert_gemm_kernel<SWIGLU, GATHER, PAIR, OUT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             kMaxSmem);
+                             static_cast<int>(gemm_smem(OUT == kScatter ? 1 : MOE_MAX_E, OUT == kScatter ? MOE_MAX_ADAPTERS + 1 : 0)));
     if (e != cudaSuccess) return e;
     done[dev].store(true);
   }
@@ -1150,7 +1025,7 @@ cudaError_t opt_in(int dev) {
 }
 
 template <bool SWIGLU, bool GATHER, bool PAIR, Out OUT>
-cudaError_t launch(const CUtensorMap& mx, const CUtensorMap& mw, const CUtensorMap& mb, GemmParams p,
+cudaError_t launch(const CUtensorMap& mx, const CUtensorMap& mw, const CUtensorMap& mb, const GemmParams& p,
                    cudaStream_t stream) {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -1159,9 +1034,8 @@ cudaError_t launch(const CUtensorMap& mx, const CUtensorMap& mw, const CUtensorM
   const int G = PAIR ? gemm_ctas() / 2 * 2 : gemm_ctas();
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(G), 1, 1);
-  cfg.blockDim = dim3(threads_of(GATHER, PAIR, OUT), 1, 1);
-  p.ring_bytes = ring_bytes_of(PAIR, p.E, p.segs);
-  cfg.dynamicSmemBytes = launch_smem(static_cast<size_t>(p.ring_bytes) + beside_ring(p.E, p.segs));
+  cfg.blockDim = dim3(threads_of(GATHER, OUT), 1, 1);
+  cfg.dynamicSmemBytes = launch_smem(gemm_smem(p.E, p.segs));
   cfg.stream = stream;
   cudaLaunchAttribute attr[2] = {pdl_attribute(), {}};
   cfg.attrs = attr;
