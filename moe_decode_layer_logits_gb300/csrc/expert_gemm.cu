@@ -36,10 +36,12 @@ cudaError_t prepare_and_launch(const ExpertGemm& g, cudaStream_t stream) {
   if (!weight_map(&mw, g.w, g.E, g.N, g.K, SWIGLU, p.weave) ||
       !row_map_of(&mx, g.n_x > 0 ? g.x : g.w, g.n_x > 0 ? g.n_x : 1, g.K, g.row_token != nullptr))
     return cudaErrorInvalidValue;
-  const bool pair = g.n_rows / g.E >= kPairMeanRows;
-  if (g.row_token)
-    return pair ? launch<SWIGLU, true, true, kRows>(mx, mw, mw, p, stream) : launch<SWIGLU, true, false, kRows>(mx, mw, mw, p, stream);
-  return pair ? launch<SWIGLU, false, true, kRows>(mx, mw, mw, p, stream) : launch<SWIGLU, false, false, kRows>(mx, mw, mw, p, stream);
+  // pairs copy the rows by their own warps, with a token list or without (four
+  // tiled copies a stage beside the weights': 3.01 ms at T = 8192, E = 256 where
+  // the warps take 2.58)
+  if (g.n_rows / g.E >= kPairMeanRows) return launch<SWIGLU, true, true, kRows>(mx, mw, mw, p, stream);
+  return g.row_token ? launch<SWIGLU, true, false, kRows>(mx, mw, mw, p, stream)
+                     : launch<SWIGLU, false, false, kRows>(mx, mw, mw, p, stream);
 }
 
 }  // namespace

@@ -55,6 +55,7 @@
 #pragma once
 
 #include <atomic>
+#include <type_traits>
 
 #include "expert_gemm.h"
 #include "host_util.h"
@@ -157,7 +158,7 @@ __device__ __forceinline__ int scatter_tiles(int total, int mt, int G) {
 // Fills the tile list; every thread of the block calls it.  Afterwards *bn_out
 // holds the rows per tile and *few_out whether the segments have few rows.
 template <bool PAIR, Out OUT>
-__device__ void list_tiles(const GemmParams& p, Tiles t, int mt, int* bn_out, int* few_out, bool report) {
+__device__ void list_tiles(const GemmParams& p, Tiles t, int mt, int walkers, int* bn_out, int* few_out, bool report) {
   if (OUT == kParts || OUT == kScatter) {  // one segment, not the caller's
     if (threadIdx.x == 0) {
       const int n = OUT == kScatter ? p.seg[p.segs] : static_cast<int>(p.n_rows);
@@ -165,7 +166,7 @@ __device__ void list_tiles(const GemmParams& p, Tiles t, int mt, int* bn_out, in
       t.start[0] = 0;
       t.count[0] = n;
       t.before[0] = 0;
-      t.before[1] = OUT == kScatter ? scatter_tiles(n, mt, gridDim.x >> 1) : (n + bn - 1) / bn;
+      t.before[1] = OUT == kScatter ? scatter_tiles(n, mt, walkers) : (n + bn - 1) / bn;
       *bn_out = bn;
       *few_out = 0;
     }
@@ -210,11 +211,11 @@ __device__ void list_tiles(const GemmParams& p, Tiles t, int mt, int* bn_out, in
     int shift = PAIR ? 8 : tile_shift(mean);  // rows per tile, as a power of two
     if (OUT == kLow) {
       // narrow weights, so few tiles: the widest rows per tile that still give
-      // every CTA one
+      // one for every five CTAs (fewer have too many pieces each to add)
       for (shift = 7; shift > 5; --shift) {
         int tiles = 0;
         for (int i = b; i < e; ++i) tiles += (t.count[i] + (1 << shift) - 1) >> shift;
-        if (__reduce_add_sync(0xFFFFFFFFu, tiles) >= static_cast<int>(gridDim.x)) break;
+        if (__reduce_add_sync(0xFFFFFFFFu, tiles) >= static_cast<int>(walkers) / 5) break;
       }
     }
     int mine = 0;
@@ -453,7 +454,8 @@ template <bool SWIGLU, bool GATHER, bool PAIR, Out OUT>
 __global__ void __launch_bounds__(512, 1)  // 128 registers: room for the next kernel's blocks beside it
 expert_gemm_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constant__ CUtensorMap tmap_w,
                    const __grid_constant__ CUtensorMap tmap_b, const __grid_constant__ GemmParams p) {
-  static_assert(OUT != kScatter || (PAIR && GATHER), "sorted rows run in pairs");
+  static_assert(!PAIR || GATHER, "pairs copy their rows by warps 6 to 9");
+  static_assert(OUT != kScatter || PAIR, "sorted rows run in pairs");
   using namespace umma;
   extern __shared__ uint8_t smem_raw[];
   __shared__ Barriers sb;
@@ -491,9 +493,10 @@ expert_gemm_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_cons
     allow_dependent_launch();
   }
   const int rows_out = (SWIGLU ? 64 : 128) * (PAIR ? 2 : 1), mt = (p.n_out + rows_out - 1) / rows_out;
+  const int walkers = static_cast<int>(PAIR ? gridDim.x >> 1 : gridDim.x);
   if (OUT == kScatter)
     for (int i = threadIdx.x; i <= p.segs; i += blockDim.x) seg[i] = p.seg[i];
-  list_tiles<PAIR, OUT>(p, t, mt, &sb.bn, &sb.few, blockIdx.x == 0);  // kParts: reads no global memory
+  list_tiles<PAIR, OUT>(p, t, mt, walkers, &sb.bn, &sb.few, blockIdx.x == 0);  // kParts: reads no global memory
   const bool few = GATHER && !PAIR && sb.few;  // rows gathered by TMA
   const int depth = OUT == kScatter ? (p.R + kBK - 1) / kBK : 0;  // K blocks of an adapter's B
   if (threadIdx.x < kMaxStages) {
@@ -503,7 +506,7 @@ expert_gemm_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_cons
     mbar_init_fence();
   }
   // this walker's pieces, one a thread
-  const Schedule s(p, t, mt, PAIR ? gridDim.x >> 1 : gridDim.x, !PAIR && OUT != kLow);
+  const Schedule s(p, t, mt, walkers, !PAIR);
   {
     const int n = s.pieces(who);
     if (threadIdx.x == 0) sb.pieces = n;
@@ -551,127 +554,138 @@ expert_gemm_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_cons
 
   if (warp == 0) {
     // -------------------------------------------------------------- loads
+    // One lane walks and copies; where TMA gathers the rows (few), the whole
+    // warp does, lane l copying rows 4 l .. 4 l + 3.
     const uint64_t once = l2_evict_first_policy(), keep = l2_evict_normal_policy();
     const int withheld = who == 0 ? p.withhold : -1;
-    auto load_weights = [&](const CUtensorMap* map, uint32_t dst, int kb, int m, int e, uint32_t bar, uint64_t pol) {
-      if (!SWIGLU) {
-        if (lane == 0) tma_load_5d<PAIR>(dst, map, kb * kBK, m * 128, 0, 0, e, bar, pol);
-      } else if (p.weave) {
-        if (lane == 0) tma_load_5d<PAIR>(dst, map, kb * kBK, 0, 0, m * 4, e, bar, pol);
-      } else if (lane < 4) {  // 16 gate rows and their 16 up rows
-        tma_load_5d<PAIR>(dst + lane * 32 * kRowBytes, map, kb * kBK, m * 64 + lane * 16, 0, 0, e, bar, pol);
-      }
-    };
-    // bytes of a stage's copies, and (few) the tokens of lane l's rows 4 l .. + 3
-    auto stage_copies = [&](const Piece& w) {
-      const int mine = PAIR ? round_up(w.nr, 16) / 2 : w.nr;  // rows in this CTA
-      const int rows = GATHER ? (few ? round_up(mine, 4) : 0) : round_up(mine, 32);
-      return static_cast<uint32_t>((PAIR ? 2 : 1) * (kBM + rows)) * kRowBytes;
-    };
-    auto raw_tokens = [&](const Piece& w) {
-      int v[4];
+    auto load = [&](auto lone_lane) {
+      constexpr bool LONE = decltype(lone_lane)::value;
+      const bool first = LONE || lane == 0;
+      auto load_weights = [&](const CUtensorMap* map, uint32_t dst, int kb, int m, int e, uint32_t bar, uint64_t pol) {
+        if (!first) return;
+        if (!SWIGLU) {
+          tma_load_5d<PAIR>(dst, map, kb * kBK, m * 128, 0, 0, e, bar, pol);
+        } else if (p.weave) {
+          tma_load_5d<PAIR>(dst, map, kb * kBK, 0, 0, m * 4, e, bar, pol);
+        } else {  // 16 gate rows and their 16 up rows at a time
 #pragma unroll
-      for (int i = 0; i < 4; ++i) v[i] = few && lane * 4 + i < w.nr ? p.row_token[w.r0 + lane * 4 + i] : 0;
-      return make_int4(v[0], v[1], v[2], v[3]);
-    };
-    int at = 0;
-    Piece w;
-    int n = 0;  // stages so far
-    Stage x{0, 0};
-    int early = 0;
-    if (OUT == kParts) {
-      // a ring of weights before the wait; their rows follow behind it.  (With
-      // more than one stage of weights in the copy engine's queue the rows wait
-      // for them, so the other forms do not run ahead.)
-      int ahead = 0;
-      while (early < nstages && next(ahead, w)) {
+          for (int i = 0; i < 4; ++i)
+            tma_load_5d<PAIR>(dst + i * 32 * kRowBytes, map, kb * kBK, m * 64 + i * 16, 0, 0, e, bar, pol);
+        }
+      };
+      auto stage_copies = [&](const Piece& w) {  // bytes, in both CTAs of a pair
+        const int mine = PAIR ? round_up(w.nr, 16) / 2 : w.nr;  // rows in this CTA
+        const int rows = GATHER ? (LONE ? 0 : round_up(mine, 4)) : round_up(mine, 32);
+        return static_cast<uint32_t>((PAIR ? 2 : 1) * (kBM + rows)) * kRowBytes;
+      };
+      auto raw_tokens = [&](const Piece& w) {
+        int v[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] = lane * 4 + i < w.nr ? p.row_token[w.r0 + lane * 4 + i] : 0;
+        return make_int4(v[0], v[1], v[2], v[3]);
+      };
+      int at = 0;
+      Piece w;
+      int n = 0;  // stages so far
+      Stage x{0, 0};
+      int early = 0;
+      if (OUT == kParts) {
+        // a ring of weights before the wait; their rows follow behind it.  (With
+        // more than one stage of weights in the copy engine's queue the rows wait
+        // for them, so the other forms do not run ahead.)
+        int ahead = 0;
+        while (early < nstages && next(ahead, w)) {
+          const uint32_t bytes = stage_copies(w);
+          for (int kb = w.kb0; kb < w.kb1 && early < nstages; ++kb, ++early) {
+            mbar_arrive_expect_tx(&sb.full[early], bytes);
+            load_weights(&tmap_w, smem_addr(ring) + static_cast<uint32_t>(early * stage_bytes), kb, w.m, w.e,
+                         full0 + early * 8, w.alone ? once : keep);
+          }
+        }
+        grid_dependency_wait();
+        // behind the wait, so that what is launched next finds the inputs ready
+        allow_dependent_launch();
+      }
+      // the tokens of a piece are loaded a piece ahead
+      int peek = 0;
+      Piece coming;
+      int4 raw = make_int4(0, 0, 0, 0);
+      if (!LONE && next(peek, coming)) raw = raw_tokens(coming);
+      bool stop = false;
+      // the next stage may be written: its last MMAs are done
+      auto freed = [&]() {
+        const bool go = n < nstages || wait(&sb.empty[x.st], x.ph ^ 1, abort_v);
+        return LONE ? go : __all_sync(0xFFFFFFFFu, go) != 0;
+      };
+      while (!stop && next(at, w)) {
+        const int mine = PAIR ? round_up(w.nr, 16) / 2 : w.nr;  // rows in this CTA
+        const int boxes = GATHER ? 0 : (mine + 31) >> 5, quads = LONE ? 0 : (mine + 3) >> 2;
         const uint32_t bytes = stage_copies(w);
-        for (int kb = w.kb0; kb < w.kb1 && early < nstages; ++kb, ++early) {
-          if (lane == 0) mbar_arrive_expect_tx(&sb.full[early], bytes);
-          __syncwarp();
-          load_weights(&tmap_w, smem_addr(ring) + static_cast<uint32_t>(early * stage_bytes), kb, w.m, w.e,
-                       full0 + early * 8, w.alone ? once : keep);
-        }
-      }
-      grid_dependency_wait();
-      // behind the wait, so that what is launched next finds the inputs ready
-      allow_dependent_launch();
-    }
-    // the tokens of a piece are loaded a piece ahead
-    int peek = 0;
-    Piece coming;
-    int4 raw = make_int4(0, 0, 0, 0);
-    if (few && next(peek, coming)) raw = raw_tokens(coming);
-    bool stop = false;
-    while (!stop && next(at, w)) {
-      const int mine = PAIR ? round_up(w.nr, 16) / 2 : w.nr;  // rows in this CTA
-      const int boxes = GATHER ? 0 : (mine + 31) >> 5, quads = few ? (mine + 3) >> 2 : 0;
-      const uint32_t bytes = stage_copies(w);
-      int4 tok = raw;
-      if (few) {
-        if (next(peek, coming)) raw = raw_tokens(coming);
-        int* v = &tok.x;
+        int4 tok = raw;
+        if (!LONE) {
+          if (next(peek, coming)) raw = raw_tokens(coming);
+          int* v = &tok.x;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          if (v[i] < 0 || v[i] >= p.n_x) {  // loads token 0, stored as zeros
-            if (p.err_flag) atomicOr(p.err_flag, MOE_FLAG_BAD_INDEX);
-            v[i] = 0;
-          }
-        }
-      }
-      const int m = PAIR ? w.m * 2 + rank : w.m, r0 = w.r0 + rank * mine;
-      const uint64_t pol = w.alone ? once : keep;
-      for (int kb = w.kb0; kb < w.kb1; ++kb, ++n, advance(x)) {
-        const int st = x.st;
-        const bool go = (n < nstages || wait(&sb.empty[st], x.ph ^ 1, abort_v)) && !*abort_v;
-        if (!__all_sync(0xFFFFFFFFu, go)) {
-          stop = true;
-          break;
-        }
-        if (n == withheld) continue;  // neither armed nor loaded: the MMA warp's wait runs out
-        const uint32_t a = smem_addr(ring) + static_cast<uint32_t>(st * stage_bytes);
-        const uint32_t b = a + kBM * kRowBytes, bar = full0 + st * 8;
-        if (OUT != kParts || n >= early) {
-          if (lane == 0 && rank == 0) mbar_arrive_expect_tx(&sb.full[st], bytes);
-          __syncwarp();
-          load_weights(&tmap_w, a, kb, m, w.e, bar, pol);
-        }
-        if (lane < quads) tma_gather4(b + lane * 4 * kRowBytes, &tmap_x, kb * kBK, tok, bar);
-        if (!GATHER && lane < boxes)
-          tma_load_2d<PAIR>(b + lane * 32 * kRowBytes, &tmap_x, kb * kBK, r0 + lane * 32, bar);
-      }
-      if (OUT == kScatter && !stop) {
-        Adapters ad(p, seg, w);
-        while (!stop && ad.get(p, seg)) {
-          for (int i = 0; i < 2 * depth; ++i, ++n, advance(x)) {
-            const int st = x.st;
-            const bool go = (n < nstages || wait(&sb.empty[st], x.ph ^ 1, abort_v)) && !*abort_v;
-            if (!__all_sync(0xFFFFFFFFu, go)) {
-              stop = true;
-              break;
+          for (int i = 0; i < 4; ++i) {
+            if (v[i] < 0 || v[i] >= p.n_x) {  // loads token 0, stored as zeros
+              if (p.err_flag) atomicOr(p.err_flag, MOE_FLAG_BAD_INDEX);
+              v[i] = 0;
             }
-            const uint32_t a = smem_addr(ring) + static_cast<uint32_t>(st * stage_bytes), bar = full0 + st * 8;
-            if (lane == 0 && rank == 0) mbar_arrive_expect_tx(&sb.full[st], 2 * kBM * kRowBytes);
-            __syncwarp();
-            load_weights(&tmap_b, a, i >> 1, m, ad.a, bar, keep);
+          }
+        }
+        const int m = PAIR ? w.m * 2 + rank : w.m, r0 = w.r0 + rank * mine;
+        const uint64_t pol = w.alone ? once : keep;
+        for (int kb = w.kb0; kb < w.kb1; ++kb, ++n, advance(x)) {
+          if (!freed()) {
+            stop = true;
+            break;
+          }
+          if (n == withheld) continue;  // neither armed nor loaded: the MMA warp's wait runs out
+          const uint32_t a = smem_addr(ring) + static_cast<uint32_t>(x.st * stage_bytes);
+          const uint32_t b = a + kBM * kRowBytes, bar = full0 + x.st * 8;
+          if (OUT != kParts || n >= early) {
+            if (first && rank == 0) mbar_arrive_expect_tx(&sb.full[x.st], bytes);
+            if (!LONE) __syncwarp();
+            load_weights(&tmap_w, a, kb, m, w.e, bar, pol);
+          }
+          if (!LONE && lane < quads) tma_gather4(b + lane * 4 * kRowBytes, &tmap_x, kb * kBK, tok, bar);
+          for (int i = 0; i < boxes; ++i)
+            tma_load_2d<PAIR>(b + i * 32 * kRowBytes, &tmap_x, kb * kBK, r0 + i * 32, bar);
+        }
+        if (OUT == kScatter && !stop) {
+          Adapters ad(p, seg, w);
+          while (!stop && ad.get(p, seg)) {
+            for (int i = 0; i < 2 * depth; ++i, ++n, advance(x)) {
+              if (!freed()) {
+                stop = true;
+                break;
+              }
+              if (rank == 0) mbar_arrive_expect_tx(&sb.full[x.st], 2 * kBM * kRowBytes);
+              load_weights(&tmap_b, smem_addr(ring) + static_cast<uint32_t>(x.st * stage_bytes), i >> 1, m, ad.a,
+                           full0 + x.st * 8, keep);
+            }
           }
         }
       }
-    }
+      if (!LONE) __syncwarp();
+      // drain: no copy may land after this CTA exits (a pair's copies are counted
+      // by its first CTA, and neither leaves before the other)
+      if (first && rank == 0) {
+        const int from = n > nstages ? n - nstages : 0;
+        Stage y{from % nstages, (from / nstages) & 1};
+        for (int i = from; i < n; ++i, advance(y))
+          if (i != withheld) wait(&sb.full[y.st], y.ph, abort_v, true);
+      }
+    };
+    if (GATHER && !PAIR && few) load(std::false_type{});
+    else if (lane == 0) load(std::true_type{});
     __syncwarp();
-    // drain: no copy may land after this CTA exits (a pair's copies are counted
-    // by its first CTA, and neither leaves before the other)
-    if (lane == 0 && rank == 0) {
-      const int from = n > nstages ? n - nstages : 0;
-      Stage y{from % nstages, (from / nstages) & 1};
-      for (int i = from; i < n; ++i, advance(y))
-        if (i != withheld) wait(&sb.full[y.st], y.ph, abort_v, true);
-    }
   } else if (warp == 1) {
     // ---------------------------------------------------------------- MMA
     if (lane == 0 && rank == 0) {
       int at = 0;
       Piece w;
+      const uint32_t a0 = desc_low(smem_addr(ring)), step = static_cast<uint32_t>(stage_bytes) >> 4;
       Stage x{0, 0};
       int seq = 0;
       bool stop = false;
@@ -688,11 +702,10 @@ expert_gemm_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_cons
             break;
           }
           fence_after_sync();
-          const uint32_t a = smem_addr(ring) + static_cast<uint32_t>(st * stage_bytes);
-          const uint32_t b = a + kBM * kRowBytes;
+          const uint32_t a = a0 + static_cast<uint32_t>(st) * step, b = a + (kBM * kRowBytes >> 4);
+          mma_bf16<PAIR>(d, a, b, idesc, kb != w.kb0);
 #pragma unroll
-          for (int kk = 0; kk < kBK / 16; ++kk)
-            mma_bf16<PAIR>(d, desc_sw128(a + kk * 32), desc_sw128(b + kk * 32), idesc, kb != w.kb0 || kk != 0);
+          for (int kk = 1; kk < kBK / 16; ++kk) mma_bf16<PAIR>(d, a + kk * 2, b + kk * 2, idesc, true);
           mma_commit<PAIR>(&sb.empty[st]);
         }
         if (OUT == kScatter && !stop) {
@@ -706,11 +719,9 @@ expert_gemm_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_cons
                 break;
               }
               fence_after_sync();
-              const uint32_t a = smem_addr(ring) + static_cast<uint32_t>(st * stage_bytes);
-              const uint32_t b = a + kBM * kRowBytes;
+              const uint32_t a = a0 + static_cast<uint32_t>(st) * step, b = a + (kBM * kRowBytes >> 4);
               const int ks = (min(kBK, p.R - (i >> 1) * kBK) + 15) >> 4;
-              for (int kk = 0; kk < ks; ++kk)
-                mma_bf16<PAIR>(d + ad.c0, desc_sw128(a + kk * 32), desc_sw128(b + kk * 32), sub, 1);
+              for (int kk = 0; kk < ks; ++kk) mma_bf16<PAIR>(d + ad.c0, a + kk * 2, b + kk * 2, sub, true);
               mma_commit<PAIR>(&sb.empty[st]);
             }
           }
@@ -806,7 +817,7 @@ expert_gemm_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_cons
         const int r = 16 * i + 4 * j + sub, rr = rank * mine + r;
         int tok = -1;
         if (r < mine && rr < w.nr) {
-          tok = p.row_token[w.r0 + rr];
+          tok = p.row_token ? p.row_token[w.r0 + rr] : w.r0 + rr;
           if (tok < 0 || tok >= p.n_x) {
             tok = -1;
             if (OUT != kScatter && p.err_flag) atomicOr(p.err_flag, MOE_FLAG_BAD_INDEX);
@@ -817,8 +828,7 @@ expert_gemm_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_cons
       }
       for (int kb = w.kb0; kb < w.kb1; ++kb, ++n, advance(x)) {
         const int st = x.st;
-        const bool go = (n < nstages || wait(&sb.empty[st], x.ph ^ 1, abort_v)) && !*abort_v;
-        if (!__all_sync(0xFFFFFFFFu, go)) {
+        if (n >= nstages && !wait(&sb.empty[st], x.ph ^ 1, abort_v)) {
           stop = true;
           break;
         }
@@ -838,8 +848,7 @@ expert_gemm_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_cons
           const int64_t first = w.r0 + ad.c0 + rank * half;
           for (int i = 0; i < 2 * depth; ++i, ++n, advance(x)) {
             const int st = x.st;
-            const bool go = (n < nstages || wait(&sb.empty[st], x.ph ^ 1, abort_v)) && !*abort_v;
-            if (!__all_sync(0xFFFFFFFFu, go)) {
+            if (n >= nstages && !wait(&sb.empty[st], x.ph ^ 1, abort_v)) {
               stop = true;
               break;
             }
@@ -918,7 +927,7 @@ __global__ void __launch_bounds__(128, 6) expert_join_kernel(const GemmParams p,
   const Tiles t{join_list, join_list + p.E, join_list + 2 * p.E};
   allow_dependent_launch();
   const int rows_out = SWIGLU ? 64 : 128, mt = (p.n_out + rows_out - 1) / rows_out;
-  list_tiles<false, OUT>(p, t, mt, &bn, &few, false);
+  list_tiles<false, OUT>(p, t, mt, G, &bn, &few, false);
   const Schedule s(p, t, mt, G, true);
   const int b = blockIdx.x, l = threadIdx.x, q = l >> 5;
   const unsigned end = s.share(b + 1), tile0 = end / s.nkb * s.nkb;
@@ -1048,7 +1057,7 @@ cudaError_t launch(const CUtensorMap& mx, const CUtensorMap& mw, const CUtensorM
     cfg.numAttrs = 2;
   }
   e = cudaLaunchKernelEx(&cfg, expert_gemm_kernel<SWIGLU, GATHER, PAIR, OUT>, mx, mw, mb, p);
-  if constexpr (!PAIR && OUT == kRows) {
+  if constexpr (!PAIR && (OUT == kRows || OUT == kLow)) {
     if (e != cudaSuccess) return e;
     cfg.gridDim = dim3(static_cast<unsigned>(G - 1), static_cast<unsigned>((p.slot_rows + 15) / 16), 1);
     cfg.blockDim = dim3(128, 1, 1);
