@@ -39,6 +39,13 @@ struct FinishParams {
 constexpr int kFinishTokens = 8;
 constexpr int kFinishPieces = kMaxCtas;  // pieces of one tile: at most one a CTA
 constexpr int kFinishBatch = 2;          // pieces loaded at once
+constexpr int kFinishPitch = 36;         // words of a row of 64 BF16 columns, and one 16-byte step of padding
+
+// Dynamic shared memory: the tokens' low-rank products, and where the rank asks
+// for it four warps' rows of B.
+constexpr size_t finish_smem(int R) {
+  return static_cast<size_t>(kFinishTokens) * R * 4 + (R > 16 ? 4 * 32 * kFinishPitch * 4 : 0);
+}
 
 // One CTA: 128 weight rows of the product and 8 tokens of one of its tiles.
 // What follows from the sizes and ids comes before the wait for the product;
@@ -119,7 +126,64 @@ __global__ void __launch_bounds__(128, 8) adapter_finish_kernel(const FinishPara
       for (int i = 0; i < kFinishTokens; ++i) v[i] += f[j][i];
   }
   __syncthreads();
-  if (o < p.n_out) {
+  if (p.R > 16) {
+    // Lanes read whole rows of B together (eight lanes 64 columns of a row) and
+    // hand each lane its own row through shared memory; read by the row's lane
+    // alone, every load touches 32 lines (29 us at T = 128, R = 64).  The next
+    // token's columns are requested before this one's are used; a token with
+    // the adapter of the one before finds them in place.
+    float* mine = low_s + kFinishTokens * p.R + q * 32 * kFinishPitch;  // this warp's [32 rows][64 columns]
+    const int l32 = l & 31, sub = l32 >> 3, chunk = l32 & 7;
+    for (int r = 0; r < p.R; r += 64) {
+      const int width = min(64, p.R - r);
+      uint4 next[8];
+      auto request = [&](int id) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int lr = 4 * i + sub;  // row of the warp's 32
+          const int oo = SWIGLU ? m * 64 + q * 16 + (lr & 15) : m * 128 + q * 32 + lr;
+          const int64_t rr = SWIGLU && (lr & 16) ? static_cast<int64_t>(p.n_out) + oo : oo;
+          next[i] = oo < p.n_out && chunk * 8 < width
+                        ? ld_keep16(p.b + (static_cast<int64_t>(id) * p.N + rr) * p.R + r + chunk * 8)
+                        : make_uint4(0, 0, 0, 0);
+        }
+      };
+      int held = -1, coming = -1;  // adapters whose columns are in shared memory, on their way
+      auto following = [&](int i, int id) {  // the next adapter of these tokens that is not `id`
+        for (++i; i < nt; ++i)
+          if (id_s[i] >= 0 && id_s[i] != id) return id_s[i];
+        return -1;
+      };
+      coming = following(-1, -1);
+      if (coming >= 0) request(coming);
+      for (int i = 0; i < nt; ++i) {
+        const int id = id_s[i];
+        if (id < 0) continue;
+        if (id != held) {
+          __syncwarp();
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            *reinterpret_cast<uint4*>(mine + (4 * k + sub) * kFinishPitch + chunk * 4) = next[k];
+          __syncwarp();
+          held = id;
+          coming = following(i, id);
+          if (coming >= 0) request(coming);
+        }
+        float sum = 0.f;
+        for (int c = 0; c < width; c += 8) {
+          float f[8];
+          unpack8(*reinterpret_cast<const uint4*>(mine + l32 * kFinishPitch + c / 2), f);
+          const float* lo = low_s + i * p.R + r + c;
+#pragma unroll
+          for (int e = 0; e < 8; ++e) sum = fmaf(lo[e], f[e], sum);
+        }
+#pragma unroll
+        for (int k = 0; k < kFinishTokens; ++k)
+          if (k == i) v[k] += sum;
+      }
+      __syncwarp();
+    }
+  } else if (o < p.n_out) {
     for (int r = 0; r < p.R; r += 8) {
       uint4 b[kFinishTokens];
 #pragma unroll
@@ -189,6 +253,9 @@ cudaError_t few_tokens(const AdapterLinear& g, cudaStream_t stream) {
   p.n_out = static_cast<int>(SWIGLU ? g.N / 2 : g.N);
   p.K = static_cast<int>(g.K);
   p.slot_rows = f.slot_rows;
+  // the last kernel's blocks start beside this one's: with their rows of B they
+  // need more of the SM's memory
+  p.ring_bytes = g.R > 16 ? kRingBytes - 72 * 1024 : kRingBytes;
   p.weave = SWIGLU && p.n_out % 16 == 0;
   p.withhold = -1;
   p.scale = g.scale;
@@ -208,7 +275,7 @@ cudaError_t few_tokens(const AdapterLinear& g, cudaStream_t stream) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(f.tiles), static_cast<unsigned>((g.T + kFinishTokens - 1) / kFinishTokens), 1);
   cfg.blockDim = dim3(128, 1, 1);
-  cfg.dynamicSmemBytes = launch_smem(static_cast<size_t>(kFinishTokens) * g.R * 4);
+  cfg.dynamicSmemBytes = launch_smem(finish_smem(g.R));
   cfg.stream = stream;
   cudaLaunchAttribute attr[1] = {pdl_attribute()};
   cfg.attrs = attr;
@@ -240,6 +307,7 @@ cudaError_t many_tokens(const AdapterLinear& g, cudaStream_t stream) {
   p.n_out = g.R;
   p.K = static_cast<int>(g.K);
   p.slot_rows = slot_rows_of(f.n_rows);
+  p.ring_bytes = kRingBytes;
   p.withhold = -1;
   p.scale = g.scale;
   for (int i = 0; i < 2; ++i) p.low[i] = reinterpret_cast<uint16_t*>(g.workspace + f.low[i]);

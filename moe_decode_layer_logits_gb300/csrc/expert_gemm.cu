@@ -27,6 +27,7 @@ cudaError_t prepare_and_launch(const ExpertGemm& g, cudaStream_t stream) {
   p.n_out = static_cast<int>(SWIGLU ? g.N / 2 : g.N);
   p.K = static_cast<int>(g.K);
   p.slot_rows = slot_rows_of(g.n_rows);
+  p.ring_bytes = kRingBytes;
   p.weave = SWIGLU && p.n_out % 16 == 0;
   p.withhold = g_withheld.exchange(-1);
 

@@ -94,6 +94,7 @@ struct GemmParams {
   int n_x;
   int E, n_out, K;
   int slot_rows;  // rows of a partial tile's slot
+  int ring_bytes;
   int weave;      // SwiGLU: one copy brings the whole weight tile (n_out a multiple of 16)
   int withhold;   // test hook: the K block CTA 0 never loads, or -1
   // adapters
@@ -451,7 +452,8 @@ struct Adapters {
 };
 
 template <bool SWIGLU, bool GATHER, bool PAIR, Out OUT>
-__global__ void __launch_bounds__(512, 1)  // 128 registers: room for the next kernel's blocks beside it
+// (the bounds: registers that leave room for the next kernel's blocks beside it)
+__global__ void __launch_bounds__(OUT == kParts ? 768 : 512, 1)
 expert_gemm_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constant__ CUtensorMap tmap_w,
                    const __grid_constant__ CUtensorMap tmap_b, const __grid_constant__ GemmParams p) {
   static_assert(!PAIR || GATHER, "pairs copy their rows by warps 6 to 9");
@@ -460,7 +462,7 @@ expert_gemm_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_cons
   extern __shared__ uint8_t smem_raw[];
   __shared__ Barriers sb;
   uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
-  Piece* piece_s = reinterpret_cast<Piece*>(ring + kRingBytes);
+  Piece* piece_s = reinterpret_cast<Piece*>(ring + p.ring_bytes);
   int* list = reinterpret_cast<int*>(piece_s + kPieces);
   const Tiles t{list, list + p.E, list + 2 * p.E};
   int* seg = list + 3 * p.E + 1;  // kScatter: the adapters' first rows
@@ -522,7 +524,7 @@ expert_gemm_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_cons
   const uint32_t tmem = sb.tmem_base;
   // a stage: 128 weight rows, then this CTA's rows (a pair's CTA holds half of the tile's)
   const int stage_bytes = (kBM + (PAIR ? kPairRows / 2 : sb.bn)) * kRowBytes;
-  const int nstages = min(kMaxStages, kRingBytes / stage_bytes);
+  const int nstages = min(kMaxStages, p.ring_bytes / stage_bytes);
   // A ring position and its parity; no division in the stage loops (with one
   // each, every warp's turn took a tenth of the HBM's rate at T = 64).
   struct Stage {
@@ -771,30 +773,46 @@ expert_gemm_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_cons
     }
   } else if (OUT == kParts) {
     // -------------------------------------------------- low-rank products
-    // low32[t, r] = scale[a] * A_a[r] . x[t], one warp per (t, r)
+    // low32[t, r] = scale[a] * A_a[r] . x[t]: a warp takes one rank row of a
+    // token, or two neighbouring ones where there are several rounds of them
     grid_dependency_wait();
-    for (int64_t job = static_cast<int64_t>(blockIdx.x) * kLowWarps + warp - 6; job < p.n_rows * p.R;
-         job += static_cast<int64_t>(gridDim.x) * kLowWarps) {
-      const int64_t row = job / p.R;
-      const int r = static_cast<int>(job - row * p.R), id = p.ids[row];
-      if (id < 0 || id >= p.L) {
-        if (id >= p.L && lane == 0 && p.err_flag) atomicOr(p.err_flag, MOE_FLAG_BAD_INDEX);
-        continue;
-      }
-      const uint16_t* ar = p.a + (static_cast<int64_t>(id) * p.R + r) * p.K;
-      const uint16_t* xr = p.x + row * p.K;
-      float sum = 0.f;
-#pragma unroll 6
-      for (int k = lane * 8; k < p.K; k += 256) {
-        float f[8], g[8];
-        unpack8(ld_keep16(xr + k), f);
-        unpack8(ld_stream16(ar + k), g);
+    const int64_t first = static_cast<int64_t>(blockIdx.x) * kLowWarps + warp - 6;
+    const int64_t warps = static_cast<int64_t>(gridDim.x) * kLowWarps;
+    auto products = [&](auto rows) {
+      constexpr int RB = decltype(rows)::value;
+      const int per = p.R / RB;
+      for (int64_t job = first; job < p.n_rows * per; job += warps) {
+        const int64_t row = job / per;
+        const int r = static_cast<int>(job - row * per) * RB, id = p.ids[row];
+        if (id < 0 || id >= p.L) {
+          if (id >= p.L && lane == 0 && p.err_flag) atomicOr(p.err_flag, MOE_FLAG_BAD_INDEX);
+          continue;
+        }
+        const uint16_t* ar = p.a + (static_cast<int64_t>(id) * p.R + r) * p.K;
+        const uint16_t* xr = p.x + row * p.K;
+        float sum[RB];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) sum = fmaf(f[i], g[i], sum);
+        for (int i = 0; i < RB; ++i) sum[i] = 0.f;
+#pragma unroll(RB == 1 ? 6 : 4)
+        for (int k = lane * 8; k < p.K; k += 256) {
+          float f[8], g[8];
+          unpack8(ld_keep16(xr + k), f);
+#pragma unroll
+          for (int i = 0; i < RB; ++i) {
+            unpack8(ld_stream16(ar + static_cast<int64_t>(i) * p.K + k), g);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) sum[i] = fmaf(f[e], g[e], sum[i]);
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < RB; ++i) {
+          sum[i] = warp_sum(sum[i]);
+          if (lane == 0) p.low32[row * p.R + r + i] = sum[i] * p.scale[id];
+        }
       }
-      sum = warp_sum(sum);
-      if (lane == 0) p.low32[job] = sum * p.scale[id];
-    }
+    };
+    if (p.n_rows * p.R > 2 * warps) products(std::integral_constant<int, 2>{});
+    else products(std::integral_constant<int, 1>{});
   } else if (GATHER && !few && warp < 6 + kLoaders) {
     // ------------------------------------------------------------- gather
     // Warp j takes rows 16 i + 4 j .. + 3 of this CTA's rows, eight lanes a
@@ -1014,8 +1032,8 @@ inline bool make_map(CUtensorMap* map, const void* base, int rank, const cuuint6
 inline int gemm_ctas() { return sm_count() < kMaxCtas ? sm_count() : kMaxCtas; }
 
 // Dynamic shared memory: the ring, the walker's pieces, the tile list, the adapters' first rows.
-inline size_t gemm_smem(int64_t E, int segs) {
-  return 1024 + kRingBytes + kPieces * sizeof(Piece) + static_cast<size_t>(3 * E + 1 + segs + 1) * sizeof(int);
+inline size_t gemm_smem(int64_t E, int segs, int ring) {
+  return 1024 + static_cast<size_t>(ring) + kPieces * sizeof(Piece) + static_cast<size_t>(3 * E + 1 + segs + 1) * sizeof(int);
 }
 
 // Opt the kernel into its dynamic shared memory, once per device.
@@ -1026,7 +1044,7 @@ cudaError_t opt_in(int dev) {
   if (!done[dev].load()) {
     const cudaError_t e =
         cudaFuncSetAttribute(expert_gemm_kernel<SWIGLU, GATHER, PAIR, OUT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             static_cast<int>(gemm_smem(OUT == kScatter ? 1 : MOE_MAX_E, OUT == kScatter ? MOE_MAX_ADAPTERS + 1 : 0)));
+                             static_cast<int>(gemm_smem(OUT == kScatter ? 1 : MOE_MAX_E, OUT == kScatter ? MOE_MAX_ADAPTERS + 1 : 0, kRingBytes)));
     if (e != cudaSuccess) return e;
     done[dev].store(true);
   }
@@ -1044,7 +1062,7 @@ cudaError_t launch(const CUtensorMap& mx, const CUtensorMap& mw, const CUtensorM
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(G), 1, 1);
   cfg.blockDim = dim3(threads_of(GATHER, OUT), 1, 1);
-  cfg.dynamicSmemBytes = launch_smem(gemm_smem(p.E, p.segs));
+  cfg.dynamicSmemBytes = launch_smem(gemm_smem(p.E, p.segs, p.ring_bytes));
   cfg.stream = stream;
   cudaLaunchAttribute attr[2] = {pdl_attribute(), {}};
   cfg.attrs = attr;
