@@ -339,12 +339,74 @@ def test_expert_linear_infinities_stay_in_their_rows(M):
     assert not np.isfinite(got[row]).any()
 
 
-def test_expert_linear_same_bits_again_and_in_any_company(M):
-    # a row's result depends on its own token and expert, and two runs agree bit for bit
-    c = draw_layer(5, 90, 12, 3, 1032, 272)
+@pytest.mark.parametrize("T,E,k", [(2, 12, 3), (90, 12, 3), (900, 4, 2)])
+def test_expert_linear_same_bits_again(M, T, E, k):
+    c = draw_layer(5, T, E, k, 1032, 272)
     a, _ = run_expert(M, c, "swiglu", True)
-    b, _ = run_expert(M, c, "swiglu", True)
-    assert torch.equal(a, b)
+    for _ in range(3):
+        b, _ = run_expert(M, c, "swiglu", True)
+        assert torch.equal(a, b)
+
+
+def ints(seed, *shape):
+    """Small integers: sums of up to 28 products are whole numbers that BF16 holds."""
+    g = torch.Generator(device="cuda")
+    g.manual_seed(seed)
+    return torch.randint(-3, 4, shape, generator=g, device="cuda", dtype=torch.int8).to(torch.bfloat16)
+
+
+@pytest.mark.parametrize("E,rows", [(80, 1), (80, 96)])
+def test_expert_linear_more_pieces_than_a_walker_keeps(M, E, rows):
+    # 512 (pairs: 256) weight tiles an expert: over 256 tiles a CTA or pair
+    N, K = 65536, 8
+    x, w = ints(1, E * rows, K), ints(2, E, N, K)
+    off = torch.arange(E + 1, device="cuda", dtype=torch.int32) * rows
+    out = M.moe_expert_linear(x, w, off, torch.full((E,), rows, device="cuda", dtype=torch.int32))
+    for e in range(E):
+        want = (x[e * rows:(e + 1) * rows].float() @ w[e].float().T).to(torch.bfloat16)
+        assert torch.equal(out[e * rows:(e + 1) * rows], want), e
+
+
+def test_expert_linear_offsets_beyond_31_bits(M):
+    # outputs, then rows of x, whose offsets in elements pass 2^31 and 2^32
+    n, N, K = 70000, 65536, 8
+    x, w = ints(3, n, K), ints(4, 1, N, K)
+    seg = torch.tensor([0, n], device="cuda", dtype=torch.int32)
+    out = M.moe_expert_linear(x, w, seg, seg[1:])
+    at = torch.tensor([0, 1, 32767, 32768, 65535, 65536, n - 1], device="cuda")
+    assert torch.equal(out[at], (x[at].float() @ w[0].float().T).to(torch.bfloat16))
+    del out
+    n, K, N = 70000, 65536, 16
+    x = torch.zeros(n, K, dtype=torch.bfloat16, device="cuda")
+    w = ints(5, 1, N, K)
+    x[:, 40000:40008] = ints(6, n, 8)
+    want = (x[:, 40000:40008].float() @ w[0, :, 40000:40008].float().T).to(torch.bfloat16)
+    seg = torch.tensor([0, n], device="cuda", dtype=torch.int32)
+    back = torch.arange(n - 1, -1, -1, device="cuda", dtype=torch.int32)
+    for tok, ref in ((None, want), (back, want.flip(0))):
+        assert torch.equal(M.moe_expert_linear(x, w, seg, seg[1:], row_token=tok), ref)
+    few = torch.tensor([n - 1, 0, 65536, 32768], device="cuda", dtype=torch.int32)
+    four = torch.tensor([0, 4], device="cuda", dtype=torch.int32)
+    assert torch.equal(M.moe_expert_linear(x, w, four, four[1:], row_token=few), want[few.long()])
+
+
+def test_expert_linear_without_any_token(M):
+    # no rows of x at all: every named token is outside, its row is zeros
+    w = ints(7, 2, 32, 64)
+    tok = torch.tensor([0, -1, 5], device="cuda", dtype=torch.int32)
+    flag = torch.zeros(1, dtype=torch.int32, device="cuda")
+    x = torch.empty(0, 64, dtype=torch.bfloat16, device="cuda")
+    out = M.moe_expert_linear(x, w, torch.tensor([0, 2, 3], device="cuda", dtype=torch.int32),
+                              torch.tensor([2, 1], device="cuda", dtype=torch.int32), row_token=tok, err_flag=flag)
+    assert not out.any() and int(flag.item()) == L.MOE_FLAG_BAD_INDEX
+
+
+def test_expert_linear_overlapping_segments_take_nothing(M):
+    c = draw_layer(8, 40, 4, 2, 64, 32)
+    c["counts"] = np.full(4, 60, np.int32)
+    c["offsets"] = np.array([0, 5, 10, 15], np.int32)
+    out, flag = run_expert(M, c, None, True)
+    assert flag == L.MOE_FLAG_BAD_INDEX and np.all(values(out) == 3.0)
 
 
 @pytest.mark.parametrize("T,gather", [(2, True), (300, False)])
@@ -433,6 +495,36 @@ def test_adapter_of_another_token_does_not_leak(M, T):
     keep = np.arange(T) != 2
     assert np.array_equal(host16(out)[keep], host16(clean)[keep])
     assert not np.isfinite(values(out)[2]).any()
+
+
+@pytest.mark.parametrize("T", [3, 700])
+def test_adapter_linear_offsets_beyond_31_bits(M, T):
+    # tables of more than 2^32 elements; one non-zero column each, so that every sum is a whole number
+    N, K, R, n = 64, 65536, 72, 1024
+    ids = torch.tensor([n - 1, 0, 700], device="cuda", dtype=torch.int32).repeat(T // 3 + 1)[:T]
+    x = torch.zeros(T, K, dtype=torch.bfloat16, device="cuda")
+    x[:, 50001] = ints(1, T)
+    w = torch.zeros(N, K, dtype=torch.bfloat16, device="cuda")
+    w[:, 50001] = ints(2, N)
+    a = torch.zeros(n, R, K, dtype=torch.bfloat16, device="cuda")
+    a[:, 71, 50001] = 1 + (torch.arange(n, device="cuda") % 3)
+    b = torch.zeros(n, N, R, dtype=torch.bfloat16, device="cuda")
+    b[:, :, 71] = ints(3, n, N)
+    scale = torch.full((n,), 2.0, device="cuda")
+    i = ids.long()
+    xv = x[:, 50001].float()[:, None]
+    want = (xv * w[:, 50001].float() + 2 * xv * a[i, 71, 50001].float()[:, None] * b[i, :, 71].float()).to(torch.bfloat16)
+    assert torch.equal(M.moe_adapter_linear(x, w, a, b, ids, scale), want)
+
+
+@pytest.mark.parametrize("T", [1, 40, 200, 600])
+def test_adapter_linear_same_bits_again_and_with_a_given_workspace(M, T):
+    c = draw_adapter(T, 272, 328, 24, 7, "mix")
+    a, _ = run_adapter(M, c, "swiglu")
+    ws = torch.full((M.lib().moe_adapter_linear_workspace(T, 272, 328, 24, 7),), 255, dtype=torch.uint8, device="cuda")
+    for _ in range(3):
+        b, _ = run_adapter(M, c, "swiglu", workspace=ws)
+        assert torch.equal(a, b)
 
 
 def test_adapter_linear_empty_batch(M):
@@ -551,6 +643,30 @@ def test_layers_on_two_streams_at_once(M, T):
     for o in got:
         for name in o:
             assert torch.equal(o[name], want[name]), name
+
+
+def test_workspaces_of_two_graphs_are_apart(M):
+    """Two captured layers replayed at the same time on two streams."""
+    _, g, p = draw_whole(50, 512, 256, 16, 4, 1)
+    _, g2, _ = draw_whole(50, 512, 256, 16, 4, 1, seed=1)
+    layer(M, g, p)
+    torch.cuda.synchronize()
+    graphs, outs = [], []
+    for inputs in (g, g2):
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            outs.append(layer(M, inputs, p))
+        graphs.append(graph)
+    streams = [torch.cuda.Stream() for _ in graphs]
+    for _ in range(5):
+        for graph, s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                graph.replay()
+    torch.cuda.synchronize()
+    for inputs, out in zip((g, g2), outs):
+        fresh = layer(M, inputs, p)
+        for name in fresh:
+            assert torch.equal(fresh[name], out[name]), name
 
 
 @pytest.mark.parametrize("call", ["route", "map", "expert", "adapter"])
