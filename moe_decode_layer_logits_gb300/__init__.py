@@ -204,6 +204,16 @@ def _opt(t, dtype, name, shape, device):
     return None if t is None else _arg(t, dtype, name, shape, device)
 
 
+def _out(t, dtype, name, shape, device):
+    """An output and its pointer: the one given, checked, or a new one."""
+    if t is None:
+        if min(shape) < 0:
+            raise ValueError(f"{name} cannot have the shape {list(shape)}")
+        t = torch.empty(shape, dtype=dtype, device=device)
+        return t, t.data_ptr()
+    return t, _arg(t, dtype, name, shape, device)
+
+
 def _flag(t, device):
     return None if t is None else _arg(t, torch.int32, "err_flag", t.shape, device)
 
@@ -221,14 +231,10 @@ def moe_group_topk_route(logits, k, routed_scale, bias=None, n_group=1, topk_gro
     score_fn = _choice(_SCORES, scores, "scores")
     handle, on = _enter(device, stream)
     try:
-        if topk_ids is None:
-            topk_ids = torch.empty((T, max(k, 0)), dtype=torch.int32, device=device)
-        if topk_w is None:
-            topk_w = torch.empty((T, max(k, 0)), dtype=torch.float32, device=device)
-        st = lib().moe_group_topk_route(lg, bs, _arg(topk_ids, torch.int32, "topk_ids", (T, k), device),
-                                        _arg(topk_w, torch.float32, "topk_w", (T, k), device), T, E, k, int(n_group),
-                                        int(topk_group), int(group_top), score_fn, 1 if renormalize else 0,
-                                        float(routed_scale), handle)
+        topk_ids, ids = _out(topk_ids, torch.int32, "topk_ids", (T, k), device)
+        topk_w, wts = _out(topk_w, torch.float32, "topk_w", (T, k), device)
+        st = lib().moe_group_topk_route(lg, bs, ids, wts, T, E, k, int(n_group), int(topk_group), int(group_top), score_fn,
+                                        1 if renormalize else 0, float(routed_scale), handle)
     finally:
         if on is not None:
             on.close()
@@ -257,19 +263,21 @@ def moe_expert_map(topk_ids, E, block=1, n_rows=None, row_map=None, row_token=No
     ids = _arg(topk_ids, torch.int32, "topk_ids", (T, k), device)
     handle, on = _enter(device, stream)
     try:
-        if row_map is None:
-            row_map = torch.empty((T, k), dtype=torch.int32, device=device)
-        if row_token is None:
-            row_token = torch.empty(n_rows, dtype=torch.int32, device=device)
-        if offsets is None:
-            offsets = torch.empty(E + 1, dtype=torch.int32, device=device)
-        if counts is None:
-            counts = torch.empty(E, dtype=torch.int32, device=device)
-        st = lib().moe_expert_map(
-            ids, _arg(row_map, torch.int32, "row_map", (T, k), device),
-            _arg(row_token, torch.int32, "row_token", (n_rows,), device),
-            _arg(offsets, torch.int32, "offsets", (E + 1,), device),
-            _arg(counts, torch.int32, "counts", (E,), device), n_rows, T, E, k, block, handle)
+        if row_map is None and row_token is None and offsets is None and counts is None:
+            # one allocation, row_token first (its fill wants 16-byte alignment)
+            buf = torch.empty(n_rows + T * k + 2 * E + 1, dtype=torch.int32, device=device)
+            row_token, row_map, offsets, counts = buf.split((n_rows, T * k, E + 1, E))
+            row_map = row_map.view(T, k)
+            tok = buf.data_ptr()
+            rm = tok + 4 * n_rows
+            off = rm + 4 * T * k
+            cnt = off + 4 * (E + 1)
+        else:
+            row_map, rm = _out(row_map, torch.int32, "row_map", (T, k), device)
+            row_token, tok = _out(row_token, torch.int32, "row_token", (n_rows,), device)
+            offsets, off = _out(offsets, torch.int32, "offsets", (E + 1,), device)
+            counts, cnt = _out(counts, torch.int32, "counts", (E,), device)
+        st = lib().moe_expert_map(ids, rm, tok, off, cnt, n_rows, T, E, k, block, handle)
     finally:
         if on is not None:
             on.close()
@@ -285,6 +293,7 @@ def _workspace(given, nbytes, device):
         if nbytes == 0:
             return None, None, 0
         given = torch.empty(nbytes, dtype=torch.uint8, device=device)
+        return given, given.data_ptr(), nbytes
     return given, _arg(given, torch.uint8, "workspace", given.shape, device), given.numel()
 
 
@@ -310,11 +319,10 @@ def moe_expert_linear(x, w, offsets, counts, row_token=None, act=None, out=None,
     L = lib()
     handle, on = _enter(device, stream)
     try:
-        if out is None:
-            out = torch.empty((n_rows, n_out), dtype=torch.bfloat16, device=device)
+        out, out_ptr = _out(out, torch.bfloat16, "out", (n_rows, n_out), device)
         ws, ws_ptr, nbytes = _workspace(workspace, L.moe_expert_linear_workspace(n_rows, E, N, K), device)
-        st = L.moe_expert_linear(*args, _arg(out, torch.bfloat16, "out", (n_rows, n_out), device), n_rows, E, N, K, act,
-                                 ws_ptr, nbytes, _flag(err_flag, device), handle)
+        st = L.moe_expert_linear(*args, out_ptr, n_rows, E, N, K, act, ws_ptr, nbytes,
+                                 _flag(err_flag, device), handle)
     finally:
         if on is not None:
             on.close()
@@ -343,11 +351,10 @@ def moe_adapter_linear(x, w, adapter_a, adapter_b, adapter_ids, adapter_scale, a
     so = lib()
     handle, on = _enter(device, stream)
     try:
-        if out is None:
-            out = torch.empty((T, n_out), dtype=torch.bfloat16, device=device)
+        out, out_ptr = _out(out, torch.bfloat16, "out", (T, n_out), device)
         ws, ws_ptr, nbytes = _workspace(workspace, so.moe_adapter_linear_workspace(T, N, K, R, L), device)
-        st = so.moe_adapter_linear(*args, _arg(out, torch.bfloat16, "out", (T, n_out), device), T, N, K, R, L, act, ws_ptr,
-                                   nbytes, _flag(err_flag, device), handle)
+        st = so.moe_adapter_linear(*args, out_ptr, T, N, K, R, L, act, ws_ptr, nbytes,
+                                   _flag(err_flag, device), handle)
     finally:
         if on is not None:
             on.close()

@@ -357,6 +357,7 @@ __global__ void __launch_bounds__(kGroupRouteWarps * 32) group_route_kernel(cons
       const int j = lane + 32 * s;
       num[s] = -1;
       key[s] = -inf;
+      if (32 * s >= live) continue;  // (the same for all lanes)
       if (j < live) {
         const int q = static_cast<int>((static_cast<unsigned>(j) * recip) >> 20);
         num[s] = chosen[q] * size + (j - q * size);
@@ -379,9 +380,11 @@ __global__ void __launch_bounds__(kGroupRouteWarps * 32) group_route_kernel(cons
     const float lim = BIAS && tau > -inf ? tau - (doubt + 4.7683716e-7f * fabsf(tau)) : tau;
     unsigned bal[EPL];
 #pragma unroll
-    for (int s = 0; s < EPL; ++s) bal[s] = __ballot_sync(0xFFFFFFFFu, num[s] >= 0 && key[s] >= lim);
+    for (int s = 0; s < EPL; ++s)
+      bal[s] = !GROUPS || 32 * s < live ? __ballot_sync(0xFFFFFFFFu, num[s] >= 0 && key[s] >= lim) : 0u;
 #pragma unroll
     for (int s = 0; s < EPL; ++s) {
+      if (GROUPS && 32 * s >= live) break;
       const int at = n + __popc(bal[s] & ((1u << lane) - 1u));
       if (((bal[s] >> lane) & 1u) && at < kCandidates) list[at] = candidate(key[s], num[s]);
       n += __popc(bal[s]);
@@ -395,21 +398,17 @@ __global__ void __launch_bounds__(kGroupRouteWarps * 32) group_route_kernel(cons
     if (lane < 8 * blocks - n) list[n + lane] = 0ull;
     __syncwarp();
     const ulonglong2* pairs = reinterpret_cast<const ulonglong2*>(list);
-    for (int b = 0; b < n; b += 64) {
-      const uint64_t v0 = b + lane < n ? list[b + lane] : ~0ull, v1 = b + lane + 32 < n ? list[b + lane + 32] : ~0ull;
-      int r0 = 0, r1 = 0;
+    for (int b = 0; b < n; b += 32) {  // usually one round
+      const uint64_t v = b + lane < n ? list[b + lane] : ~0ull;
+      int r = 0;
       for (int c = 0; c < blocks; ++c) {
         ulonglong2 o[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) o[i] = pairs[4 * c + i];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          r0 += (o[i].x > v0 ? 1 : 0) + (o[i].y > v0 ? 1 : 0);
-          r1 += (o[i].x > v1 ? 1 : 0) + (o[i].y > v1 ? 1 : 0);
-        }
+        for (int i = 0; i < 4; ++i) r += (o[i].x > v ? 1 : 0) + (o[i].y > v ? 1 : 0);
       }
-      if (b + lane < n && r0 <= p.k) best[r0] = v0;
-      if (b + lane + 32 < n && r1 <= p.k) best[r1] = v1;
+      if (b + lane < n && r <= p.k) best[r] = v;
     }
     __syncwarp();
     const uint64_t mine = lane < p.k ? best[lane] : 0ull;
