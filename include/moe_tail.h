@@ -313,10 +313,6 @@ int64_t moe_adapter_linear_workspace(int64_t T, int64_t N, int64_t K, int32_t R,
  *   out_bf16       [T, N or N/2] BF16, written; must not overlap any input
  *   workspace      device memory of at least moe_adapter_linear_workspace()
  *                  bytes, 16-byte aligned; as in moe_expert_linear
- *                  (w is a model parameter: for small batches the kernel starts
- *                  copying it before it waits for the previous kernel on the
- *                  stream, so it must not be written by a kernel that may still
- *                  be running on `stream` when this call is made)
  *   err_flag       device int32 or NULL (MOE_FLAG_BAD_INDEX, MOE_FLAG_TIMEOUT)
  *   T >= 0; N and K as in moe_expert_linear; R % 8 == 0, 8 <= R <=
  *   MOE_MAX_RANK; 1 <= L <= MOE_MAX_ADAPTERS; T * R < 2^31.

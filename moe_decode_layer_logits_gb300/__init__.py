@@ -335,9 +335,8 @@ def moe_adapter_linear(x, w, adapter_a, adapter_b, adapter_ids, adapter_scale, a
     """One projection for all tokens with each token's low-rank adapter beside
     it: act(w @ x[t] + scale[a] * b[a] @ (a[a] @ x[t])), a = adapter_ids[t]
     (negative: none).  x [T, K], w [N, K], adapter_a [L, R, K], adapter_b
-    [L, N, R] BF16, adapter_ids [T] int32, adapter_scale [L] FP32.  w must not
-    be written by a kernel still running on the stream (small batches start
-    copying it before that kernel ends); workspace as in moe_expert_linear."""
+    [L, N, R] BF16, adapter_ids [T] int32, adapter_scale [L] FP32;
+    workspace as in moe_expert_linear."""
     if x.dim() != 2 or w.dim() != 2 or adapter_a.dim() != 3 or adapter_b.dim() != 3:
         raise ValueError("x must be [T, K], w [N, K], adapter_a [L, R, K] and adapter_b [L, N, R]")
     (T, K), N, (L, R, _), device = x.shape, w.shape[0], adapter_a.shape, x.device

@@ -265,7 +265,7 @@ cudaError_t few_tokens(const AdapterLinear& g, cudaStream_t stream) {
   p.R = g.R;
   p.L = g.L;
   CUtensorMap mx, mw;
-  if (!weight_map(&mw, g.w, 1, g.N, g.K, SWIGLU, p.weave) || !row_map_of(&mx, g.x, g.T, g.K, false))
+  if (!weight_map(&mw, g.w, 1, g.N, g.K, SWIGLU, p.weave) || !row_map_of(&mx, g.x, g.T, g.K))
     return cudaErrorInvalidValue;
   const cudaError_t e = launch<SWIGLU, false, false, kParts>(mx, mw, mw, p, stream);
   if (e != cudaSuccess) return e;
@@ -311,12 +311,12 @@ cudaError_t many_tokens(const AdapterLinear& g, cudaStream_t stream) {
   p.withhold = -1;
   p.scale = g.scale;
   for (int i = 0; i < 2; ++i) p.low[i] = reinterpret_cast<uint16_t*>(g.workspace + f.low[i]);
-  CUtensorMap mx, ma, mw, mb;
+  CUtensorMap ma, mw, mb;
   const bool weave = SWIGLU && g.N / 2 % 16 == 0;
-  if (!row_map_of(&mx, g.x, g.T, g.K, true) || !weight_map(&ma, g.a, g.L, g.R, g.K, false, false) ||
-      !weight_map(&mw, g.w, 1, g.N, g.K, SWIGLU, weave) || !weight_map(&mb, g.b, g.L, g.N, g.R, SWIGLU, weave))
+  if (!weight_map(&ma, g.a, g.L, g.R, g.K, false, false) || !weight_map(&mw, g.w, 1, g.N, g.K, SWIGLU, weave) ||
+      !weight_map(&mb, g.b, g.L, g.N, g.R, SWIGLU, weave))
     return cudaErrorInvalidValue;
-  e = launch<false, true, false, kLow>(mx, ma, ma, p, stream);
+  e = launch<false, true, false, kLow>(ma, ma, ma, p, stream);
   if (e != cudaSuccess) return e;
 
   p.offsets = nullptr;
@@ -328,7 +328,7 @@ cudaError_t many_tokens(const AdapterLinear& g, cudaStream_t stream) {
   p.n_out = static_cast<int>(SWIGLU ? g.N / 2 : g.N);
   p.weave = weave;
   p.out = g.out;
-  return launch<SWIGLU, true, true, kScatter>(mx, mw, mb, p, stream);
+  return launch<SWIGLU, true, true, kScatter>(mw, mw, mb, p, stream);
 }
 
 }  // namespace

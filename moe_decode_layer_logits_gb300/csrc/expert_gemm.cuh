@@ -14,14 +14,13 @@
 //    lane issues the MMAs;
 //  - warps 2..5 read the finished accumulator while the next tile's MMAs run,
 //    apply the activation to the FP32 sums and store BF16 once;
-//  - with a token list, tiles of up to 32 rows are gathered by warp 0 (TMA, four
-//    rows a copy), larger ones by warps 6..9 with 16-byte asynchronous copies
-//    (eight lanes a row of the stage) that arrive on the stage's own barrier as
-//    they land, and warp 10 passes that on behind a proxy fence.  (The fence
-//    waits for its thread's copies in flight: in the copying warps it left one
-//    stage in flight.  A TMA gather costs the copy engine about 50 cycles
-//    whatever its size, so 64 a K block took 13.8 ms at T = 8192 against 3.0;
-//    at T = 64 the relay's latency costs 2053 us against @G4@.)
+//  - with a token list the rows are gathered by warps 6..9 with 16-byte
+//    asynchronous copies (eight lanes a row of the stage) that arrive on the
+//    stage's own barrier as they land, and warp 10 passes that on behind a proxy
+//    fence.  (The fence waits for its thread's copies in flight: in the copying
+//    warps it left one stage in flight.  A TMA gather of four rows a copy costs
+//    the copy engine about 50 cycles whatever its size: 1559 us against 1561 at
+//    T = 64, where experts have one or two rows, and 2106 against 1809 at 512.)
 // With SwiGLU a tile holds 64 gate and the 64 matching up rows, interleaved by
 // 16, so that a gate and its up sit 16 tensor-memory lanes apart, in one warp.
 //
@@ -44,9 +43,10 @@
 //             low-rank product of an adapter, 16 significant bits;
 //  - kParts   one segment: every piece left as an FP32 partial tile, for the
 //             caller's own last kernel, and the adapters' low-rank products of
-//             the rows computed by further warps beside it.  The weights are a
-//             parameter, so the first stages are requested before the wait for
-//             the previous kernel;
+//             the rows computed by further warps beside it.  The first stages'
+//             weights are requested into the L2 before the wait for the previous
+//             kernel (T = 1, K = 6144, N = 4096: 13.4 us; copied into shared
+//             memory before it 15.5; two rings of them 14.4);
 //  - kScatter rows sorted by adapter, every segment starting on a multiple of
 //             16 rows: behind a tile's K blocks come, for each adapter that has
 //             rows in the tile, its B against the two parts of its low-rank
@@ -115,8 +115,7 @@ struct Barriers {
   uint64_t drained;
   uint32_t tmem_base;
   int abort_flag;
-  int bn, few;
-  int pieces;
+  int bn, pieces;
 };
 
 __host__ __device__ inline int round_up(int v, int m) { return (v + m - 1) / m * m; }
@@ -137,9 +136,6 @@ __device__ __forceinline__ int tile_shift(int mean) {
   return want <= 32 ? 5 : want <= 64 ? 6 : 7;
 }
 
-// A gather of up to this mean of rows is TMA's.
-constexpr int kFewRows = 4;
-
 // Row tiles of the one segment of kScatter: of the few numbers that hold it,
 // the one whose rounds over the pairs take the fewest rows.
 __device__ __forceinline__ int scatter_tiles(int total, int mt, int G) {
@@ -157,9 +153,9 @@ __device__ __forceinline__ int scatter_tiles(int total, int mt, int G) {
 }
 
 // Fills the tile list; every thread of the block calls it.  Afterwards *bn_out
-// holds the rows per tile and *few_out whether the segments have few rows.
+// holds the rows per tile.
 template <bool PAIR, Out OUT>
-__device__ void list_tiles(const GemmParams& p, Tiles t, int mt, int walkers, int* bn_out, int* few_out, bool report) {
+__device__ void list_tiles(const GemmParams& p, Tiles t, int mt, int walkers, int* bn_out, bool report) {
   if (OUT == kParts || OUT == kScatter) {  // one segment, not the caller's
     if (threadIdx.x == 0) {
       const int n = OUT == kScatter ? p.seg[p.segs] : static_cast<int>(p.n_rows);
@@ -169,7 +165,6 @@ __device__ void list_tiles(const GemmParams& p, Tiles t, int mt, int walkers, in
       t.before[0] = 0;
       t.before[1] = OUT == kScatter ? scatter_tiles(n, mt, walkers) : (n + bn - 1) / bn;
       *bn_out = bn;
-      *few_out = 0;
     }
   } else if (threadIdx.x < 32) {
     // lane l takes `per` neighbouring segments, eight loaded at once
@@ -235,7 +230,6 @@ __device__ void list_tiles(const GemmParams& p, Tiles t, int mt, int walkers, in
     if (lane == 31) {
       t.before[p.E] = upto;
       *bn_out = 1 << shift;
-      *few_out = mean <= kFewRows;
     }
   }
   __syncthreads();
@@ -472,6 +466,9 @@ expert_gemm_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_cons
   volatile int* abort_v = &sb.abort_flag;
 
   if (threadIdx.x < kMaxStages) {
+    // a stage is full when its copies have landed and, where other warps gather
+    // the rows, they have been reported (by each CTA of a pair)
+    mbar_init(&sb.full[threadIdx.x], 1 + (GATHER ? (PAIR ? 2 : 1) : 0));
     mbar_init(&sb.landed[threadIdx.x], 32 * kLoaders);
     mbar_init(&sb.empty[threadIdx.x], 1);
     mbar_init_fence();
@@ -485,7 +482,7 @@ expert_gemm_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_cons
     mbar_init_fence();
   } else if (threadIdx.x == kMaxStages + 3) {
     prefetch_map(&tmap_w);
-    prefetch_map(&tmap_x);
+    if (!GATHER) prefetch_map(&tmap_x);
   }
   if (warp == 1) tmem_alloc<PAIR>(&sb.tmem_base, 2 * kAccCols);
   if (OUT != kParts) {
@@ -498,15 +495,8 @@ expert_gemm_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_cons
   const int walkers = static_cast<int>(PAIR ? gridDim.x >> 1 : gridDim.x);
   if (OUT == kScatter)
     for (int i = threadIdx.x; i <= p.segs; i += blockDim.x) seg[i] = p.seg[i];
-  list_tiles<PAIR, OUT>(p, t, mt, walkers, &sb.bn, &sb.few, blockIdx.x == 0);  // kParts: reads no global memory
-  const bool few = GATHER && !PAIR && sb.few;  // rows gathered by TMA
+  list_tiles<PAIR, OUT>(p, t, mt, walkers, &sb.bn, blockIdx.x == 0);  // kParts: reads no global memory
   const int depth = OUT == kScatter ? (p.R + kBK - 1) / kBK : 0;  // K blocks of an adapter's B
-  if (threadIdx.x < kMaxStages) {
-    // a stage is full when its copies have landed and, where other warps gather
-    // the rows, they have been reported (by each CTA of a pair)
-    mbar_init(&sb.full[threadIdx.x], 1 + (GATHER && !few ? (PAIR ? 2 : 1) : 0));
-    mbar_init_fence();
-  }
   // this walker's pieces, one a thread
   const Schedule s(p, t, mt, walkers, !PAIR);
   {
@@ -556,15 +546,10 @@ expert_gemm_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_cons
 
   if (warp == 0) {
     // -------------------------------------------------------------- loads
-    // One lane walks and copies; where TMA gathers the rows (few), the whole
-    // warp does, lane l copying rows 4 l .. 4 l + 3.
-    const uint64_t once = l2_evict_first_policy(), keep = l2_evict_normal_policy();
-    const int withheld = who == 0 ? p.withhold : -1;
-    auto load = [&](auto lone_lane) {
-      constexpr bool LONE = decltype(lone_lane)::value;
-      const bool first = LONE || lane == 0;
+    if (lane == 0) {  // one lane walks and copies
+      const uint64_t once = l2_evict_first_policy(), keep = l2_evict_normal_policy();
+      const int withheld = who == 0 ? p.withhold : -1;
       auto load_weights = [&](const CUtensorMap* map, uint32_t dst, int kb, int m, int e, uint32_t bar, uint64_t pol) {
-        if (!first) return;
         if (!SWIGLU) {
           tma_load_5d<PAIR>(dst, map, kb * kBK, m * 128, 0, 0, e, bar, pol);
         } else if (p.weave) {
@@ -575,67 +560,40 @@ expert_gemm_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_cons
             tma_load_5d<PAIR>(dst + i * 32 * kRowBytes, map, kb * kBK, m * 64 + i * 16, 0, 0, e, bar, pol);
         }
       };
-      auto stage_copies = [&](const Piece& w) {  // bytes, in both CTAs of a pair
-        const int mine = PAIR ? round_up(w.nr, 16) / 2 : w.nr;  // rows in this CTA
-        const int rows = GATHER ? (LONE ? 0 : round_up(mine, 4)) : round_up(mine, 32);
-        return static_cast<uint32_t>((PAIR ? 2 : 1) * (kBM + rows)) * kRowBytes;
-      };
-      auto raw_tokens = [&](const Piece& w) {
-        int v[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) v[i] = lane * 4 + i < w.nr ? p.row_token[w.r0 + lane * 4 + i] : 0;
-        return make_int4(v[0], v[1], v[2], v[3]);
+      // bytes of a stage's copies, in both CTAs of a pair
+      auto stage_copies = [&](const Piece& w) {
+        return static_cast<uint32_t>((PAIR ? 2 : 1) * kBM + (GATHER ? 0 : round_up(w.nr, 32))) * kRowBytes;
       };
       int at = 0;
       Piece w;
       int n = 0;  // stages so far
       Stage x{0, 0};
-      int early = 0;
       if (OUT == kParts) {
-        // a ring of weights before the wait; their rows follow behind it.  (With
-        // more than one stage of weights in the copy engine's queue the rows wait
-        // for them, so the other forms do not run ahead.)
-        int ahead = 0;
+        // a ring of weights into the L2 before the wait (not into shared memory: a
+        // kernel still running may write them)
+        int ahead = 0, early = 0;
         while (early < nstages && next(ahead, w)) {
-          const uint32_t bytes = stage_copies(w);
           for (int kb = w.kb0; kb < w.kb1 && early < nstages; ++kb, ++early) {
-            mbar_arrive_expect_tx(&sb.full[early], bytes);
-            load_weights(&tmap_w, smem_addr(ring) + static_cast<uint32_t>(early * stage_bytes), kb, w.m, w.e,
-                         full0 + early * 8, w.alone ? once : keep);
+            if (!SWIGLU) {
+              tma_prefetch_5d(&tmap_w, kb * kBK, w.m * 128, 0, 0, w.e);
+            } else if (p.weave) {
+              tma_prefetch_5d(&tmap_w, kb * kBK, 0, 0, w.m * 4, w.e);
+            } else {
+              for (int i = 0; i < 4; ++i) tma_prefetch_5d(&tmap_w, kb * kBK, w.m * 64 + i * 16, 0, 0, w.e);
+            }
           }
         }
         grid_dependency_wait();
         // behind the wait, so that what is launched next finds the inputs ready
         allow_dependent_launch();
       }
-      // the tokens of a piece are loaded a piece ahead
-      int peek = 0;
-      Piece coming;
-      int4 raw = make_int4(0, 0, 0, 0);
-      if (!LONE && next(peek, coming)) raw = raw_tokens(coming);
       bool stop = false;
       // the next stage may be written: its last MMAs are done
-      auto freed = [&]() {
-        const bool go = n < nstages || wait(&sb.empty[x.st], x.ph ^ 1, abort_v);
-        return LONE ? go : __all_sync(0xFFFFFFFFu, go) != 0;
-      };
+      auto freed = [&]() { return n < nstages || wait(&sb.empty[x.st], x.ph ^ 1, abort_v); };
       while (!stop && next(at, w)) {
-        const int mine = PAIR ? round_up(w.nr, 16) / 2 : w.nr;  // rows in this CTA
-        const int boxes = GATHER ? 0 : (mine + 31) >> 5, quads = LONE ? 0 : (mine + 3) >> 2;
+        const int boxes = GATHER ? 0 : (w.nr + 31) >> 5;
         const uint32_t bytes = stage_copies(w);
-        int4 tok = raw;
-        if (!LONE) {
-          if (next(peek, coming)) raw = raw_tokens(coming);
-          int* v = &tok.x;
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            if (v[i] < 0 || v[i] >= p.n_x) {  // loads token 0, stored as zeros
-              if (p.err_flag) atomicOr(p.err_flag, MOE_FLAG_BAD_INDEX);
-              v[i] = 0;
-            }
-          }
-        }
-        const int m = PAIR ? w.m * 2 + rank : w.m, r0 = w.r0 + rank * mine;
+        const int m = PAIR ? w.m * 2 + rank : w.m;
         const uint64_t pol = w.alone ? once : keep;
         for (int kb = w.kb0; kb < w.kb1; ++kb, ++n, advance(x)) {
           if (!freed()) {
@@ -645,14 +603,9 @@ expert_gemm_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_cons
           if (n == withheld) continue;  // neither armed nor loaded: the MMA warp's wait runs out
           const uint32_t a = smem_addr(ring) + static_cast<uint32_t>(x.st * stage_bytes);
           const uint32_t b = a + kBM * kRowBytes, bar = full0 + x.st * 8;
-          if (OUT != kParts || n >= early) {
-            if (first && rank == 0) mbar_arrive_expect_tx(&sb.full[x.st], bytes);
-            if (!LONE) __syncwarp();
-            load_weights(&tmap_w, a, kb, m, w.e, bar, pol);
-          }
-          if (!LONE && lane < quads) tma_gather4(b + lane * 4 * kRowBytes, &tmap_x, kb * kBK, tok, bar);
-          for (int i = 0; i < boxes; ++i)
-            tma_load_2d<PAIR>(b + i * 32 * kRowBytes, &tmap_x, kb * kBK, r0 + i * 32, bar);
+          if (rank == 0) mbar_arrive_expect_tx(&sb.full[x.st], bytes);
+          load_weights(&tmap_w, a, kb, m, w.e, bar, pol);
+          for (int i = 0; i < boxes; ++i) tma_load_2d(b + i * 32 * kRowBytes, &tmap_x, kb * kBK, w.r0 + i * 32, bar);
         }
         if (OUT == kScatter && !stop) {
           Adapters ad(p, seg, w);
@@ -669,18 +622,15 @@ expert_gemm_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_cons
           }
         }
       }
-      if (!LONE) __syncwarp();
       // drain: no copy may land after this CTA exits (a pair's copies are counted
       // by its first CTA, and neither leaves before the other)
-      if (first && rank == 0) {
+      if (rank == 0) {
         const int from = n > nstages ? n - nstages : 0;
         Stage y{from % nstages, (from / nstages) & 1};
         for (int i = from; i < n; ++i, advance(y))
           if (i != withheld) wait(&sb.full[y.st], y.ph, abort_v, true);
       }
-    };
-    if (GATHER && !PAIR && few) load(std::false_type{});
-    else if (lane == 0) load(std::true_type{});
+    }
     __syncwarp();
   } else if (warp == 1) {
     // ---------------------------------------------------------------- MMA
@@ -813,7 +763,7 @@ expert_gemm_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_cons
     };
     if (p.n_rows * p.R > 2 * warps) products(std::integral_constant<int, 2>{});
     else products(std::integral_constant<int, 1>{});
-  } else if (GATHER && !few && warp < 6 + kLoaders) {
+  } else if (GATHER && warp < 6 + kLoaders) {
     // ------------------------------------------------------------- gather
     // Warp j takes rows 16 i + 4 j .. + 3 of this CTA's rows, eight lanes a
     // row, 16 bytes a lane, at their place in the 128-byte swizzle.
@@ -888,7 +838,7 @@ expert_gemm_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_cons
       }
     }
     copy_drain();
-  } else if (GATHER && !few) {
+  } else if (GATHER) {
     // -------------------------------------------------- gathered rows are in
     if (lane == 0) {
       int at = 0;
@@ -940,12 +890,12 @@ constexpr int kJoinBatch = 2;  // pieces loaded at once
 template <bool SWIGLU, Out OUT>
 __global__ void __launch_bounds__(128, 6) expert_join_kernel(const GemmParams p, int G) {
   extern __shared__ int join_list[];
-  __shared__ int bn, few, pieces;
+  __shared__ int bn, pieces;
   __shared__ int piece_s[kMaxCtas];
   const Tiles t{join_list, join_list + p.E, join_list + 2 * p.E};
   allow_dependent_launch();
   const int rows_out = SWIGLU ? 64 : 128, mt = (p.n_out + rows_out - 1) / rows_out;
-  list_tiles<false, OUT>(p, t, mt, G, &bn, &few, false);
+  list_tiles<false, OUT>(p, t, mt, G, &bn, false);
   const Schedule s(p, t, mt, G, true);
   const int b = blockIdx.x, l = threadIdx.x, q = l >> 5;
   const unsigned end = s.share(b + 1), tile0 = end / s.nkb * s.nkb;
@@ -1102,10 +1052,10 @@ inline bool weight_map(CUtensorMap* map, const void* w, int64_t E, int64_t N, in
   return make_map(map, w, 5, dims, strides, box);
 }
 
-// Rows of x in boxes of 32, or of one for the gather.
-inline bool row_map_of(CUtensorMap* map, const void* x, int64_t n_x, int64_t K, bool gather) {
+// Rows of x in boxes of 32.
+inline bool row_map_of(CUtensorMap* map, const void* x, int64_t n_x, int64_t K) {
   const cuuint64_t dims[2] = {static_cast<cuuint64_t>(K), static_cast<cuuint64_t>(n_x)}, row = static_cast<cuuint64_t>(K) * 2;
-  const cuuint32_t box[2] = {umma::kBK, gather ? 1u : 32u};
+  const cuuint32_t box[2] = {umma::kBK, 32};
   return make_map(map, x, 2, dims, &row, box);
 }
 

@@ -527,6 +527,36 @@ def test_adapter_linear_same_bits_again_and_with_a_given_workspace(M, T):
         assert torch.equal(a, b)
 
 
+@pytest.mark.parametrize("T", [1, 40, 300])
+def test_adapter_linear_reads_what_the_kernels_before_it_wrote(M, T):
+    # the weights, the tokens and an adapter's tables are outputs of calls just made on the stream
+    K, N, R, n = 512, 768, 8, 3
+    g = torch.Generator(device="cuda").manual_seed(T)
+    draw = lambda *s: (torch.randn(*s, generator=g, device="cuda") / 16).to(torch.bfloat16)
+    ids = (torch.arange(T, device="cuda") % (n + 1) - 1).int()
+    scale = torch.rand(n, generator=g, device="cuda")
+
+    def made(rows, cols, out):  # rows x cols as one expert's products
+        off, cnt = torch.zeros(1, dtype=torch.int32, device="cuda"), torch.tensor([rows], dtype=torch.int32, device="cuda")
+        x, w = draw(rows, 4096), draw(1, cols, 4096)
+        return lambda: M.moe_expert_linear(x, w, off, cnt, out=out)
+
+    x, w = torch.empty(T, K, dtype=torch.bfloat16, device="cuda"), torch.empty(N, K, dtype=torch.bfloat16, device="cuda")
+    a, b = (torch.empty(*s, dtype=torch.bfloat16, device="cuda") for s in ((n * R, K), (n * N, R)))
+    calls = [made(T, K, x), made(n * R, K, a), made(n * N, R, b), made(N, K, w)]
+    run = lambda: M.moe_adapter_linear(x, w, a.view(n, R, K), b.view(n, N, R), ids, scale, act="swiglu")
+    for c in calls:
+        c()
+    torch.cuda.synchronize()
+    want = run()
+    for order in (calls, calls[::-1]):
+        for t in (x, w, a, b):
+            t.fill_(float("nan"))
+        for c in order:
+            c()
+        assert torch.equal(run(), want)
+
+
 def test_adapter_linear_empty_batch(M):
     c = draw_adapter(4, 64, 64, 8, 2, "mix")
     e = torch.empty(0, 64, dtype=torch.bfloat16, device="cuda")
