@@ -254,7 +254,7 @@ __global__ void __launch_bounds__(kGroupRouteWarps * 32) group_route_kernel(cons
     for (int s = 0; s < EPL; ++s) {
       const float sc = SOFTMAX ? e[s] * inv : __fdividef(1.f, 1.f + __expf(fminf(-key[s], 80.f)));
       key[s] = sc + bias[s];
-      if (isnan(key[s])) key[s] = -inf;
+      if (num[s] < 0 || isnan(key[s])) key[s] = -inf;
     }
   }
 
@@ -308,7 +308,7 @@ __global__ void __launch_bounds__(kGroupRouteWarps * 32) group_route_kernel(cons
         } else {
           // the values that may be among a group's best, again in 64 bits
           const float need = two ? b2 : b1;
-          const float lim = need > -inf ? need - (doubt + 4.7683716e-7f * fabsf(need)) : need;
+          const float lim = fabsf(need) < inf ? need - (doubt + 4.7683716e-7f * fabsf(need)) : need;
           int n = 0;
           for (int j = 0; j < (size + P - 1) / P; ++j) {
             const int i = g * size + j * P + sub;
@@ -370,14 +370,15 @@ __global__ void __launch_bounds__(kGroupRouteWarps * 32) group_route_kernel(cons
   int n = 0;
   if (!exactly) {
     // tau: the smallest of G >= k maxima over G groups of lanes is met by at
-    // least k keys, so every one of the k best is >= tau; what may be as good
-    // within the doubt is a candidate too
+    // least k keys, so every one of the k best is >= tau (places without an
+    // expert hold -inf and are in no group's way); what may be as good within
+    // the doubt is a candidate too.  An infinite tau is exact.
     float tau = key[0];
 #pragma unroll
     for (int s = 1; s < EPL; ++s) tau = fmaxf(tau, key[s]);
     for (int d = 1; d < 32 && 32 / (2 * d) >= p.k; d <<= 1) tau = fmaxf(tau, __shfl_xor_sync(0xFFFFFFFFu, tau, d));
     tau = order_value(__reduce_min_sync(0xFFFFFFFFu, order_key(tau)));
-    const float lim = BIAS && tau > -inf ? tau - (doubt + 4.7683716e-7f * fabsf(tau)) : tau;
+    const float lim = BIAS && fabsf(tau) < inf ? tau - (doubt + 4.7683716e-7f * fabsf(tau)) : tau;
     unsigned bal[EPL];
 #pragma unroll
     for (int s = 0; s < EPL; ++s)

@@ -164,6 +164,24 @@ def test_group_route_ties_and_rows_without_numbers(M, scores, bias, E, G, TG, k)
         check_route(M, lg, k, dict(bias=b, n_group=G, topk_group=TG, group_top=2, scores=scores, renormalize=renorm))
 
 
+@pytest.mark.parametrize("scores", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("E,G,TG", [(4, 1, 1), (5, 1, 1), (31, 1, 1), (33, 1, 1), (36, 4, 2), (65, 1, 1), (96, 6, 4),
+                                    (129, 1, 1), (260, 1, 1), (260, 13, 4)])
+def test_group_route_biases_of_any_size_and_all_experts_chosen(M, scores, E, G, TG):
+    # choice values below 0 and infinite ones, with fewer experts than lanes hold; k up to every live expert
+    rng = np.random.default_rng([204, E, G])
+    lg = rng.standard_normal((9, E)).astype(np.float32)
+    lg[5] = -np.inf
+    lg[6, ::2] = np.inf
+    most = min(32, E // G * TG)
+    some = np.where(np.arange(E) % 3 == 0, np.inf, rng.standard_normal(E)).astype(np.float32)
+    for b in (rng.standard_normal(E).astype(np.float32) - 3, np.full(E, np.inf, np.float32), np.full(E, -np.inf, np.float32),
+              some, -some, np.full(E, 3e38, np.float32), np.full(E, -3e38, np.float32)):
+        for k in sorted({1, (most + 1) // 2, most}):
+            for top in (1, 2):
+                check_route(M, lg, k, dict(bias=b, n_group=G, topk_group=TG, group_top=top, scores=scores))
+
+
 def test_group_route_equals_the_topk_route(M):
     lg = devn(np.random.default_rng(203).standard_normal((50, 256)).astype(np.float32))
     ids, w = M.moe_group_topk_route(lg, 8, 2.5, scores="softmax")
