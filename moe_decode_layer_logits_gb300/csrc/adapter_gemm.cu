@@ -8,13 +8,17 @@
 //    adds the pieces in order, expands each token's low-rank product against its
 //    own B in FP32, applies the activation and rounds once.  It starts while the
 //    first runs and requests the B rows into the L2 meanwhile.  Bound by the
-//    weights' bytes and, at this size, by the latency of two launches.
+//    weights' bytes and, at this size, by the latency of two launches (K = 6144,
+//    N = 4096, R = 16, T = 1: 13.4 us for 7.5 us of bytes; K = 2048, N = 6144,
+//    T = 64, 64 adapters: 13.7 for 5.3).
 //  - more tokens: the tokens are sorted by adapter (segments start on multiples
 //    of 16 rows), the low-rank products are the expert products of A (kLow),
 //    and the shared projection runs in CTA pairs over the sorted rows with the
 //    adapters' B as further K blocks of their own columns (kScatter).  A tile of
 //    256 rows reads the shared weights once however many adapters it holds.
-//    Bound by the tensor cores.
+//    Bound by the tensor cores (K = 6144, N = 4096 SwiGLU, R = 64, T = 4096,
+//    8 adapters: 204 us, 1037 TFLOP/s, of which the sort takes 8, the low-rank
+//    products 38).
 #include "expert_gemm.cuh"
 #include "expert_map.h"
 
@@ -22,9 +26,13 @@ namespace moe {
 
 namespace {
 
-// Few tokens: one row tile, or as many as keep the low-rank products (a warp
-// each) behind the weights' stream.
-bool few_form(int64_t T, int R) { return T <= kSoloRows || (T <= 512 && T * R <= 8192); }
+// Few tokens: while the low-rank products (a warp each, and B read by each
+// token) and the FP32 partial tiles cost less than the sort and the two further
+// products.  64 adapters in use, few / many: K = 2048, N = 6144, T = 64 R = 16
+// 14 / 65 us, T = 256 R = 64 58 / 69, T = 1024 R = 16 78 / 81, T = 64 R = 128
+// 76 / 88, T = 16 R = 256 90 / 68; K = 7168, N = 18432, R = 16, T = 256 120 / 207,
+// T = 512 231 / 218, T = 1024 R = 8 429 / 260.
+bool few_form(int64_t T, int64_t N, int R) { return T * N <= 1 << 23 && T * R <= (R <= 128 ? 16384 : 2048); }
 
 struct FinishParams {
   const float* partial;
@@ -335,11 +343,11 @@ cudaError_t many_tokens(const AdapterLinear& g, cudaStream_t stream) {
 
 int64_t adapter_workspace(int64_t T, int64_t N, int64_t K, int R, int L) {
   (void)K;
-  return static_cast<int64_t>(few_form(T, R) ? Few(T, N, R).bytes : Many(T, R, L).bytes);
+  return static_cast<int64_t>(few_form(T, N, R) ? Few(T, N, R).bytes : Many(T, R, L).bytes);
 }
 
 cudaError_t launch_adapter_linear(const AdapterLinear& g, cudaStream_t stream) {
-  if (few_form(g.T, g.R)) return g.swiglu ? few_tokens<true>(g, stream) : few_tokens<false>(g, stream);
+  if (few_form(g.T, g.N, g.R)) return g.swiglu ? few_tokens<true>(g, stream) : few_tokens<false>(g, stream);
   return g.swiglu ? many_tokens<true>(g, stream) : many_tokens<false>(g, stream);
 }
 

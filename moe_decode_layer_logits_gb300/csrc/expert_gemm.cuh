@@ -37,6 +37,15 @@
 // as FP32 partial tiles, and a second small kernel adds them in order (no
 // atomics: the same inputs give the same bits).  Pairs take whole tiles.
 //
+// Measured, SwiGLU, 256 experts of K = 6144, N = 4096, 8 a token, token list:
+// T = 1 72 us (403 MB: 83% of the copy rate; the rest is launch, first stages
+// and the join), T = 64 1.56 ms and T = 512 1.81 ms (107 and 105%: reads alone
+// are faster than a copy), T = 4096 2.00 ms (96%), T = 8192 2.56 ms (1290
+// TFLOP/s); 64 experts, T = 16384, 3.79 ms (1740 TFLOP/s, 91% of the tensor
+// rate).  Weights' bytes bound it up to about 150 rows an expert, then the
+// stages' turn-around (about 0.33 us for 64 wide K blocks whatever the rows)
+// until the tiles are full.
+//
 // What becomes of the sums is the kernel's Out:
 //  - kRows    act, one rounding, row r of the output;
 //  - kLow     scaled by the segment, left as two BF16 parts (value and rest): the

@@ -451,6 +451,8 @@ ADAPTER = [  # T, N, K, R, L, ids
     (200, 272, 320, 32, 4, "runs"), (300, 512, 512, 64, 9, "mix"), (1000, 256, 264, 16, 8, "runs"),
     (513, 16, 8, 8, 2, "mix"), (128, 512, 256, 128, 1, "one"), (1100, 272, 192, 72, 300, "mix"), (33, 64, 64, 16, 1024, "each"),
     (2100, 128, 128, 40, 12, "runs"), (260, 128, 256, 136, 3, "none"),
+    (2048, 272, 136, 8, 40, "mix"), (2049, 272, 136, 8, 40, "mix"), (1400, 144, 264, 16, 7, "mix"), (8, 272, 256, 256, 3, "mix"),
+    (1, 64, 64, 256, 2, "one"), (9, 272, 264, 256, 3, "mix"), (200, 272, 320, 104, 4, "runs"), (130, 65536, 64, 8, 3, "mix"),
 ]
 
 
@@ -486,7 +488,7 @@ def test_adapter_linear(M, T, N, K, R, L_, ids, act):
     check_adapter(c, values(out), act, f"T={T} N={N} K={K} R={R} L={L_} {ids}")
 
 
-@pytest.mark.parametrize("T", [5, 90, 400])
+@pytest.mark.parametrize("T", [5, 90, 400, 1100])
 def test_adapter_linear_ids_outside(M, T):
     c = draw_adapter(T, 144, 136, 16, 4, "mix")
     c["ids"][1], c["ids"][-1], c["ids"][2] = 4, 2 ** 31 - 1, -2 ** 31
@@ -495,7 +497,7 @@ def test_adapter_linear_ids_outside(M, T):
     check_adapter(c, values(out), None, "outside")
 
 
-@pytest.mark.parametrize("T", [3, 100, 600])
+@pytest.mark.parametrize("T", [3, 100, 600, 1100])
 def test_adapter_of_another_token_does_not_leak(M, T):
     # NaN and infinities in one adapter, and in one token, reach the tokens they belong to only
     c = draw_adapter(T, 144, 136, 16, 3, "mix")
@@ -535,7 +537,7 @@ def test_adapter_linear_offsets_beyond_31_bits(M, T):
     assert torch.equal(M.moe_adapter_linear(x, w, a, b, ids, scale), want)
 
 
-@pytest.mark.parametrize("T", [1, 40, 200, 600])
+@pytest.mark.parametrize("T", [1, 40, 200, 600, 1000])
 def test_adapter_linear_same_bits_again_and_with_a_given_workspace(M, T):
     c = draw_adapter(T, 272, 328, 24, 7, "mix")
     a, _ = run_adapter(M, c, "swiglu")
@@ -545,7 +547,7 @@ def test_adapter_linear_same_bits_again_and_with_a_given_workspace(M, T):
         assert torch.equal(a, b)
 
 
-@pytest.mark.parametrize("T", [1, 40, 300])
+@pytest.mark.parametrize("T", [1, 40, 300, 2100])
 def test_adapter_linear_reads_what_the_kernels_before_it_wrote(M, T):
     # the weights, the tokens and an adapter's tables are outputs of calls just made on the stream
     K, N, R, n = 512, 768, 8, 3
@@ -613,7 +615,8 @@ def draw_whole(T, H, I, E, k, block, seed=0):
     return {**c, **f}, {**{n: dev(v) for n, v in c.items()}, **{n: devn(v) for n, v in f.items()}}, dict(E=E, k=k, block=block)
 
 
-@pytest.mark.parametrize("T,H,I,E,k,block", [(1, 512, 128, 16, 4, 1), (28, 264, 136, 24, 3, 16), (300, 256, 128, 16, 4, 1)])
+@pytest.mark.parametrize("T,H,I,E,k,block", [(1, 512, 128, 16, 4, 1), (28, 264, 136, 24, 3, 16), (300, 256, 128, 16, 4, 1),
+                                               (1100, 128, 72, 16, 4, 1)])
 def test_layer_step_by_step(M, T, H, I, E, k, block):
     """The operators as a layer uses them, each step against its definition on
     the GPU's own inputs of that step."""
@@ -641,7 +644,7 @@ def test_layer_step_by_step(M, T, H, I, E, k, block):
     check_bf16(f"layer T={T} normed", host16(o["no"]), ref["normed"], ref["normed64"], dn)
 
 
-@pytest.mark.parametrize("T", [1, 40, 300])
+@pytest.mark.parametrize("T", [1, 40, 300, 1100])
 def test_layer_captured_and_replayed(M, T):
     _, g, p = draw_whole(T, 256, 128, 16, 4, 1)
     eager = layer(M, g, p)
@@ -670,7 +673,7 @@ def test_layer_captured_and_replayed(M, T):
         assert torch.equal(fresh[name], out[name]), name
 
 
-@pytest.mark.parametrize("T", [2, 60])
+@pytest.mark.parametrize("T", [2, 60, 1100])
 def test_layers_on_two_streams_at_once(M, T):
     _, g, p = draw_whole(T, 512, 256, 16, 4, 1)
     want = layer(M, g, p)
@@ -718,7 +721,7 @@ def test_workspaces_of_two_graphs_are_apart(M):
 
 
 @pytest.mark.parametrize("call", ["route", "map", "expert", "adapter"])
-@pytest.mark.parametrize("T", [2, 300])
+@pytest.mark.parametrize("T", [2, 300, 1100])
 def test_refused_launch_is_reported_and_the_next_call_is_clean(M, call, T):
     _, g, p = draw_whole(T, 256, 128, 16, 4, 1)
     o = layer(M, g, p)
