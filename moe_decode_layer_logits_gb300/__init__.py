@@ -207,8 +207,6 @@ def _opt(t, dtype, name, shape, device):
 def _out(t, dtype, name, shape, device):
     """An output and its pointer: the one given, checked, or a new one."""
     if t is None:
-        if min(shape) < 0:
-            raise ValueError(f"{name} cannot have the shape {list(shape)}")
         t = torch.empty(shape, dtype=dtype, device=device)
         return t, t.data_ptr()
     return t, _arg(t, dtype, name, shape, device)
@@ -227,6 +225,8 @@ def moe_group_topk_route(logits, k, routed_scale, bias=None, n_group=1, topk_gro
     if logits.dim() != 2:
         raise ValueError("logits must have 2 dimensions")
     (T, E), k, device = logits.shape, int(k), logits.device
+    if k < 0:
+        raise ValueError(f"k cannot be {k}")
     lg, bs = _arg(logits, torch.float32, "logits", (T, E), device), _opt(bias, torch.float32, "bias", (E,), device)
     score_fn = _choice(_SCORES, scores, "scores")
     handle, on = _enter(device, stream)
@@ -260,23 +260,16 @@ def moe_expert_map(topk_ids, E, block=1, n_rows=None, row_map=None, row_token=No
     (T, k), E, block, device = topk_ids.shape, int(E), int(block), topk_ids.device
     if n_rows is None:
         n_rows = moe_expert_rows(T, E, k, block) if row_token is None else row_token.numel()
+    if n_rows < 0 or E < 0:
+        raise ValueError(f"n_rows and E cannot be {n_rows} and {E}")
     ids = _arg(topk_ids, torch.int32, "topk_ids", (T, k), device)
     handle, on = _enter(device, stream)
     try:
-        if row_map is None and row_token is None and offsets is None and counts is None:
-            # one allocation, row_token first (its fill wants 16-byte alignment)
-            buf = torch.empty(n_rows + T * k + 2 * E + 1, dtype=torch.int32, device=device)
-            row_token, row_map, offsets, counts = buf.split((n_rows, T * k, E + 1, E))
-            row_map = row_map.view(T, k)
-            tok = buf.data_ptr()
-            rm = tok + 4 * n_rows
-            off = rm + 4 * T * k
-            cnt = off + 4 * (E + 1)
-        else:
-            row_map, rm = _out(row_map, torch.int32, "row_map", (T, k), device)
-            row_token, tok = _out(row_token, torch.int32, "row_token", (n_rows,), device)
-            offsets, off = _out(offsets, torch.int32, "offsets", (E + 1,), device)
-            counts, cnt = _out(counts, torch.int32, "counts", (E,), device)
+        # (four allocations: views of one take longer to make than they save)
+        row_map, rm = _out(row_map, torch.int32, "row_map", (T, k), device)
+        row_token, tok = _out(row_token, torch.int32, "row_token", (n_rows,), device)
+        offsets, off = _out(offsets, torch.int32, "offsets", (E + 1,), device)
+        counts, cnt = _out(counts, torch.int32, "counts", (E,), device)
         st = lib().moe_expert_map(ids, rm, tok, off, cnt, n_rows, T, E, k, block, handle)
     finally:
         if on is not None:
