@@ -555,7 +555,7 @@ expert_gemm_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_cons
 
   if (warp == 0) {
     // -------------------------------------------------------------- loads
-    if (lane == 0) {  // one lane walks and copies
+    if (elect_one()) {  // one lane walks and copies
       const uint64_t once = l2_evict_first_policy(), keep = l2_evict_normal_policy();
       const int withheld = who == 0 ? p.withhold : -1;
       auto load_weights = [&](const CUtensorMap* map, uint32_t dst, int kb, int m, int e, uint32_t bar, uint64_t pol) {
@@ -643,7 +643,7 @@ expert_gemm_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_cons
     __syncwarp();
   } else if (warp == 1) {
     // ---------------------------------------------------------------- MMA
-    if (lane == 0 && rank == 0) {
+    if (rank == 0 && elect_one()) {
       int at = 0;
       Piece w;
       const uint32_t a0 = desc_low(smem_addr(ring)), step = static_cast<uint32_t>(stage_bytes) >> 4;

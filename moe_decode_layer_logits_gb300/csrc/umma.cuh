@@ -177,6 +177,20 @@ __device__ __forceinline__ uint64_t l2_evict_normal_policy() {
   return pol;
 }
 
+// True in one lane of the warp (all 32 call it).  Behind it the compiler knows
+// that one thread runs; behind a comparison of the lane's number it issues each
+// tensor-core or copy instruction from a loop over the threads that may be
+// there.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t one;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xFFFFFFFF;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(one));
+  return one != 0;
+}
+
 // Bounded wait; gives up early once the abort flag is raised unless `drain`
 // is set (a drain must see the phase, abort or not).
 __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag, bool drain = false) {
