@@ -9,15 +9,15 @@
 //    own B in FP32, applies the activation and rounds once.  It starts while the
 //    first runs and requests the B rows into the L2 meanwhile.  Bound by the
 //    weights' bytes and, at this size, by the latency of two launches (K = 6144,
-//    N = 4096, R = 16, T = 1: 13.4 us for 7.5 us of bytes; K = 2048, N = 6144,
-//    T = 64, 64 adapters: 13.7 for 5.3).
+//    N = 4096, R = 16, T = 1: 13 us for 7.5 us of bytes; K = 2048, N = 6144,
+//    T = 64, 64 adapters: 12.9 for 5.3).
 //  - more tokens: the tokens are sorted by adapter (segments start on multiples
 //    of 16 rows), the low-rank products are the expert products of A (kLow),
 //    and the shared projection runs in CTA pairs over the sorted rows with the
 //    adapters' B as further K blocks of their own columns (kScatter).  A tile of
 //    256 rows reads the shared weights once however many adapters it holds.
 //    Bound by the tensor cores (K = 6144, N = 4096 SwiGLU, R = 64, T = 4096,
-//    8 adapters: 204 us, 1037 TFLOP/s, of which the sort takes 8, the low-rank
+//    8 adapters: 175 us, 1209 TFLOP/s, of which the sort takes 8, the low-rank
 //    products 38).
 #include "expert_gemm.cuh"
 #include "expert_map.h"

@@ -10,8 +10,8 @@ std::atomic<int> g_withheld{-1};
 
 // Pairs from a mean of this many rows an expert, the batch size divided over all
 // of them (no device value decides on the host).  gate_up, E = 256, K = 6144,
-// N = 4096: at a mean of 64 both forms take 1955 us, at 93 they take 1968
-// (single) and 1975; at 128 single CTAs take 2410 us and pairs 2000.
+// N = 4096, single CTAs / pairs: a mean of 93 rows 1950 / 1951 us, 112 1943 / 1959,
+// 128 2188 / 1968; E = 8, a mean of 125 116 / 108.
 constexpr int64_t kPairMeanRows = 96;
 
 template <bool SWIGLU>
@@ -37,8 +37,8 @@ cudaError_t prepare_and_launch(const ExpertGemm& g, cudaStream_t stream) {
   CUtensorMap mx, mw;
   if (!weight_map(&mw, g.w, g.E, g.N, g.K, SWIGLU, p.weave)) return cudaErrorInvalidValue;
   // pairs copy the rows by their own warps, with a token list or without (four
-  // tiled copies a stage beside the weights': 3.01 ms at T = 8192, E = 256 where
-  // the warps take 2.58)
+  // tiled copies a stage beside the weights' were slower by a sixth at T = 8192,
+  // E = 256)
   if (g.n_rows / g.E >= kPairMeanRows) return launch<SWIGLU, true, true, kRows>(mw, mw, mw, p, stream);
   if (g.row_token) return launch<SWIGLU, true, false, kRows>(mw, mw, mw, p, stream);
   if (!row_map_of(&mx, g.x, g.n_x, g.K)) return cudaErrorInvalidValue;

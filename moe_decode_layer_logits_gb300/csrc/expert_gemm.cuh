@@ -13,7 +13,9 @@
 //  - warp 1 owns the tensor memory, two accumulators of 256 columns, and one
 //    lane issues the MMAs;
 //  - warps 2..5 read the finished accumulator while the next tile's MMAs run,
-//    apply the activation to the FP32 sums and store BF16 once;
+//    apply the activation to the FP32 sums and store BF16 once (in pairs, whose
+//    tiles have more columns, warps 11..14 too: with four warps the MMAs waited
+//    for them a tenth of the time, adapter T = 4096 177 us against 170);
 //  - with a token list the rows are gathered by warps 6..9 with 16-byte
 //    asynchronous copies (eight lanes a row of the stage) that arrive on the
 //    stage's own barrier as they land, and warp 10 passes that on behind a proxy
@@ -38,13 +40,14 @@
 // atomics: the same inputs give the same bits).  Pairs take whole tiles.
 //
 // Measured, SwiGLU, 256 experts of K = 6144, N = 4096, 8 a token, token list:
-// T = 1 72 us (403 MB: 83% of the copy rate; the rest is launch, first stages
+// T = 1 70 us (403 MB: 85% of the copy rate; the rest is launch, first stages
 // and the join), T = 64 1.56 ms and T = 512 1.81 ms (107 and 105%: reads alone
-// are faster than a copy), T = 4096 2.00 ms (96%), T = 8192 2.56 ms (1290
-// TFLOP/s); 64 experts, T = 16384, 3.79 ms (1740 TFLOP/s, 91% of the tensor
-// rate).  Weights' bytes bound it up to about 150 rows an expert, then the
-// stages' turn-around (about 0.33 us for 64 wide K blocks whatever the rows)
-// until the tiles are full.
+// are faster than a copy), T = 4096 1.97 ms (98%), T = 8192 uneven 2.43 ms
+// (1360 TFLOP/s, 81% of the copy rate); 64 experts, T = 16384, 3.57 ms (1850
+// TFLOP/s, 97% of the tensor rate).  Weights' bytes bound it up to about 150
+// rows an expert, the tensor cores where tiles are full; between them both
+// matter (a stage turns around in 0.21 us or more whatever its rows, and loads
+// that miss the L2 come later than that).
 //
 // What becomes of the sums is the kernel's Out:
 //  - kRows    act, one rounding, row r of the output;
@@ -87,8 +90,9 @@ constexpr int kLowWarps = 8;    // kParts: warps that compute low-rank products
 
 enum Out { kRows, kLow, kParts, kScatter };
 
-constexpr int threads_of(bool gather, Out out) {
-  return 192 + (gather ? 32 * (kLoaders + 1) : 0) + (out == kParts ? 32 * kLowWarps : 0);
+// Pairs have a second set of epilogue warps, behind the others.
+constexpr int threads_of(bool gather, bool pair, Out out) {
+  return 192 + (gather ? 32 * (kLoaders + 1) : 0) + (out == kParts ? 32 * kLowWarps : 0) + (pair ? 128 : 0);
 }
 
 struct GemmParams {
@@ -483,7 +487,7 @@ expert_gemm_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_cons
     mbar_init_fence();
   } else if (threadIdx.x < kMaxStages + 2) {
     mbar_init(&sb.acc_full[threadIdx.x - kMaxStages], 1);
-    mbar_init(&sb.acc_empty[threadIdx.x - kMaxStages], PAIR ? 8 : 4);
+    mbar_init(&sb.acc_empty[threadIdx.x - kMaxStages], PAIR ? 16 : 4);
     mbar_init_fence();
   } else if (threadIdx.x == kMaxStages + 2) {
     mbar_init(&sb.drained, 1);
@@ -693,7 +697,7 @@ expert_gemm_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_cons
       mma_commit<PAIR>(&sb.drained);  // also after an abort: fires once the issued MMAs are done
     }
     __syncwarp();
-  } else if (warp < 6) {
+  } else if (warp < 6 || (PAIR && warp > 6 + kLoaders)) {
     // ----------------------------------------------------------- epilogue
     const int q = warp & 3;  // this warp's quarter of the tensor-memory lanes
     if (OUT == kParts) grid_dependency_wait();
@@ -709,7 +713,7 @@ expert_gemm_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_cons
       const uint32_t d = tmem + acc * kAccCols + (static_cast<uint32_t>(q * 32) << 16);
       float* part = p.partial + static_cast<int64_t>(w.part) * p.slot_rows * kBM + q * 32 + lane;
 #pragma unroll 1
-      for (int c = 0; c < w.nr; c += 32) {
+      for (int c = PAIR && warp >= 6 ? 32 : 0; c < w.nr; c += PAIR ? 64 : 32) {  // two sets of warps take turns
         uint32_t raw[32];
         tmem_ld32(d + static_cast<uint32_t>(c), raw);
         if (OUT == kParts || w.part >= 0) {
@@ -1020,7 +1024,7 @@ cudaError_t launch(const CUtensorMap& mx, const CUtensorMap& mw, const CUtensorM
   const int G = PAIR ? gemm_ctas() / 2 * 2 : gemm_ctas();
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(G), 1, 1);
-  cfg.blockDim = dim3(threads_of(GATHER, OUT), 1, 1);
+  cfg.blockDim = dim3(threads_of(GATHER, PAIR, OUT), 1, 1);
   cfg.dynamicSmemBytes = launch_smem(gemm_smem(p.E, p.segs, p.ring_bytes));
   cfg.stream = stream;
   cudaLaunchAttribute attr[2] = {pdl_attribute(), {}};
