@@ -648,6 +648,9 @@ expert_gemm_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_cons
   } else if (warp == 1) {
     // ---------------------------------------------------------------- MMA
     if (rank == 0 && elect_one()) {
+      // before the first bounded wait, whose probes are for this kernel's own
+      // loads: those begin behind the previous kernel, which may run long
+      if (OUT == kParts) grid_dependency_wait();
       int at = 0;
       Piece w;
       const uint32_t a0 = desc_low(smem_addr(ring)), step = static_cast<uint32_t>(stage_bytes) >> 4;
