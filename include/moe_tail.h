@@ -281,6 +281,12 @@ int64_t moe_expert_linear_workspace(int64_t n_rows, int64_t E, int64_t N, int64_
  *             preparation and mean nothing afterwards; two calls that may run
  *             at the same time need one each.
  *   err_flag  device int32 or NULL (MOE_FLAG_BAD_INDEX, MOE_FLAG_TIMEOUT)
+ *
+ * Every wait inside the kernels is bounded (2^21 probes).  If one runs out,
+ * what its thread block (or pair) had left to compute is written as NaN, the
+ * rest is right, MOE_FLAG_TIMEOUT is OR-ed into *err_flag and the call still
+ * returns MOE_OK, as the launch was made.
+ *
  *   n_rows >= 0 and < 2^31; 1 <= E <= MOE_MAX_E; 8 <= N, K <= MOE_MAX_DIM;
  *   K % 8 == 0; N % 8 == 0 (N % 16 == 0 with SwiGLU).
  */
@@ -313,7 +319,8 @@ int64_t moe_adapter_linear_workspace(int64_t T, int64_t N, int64_t K, int32_t R,
  *   out_bf16       [T, N or N/2] BF16, written; must not overlap any input
  *   workspace      device memory of at least moe_adapter_linear_workspace()
  *                  bytes, 16-byte aligned; as in moe_expert_linear
- *   err_flag       device int32 or NULL (MOE_FLAG_BAD_INDEX, MOE_FLAG_TIMEOUT)
+ *   err_flag       device int32 or NULL (MOE_FLAG_BAD_INDEX; MOE_FLAG_TIMEOUT
+ *                  and NaN as in moe_expert_linear)
  *   T >= 0; N and K as in moe_expert_linear; R % 8 == 0, 8 <= R <=
  *   MOE_MAX_RANK; 1 <= L <= MOE_MAX_ADAPTERS; T * R < 2^31.
  */
@@ -349,12 +356,13 @@ int moe_debug_withhold_stream_stage(int32_t stage);
 int moe_debug_withhold_router_stage(int32_t kb);
 
 /*
- * Test hook of the bounded waits of the expert products; no counterpart on
- * the pages.  The next launch of the product kernel issues no loads for K
- * block `stage` (counted over all tiles of that thread block) in its first thread block, so
- * that block gives up after its bounded wait: MOE_FLAG_TIMEOUT is set, the
- * launch completes, its outputs are invalid, and the next launch is
- * unaffected.  stage -1 cancels the request.  Returns MOE_OK, or
+ * Test hook of the bounded waits of the expert and adapter products; no
+ * counterpart on the pages.  The product launches of the next
+ * moe_expert_linear or moe_adapter_linear call issue no loads for K block
+ * `stage` (counted over all tiles of that thread block) in their first thread
+ * block, so that block gives up after its bounded wait: what it had left to
+ * compute is written as NaN, MOE_FLAG_TIMEOUT is set, the launch completes,
+ * and the next call is unaffected.  stage -1 cancels the request.  Returns MOE_OK, or
  * MOE_ERR_INVALID_ARG for stage < -1.  Not for production use.
  */
 int moe_debug_withhold_expert_stage(int32_t stage);

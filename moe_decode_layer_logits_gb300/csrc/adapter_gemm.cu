@@ -265,7 +265,7 @@ cudaError_t few_tokens(const AdapterLinear& g, cudaStream_t stream) {
   // need more of the SM's memory
   p.ring_bytes = g.R > 16 ? kRingBytes - 72 * 1024 : kRingBytes;
   p.weave = SWIGLU && p.n_out % 16 == 0;
-  p.withhold = -1;
+  p.withhold = take_withheld_stage();
   p.scale = g.scale;
   p.a = g.a;
   p.ids = g.ids;
@@ -316,7 +316,7 @@ cudaError_t many_tokens(const AdapterLinear& g, cudaStream_t stream) {
   p.K = static_cast<int>(g.K);
   p.slot_rows = slot_rows_of(f.n_rows);
   p.ring_bytes = kRingBytes;
-  p.withhold = -1;
+  p.withhold = take_withheld_stage();
   p.scale = g.scale;
   for (int i = 0; i < 2; ++i) p.low[i] = reinterpret_cast<uint16_t*>(g.workspace + f.low[i]);
   CUtensorMap ma, mw, mb;

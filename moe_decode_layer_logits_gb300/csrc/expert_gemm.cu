@@ -5,8 +5,7 @@ namespace moe {
 
 namespace {
 
-// Test hook of the bounded waits: the stage that the next launch withholds.
-std::atomic<int> g_withheld{-1};
+std::atomic<int> g_withheld{-1};  // take_withheld_stage()
 
 // Pairs from a mean of this many rows an expert, the batch size divided over all
 // of them (no device value decides on the host).  gate_up, E = 256, K = 6144,
@@ -32,7 +31,7 @@ cudaError_t prepare_and_launch(const ExpertGemm& g, cudaStream_t stream) {
   p.slot_rows = slot_rows_of(g.n_rows);
   p.ring_bytes = kRingBytes;
   p.weave = SWIGLU && p.n_out % 16 == 0;
-  p.withhold = g_withheld.exchange(-1);
+  p.withhold = take_withheld_stage();
 
   CUtensorMap mx, mw;
   if (!weight_map(&mw, g.w, g.E, g.N, g.K, SWIGLU, p.weave)) return cudaErrorInvalidValue;
@@ -46,6 +45,8 @@ cudaError_t prepare_and_launch(const ExpertGemm& g, cudaStream_t stream) {
 }
 
 }  // namespace
+
+int take_withheld_stage() { return g_withheld.exchange(-1); }
 
 int64_t expert_gemm_workspace(int64_t n_rows) {
   return n_rows <= 0 ? 0 : static_cast<int64_t>(gemm_ctas()) * 2 * slot_rows_of(n_rows) * umma::kBM * 4;

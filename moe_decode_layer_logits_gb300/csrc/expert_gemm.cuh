@@ -694,6 +694,7 @@ expert_gemm_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_cons
             }
           }
         }
+        if (stop) break;  // (a peer's epilogue must not take half a sum for a whole one)
         mma_commit<PAIR>(&sb.acc_full[acc]);
         ++seq;
       }
@@ -707,18 +708,26 @@ expert_gemm_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_cons
     int at = 0;
     Piece w;
     int seq = 0;
+    bool dead = false;  // a wait ran out: this and all later pieces are left as NaN
     while (next(at, w)) {
       const int acc = seq & 1, use = seq >> 1;
       ++seq;
-      const bool ok = wait(&sb.acc_full[acc], use & 1, abort_v) && !*abort_v;
-      if (!__all_sync(0xFFFFFFFFu, ok)) break;
+      if (!dead) {
+        const bool ok = wait(&sb.acc_full[acc], use & 1, abort_v) && !*abort_v;
+        dead = !__all_sync(0xFFFFFFFFu, ok);
+      }
       fence_after_sync();
       const uint32_t d = tmem + acc * kAccCols + (static_cast<uint32_t>(q * 32) << 16);
       float* part = p.partial + static_cast<int64_t>(w.part) * p.slot_rows * kBM + q * 32 + lane;
 #pragma unroll 1
       for (int c = PAIR && warp >= 6 ? 32 : 0; c < w.nr; c += PAIR ? 64 : 32) {  // two sets of warps take turns
         uint32_t raw[32];
-        tmem_ld32(d + static_cast<uint32_t>(c), raw);
+        if (!dead) {
+          tmem_ld32(d + static_cast<uint32_t>(c), raw);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 32; ++i) raw[i] = 0x7FC00000u;
+        }
         if (OUT == kParts || w.part >= 0) {
 #pragma unroll
           for (int i = 0; i < 32; ++i)
@@ -732,7 +741,7 @@ expert_gemm_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_cons
       }
       fence_before_sync();
       __syncwarp();
-      if (lane == 0) {
+      if (lane == 0 && !dead) {
         if (PAIR) arrive_cluster(acc_empty0 + acc * 8);
         else mbar_arrive(&sb.acc_empty[acc]);
       }

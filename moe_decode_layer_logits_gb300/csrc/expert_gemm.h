@@ -24,6 +24,10 @@ int64_t expert_gemm_workspace(int64_t n_rows);
 
 cudaError_t launch_expert_gemm(const ExpertGemm& g, cudaStream_t stream);
 
+// Test hook of the bounded waits: the stage that the next call's product
+// launches withhold, or -1; taking it clears it.
+int take_withheld_stage();
+
 // MOE_OK if N, K and act are sizes that the products take.
 int check_linear(int64_t N, int64_t K, int32_t act);
 
