@@ -197,7 +197,8 @@ int moe_tail_fused(const float* logits, int64_t E, int32_t k, float routed_scale
  *   stay (n_group == 1: all experts)
  *   ids = the k largest c inside them, in descending order
  *   w_j = routed_scale * s[ids_j], divided by the sum of the k scores if
- *         renormalize is 1 (all zero where that sum is zero)
+ *         renormalize is 1 (all zero where that sum is zero; a score below
+ *         2^-1022 counts as zero)
  *
  * The bias moves the choice only, never the weights.  Without a bias (NULL)
  * the experts are ordered by their logits, of which s is a monotone function,

@@ -74,11 +74,10 @@ __device__ __forceinline__ float logit(float l) { return isnan(l) ? __int_as_flo
 __device__ __forceinline__ double sigmoid_f64(float l) { return 1.0 / (1.0 + exp(-static_cast<double>(l))); }
 
 // The choice of one token in 64 bits.  `sc` and `key` are E values each of
-// this warp's shared memory.  Lane j < k gets the j-th id and its score.  The
-// 64-bit pipe is narrow, so it computes the values, and their integer keys are
-// compared.
+// this warp's shared memory.  Lane j < k gets the j-th id.  The 64-bit pipe is
+// narrow, so it computes the values, and their integer keys are compared.
 __device__ __noinline__ void group_select_f64(const GroupRouteParams& p, const float* __restrict__ row, double* sc,
-                                              uint64_t* key, int& id, double& score) {
+                                              uint64_t* key, int& id) {
   const int lane = threadIdx.x & 31;
   const double inf = __longlong_as_double(0x7FF0000000000000ll);
   double m = -inf, sum = 1.0;
@@ -136,7 +135,6 @@ __device__ __noinline__ void group_select_f64(const GroupRouteParams& p, const f
   }
   // k rounds: the largest key, the lowest expert among equals
   id = 0;
-  score = 0.0;
   for (int r = 0; r < p.k; ++r) {
     uint64_t b = 0ull;
     int at = 0x7FFFFFFF;
@@ -150,7 +148,7 @@ __device__ __noinline__ void group_select_f64(const GroupRouteParams& p, const f
       const int oa = __shfl_xor_sync(0xFFFFFFFFu, at, off);
       if (ob > b || (ob == b && oa < at)) { b = ob; at = oa; }
     }
-    if (lane == r) { id = at; score = sc[at]; }
+    if (lane == r) id = at;
     __syncwarp();
     if (lane == 0) key[at] = 0ull;
     __syncwarp();
@@ -452,16 +450,21 @@ __global__ void __launch_bounds__(kGroupRouteWarps * 32) group_route_kernel(cons
       }
     }
   }
-  float w = 0.f;
   if (exactly) {
-    double s64;
     __syncwarp();
-    group_select_f64(p, row, reinterpret_cast<double*>(mem), reinterpret_cast<uint64_t*>(mem) + p.E, id, s64);
-    if (lane < p.k) w = static_cast<float>(s64);
-  } else if (lane < p.k) {
-    const float l = lv[id];
-    w = SOFTMAX ? (m == -inf ? 0.f : (l == m ? 1.f : expf(l - m)) * inv) : 1.f / (1.f + expf(-l));
+    group_select_f64(p, row, reinterpret_cast<double*>(mem), reinterpret_cast<uint64_t*>(mem) + p.E, id);
   }
+  // The weights, the same way whatever made the choice.  Divided by their sum,
+  // only the scores' ratios count: where the best chosen score is below e^-16
+  // they are taken relative to it, as scores of 32 bits end at e^-103 (and
+  // 1 / (1 + expf(-l)) at e^-88).  A score below 2^-1022 counts as 0.
+  const float l = lane < p.k ? (exactly ? logit(row[id]) : lv[id]) : -inf;
+  const float top = p.renorm ? order_value(__reduce_max_sync(0xFFFFFFFFu, order_key(l))) : inf;
+  const float ref = SOFTMAX ? m : 0.f;
+  float w;
+  if (top - ref < -16.f) w = l - ref < -708.39642f ? 0.f : expf(l - top) / (SOFTMAX ? 1.f : 1.f + expf(l));
+  else if (SOFTMAX) w = m == -inf ? 0.f : (l == m ? 1.f : expf(l - m)) * inv;
+  else w = l < -80.f ? expf(l) / (1.f + expf(l)) : 1.f / (1.f + expf(-l));
   if (p.renorm) {
     const float sum = warp_sum(w);
     w = sum > 0.f ? w / sum : 0.f;

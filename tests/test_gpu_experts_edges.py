@@ -8,9 +8,10 @@ import numpy as np
 import pytest
 import torch
 
+import oracle as O
 from _guard import Guarded, check_all
 from moe_decode_layer_logits_gb300 import _lib as L
-from test_gpu_experts import (M, check_adapter, dev, devn, draw_adapter, draw_layer, run_adapter, run_expert,  # noqa: F401
+from test_gpu_experts import (M, U, check_adapter, dev, devn, draw_adapter, draw_layer, run_adapter, run_expert,  # noqa: F401
                               values)
 
 pytestmark = pytest.mark.gpu
@@ -75,3 +76,61 @@ def test_adapter_linear_leaves_nan_where_a_wait_ran_out(M, T, few, act):
         assert not lost.all(1)[torch.from_numpy(c["ids"] < 0).cuda()].any()
     again, flag = run_adapter(M, c, act)
     assert flag == 0 and torch.equal(again, want)
+
+
+def check_weights(M, lg, k, kw, scale=2.5):
+    """ids and weights against the 64-bit definition, relative to each weight.
+    The argument of an exponential is a difference rounded by 2^-24 of its own
+    size, D at most (from the row's maximum, or from the best chosen logit
+    where that lies 16 below it; no difference for a sigmoid of 16 or less);
+    terms more than 745 down, -inf among them, are 0 in FP32 and FP64 alike and
+    have no rounding.  The rest as in test_gpu_experts.py.  1e-37: below FP32's normal numbers."""
+    ids, w = M.moe_group_topk_route(devn(lg), k, scale, **{**kw, "bias": None if kw.get("bias") is None else devn(kw["bias"])})
+    rids, rw = O.group_topk_route(lg, k, scale, **kw)
+    assert np.array_equal(ids.cpu().numpy(), rids)
+    z = np.take_along_axis(lg.astype(np.float64), rids.astype(np.int64), 1)
+    top = z.max(1, keepdims=True)
+    ref = lg.max(1, keepdims=True).astype(np.float64) if kw["scores"] == "softmax" else np.zeros_like(top)
+    with np.errstate(invalid="ignore"):
+        d = np.abs(z - np.where(top - ref < -16, top, ref))
+    D = np.where(d < 745, d, 0.0).max(1, keepdims=True)
+    tol = np.abs(rw) * U * (2 * (D + lg.shape[1] / 32 + 12) + k + 4) + 1e-37
+    assert np.all(np.abs(w.cpu().numpy() - rw) <= tol)
+    return rw
+
+
+@pytest.mark.parametrize("E,G,TG,k", [(64, 1, 1, 2), (64, 8, 3, 8), (256, 8, 4, 8), (1024, 32, 5, 32)])
+@pytest.mark.parametrize("bias", [False, True])
+def test_group_route_renormalised_weights_of_tiny_sigmoids(M, E, G, TG, k, bias):
+    rng = np.random.default_rng([301, E, k])
+    lg = rng.uniform(-120, -90, (16, E)).astype(np.float32)  # every score below the smallest FP32 number, or near it
+    lg[1] = -92
+    lg[2] = rng.uniform(-700, -695, E)
+    lg[3] = rng.uniform(-700, 0, E)
+    lg[4] = rng.uniform(-100, -15, E)
+    lg[5] = rng.uniform(-17, -15, E)
+    lg[6] = rng.uniform(-110, -80, E)
+    lg[7, ::5] = -np.inf
+    lg[8] = np.finfo(np.float32).min
+    lg[9, 3] = 1.0
+    lg[10] = rng.uniform(-95, 0, E)
+    b = (rng.standard_normal(E) * 0.1).astype(np.float32) if bias else None
+    for top in (1, 2):
+        kw = dict(bias=b, n_group=G, topk_group=TG, group_top=top, scores="sigmoid")
+        rw = check_weights(M, lg, k, {**kw, "renormalize": True})
+        assert np.allclose(rw[:8].sum(1), 2.5)              # (the definition has no zero rows there)
+        check_weights(M, lg, k, {**kw, "renormalize": False})
+
+
+@pytest.mark.parametrize("E,G,TG,k", [(64, 1, 1, 2), (64, 8, 3, 8), (256, 8, 4, 8), (512, 16, 3, 20)])
+def test_group_route_renormalised_weights_of_softmax_scores_far_below_the_largest(M, E, G, TG, k):
+    # the bias takes out the expert that has the mass; the chosen lie 20 to 700 below it
+    rng = np.random.default_rng([302, E, k])
+    lg = rng.standard_normal((12, E)).astype(np.float32)
+    for t, gap in enumerate([0, 10, 15.9, 16.1, 20, 60, 87, 95, 104, 150, 400, 690]):
+        lg[t, 5] = lg[t].max() + gap
+    b = (rng.standard_normal(E) * 0.1).astype(np.float32)
+    b[5] = -9.0
+    for top in (1, 2):
+        rw = check_weights(M, lg, k, dict(bias=b, n_group=G, topk_group=TG, group_top=top, scores="softmax", renormalize=True))
+        assert np.allclose(rw.sum(1), 2.5)
