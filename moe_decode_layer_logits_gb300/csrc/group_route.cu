@@ -297,10 +297,17 @@ __global__ void __launch_bounds__(kGroupRouteWarps * 32) group_route_kernel(cons
     }
     bool in = g < p.n_group && rank < p.topk_group;
     if (BIAS || p.group_top == 2) {  // otherwise the scores are logits, and exact
-      const unsigned last = __ballot_sync(0xFFFFFFFFu, g < p.n_group && rank == p.topk_group - 1);
-      const unsigned next = __ballot_sync(0xFFFFFFFFu, g < p.n_group && rank == p.topk_group);
-      const float lo = __shfl_sync(0xFFFFFFFFu, gs, __ffs(last) - 1), hi = __shfl_sync(0xFFFFFFFFu, gs, __ffs(next) - 1);
-      if (too_close(lo, hi, 2.f * doubt)) {
+      // A group's score is as uncertain as its values, whose roundings go by
+      // their own size (they may cancel in the sum): twice doubt / 2 and 2^-24
+      // of each value and of the sum.  A sum at the end of the range may
+      // stand for anything beyond it.
+      const float big = 3.4028235e38f;
+      const float err = doubt + 2.3841858e-7f * (fabsf(b1) + (two ? fabsf(b2) : 0.f));
+      const float low = gs == inf ? big : gs == -inf ? -inf : gs - err, high = gs == -inf ? -big : gs == inf ? inf : gs + err;
+      const bool group = g < p.n_group, stays = group && rank < p.topk_group;
+      const float lo = order_value(__reduce_min_sync(0xFFFFFFFFu, stays ? order_key(low) : 0xFFFFFFFFu));
+      const float hi = order_value(__reduce_max_sync(0xFFFFFFFFu, group && !stays ? order_key(high) : 0u));
+      if (!(lo > hi)) {
         if (SOFTMAX || !BIAS) {
           exactly = true;
         } else {

@@ -134,3 +134,27 @@ def test_group_route_renormalised_weights_of_softmax_scores_far_below_the_larges
     for top in (1, 2):
         rw = check_weights(M, lg, k, dict(bias=b, n_group=G, topk_group=TG, group_top=top, scores="softmax", renormalize=True))
         assert np.allclose(rw.sum(1), 2.5)
+
+
+@pytest.mark.parametrize("scores", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("size,G,TG,big", [(2, 8, 3, 1e4), (2, 16, 7, 3e5), (2, 4, 1, 300.0), (16, 8, 4, 1e5), (32, 8, 3, 2e6)])
+def test_group_route_group_scores_whose_large_biases_cancel(M, scores, size, G, TG, big):
+    # a group's two best choice values are +B + s and -B + s': each is rounded by
+    # up to 2^-24 B in 32 bits, while the groups' sums differ by the scores alone
+    rng = np.random.default_rng([303, size, G, int(big)])
+    E = size * G
+    lg = rng.standard_normal((200, E)).astype(np.float32)
+    b = np.full(E, -4 * big, np.float32)
+    for g in range(G):
+        B = np.float32(big * rng.uniform(0.9, 1.1))
+        b[g * size + rng.integers(size // 2)] = B
+        b[g * size + size // 2 + rng.integers(size - size // 2)] = -B
+    k = min(8, size * TG)
+    kw = dict(bias=b, n_group=G, topk_group=TG, group_top=2, scores=scores, renormalize=True)
+    check_weights(M, lg, k, kw)
+    # groups of which some are masked by the type's lowest value, or hold nothing but it
+    b[:size] = np.finfo(np.float32).min
+    b[size:size + 1] = np.finfo(np.float32).min
+    check_weights(M, lg, k, {**kw, "bias": b})
+    b[:size] = -np.inf
+    check_weights(M, lg, k, {**kw, "bias": b})
