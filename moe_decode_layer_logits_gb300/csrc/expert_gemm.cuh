@@ -165,6 +165,11 @@ __device__ __forceinline__ int scatter_tiles(int total, int mt, int G) {
   return best;
 }
 
+// Row tiles of 2^shift rows that hold `count` rows (up to 2^31 - 1 of them).
+__host__ __device__ inline int row_tiles(int count, int shift) {
+  return (count >> shift) + ((count & ((1 << shift) - 1)) != 0 ? 1 : 0);
+}
+
 // Fills the tile list; every thread of the block calls it.  Afterwards *bn_out
 // holds the rows per tile.
 template <bool PAIR, Out OUT>
@@ -223,12 +228,12 @@ __device__ void list_tiles(const GemmParams& p, Tiles t, int mt, int walkers, in
       // one for every five CTAs (fewer have too many pieces each to add)
       for (shift = 7; shift > 5; --shift) {
         int tiles = 0;
-        for (int i = b; i < e; ++i) tiles += (t.count[i] + (1 << shift) - 1) >> shift;
+        for (int i = b; i < e; ++i) tiles += row_tiles(t.count[i], shift);
         if (__reduce_add_sync(0xFFFFFFFFu, tiles) >= static_cast<int>(walkers) / 5) break;
       }
     }
     int mine = 0;
-    for (int i = b; i < e; ++i) mine += (t.count[i] + (1 << shift) - 1) >> shift;
+    for (int i = b; i < e; ++i) mine += row_tiles(t.count[i], shift);
     int upto = mine;
 #pragma unroll
     for (int off = 1; off < 32; off <<= 1) {
@@ -238,7 +243,7 @@ __device__ void list_tiles(const GemmParams& p, Tiles t, int mt, int walkers, in
     int at = upto - mine;
     for (int i = b; i < e; ++i) {
       t.before[i] = at;
-      at += (t.count[i] + (1 << shift) - 1) >> shift;
+      at += row_tiles(t.count[i], shift);
     }
     if (lane == 31) {
       t.before[p.E] = upto;
@@ -390,7 +395,7 @@ __device__ __forceinline__ void store_cols(const GemmParams& p, const Piece& w, 
     const float other = __shfl_xor_sync(0xFFFFFFFFu, second ? v[i] : v[i + 1], SWIGLU ? 16 : 1);
     const float a = second ? other : v[i], b = second ? v[i + 1] : other;
     const int r = second ? i + 1 : i;
-    int64_t row = w.r0 + c + r;
+    int64_t row = static_cast<int64_t>(w.r0) + c + r;
     bool live = r < left && o < p.n_out;
     if (OUT == kScatter) {
       const int t0 = __shfl_sync(0xFFFFFFFFu, static_cast<int>(aux), i);

@@ -11,7 +11,7 @@ import torch
 import oracle as O
 from _guard import Guarded, check_all
 from moe_decode_layer_logits_gb300 import _lib as L
-from test_gpu_experts import (M, U, check_adapter, dev, devn, draw_adapter, draw_layer, run_adapter, run_expert,  # noqa: F401
+from test_gpu_experts import (M, U, check_adapter, dev, devn, draw_adapter, draw_layer, ints, run_adapter, run_expert,  # noqa: F401
                               values)
 
 pytestmark = pytest.mark.gpu
@@ -158,3 +158,19 @@ def test_group_route_group_scores_whose_large_biases_cancel(M, scores, size, G, 
     check_weights(M, lg, k, {**kw, "bias": b})
     b[:size] = -np.inf
     check_weights(M, lg, k, {**kw, "bias": b})
+
+
+def test_expert_linear_of_the_most_rows(M):
+    # 2^31 - 1 rows, nearly all of one expert: row counts next to the end of 32 bits
+    n, K, N = 2 ** 31 - 1, 8, 8
+    x, w = ints(8, 7, K), ints(9, 2, N, K)
+    token = torch.randint(0, 7, (n,), dtype=torch.int32, device="cuda")
+    seg = torch.tensor([0, 5, n], device="cuda", dtype=torch.int32)
+    flag = torch.zeros(1, dtype=torch.int32, device="cuda")
+    out = M.moe_expert_linear(x, w, seg, seg[1:] - seg[:2], row_token=token, err_flag=flag)
+    assert int(flag.item()) == 0
+    want = torch.einsum("tk,enk->etn", x.float(), w.float()).to(torch.bfloat16)
+    assert torch.equal(out[:5], want[0][token[:5].long()])
+    for a in range(5, n, 1 << 26):
+        b = min(n, a + (1 << 26))
+        assert torch.equal(out[a:b], want[1][token[a:b].long()]), a
