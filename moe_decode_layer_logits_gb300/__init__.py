@@ -162,7 +162,8 @@ def _choice(table, value, name):
     return table[value]
 
 
-_raw_stream = torch._C._cuda_getCurrentRawStream  # the current stream's handle, without a Stream object
+# the current stream's handle, without a Stream object; None in a torch built without CUDA
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
 def _enter(device, stream):
@@ -173,7 +174,7 @@ def _enter(device, stream):
     no context."""
     if device.type != "cuda":
         raise TypeError("the tensors must be CUDA tensors (there is no CPU path)")
-    if stream is None and device.index == torch.cuda.current_device():
+    if stream is None and _raw_stream is not None and device.index == torch.cuda.current_device():
         return _raw_stream(device.index), None
     with contextlib.ExitStack() as on:
         on.enter_context(torch.cuda.device(device))

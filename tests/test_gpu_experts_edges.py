@@ -174,3 +174,15 @@ def test_expert_linear_of_the_most_rows(M):
     for a in range(5, n, 1 << 26):
         b = min(n, a + (1 << 26))
         assert torch.equal(out[a:b], want[1][token[a:b].long()]), a
+
+
+def test_calls_without_the_short_way_to_the_stream(M, monkeypatch):
+    ids = torch.tensor([[1, 0], [1, 2]], dtype=torch.int32, device="cuda")
+    want = M.moe_expert_map(ids, 4)
+    monkeypatch.setattr(M, "_raw_stream", None)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        got = M.moe_expert_map(ids, 4)
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
