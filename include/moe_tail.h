@@ -307,8 +307,7 @@ int64_t moe_adapter_linear_workspace(int64_t T, int64_t N, int64_t K, int32_t R,
  *   y      = W . x[t] + B_a . v                  (no adapter: y = W . x[t])
  *   out[t] = y  or  silu(y[0 .. N/2)) * y[N/2 .. N)          (act)
  *
- * FP32 sums; v is carried with at least 16 significant bits; one rounding to
- * BF16 at the end.
+ * FP32 sums, v among them; one rounding to BF16 at the end.
  *
  *   x_bf16         [T, K] BF16
  *   w_bf16         [N, K] BF16

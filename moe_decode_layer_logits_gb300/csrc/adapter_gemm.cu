@@ -234,15 +234,15 @@ struct Few {
 
 struct Many {
   int64_t n_rows;
-  size_t token, seg, counts, low[2], parts, bytes;
+  size_t token, seg, counts, low[kLowParts], parts, bytes;
   Many(int64_t T, int R, int L) {
     n_rows = moe_expert_rows(T, L + 1, 1, 16);
     token = 0;
     seg = up256(static_cast<size_t>(n_rows) * 4);
     counts = seg + up256((static_cast<size_t>(L) + 2) * 4);
     low[0] = counts + up256((static_cast<size_t>(L) + 1) * 4);
-    low[1] = low[0] + up256(static_cast<size_t>(n_rows) * R * 2);
-    parts = low[1] + up256(static_cast<size_t>(n_rows) * R * 2);
+    for (int i = 1; i < kLowParts; ++i) low[i] = low[i - 1] + up256(static_cast<size_t>(n_rows) * R * 2);
+    parts = low[kLowParts - 1] + up256(static_cast<size_t>(n_rows) * R * 2);
     bytes = parts + static_cast<size_t>(expert_gemm_workspace(n_rows));
   }
 };
@@ -318,7 +318,7 @@ cudaError_t many_tokens(const AdapterLinear& g, cudaStream_t stream) {
   p.ring_bytes = kRingBytes;
   p.withhold = take_withheld_stage();
   p.scale = g.scale;
-  for (int i = 0; i < 2; ++i) p.low[i] = reinterpret_cast<uint16_t*>(g.workspace + f.low[i]);
+  for (int i = 0; i < kLowParts; ++i) p.low[i] = reinterpret_cast<uint16_t*>(g.workspace + f.low[i]);
   CUtensorMap ma, mw, mb;
   const bool weave = SWIGLU && g.N / 2 % 16 == 0;
   if (!weight_map(&ma, g.a, g.L, g.R, g.K, false, false) || !weight_map(&mw, g.w, 1, g.N, g.K, SWIGLU, weave) ||

@@ -51,8 +51,8 @@
 //
 // What becomes of the sums is the kernel's Out:
 //  - kRows    act, one rounding, row r of the output;
-//  - kLow     scaled by the segment, left as two BF16 parts (value and rest): the
-//             low-rank product of an adapter, 16 significant bits;
+//  - kLow     scaled by the segment, left as three BF16 parts that add up to the
+//             FP32 value: the low-rank product of an adapter;
 //  - kParts   one segment: every piece left as an FP32 partial tile, for the
 //             caller's own last kernel, and the adapters' low-rank products of
 //             the rows computed by further warps beside it.  The first stages'
@@ -61,7 +61,7 @@
 //             memory before it 15.5; two rings of them 14.4);
 //  - kScatter rows sorted by adapter, every segment starting on a multiple of
 //             16 rows: behind a tile's K blocks come, for each adapter that has
-//             rows in the tile, its B against the two parts of its low-rank
+//             rows in the tile, its B against the three parts of its low-rank
 //             product, added to that adapter's columns only (so no other token
 //             can see it); act, one rounding, the row's token of the output.
 #pragma once
@@ -86,7 +86,7 @@ constexpr int kMaxCtas = 256;   // of a launch
 constexpr int kLoaders = 4;     // gathering warps
 
 constexpr int kLowWarps = 8;    // kParts: warps that compute low-rank products
-
+constexpr int kLowParts = 3;    // BF16 parts of a low-rank product: 3 x 8 bits hold FP32's 24
 
 enum Out { kRows, kLow, kParts, kScatter };
 
@@ -116,7 +116,7 @@ struct GemmParams {
   const int32_t* ids;     // kParts: [n_rows]
   float* low32;           // kParts: [n_rows, R] low-rank products
   int L;
-  uint16_t* low[2];       // kLow, kScatter: [n_rows, R] value and rest
+  uint16_t* low[kLowParts];  // kLow, kScatter: [n_rows, R] each
   const int32_t* seg;     // kScatter: [segs + 1] first rows by adapter, then the end
   int segs, R;            // kScatter: the last segment's rows have no adapter
 };
@@ -405,13 +405,20 @@ __device__ __forceinline__ void store_cols(const GemmParams& p, const Piece& w, 
     }
     if (OUT == kLow) {
       const float f = __uint_as_float(aux), x = f * a, y = f * b;
-      const uint32_t hi = pack_bf16x2(x, y);
-      // the rest of an infinite value is none
-      const float rx = x - bf16lo(hi), ry = y - bf16hi(hi);
-      const uint32_t rest = pack_bf16x2(isfinite(x) ? rx : 0.f, isfinite(y) ? ry : 0.f);
-      if (live) {
-        *reinterpret_cast<uint32_t*>(p.low[0] + row * p.n_out + o) = hi;
-        *reinterpret_cast<uint32_t*>(p.low[1] + row * p.n_out + o) = rest;
+      // each part is what BF16 holds of what the ones before leave, which FP32
+      // holds exactly; an infinite value leaves nothing, and a finite one beyond
+      // BF16's largest starts with that
+      float rx = x, ry = y;
+#pragma unroll
+      for (int part = 0; part < kLowParts; ++part) {
+        uint32_t u = pack_bf16x2(rx, ry);
+        if (part == 0) {
+          if (isfinite(x) && isinf(bf16lo(u))) --u;
+          if (isfinite(y) && isinf(bf16hi(u))) u -= 0x10000u;
+        }
+        if (live) *reinterpret_cast<uint32_t*>(p.low[part] + row * p.n_out + o) = u;
+        rx = isfinite(x) ? rx - bf16lo(u) : 0.f;
+        ry = isfinite(y) ? ry - bf16hi(u) : 0.f;
       }
     } else {
       const bool bad = OUT == kRows && ((aux >> r) & 1u);
@@ -628,13 +635,13 @@ expert_gemm_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_cons
         if (OUT == kScatter && !stop) {
           Adapters ad(p, seg, w);
           while (!stop && ad.get(p, seg)) {
-            for (int i = 0; i < 2 * depth; ++i, ++n, advance(x)) {
+            for (int i = 0; i < kLowParts * depth; ++i, ++n, advance(x)) {
               if (!freed()) {
                 stop = true;
                 break;
               }
               if (rank == 0) mbar_arrive_expect_tx(&sb.full[x.st], 2 * kBM * kRowBytes);
-              load_weights(&tmap_b, smem_addr(ring) + static_cast<uint32_t>(x.st * stage_bytes), i >> 1, m, ad.a,
+              load_weights(&tmap_b, smem_addr(ring) + static_cast<uint32_t>(x.st * stage_bytes), i / kLowParts, m, ad.a,
                            full0 + x.st * 8, keep);
             }
           }
@@ -685,7 +692,7 @@ expert_gemm_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_cons
           Adapters ad(p, seg, w);
           while (!stop && ad.get(p, seg)) {
             const uint32_t sub = idesc_bf16(2 * kBM, ad.n);
-            for (int i = 0; i < 2 * depth; ++i, advance(x)) {
+            for (int i = 0; i < kLowParts * depth; ++i, advance(x)) {
               const int st = x.st;
               if (!wait(&sb.full[st], x.ph, abort_v)) {
                 stop = true;
@@ -693,7 +700,7 @@ expert_gemm_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_cons
               }
               fence_after_sync();
               const uint32_t a = a0 + static_cast<uint32_t>(st) * step, b = a + (kBM * kRowBytes >> 4);
-              const int ks = (min(kBK, p.R - (i >> 1) * kBK) + 15) >> 4;
+              const int ks = (min(kBK, p.R - i / kLowParts * kBK) + 15) >> 4;
               for (int kk = 0; kk < ks; ++kk) mma_bf16<PAIR>(d + ad.c0, a + kk * 2, b + kk * 2, sub, true);
               mma_commit<PAIR>(&sb.empty[st]);
             }
@@ -844,15 +851,15 @@ expert_gemm_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_cons
         while (!stop && ad.get(p, seg)) {
           const int half = ad.n / 2;
           const int64_t first = w.r0 + ad.c0 + rank * half;
-          for (int i = 0; i < 2 * depth; ++i, ++n, advance(x)) {
+          for (int i = 0; i < kLowParts * depth; ++i, ++n, advance(x)) {
             const int st = x.st;
             if (n >= nstages && !wait(&sb.empty[st], x.ph ^ 1, abort_v)) {
               stop = true;
               break;
             }
             const uint32_t b = smem_addr(ring) + static_cast<uint32_t>(st * stage_bytes + kBM * kRowBytes);
-            const int col = (i >> 1) * kBK + chunk * 8;
-            const uint16_t* low = p.low[i & 1];
+            const int col = i / kLowParts * kBK + chunk * 8;
+            const uint16_t* low = p.low[i % kLowParts];
 #pragma unroll
             for (int h = 0; h < 8; ++h) {
               const int r = 16 * h + 4 * j + sub;
@@ -879,7 +886,7 @@ expert_gemm_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_cons
         int stages = w.kb1 - w.kb0;
         if (OUT == kScatter) {
           Adapters ad(p, seg, w);
-          while (ad.get(p, seg)) stages += 2 * depth;
+          while (ad.get(p, seg)) stages += kLowParts * depth;
         }
         for (int i = 0; i < stages; ++i, advance(x)) {
           const int st = x.st;

@@ -186,3 +186,44 @@ def test_calls_without_the_short_way_to_the_stream(M, monkeypatch):
         got = M.moe_expert_map(ids, 4)
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+@pytest.mark.parametrize("T,R", [(3, 16), (200, 72), (1100, 16), (1100, 72), (2100, 256)])  # few tokens, then many
+def test_adapter_linear_keeps_the_low_rank_product_in_32_bits(M, T, R):
+    # whole numbers: W = D - A, B = 1, so that y = D x; A x has up to 21 bits
+    # (64 * 127 * 255) and has to cancel to the last
+    g = torch.Generator(device="cuda").manual_seed(R)
+    draw = lambda lim, *s: torch.randint(-lim, lim + 1, s, generator=g, device="cuda").to(torch.bfloat16)
+    K = 64
+    x, a = draw(127, T, K), draw(255, 2, R, K)
+    a[1] = a[0]
+    at = torch.arange(R, device="cuda") % K
+    w = -a[0].float()
+    keep = w[torch.arange(R, device="cuda"), at]
+    w[torch.arange(R, device="cuda"), at] = torch.where(keep >= 255, keep - 1, keep + 1)
+    sign = torch.where(keep >= 255, -1.0, 1.0)
+    b = torch.eye(R, device="cuda", dtype=torch.bfloat16).repeat(2, 1, 1)
+    ids = (torch.arange(T, device="cuda") % 2).int()
+    out = M.moe_adapter_linear(x, w.to(torch.bfloat16), a, b, ids, torch.ones(2, device="cuda"))
+    assert int((x.double() @ a[0].double().T).abs().max()) > 2 ** 17  # (more than two BF16 hold)
+    assert torch.equal(out.float(), x.float()[:, at] * sign)
+
+
+@pytest.mark.parametrize("T", [2, 1100])
+def test_adapter_linear_low_rank_products_beyond_the_largest_bf16(M, T):
+    # v = (2 - 2^-7 + 2^-8 + 2^-9) 2^127: finite in FP32, infinite if rounded to BF16
+    K, N, R = 64, 64, 16
+    x = torch.zeros(T, K, device="cuda")
+    x[:, 0], x[:, 1] = torch.finfo(torch.bfloat16).max, 1.5 * 2.0 ** 119
+    x[1::2] *= -1
+    a = torch.zeros(1, R, K, device="cuda")
+    a[0, :, :2] = 1
+    b = torch.zeros(1, N, R, device="cuda")
+    b[0, torch.arange(N), torch.arange(N) % R] = 2.0 ** -126
+    w = torch.zeros(N, K, dtype=torch.bfloat16, device="cuda")
+    bf = lambda t: t.to(torch.bfloat16)
+    out = M.moe_adapter_linear(bf(x), w, bf(a), bf(b), torch.zeros(T, dtype=torch.int32, device="cuda"),
+                               torch.ones(1, device="cuda"))
+    want = torch.full((T, N), 4.0, device="cuda")           # 3.996 in BF16
+    want[1::2] *= -1
+    assert torch.equal(out.float(), want)
