@@ -74,10 +74,11 @@ __device__ __forceinline__ float logit(float l) { return isnan(l) ? __int_as_flo
 __device__ __forceinline__ double sigmoid_f64(float l) { return 1.0 / (1.0 + exp(-static_cast<double>(l))); }
 
 // The choice of one token in 64 bits.  `sc` and `key` are E values each of
-// this warp's shared memory.  Lane j < k gets the j-th id.  The 64-bit pipe is
-// narrow, so it computes the values, and their integer keys are compared.
+// this warp's shared memory.  Lane j < k gets the j-th id and its logit.  The
+// 64-bit pipe is narrow, so it computes the values, and their integer keys are
+// compared.
 __device__ __noinline__ void group_select_f64(const GroupRouteParams& p, const float* __restrict__ row, double* sc,
-                                              uint64_t* key, int& id) {
+                                              uint64_t* key, int& id, float& l) {
   const int lane = threadIdx.x & 31;
   const double inf = __longlong_as_double(0x7FF0000000000000ll);
   double m = -inf, sum = 1.0;
@@ -153,6 +154,7 @@ __device__ __noinline__ void group_select_f64(const GroupRouteParams& p, const f
     if (lane == 0) key[at] = 0ull;
     __syncwarp();
   }
+  l = logit(row[id]);
 }
 
 // Adds v to the two largest values b1 >= b2 so far.
@@ -175,6 +177,32 @@ __device__ __forceinline__ int candidate_expert(uint64_t c) {
 __device__ __forceinline__ bool too_close(float a, float b, float doubt) {
   const float inf = __int_as_float(0x7F800000);
   return !(a - b > doubt + 4.7683716e-7f * fmaxf(fabsf(a), fabsf(b))) && !(b == -inf && a > -inf);
+}
+
+// Smallest and largest of the warp's values.
+__device__ __forceinline__ float warp_least(float v) {
+  float r;
+  asm volatile("redux.sync.min.f32 %0, %1, 0xFFFFFFFF;" : "=f"(r) : "f"(v));
+  return r;
+}
+__device__ __forceinline__ float warp_most(float v) {
+  float r;
+  asm volatile("redux.sync.max.f32 %0, %1, 0xFFFFFFFF;" : "=f"(r) : "f"(v));
+  return r;
+}
+
+// The score of a chosen logit l (-inf: none) in a row with small ones, m and
+// inv the softmax' maximum and 1 / sum.  Divided by their sum, only the scores'
+// ratios count: where the best chosen score is below e^-16 they are taken
+// relative to it, as scores of 32 bits end at e^-103 (and 1 / (1 + expf(-l)) at
+// e^-88).  A score below 2^-1022 counts as 0.
+template <bool SOFTMAX>
+__device__ __forceinline__ float small_weight(float l, float m, float inv, int renorm) {
+  const float inf = __int_as_float(0x7F800000), ref = SOFTMAX ? m : 0.f;
+  const float top = renorm ? warp_most(l) : inf;
+  if (top - ref < -16.f) return l - ref < -708.39642f ? 0.f : expf(l - top) / (SOFTMAX ? 1.f : 1.f + expf(l));
+  if (SOFTMAX) return m == -inf ? 0.f : (l == m ? 1.f : expf(l - m)) * inv;
+  return l < -80.f ? expf(l) / (1.f + expf(l)) : 1.f / (1.f + expf(-l));
 }
 
 // Shared memory of one warp, in bytes: the larger of the 32-bit selection's
@@ -305,8 +333,7 @@ __global__ void __launch_bounds__(kGroupRouteWarps * 32) group_route_kernel(cons
       const float err = doubt + 2.3841858e-7f * (fabsf(b1) + (two ? fabsf(b2) : 0.f));
       const float low = gs == inf ? big : gs == -inf ? -inf : gs - err, high = gs == -inf ? -big : gs == inf ? inf : gs + err;
       const bool group = g < p.n_group, stays = group && rank < p.topk_group;
-      const float lo = order_value(__reduce_min_sync(0xFFFFFFFFu, stays ? order_key(low) : 0xFFFFFFFFu));
-      const float hi = order_value(__reduce_max_sync(0xFFFFFFFFu, group && !stays ? order_key(high) : 0u));
+      const float lo = warp_least(stays ? low : inf), hi = warp_most(group && !stays ? high : -inf);
       if (!(lo > hi)) {
         if (SOFTMAX || !BIAS) {
           exactly = true;
@@ -457,21 +484,16 @@ __global__ void __launch_bounds__(kGroupRouteWarps * 32) group_route_kernel(cons
       }
     }
   }
+  float l = lv[id];
   if (exactly) {
     __syncwarp();
-    group_select_f64(p, row, reinterpret_cast<double*>(mem), reinterpret_cast<uint64_t*>(mem) + p.E, id);
+    group_select_f64(p, row, reinterpret_cast<double*>(mem), reinterpret_cast<uint64_t*>(mem) + p.E, id, l);
   }
-  // The weights, the same way whatever made the choice.  Divided by their sum,
-  // only the scores' ratios count: where the best chosen score is below e^-16
-  // they are taken relative to it, as scores of 32 bits end at e^-103 (and
-  // 1 / (1 + expf(-l)) at e^-88).  A score below 2^-1022 counts as 0.
-  const float l = lane < p.k ? (exactly ? logit(row[id]) : lv[id]) : -inf;
-  const float top = p.renorm ? order_value(__reduce_max_sync(0xFFFFFFFFu, order_key(l))) : inf;
-  const float ref = SOFTMAX ? m : 0.f;
-  float w;
-  if (top - ref < -16.f) w = l - ref < -708.39642f ? 0.f : expf(l - top) / (SOFTMAX ? 1.f : 1.f + expf(l));
-  else if (SOFTMAX) w = m == -inf ? 0.f : (l == m ? 1.f : expf(l - m)) * inv;
-  else w = l < -80.f ? expf(l) / (1.f + expf(l)) : 1.f / (1.f + expf(-l));
+  if (lane >= p.k) l = -inf;
+  // The weights, the same way whatever made the choice.
+  float w = 0.f;
+  if (lane < p.k) w = SOFTMAX ? (m == -inf ? 0.f : (l == m ? 1.f : expf(l - m)) * inv) : 1.f / (1.f + expf(-l));
+  if (__any_sync(0xFFFFFFFFu, lane < p.k && l - (SOFTMAX ? m : 0.f) < -16.f)) w = small_weight<SOFTMAX>(l, m, inv, p.renorm);
   if (p.renorm) {
     const float sum = warp_sum(w);
     w = sum > 0.f ? w / sum : 0.f;
