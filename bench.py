@@ -58,7 +58,7 @@ def parse_args():
     ap.add_argument("--no-cpu-baseline", action="store_true")
     ap.add_argument("--min-timed-s", type=float, default=1.0,
                     help="repeat the K-step timed region until this much time is covered")
-    ap.add_argument("--ncu-case", choices=["decode", "decode1", "prefill", "router"], default=None,
+    ap.add_argument("--ncu-case", choices=["decode", "decode1", "prefill", "router", "routing", "experts", "adapters"], default=None,
                     help="run a small fixed case for an ncu capture and exit (no timing, no JSON)")
     return ap.parse_args()
 
@@ -854,7 +854,10 @@ def run_ncu_case(case):
     tail on each layer, twice; decode1 -- the same with 48 layers at T=1
     (154 MB, mostly gate weights); prefill -- 2 sets at T=2048 (605 MB), route, finalize and the
     router-less fused tail on each set, twice; router -- the router GEMM on 2
-    inputs at T=8192 (x 100 MB each), twice."""
+    inputs at T=8192 (x 100 MB each), twice; routing -- grouped routing and
+    expert map at T=8192, experts -- products of 64 experts at T=64 and of 48
+    at T=1600 (3.2 GB of weights), adapters -- the adapter projection at T=64
+    and T=4096, each twice with another 256 MB written in between."""
     import torch
     import moe_decode_layer_logits_gb300 as M
     from moe_decode_layer_logits_gb300.inputs import device_layer
@@ -867,6 +870,9 @@ def run_ncu_case(case):
             for d in sets:
                 M.moe_router_logits_fp32(d["x"], d["w_gate"], logits_out=d["logits"])
         torch.cuda.synchronize()
+        return
+    if case in ("routing", "experts", "adapters"):
+        run_expert_ncu_case(torch, M, case)
         return
     if case == "decode":
         sets = [device_layer(T_DEC, H_DEC, E_DEC, K_DEC, seed=i, scale=SCALE) for i in range(12)]
@@ -891,6 +897,38 @@ def run_ncu_case(case):
                 M.moe_tail_fused(d["logits"], K_DEC, SCALE, d["rows"], d["map"], d["shared"], d["residual"],
                                  d["gamma"], d["eps"], residual_out=d["residual_out"], normed_out=d["normed_out"],
                                  want_route=False)
+    torch.cuda.synchronize()
+
+
+def run_expert_ncu_case(torch, M, case):
+    g = torch.Generator(device="cuda")
+    g.manual_seed(300)
+    randn = lambda std, *s: torch.randn(*s, generator=g, device="cuda", dtype=torch.bfloat16) * std
+    calls = []
+    if case == "routing":
+        lg = torch.randn(8192, 256, generator=g, device="cuda") * 1.5
+        bias = torch.randn(256, generator=g, device="cuda") * 0.1
+        ids, _ = M.moe_group_topk_route(lg, 8, SCALE, bias=bias, n_group=8, topk_group=4)
+        calls += [lambda: M.moe_group_topk_route(lg, 8, SCALE, bias=bias, n_group=8, topk_group=4),
+                  lambda: M.moe_expert_map(ids, 256, block=128)]
+    elif case == "experts":
+        w = randn(0.02, 64, 4096, 6144)
+        for T, E in ((64, 64), (1600, 48)):
+            x = randn(1.0, T, 6144)
+            ids = torch.rand(T, E, generator=g, device="cuda").topk(8, dim=1).indices.to(torch.int32)
+            _, row_token, offsets, counts = M.moe_expert_map(ids, E)
+            calls.append(lambda x=x, w=w[:E], o=offsets, c=counts, t=row_token:
+                         M.moe_expert_linear(x, w, o, c, row_token=t, act="swiglu"))
+    else:
+        for T, K, N, R, n, act in ((64, 2048, 6144, 16, 64, None), (4096, 6144, 4096, 64, 8, "swiglu")):
+            a = (randn(1.0, T, K), randn(0.02, N, K), randn(K ** -0.5, n, R, K), randn(0.05, n, N, R),
+                 (torch.arange(T, device="cuda") * n // T).int(), torch.ones(n, device="cuda"))
+            calls.append(lambda a=a, act=act: M.moe_adapter_linear(*a, act=act))
+    other = torch.empty(1 << 28, dtype=torch.uint8, device="cuda")
+    for _ in range(2):
+        for call in calls:
+            other.zero_()
+            call()
     torch.cuda.synchronize()
 
 

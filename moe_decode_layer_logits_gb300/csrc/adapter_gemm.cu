@@ -9,16 +9,16 @@
 //    own B in FP32, applies the activation and rounds once.  It starts while the
 //    first runs and requests the B rows into the L2 meanwhile.  Bound by the
 //    weights' bytes and, at this size, by the latency of two launches (K = 6144,
-//    N = 4096, R = 16, T = 1: 13 us for 7.5 us of bytes; K = 2048, N = 6144,
-//    T = 64, 64 adapters: 12.9 for 5.3).
+//    N = 4096, R = 16, T = 1: 13.8 us for 7.5 us of bytes; K = 2048, N = 6144,
+//    T = 64, 64 adapters: 13.4 for 5.3).
 //  - more tokens: the tokens are sorted by adapter (segments start on multiples
 //    of 16 rows), the low-rank products are the expert products of A (kLow),
 //    and the shared projection runs in CTA pairs over the sorted rows with the
 //    adapters' B as further K blocks of their own columns (kScatter).  A tile of
 //    256 rows reads the shared weights once however many adapters it holds.
 //    Bound by the tensor cores (K = 6144, N = 4096 SwiGLU, R = 64, T = 4096,
-//    8 adapters: 175 us, 1209 TFLOP/s, of which the sort takes 8, the low-rank
-//    products 38).
+//    8 adapters: 181 us, 1170 TFLOP/s; one by one with cold caches the sort
+//    takes 10, the low-rank products 22, their join 18, the projection 133).
 #include "expert_gemm.cuh"
 #include "expert_map.h"
 
@@ -29,9 +29,10 @@ namespace {
 // Few tokens: while the low-rank products (a warp each, and B read by each
 // token) and the FP32 partial tiles cost less than the sort and the two further
 // products.  64 adapters in use, few / many: K = 2048, N = 6144, T = 64 R = 16
-// 14 / 65 us, T = 256 R = 64 58 / 69, T = 1024 R = 16 78 / 81, T = 64 R = 128
-// 76 / 88, T = 16 R = 256 90 / 68; K = 7168, N = 18432, R = 16, T = 256 120 / 207,
-// T = 512 231 / 218, T = 1024 R = 8 429 / 260.
+// 13 / 66 us, T = 512 R = 16 38 / 70, T = 256 R = 64 57 / 65, T = 1024 R = 16
+// 66 / 79, T = 64 R = 128 76 / 82, T = 16 R = 256 93 / 68; K = 7168, N = 18432,
+// R = 16, T = 256 95 / 195, T = 1024 R = 8 305 / 264.  K is not in the rule: at
+// K = 7168, N = 18432, T = 512 R = 16 it takes many where few is ahead, 172 / 201.
 bool few_form(int64_t T, int64_t N, int R) { return T * N <= 1 << 23 && T * R <= (R <= 128 ? 16384 : 2048); }
 
 struct FinishParams {

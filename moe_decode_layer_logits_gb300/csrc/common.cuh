@@ -58,11 +58,16 @@ __device__ __forceinline__ void unpack8(const uint4& v, float f[8]) {
 
 // Programmatic dependent launch.  Every kernel of this library is launched
 // with programmatic stream serialisation, so it may start while the previous
-// kernel on the stream is still running.  It lets its own dependent start
-// early (launch_dependents), and it reads or writes no global memory before
-// grid_dependency_wait(), which returns once the previous grid has finished
-// and its writes are visible.  Without a programmatic predecessor both are
-// no-ops.
+// kernel on the stream is still running, and lets its own dependent start
+// early (launch_dependents).  grid_dependency_wait() returns once the previous
+// grid has finished and its writes are visible; all writes come behind it, and
+// all reads whose value decides a result, but for two: the decode router's
+// gate weights, which its call wants unwritten by running kernels, and the
+// segments and ids that expert_join_kernel and adapter_finish_kernel read,
+// whose predecessor is their own call's product, which triggers behind its own
+// wait, so that whatever wrote them has ended.  (Requests into the L2 hand
+// over no data; what is read early to address them is read again.)  Without a
+// programmatic predecessor both are no-ops.
 __device__ __forceinline__ void allow_dependent_launch() {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }

@@ -7,10 +7,15 @@ namespace {
 
 std::atomic<int> g_withheld{-1};  // take_withheld_stage()
 
-// Pairs from a mean of this many rows an expert, the batch size divided over all
-// of them (no device value decides on the host).  gate_up, E = 256, K = 6144,
+// Pairs from a mean of this many rows an expert, the rows of the call divided
+// over all of them.  No device value decides on the host, so those are the rows
+// the call has room for: padding and rows of dropped slots count, and a call
+// that has much of either runs in pairs with few rows each.  gate_up, E = 256, K = 6144,
 // N = 4096, single CTAs / pairs: a mean of 93 rows 1950 / 1951 us, 112 1943 / 1959,
-// 128 2188 / 1968; E = 8, a mean of 125 116 / 108.
+// 128 2188 / 1968; E = 8, a mean of 125 116 / 108.  With room for more rows than
+// there are: T = 64 on segments of 128 (2 rows an expert) 1589 / 1643, T = 1024
+// with 32 of 256 experts present (33 rows) 252 / 253.  With few tiles: E = 8, a
+// mean of 125, N = 256 27 / 32, N = 1024 37 / 36, a mean of 250, N = 2048 83 / 58.
 constexpr int64_t kPairMeanRows = 96;
 
 template <bool SWIGLU>

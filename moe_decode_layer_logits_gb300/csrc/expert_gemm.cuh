@@ -15,7 +15,8 @@
 //  - warps 2..5 read the finished accumulator while the next tile's MMAs run,
 //    apply the activation to the FP32 sums and store BF16 once (in pairs, whose
 //    tiles have more columns, warps 11..14 too: with four warps the MMAs waited
-//    for them a tenth of the time, adapter T = 4096 177 us against 170);
+//    for them a tenth of the time, adapter T = 4096, when its low-rank product
+//    had two parts, 182 us against 175);
 //  - with a token list the rows are gathered by warps 6..9 with 16-byte
 //    asynchronous copies (eight lanes a row of the stage) that arrive on the
 //    stage's own barrier as they land, and warp 10 passes that on behind a proxy
@@ -40,11 +41,13 @@
 // atomics: the same inputs give the same bits).  Pairs take whole tiles.
 //
 // Measured, SwiGLU, 256 experts of K = 6144, N = 4096, 8 a token, token list:
-// T = 1 70 us (403 MB: 85% of the copy rate; the rest is launch, first stages
-// and the join), T = 64 1.56 ms and T = 512 1.81 ms (107 and 105%: reads alone
-// are faster than a copy), T = 4096 1.97 ms (98%), T = 8192 uneven 2.43 ms
-// (1360 TFLOP/s, 81% of the copy rate); 64 experts, T = 16384, 3.57 ms (1850
-// TFLOP/s, 97% of the tensor rate).  Weights' bytes bound it up to about 150
+// even experts unless said otherwise, on two boxes: T = 64 1.56 and 1.60 ms,
+// T = 512 1.81 and 1.85 ms (103 to 107% of the copy rate: reads alone are
+// faster than a copy), T = 4096 1.97 and 2.02 ms (98 and 96%), T = 8192 uneven
+// 2.43 and 2.50 ms (1360 TFLOP/s and 81% of the copy rate in the first), 2.8 ms
+// in a second of it (power); with 64 experts, T = 1 70 us (403 MB: 85% of the
+// copy rate; the rest is launch, first stages and the join), T = 16384 3.57 and
+// 3.78 ms (1850 and 1750 TFLOP/s).  Weights' bytes bound it up to about 150
 // rows an expert, the tensor cores where tiles are full; between them both
 // matter (a stage turns around in 0.21 us or more whatever its rows, and loads
 // that miss the L2 come later than that).

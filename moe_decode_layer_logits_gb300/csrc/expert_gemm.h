@@ -10,7 +10,7 @@ struct ExpertGemm {
   const void* x;             // [n_x, K] BF16
   const int32_t* row_token;  // [n_rows] or null
   const void* w;             // [E, N, K] BF16
-  const int32_t* offsets;    // [E], null: one segment of all rows (E = 1)
+  const int32_t* offsets;    // [E]
   const int32_t* counts;     // [E]
   void* out;                 // [n_rows, N or N/2] BF16
   int64_t n_x, n_rows, E, N, K;

@@ -7,7 +7,7 @@
 // the counts are added up over the warps and, through distributed shared
 // memory, over the cluster, and scanned over the experts; then each warp walks
 // its slots once more, 32 at a time and in order, and gives every slot its
-// place (equal experts within the 32 by a warp match).  Integer counts only:
+// place (equal experts within the 32 by ballots on the bits of the expert).  Integer counts only:
 // the layout does not depend on the order of the atomics.  Bound by latency:
 // two passes over a warp's slots and two cluster barriers; more warps shorten
 // the walks until adding up their counts costs as much.
