@@ -449,14 +449,28 @@ __global__ void __launch_bounds__(kGroupRouteWarps * 32) group_route_kernel(cons
     const uint64_t mine = lane < p.k ? best[lane] : 0ull;
     id = lane < p.k ? candidate_expert(mine) : 0;
     if (BIAS) {
-      bool close = false;
+      // the same logit and bias are a tie in any precision
+      auto doubtful = [&](uint64_t better, uint64_t worse) {
+        return too_close(order_value(static_cast<uint32_t>(better >> 32)), order_value(static_cast<uint32_t>(worse >> 32)),
+                         doubt);
+      };
+      auto equal = [&](int x, int y) { return lv[x] == lv[y] && p.bias[x] == p.bias[y]; };
+      bool close = false, tied = false;
       if (lane < p.k && lane + 1 < n) {
         const uint64_t next = best[lane + 1];
-        close = too_close(order_value(static_cast<uint32_t>(mine >> 32)),
-                          order_value(static_cast<uint32_t>(next >> 32)), doubt);
-        if (close) {  // the same logit and bias are a tie in any precision
-          const int o = candidate_expert(next);
-          close = lv[id] != lv[o] || p.bias[id] != p.bias[o];
+        close = doubtful(mine, next);
+        if (close && equal(id, candidate_expert(next))) {
+          close = false;
+          tied = lane == p.k - 1;
+        }
+      }
+      if (__any_sync(0xFFFFFFFFu, tied)) {
+        // behind those equal to the last one chosen may stand one that only 64
+        // bits tell from them
+        const uint64_t last = best[p.k - 1];
+        for (int at = lane; at < n; at += 32) {
+          const uint64_t v = list[at];
+          if (v < last && doubtful(last, v) && !equal(candidate_expert(last), candidate_expert(v))) close = true;
         }
       }
       if (__any_sync(0xFFFFFFFFu, close)) {

@@ -227,3 +227,26 @@ def test_adapter_linear_low_rank_products_beyond_the_largest_bf16(M, T):
     want = torch.full((T, N), 4.0, device="cuda")           # 3.996 in BF16
     want[1::2] *= -1
     assert torch.equal(out.float(), want)
+
+
+@pytest.mark.parametrize("scores", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("E,G,TG,k", [(16, 1, 1, 5), (64, 4, 2, 6), (256, 1, 1, 8), (600, 1, 1, 3)])
+def test_group_route_equal_experts_before_a_better_one_that_32_bits_cannot_tell(M, scores, E, G, TG, k):
+    # masked experts of the same bias are equal in any precision; one among them
+    # has a score that only 64 bits see, and comes first although it stands last
+    rng = np.random.default_rng([304, E, k])
+    lg = np.full((40, E), -np.inf, np.float32)
+    b = np.full(E, 0.25, np.float32)
+    size = E // G
+    for t in range(len(lg)):
+        live = rng.permutation(size)[:k - 1]           # fewer than k experts of any weight
+        lg[t, live] = rng.standard_normal(k - 1)
+        rest = np.setdiff1d(np.arange(size), live)
+        some = rng.permutation(rest[1:])[:1 + t % 3]
+        lg[t, some] = rng.uniform(-32, -20, len(some))  # 64 bits: 0.25 + 1e-14 .. 2e-9
+    for top in (1, 2):
+        check_weights(M, lg, k, dict(bias=b, n_group=G, topk_group=TG, group_top=top, scores=scores, renormalize=True))
+    lg[::2] = np.where(np.isinf(lg[::2]), np.float32(np.nan), lg[::2])
+    ids, _ = M.moe_group_topk_route(devn(lg), k, 1.0, bias=devn(b), n_group=G, topk_group=TG, scores=scores)
+    assert np.array_equal(ids.cpu().numpy(), O.group_topk_route(lg, k, 1.0, bias=b, n_group=G, topk_group=TG,
+                                                               scores=scores)[0])
