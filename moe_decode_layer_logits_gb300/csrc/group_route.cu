@@ -20,7 +20,7 @@
 // choice, a lower bound for the k-th value, ranks among the values above it),
 // so small batches are bound by its latency and large ones by its
 // instructions (two thirds of the cycles issue one); the data is 4 E bytes a
-// token.  E = 256 in 8 groups, sigmoid with a bias: T = 1 3.1 us, T = 8192
+// token.  E = 256 in 8 groups, sigmoid with a bias: T = 1 3.2 us, T = 8192
 // 12.6 us.
 #include "host_util.h"
 #include "common.cuh"
