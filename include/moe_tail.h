@@ -74,6 +74,12 @@ typedef enum moe_status {
 #define MOE_ACT_NONE 0   /* out = y, N outputs */
 #define MOE_ACT_SWIGLU 1 /* out = silu(y[0 .. N/2)) * y[N/2 .. N): gate rows first, N/2 outputs */
 
+/* Formats of microscaled 4-bit floating point: elements are E2M1 codes (bit 3
+ * the sign; 0, 0.5, 1, 1.5, 2, 3, 4, 6), two in a byte, the even element in the
+ * low half, and each block of neighbours in a row shares a scale byte. */
+#define MOE_FP4_NV 0 /* 16 neighbours, an E4M3 scale without sign (top bit 0), an FP32 scale over all */
+#define MOE_FP4_MX 1 /* 32 neighbours, an E8M0 scale: 2^(byte - 127) */
+
 /* Bits written (OR-ed) into the optional device error flag. */
 #define MOE_FLAG_BAD_INDEX 1 /* some map[t,j] was outside [0, n_rows) */
 #define MOE_FLAG_TIMEOUT 2   /* a bounded pipeline wait ran out (outputs of that launch are invalid) */
@@ -329,6 +335,99 @@ int moe_adapter_linear(const void* x_bf16, const void* w_bf16, const void* adapt
                        const float* adapter_scale, void* out_bf16, int64_t T, int64_t N, int64_t K,
                        int32_t R, int32_t L, int32_t act, void* workspace, int64_t workspace_bytes,
                        int32_t* err_flag, cudaStream_t stream);
+
+/*
+ * BF16 rows to 4-bit codes with a scale for each block.  With g the global scale
+ * (1 without one; MOE_FP4_NV only) and amax a block's largest |x|:
+ *
+ *   MOE_FP4_NV  s = e4m3(amax / (6 g))         nearest even, at most 448
+ *   MOE_FP4_MX  s = 2^(floor(log2 amax) - 2)    at least 2^-127 (also for zeros)
+ *   code = e2m1(x / (s g))                      nearest even, at most 6 (s = 0: code 0)
+ *
+ * so that x is about code * s * g.  The roundings are those of the exact
+ * quotients.  A block that holds an infinity or a NaN gets a NaN scale (0x7F,
+ * 0xFF) and zero codes, so that every product with it is NaN; so does every
+ * block if g is not between 2^-100 and 2^100.
+ *
+ *   x_bf16       [T, K] BF16
+ *   global_scale device FP32 [1] or NULL (MOE_FP4_MX: NULL)
+ *   codes        [T, K / 2] bytes, written, 16-byte aligned
+ *   scales       [T, K / block] bytes, written, 4-byte aligned
+ *   T >= 0; K a multiple of 64 (MOE_FP4_NV) or 128 (MOE_FP4_MX), at most
+ *   MOE_MAX_DIM.
+ */
+int moe_fp4_quantize(const void* x_bf16, const float* global_scale, void* codes, void* scales, int64_t T,
+                     int64_t K, int32_t format, cudaStream_t stream);
+
+/*
+ * The values that codes and scales stand for: out = code * s * g, rounded to
+ * BF16 once (nearest even).  Arguments as in moe_fp4_quantize.
+ */
+int moe_fp4_dequantize(const void* codes, const void* scales, const float* global_scale, void* out_bf16,
+                       int64_t T, int64_t K, int32_t format, cudaStream_t stream);
+
+/* Bytes of moe_fp4_weight_scales' output (host only); -1 for sizes out of range. */
+int64_t moe_fp4_weight_scales_bytes(int64_t E, int64_t N, int64_t K, int32_t format, int32_t act);
+
+/*
+ * The scales of weights in the order in which the products read them; made once
+ * when weights are loaded (the codes stay as they are).  The order depends on
+ * `act`, which the products are then called with.
+ *
+ *   scales [E, N, K / block] bytes (E = 1 for moe_fp4_linear), 4-byte aligned
+ *   tiled  moe_fp4_weight_scales_bytes() bytes, written, 16-byte aligned
+ *   1 <= E <= MOE_MAX_E; N, K, act as in moe_fp4_linear.
+ */
+int moe_fp4_weight_scales(const void* scales, void* tiled, int64_t E, int64_t N, int64_t K, int32_t format,
+                          int32_t act, cudaStream_t stream);
+
+/* Workspace of moe_fp4_linear (E = 1) and moe_fp4_expert_linear in bytes (host
+ * only); -1 for sizes out of range. */
+int64_t moe_fp4_linear_workspace(int64_t n_rows, int64_t E, int64_t N, int64_t K);
+
+/*
+ * A projection of all rows, both operands in 4 bits:
+ *
+ *   y      = factor * (W . x[t])
+ *   out[t] = y  or  silu(y[0 .. N/2)) * y[N/2 .. N)          (act)
+ *
+ * FP32 sums of exact products of codes and block scales; the factor and the
+ * activation work on the FP32 sums; one rounding to BF16.
+ *
+ *   x_codes   [T, K / 2], x_scales [T, K / block]: as moe_fp4_quantize writes them
+ *   w_codes   [N, K / 2], 16-byte aligned
+ *   w_scales  as moe_fp4_weight_scales writes them for E = 1 and this act
+ *   factor    device FP32 [1] or NULL (1): the global scales of x and W multiplied
+ *   out_bf16  [T, N or N/2] BF16, written; must not overlap any input
+ *   workspace device memory of at least moe_fp4_linear_workspace() bytes,
+ *             16-byte aligned; as in moe_expert_linear
+ *   err_flag  device int32 or NULL (MOE_FLAG_TIMEOUT and NaN as in
+ *             moe_expert_linear)
+ *   T >= 0 and < 2^31; K as in moe_fp4_quantize; 8 <= N <= MOE_MAX_DIM, N % 8 == 0
+ *   (N % 16 == 0 with SwiGLU).
+ */
+int moe_fp4_linear(const void* x_codes, const void* x_scales, const void* w_codes, const void* w_scales,
+                   const float* factor, void* out_bf16, int64_t T, int64_t N, int64_t K, int32_t format, int32_t act,
+                   void* workspace, int64_t workspace_bytes, int32_t* err_flag, cudaStream_t stream);
+
+/*
+ * The experts' products of moe_expert_linear with both operands in 4 bits: for
+ * every expert e and every row r of its segment
+ *
+ *   y      = factor[e] * (W_e . x[src])      src = row_token[r], or r without row_token
+ *   out[r] = y  or  silu(y[0 .. N/2)) * y[N/2 .. N)          (act)
+ *
+ *   x_codes   [n_x, K / 2], x_scales [n_x, K / block]
+ *   w_codes   [E, N, K / 2], w_scales as moe_fp4_weight_scales writes them
+ *   factor    [E] FP32 or NULL (ones)
+ * Everything else (segments, tokens, rows in no segment, workspace, error flag)
+ * as in moe_expert_linear, sizes as in moe_fp4_linear.
+ */
+int moe_fp4_expert_linear(const void* x_codes, const void* x_scales, int64_t n_x, const int32_t* row_token,
+                          const void* w_codes, const void* w_scales, const float* factor, const int32_t* offsets,
+                          const int32_t* counts, void* out_bf16, int64_t n_rows, int64_t E, int64_t N, int64_t K,
+                          int32_t format, int32_t act, void* workspace, int64_t workspace_bytes, int32_t* err_flag,
+                          cudaStream_t stream);
 
 /*
  * Test hook of the bounded waits; no counterpart on the pages.  The next

@@ -14,6 +14,11 @@ allocated with torch when not given.
 * ``moe_expert_map(ids, E, block)``          -> (row_map, row_token, offsets, counts) int32
 * ``moe_expert_linear(x, w, offsets, counts, ...)`` -> expert rows BF16 [n_rows, N or N/2]
 * ``moe_adapter_linear(x, w, a, b, ids, scale, ...)`` -> BF16 [T, N or N/2]
+* ``moe_fp4_quantize(x, format, ...)``       -> (codes [T, K/2], scales [T, K/block]) uint8
+* ``moe_fp4_dequantize(codes, scales, ...)`` -> BF16 [T, K]
+* ``moe_fp4_weight_scales(scales, ...)``     -> uint8, the order the 4-bit products read
+* ``moe_fp4_linear(x, x_scales, w, w_scales, ...)`` -> BF16 [T, N or N/2]
+* ``moe_fp4_expert_linear(x, x_scales, w, w_scales, offsets, counts, ...)`` -> expert rows BF16
 """
 
 from __future__ import annotations
@@ -41,6 +46,11 @@ __all__ = [
     "moe_expert_map",
     "moe_expert_linear",
     "moe_adapter_linear",
+    "moe_fp4_quantize",
+    "moe_fp4_dequantize",
+    "moe_fp4_weight_scales",
+    "moe_fp4_linear",
+    "moe_fp4_expert_linear",
     "MoeTailError",
     "lib",
 ]
@@ -352,6 +362,167 @@ def moe_adapter_linear(x, w, adapter_a, adapter_b, adapter_ids, adapter_scale, a
         if on is not None:
             on.close()
     check(st, "moe_adapter_linear")
+    return out
+
+
+_FP4 = {"nvfp4": _lib.MOE_FP4_NV, "mxfp4": _lib.MOE_FP4_MX}
+_FP4_BLOCK = {_lib.MOE_FP4_NV: 16, _lib.MOE_FP4_MX: 32}
+
+
+def _fp4_block(K, fmt):
+    """Elements that share a scale; K in whole words of scales, as the library takes it."""
+    block = _FP4_BLOCK[fmt]
+    if K % (4 * block):
+        raise ValueError(f"K must be a multiple of {4 * block}, got {K}")
+    return block
+
+
+def _global_scale(t, device):
+    if t is None:
+        return None
+    if t.numel() != 1:
+        raise ValueError("global_scale must have one element")
+    return _arg(t, torch.float32, "global_scale", t.shape, device)
+
+
+def moe_fp4_quantize(x, format="nvfp4", global_scale=None, codes=None, scales=None, stream=None):
+    """Rows x [T, K] BF16 to 4 bits: (codes [T, K/2], scales [T, K/block])
+    uint8, two E2M1 codes a byte.  "nvfp4": an E4M3 scale for each 16
+    neighbours, amax / (6 global_scale) rounded; "mxfp4": a power of two for
+    each 32.  x is about code * scale * global_scale (an FP32 tensor of one
+    element; nvfp4 only)."""
+    if x.dim() != 2:
+        raise ValueError("x must have 2 dimensions")
+    (T, K), device, fmt = x.shape, x.device, _choice(_FP4, format, "format")
+    block = _fp4_block(K, fmt)
+    args = _arg(x, torch.bfloat16, "x", (T, K), device), _global_scale(global_scale, device)
+    handle, on = _enter(device, stream)
+    try:
+        codes, c = _out(codes, torch.uint8, "codes", (T, K // 2), device)
+        scales, s = _out(scales, torch.uint8, "scales", (T, K // block), device)
+        st = lib().moe_fp4_quantize(*args, c, s, T, K, fmt, handle)
+    finally:
+        if on is not None:
+            on.close()
+    check(st, "moe_fp4_quantize")
+    return codes, scales
+
+
+def moe_fp4_dequantize(codes, scales, format="nvfp4", global_scale=None, out=None, stream=None):
+    """What codes [T, K/2] and scales [T, K/block] stand for, code * scale *
+    global_scale, as BF16 [T, K]."""
+    if codes.dim() != 2:
+        raise ValueError("codes must have 2 dimensions")
+    (T, half), device, fmt = codes.shape, codes.device, _choice(_FP4, format, "format")
+    K = 2 * half
+    block = _fp4_block(K, fmt)
+    args = (_arg(codes, torch.uint8, "codes", (T, half), device), _arg(scales, torch.uint8, "scales", (T, K // block), device),
+            _global_scale(global_scale, device))
+    handle, on = _enter(device, stream)
+    try:
+        out, o = _out(out, torch.bfloat16, "out", (T, K), device)
+        st = lib().moe_fp4_dequantize(*args, o, T, K, fmt, handle)
+    finally:
+        if on is not None:
+            on.close()
+    check(st, "moe_fp4_dequantize")
+    return out
+
+
+def moe_fp4_weight_scales(scales, format="nvfp4", act=None, out=None, stream=None):
+    """The scales of 4-bit weights, [N, K/block] or [E, N, K/block] uint8, in
+    the order in which moe_fp4_linear and moe_fp4_expert_linear read them
+    when called with this act.  Made once, when weights are loaded."""
+    if scales.dim() not in (2, 3):
+        raise ValueError("scales must be [N, K/block] or [E, N, K/block]")
+    device, fmt, act = scales.device, _choice(_FP4, format, "format"), _choice(_ACTS, act, "act")
+    E, (N, cols) = (scales.shape[0] if scales.dim() == 3 else 1), scales.shape[-2:]
+    K = cols * _FP4_BLOCK[fmt]
+    _fp4_block(K, fmt)
+    sc = _arg(scales, torch.uint8, "scales", scales.shape, device)
+    L = lib()
+    nbytes = L.moe_fp4_weight_scales_bytes(E, N, K, fmt, act)
+    if nbytes < 0:
+        raise ValueError("sizes out of range")
+    handle, on = _enter(device, stream)
+    try:
+        out, o = _out(out, torch.uint8, "out", (nbytes,), device)
+        st = L.moe_fp4_weight_scales(sc, o, E, N, K, fmt, act, handle)
+    finally:
+        if on is not None:
+            on.close()
+    check(st, "moe_fp4_weight_scales")
+    return out
+
+
+def _fp4_operands(x, x_scales, w, w_scales, format, factor, act, E):
+    """Checks common to both 4-bit products: (pointers of x, x_scales, w,
+    w_scales and factor, sizes (n_x, N, K), format, act)."""
+    device, fmt, act = x.device, _choice(_FP4, format, "format"), _choice(_ACTS, act, "act")
+    (n_x, half), N = x.shape, w.shape[-2]
+    K = 2 * half
+    block = _fp4_block(K, fmt)
+    nbytes = lib().moe_fp4_weight_scales_bytes(E, N, K, fmt, act)
+    if nbytes < 0:
+        raise ValueError("sizes out of range")
+    return ((_arg(x, torch.uint8, "x", (n_x, half), device),
+             _arg(x_scales, torch.uint8, "x_scales", (n_x, K // block), device),
+             _arg(w, torch.uint8, "w", w.shape, device), _arg(w_scales, torch.uint8, "w_scales", (nbytes,), device),
+             _opt(factor, torch.float32, "factor", (E,), device)), (n_x, N, K), fmt, act)
+
+
+def moe_fp4_linear(x, x_scales, w, w_scales, format="nvfp4", factor=None, act=None, out=None, workspace=None,
+                   err_flag=None, stream=None):
+    """One projection of all rows, both operands in 4 bits: act(factor * (w @
+    x[t])).  x [T, K/2] and x_scales as moe_fp4_quantize gives them, w
+    [N, K/2] uint8, w_scales as moe_fp4_weight_scales gives them for this act,
+    factor [1] FP32 (the global scales of x and w multiplied); workspace as
+    in moe_expert_linear."""
+    if x.dim() != 2 or w.dim() != 2 or x.shape[1] != w.shape[1]:
+        raise ValueError("x must be [T, K/2] and w [N, K/2]")
+    device = x.device
+    ptrs, (T, N, K), fmt, act = _fp4_operands(x, x_scales, w, w_scales, format, factor, act, 1)
+    n_out = N // 2 if act == _lib.MOE_ACT_SWIGLU else N
+    L = lib()
+    handle, on = _enter(device, stream)
+    try:
+        out, out_ptr = _out(out, torch.bfloat16, "out", (T, n_out), device)
+        ws, ws_ptr, nbytes = _workspace(workspace, L.moe_fp4_linear_workspace(T, 1, N, K), device)
+        st = L.moe_fp4_linear(*ptrs, out_ptr, T, N, K, fmt, act, ws_ptr, nbytes, _flag(err_flag, device), handle)
+    finally:
+        if on is not None:
+            on.close()
+    check(st, "moe_fp4_linear")
+    return out
+
+
+def moe_fp4_expert_linear(x, x_scales, w, w_scales, offsets, counts, format="nvfp4", factor=None, row_token=None,
+                          act=None, out=None, workspace=None, err_flag=None, stream=None):
+    """moe_expert_linear with both operands in 4 bits: out[r] = act(factor[e] *
+    (w[e] @ x[src])) for the rows r of each expert's segment.  x [n, K/2],
+    w [E, N, K/2] uint8, x_scales and w_scales as in moe_fp4_linear, factor [E]
+    FP32; the rest as in moe_expert_linear."""
+    if x.dim() != 2 or w.dim() != 3 or x.shape[1] != w.shape[2]:
+        raise ValueError("x must be [n, K/2] and w [E, N, K/2]")
+    E, device = w.shape[0], x.device
+    if offsets.dim() != 1 or offsets.shape[0] not in (E, E + 1):
+        raise ValueError("offsets must have E or E + 1 entries")
+    (xp, xs, wp, wsc, fac), (n_x, N, K), fmt, act = _fp4_operands(x, x_scales, w, w_scales, format, factor, act, E)
+    n_rows = n_x if row_token is None else row_token.numel()
+    n_out = N // 2 if act == _lib.MOE_ACT_SWIGLU else N
+    tok = _opt(row_token, torch.int32, "row_token", (n_rows,), device)
+    off, cnt = _arg(offsets, torch.int32, "offsets", offsets.shape, device), _arg(counts, torch.int32, "counts", (E,), device)
+    L = lib()
+    handle, on = _enter(device, stream)
+    try:
+        out, out_ptr = _out(out, torch.bfloat16, "out", (n_rows, n_out), device)
+        ws, ws_ptr, nbytes = _workspace(workspace, L.moe_fp4_linear_workspace(n_rows, E, N, K), device)
+        st = L.moe_fp4_expert_linear(xp, xs, n_x, tok, wp, wsc, fac, off, cnt, out_ptr, n_rows, E, N, K, fmt, act, ws_ptr,
+                                     nbytes, _flag(err_flag, device), handle)
+    finally:
+        if on is not None:
+            on.close()
+    check(st, "moe_fp4_expert_linear")
     return out
 
 

@@ -30,6 +30,8 @@ MOE_SCORE_SOFTMAX = 0
 MOE_SCORE_SIGMOID = 1
 MOE_ACT_NONE = 0
 MOE_ACT_SWIGLU = 1
+MOE_FP4_NV = 0
+MOE_FP4_MX = 1
 
 _vp = ctypes.c_void_p
 _i64 = ctypes.c_int64
@@ -54,6 +56,14 @@ SIGNATURES = {
     "moe_adapter_linear_workspace": (_i64, [_i64, _i64, _i64, _i32, _i32]),
     "moe_adapter_linear": (ctypes.c_int, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _i64, _i64, _i64, _i32, _i32, _i32, _vp,
                                           _i64, _vp, _vp]),
+    "moe_fp4_quantize": (ctypes.c_int, [_vp, _vp, _vp, _vp, _i64, _i64, _i32, _vp]),
+    "moe_fp4_dequantize": (ctypes.c_int, [_vp, _vp, _vp, _vp, _i64, _i64, _i32, _vp]),
+    "moe_fp4_weight_scales_bytes": (_i64, [_i64, _i64, _i64, _i32, _i32]),
+    "moe_fp4_weight_scales": (ctypes.c_int, [_vp, _vp, _i64, _i64, _i64, _i32, _i32, _vp]),
+    "moe_fp4_linear_workspace": (_i64, [_i64, _i64, _i64, _i64]),
+    "moe_fp4_linear": (ctypes.c_int, [_vp, _vp, _vp, _vp, _vp, _vp, _i64, _i64, _i64, _i32, _i32, _vp, _i64, _vp, _vp]),
+    "moe_fp4_expert_linear": (ctypes.c_int, [_vp, _vp, _i64, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i64, _i64, _i64, _i64,
+                                             _i32, _i32, _vp, _i64, _vp, _vp]),
     "moe_debug_withhold_stream_stage": (ctypes.c_int, [_i32]),
     "moe_debug_withhold_router_stage": (ctypes.c_int, [_i32]),
     "moe_debug_withhold_expert_stage": (ctypes.c_int, [_i32]),

@@ -8,5 +8,7 @@ from .oracle import *  # noqa: F401,F403
 from .oracle import __all__ as _tail
 from .experts import *  # noqa: F401,F403
 from .experts import __all__ as _experts
+from .fp4 import *  # noqa: F401,F403
+from .fp4 import __all__ as _fp4
 
-__all__ = [*_tail, *_experts]
+__all__ = [*_tail, *_experts, *_fp4]
