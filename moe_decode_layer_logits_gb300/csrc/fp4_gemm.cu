@@ -1,88 +1,651 @@
-// Products of 4-bit rows with 4-bit weights: the plain kernel.  A block takes
-// 32 outputs of an expert; a thread one of them for four of its rows at a time.
-#include "common.cuh"
+// Products of rows with weights, both in microscaled 4-bit floating point, on
+// the block-scaled tensor-core instructions:
+// out[r, :] = act(f_e W_e x[src(r)]) for the rows r of segment e.
+//
+// The frame is that of the BF16 products (expert_gemm.cuh, whose tile lists,
+// schedule, epilogue stores and join kernel are used here): the weights are the M
+// side (128 rows a CTA) and the rows the N side with an N of the segment's own
+// size; persistent CTAs, one per SM, single ones with the last round split along
+// K, or pairs (cta_group::2) for large segments.  A stage of the ring holds the
+// same 128 bytes of a row, which are 256 elements here, and beside them the
+// scales:
+//
+//   [128 weight rows: 16 KB][their scales: S words x 512 B][rows][rows' scales]
+//
+// S = 4 (a scale for each 16) or 2 (32) words of four neighbouring scales a row.
+// The tensor core takes scales from tensor memory, word w of 128 rows as four
+// columns [row % 32][row / 32], which tcgen05.cp fills from 512 bytes in the same
+// order.  Weights' scales lie in global memory like that, so one tiled copy brings
+// them.  Those of the rows come with the rows, copied by the gathering warps one
+// row a lane to the place of the row's own word 0 .. S - 1 block, so that the four
+// rows of equal row % 32 fill the same four 16-byte places as their four words
+// will; the relay warp, which stands between the copies and the MMAs anyway,
+// transposes these 4 x 4 words in place.
+//
+// Tensor memory of a pair: accumulators [0, 208) and [256, 464), scales of two
+// stages in between and behind; a stage's scales are copied once the MMAs of the
+// stage before the last have completed.  Single CTAs (up to 128 rows a tile) have
+// scale columns for each of up to eight stages.
+#include "expert_gemm.cuh"
 #include "fp4.h"
-#include "host_util.h"
 
 namespace moe {
 
 namespace {
 
-__device__ __forceinline__ float code_value(uint32_t c) {
-  const uint32_t m = c & 7u;
-  const float v = m < 2 ? 0.5f * static_cast<float>(m) : __uint_as_float(((m >> 1) + 126u) << 23 | (m & 1u) << 22);
-  return c & 8u ? -v : v;
+using namespace umma;
+
+constexpr int kFp4Stages = 8;      // most stages of the ring
+constexpr int kFp4PairRows = 208;  // rows of a pair's tile
+
+struct Fp4Params {
+  GemmParams g;  // x, K: in units of four elements (a BF16 number's bytes)
+  const uint8_t* x_scales;
+  const float* factor;
+  int row_scales;   // scale bytes of a row of x
+  int whole_scales; // a stage's scales of a row are one aligned piece
+};
+
+struct Fp4Barriers {
+  uint64_t full[kFp4Stages], empty[kFp4Stages], landed[kFp4Stages];
+  uint64_t acc_full[2], acc_empty[2];
+  uint64_t drained;
+  uint32_t tmem_base;
+  int abort_flag;
+  int bn, pieces;
+};
+
+constexpr int kFp4Threads(bool pair) { return 32 * (6 + kLoaders + 1) + (pair ? 128 : 0); }
+
+// Instruction descriptor: E2M1 A and B, both K-major, FP32 D, M x N; scales E4M3
+// or E8M0, at byte `id` of each word.
+template <int FORMAT>
+__device__ __forceinline__ uint32_t idesc_fp4(int M, int N, int id) {
+  return (static_cast<uint32_t>(id) << 4) | (1u << 7) | (1u << 10) | (static_cast<uint32_t>(N >> 3) << 17) |
+         (FORMAT == MOE_FP4_MX ? 1u << 23 : 0u) | (static_cast<uint32_t>(M >> 4) << 24) | (static_cast<uint32_t>(id) << 29);
 }
 
-template <int FORMAT>
-__device__ __forceinline__ float scale_value(uint32_t b) {
-  if (FORMAT == MOE_FP4_MX)
-    return b == 0xFFu ? __uint_as_float(0x7FC00000u) : b > 0 ? __uint_as_float(b << 23) : 0x1p-127f;
-  const uint32_t a = b & 0x7Fu;
-  const float v = a == 0x7Fu ? __uint_as_float(0x7FC00000u)
-                  : a >= 8   ? __uint_as_float(((a >> 3) + 120u) << 23 | (a & 7u) << 20)
-                             : static_cast<float>(a) * 0x1p-9f;
-  return v;
+// D (+)= A B with scales; 64 elements of K.
+#define MOE_FP4_MMA(group, kind)                                                                                      \
+  asm volatile(                                                                                                       \
+      "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\t"                                                                     \
+      "mov.b64 a, {%1, %7};\n\t"                                                                                      \
+      "mov.b64 b, {%2, %7};\n\t"                                                                                      \
+      "setp.ne.b32 p, %4, 0;\n\t"                                                                                     \
+      "tcgen05.mma.cta_group::" group ".kind::" kind " [%0], a, b, %3, [%5], [%6], p;\n\t}" ::"r"(d),                \
+      "r"(a_low), "r"(b_low), "r"(idesc), "r"(static_cast<uint32_t>(accumulate)), "r"(sfa), "r"(sfb), "n"(kDescHigh)  \
+      : "memory")
+
+template <bool PAIR, int FORMAT>
+__device__ __forceinline__ void mma_fp4(uint32_t d, uint32_t a_low, uint32_t b_low, uint32_t idesc, uint32_t sfa,
+                                        uint32_t sfb, bool accumulate) {
+  if constexpr (PAIR && FORMAT == MOE_FP4_NV) MOE_FP4_MMA("2", "mxf4nvf4.block_scale.scale_vec::4X");
+  else if constexpr (PAIR) MOE_FP4_MMA("2", "mxf4.block_scale.scale_vec::2X");
+  else if constexpr (FORMAT == MOE_FP4_NV) MOE_FP4_MMA("1", "mxf4nvf4.block_scale.scale_vec::4X");
+  else MOE_FP4_MMA("1", "mxf4.block_scale.scale_vec::2X");
+}
+#undef MOE_FP4_MMA
+
+// 32 x 16 bytes at `low` (a descriptor's low word; no swizzle, 8 rows each 128
+// bytes) to four columns of tensor memory, in all four quarters of the lanes; in a
+// pair both CTAs copy their own.  It comes before MMAs that the thread issues
+// behind it.
+template <bool PAIR>
+__device__ __forceinline__ void copy_scales(uint32_t col, uint32_t low) {
+  constexpr uint32_t kHigh = (128u >> 4) | (1u << 14);
+  if constexpr (PAIR)
+    asm volatile("{\n\t.reg .b64 s;\n\tmov.b64 s, {%1, %2};\n\ttcgen05.cp.cta_group::2.32x128b.warpx4 [%0], s;\n\t}" ::"r"(col),
+                 "r"(low), "n"(kHigh)
+                 : "memory");
+  else
+    asm volatile("{\n\t.reg .b64 s;\n\tmov.b64 s, {%1, %2};\n\ttcgen05.cp.cta_group::1.32x128b.warpx4 [%0], s;\n\t}" ::"r"(col),
+                 "r"(low), "n"(kHigh)
+                 : "memory");
 }
 
-template <int FORMAT>
-__global__ void __launch_bounds__(128) fp4_plain_kernel(const Fp4Gemm g, int n_out, int tiles, int stages) {
-  grid_dependency_wait();
-  allow_dependent_launch();
-  const int e = blockIdx.y, o = blockIdx.x * 32 + (threadIdx.x & 31), sub = threadIdx.x >> 5;
-  const int64_t beg = g.offsets ? g.offsets[e] : 0, cnt = g.offsets ? g.counts[e] : g.n_rows;
-  if (beg < 0 || cnt < 0 || beg + cnt > g.n_rows) {
-    if (blockIdx.x == 0 && threadIdx.x == 0 && g.err_flag) atomicOr(g.err_flag, MOE_FLAG_BAD_INDEX);
+// BYTES (16 or 8) from global to shared memory, asynchronously; the first n of
+// them, zeros behind.
+template <int BYTES>
+__device__ __forceinline__ void copy_async(uint32_t dst, const void* src, int n) {
+  if constexpr (BYTES == 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %3, %2;" ::"r"(dst), "l"(src), "r"(n), "n"(BYTES) : "memory");
+}
+
+// Row tiles of a pair that hold `count` rows.
+__device__ __forceinline__ int pair_tiles(int count) { return count / kFp4PairRows + (count % kFp4PairRows != 0 ? 1 : 0); }
+
+// Row tiles of the one segment of the plain projection in pairs: of the few numbers that hold it,
+// the one whose rounds over the pairs take the fewest rows.
+__device__ __forceinline__ int segment_tiles(int total, int mt, int G) {
+  const int least = pair_tiles(total);
+  int best = least;
+  long long cost = -1;
+  for (int n = least; n < least + 8 && n > 0; ++n) {
+    const long long c = ((static_cast<long long>(n) * mt + G - 1) / G) * round_up((total + n - 1) / n, 16);
+    if (cost < 0 || c < cost) {
+      cost = c;
+      best = n;
+    }
+  }
+  return best;
+}
+
+// The tile list; every thread calls it.  ONE: a single segment of all rows.
+template <bool PAIR, bool ONE>
+__device__ void list_fp4(const GemmParams& p, Tiles t, int mt, int walkers, int* bn_out) {
+  if (!PAIR) {
+    list_tiles<false, ONE ? kParts : kRows>(p, t, mt, walkers, bn_out, blockIdx.x == 0);
     return;
   }
-  if (o >= n_out) return;
-  const float f = g.factor ? g.factor[e] : 1.f;
-  constexpr int B = fp4_block(FORMAT), S = fp4_stage_scales(FORMAT);
-  for (int64_t r = beg + sub; r < beg + cnt; r += 4) {
-    const int64_t tok = g.row_token ? g.row_token[r] : r;
-    float y[2] = {0.f, 0.f};
-    if (tok < 0 || tok >= g.n_x) {
-      if (g.err_flag) atomicOr(g.err_flag, MOE_FLAG_BAD_INDEX);
-    } else {
-      for (int part = 0; part < (g.swiglu ? 2 : 1); ++part) {
-        const int64_t row = static_cast<int64_t>(e) * g.N + o + part * n_out;
-        const int tr = g.swiglu ? (o & 63) / 16 * 32 + part * 16 + (o & 15) : o & 127;
-        const uint8_t* ws = g.w_scales + (static_cast<int64_t>(e) * tiles + (g.swiglu ? o / 64 : o / 128)) * stages * 128 * S;
-        for (int64_t k = 0; k < g.K; k += B) {
-          const int64_t st = k / 256, in = k % 256 / B;
-          float sum = 0.f;
-          for (int j = 0; j < B; j += 2) {
-            const uint32_t a = g.w[(row * g.K + k + j) / 2], b = g.x[(tok * g.K + k + j) / 2];
-            sum += code_value(a & 15u) * code_value(b & 15u) + code_value(a >> 4) * code_value(b >> 4);
-          }
-          y[part] += sum * scale_value<FORMAT>(ws[st * 128 * S + in / 4 * 512 + (tr & 31) * 16 + (tr >> 5) * 4 + (in & 3)]) *
-                     scale_value<FORMAT>(g.x_scales[tok * (g.K / B) + k / B]);
-        }
-        y[part] *= f;
-      }
-      if (g.swiglu) y[0] = y[0] / (1.f + expf(-y[0])) * y[1];
+  if (ONE) {
+    if (threadIdx.x == 0) {
+      t.start[0] = 0;
+      t.count[0] = static_cast<int>(p.n_rows);
+      t.before[0] = 0;
+      t.before[1] = segment_tiles(t.count[0], mt, walkers);
+      *bn_out = kFp4PairRows;
     }
-    static_cast<uint16_t*>(g.out)[r * n_out + o] = static_cast<uint16_t>(pack_bf16x2(y[0], 0.f));
+    __syncthreads();
+    return;
   }
+  // checked segments from the BF16 products' list, then tiles of this kernel's rows
+  list_tiles<true, kRows>(p, t, mt, walkers, bn_out, blockIdx.x == 0);
+  if (threadIdx.x < 32) {
+    const int lane = threadIdx.x, per = (p.E + 31) / 32, b = min(p.E, lane * per), e = min(p.E, b + per);
+    int mine = 0;
+    for (int i = b; i < e; ++i) mine += pair_tiles(t.count[i]);
+    int upto = mine;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const int v = __shfl_up_sync(0xFFFFFFFFu, upto, off);
+      if (lane >= off) upto += v;
+    }
+    int at = upto - mine;
+    for (int i = b; i < e; ++i) {
+      t.before[i] = at;
+      at += pair_tiles(t.count[i]);
+    }
+    if (lane == 31) {
+      t.before[p.E] = upto;
+      *bn_out = kFp4PairRows;
+    }
+  }
+  __syncthreads();
+}
+
+template <int FORMAT, bool SWIGLU, bool PAIR, bool ONE>
+__global__ void __launch_bounds__(512, 1)
+fp4_gemm_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid_constant__ CUtensorMap tmap_s,
+                const __grid_constant__ Fp4Params q) {
+  const GemmParams& p = q.g;
+  constexpr int kWords = fp4_stage_scales(FORMAT) / 4;  // of a row and stage
+  constexpr int kScales = kWords * 512;                 // bytes of 128 rows' scales
+  constexpr int kGroups = PAIR ? 2 : 1;                 // of 128 rows whose scales a stage holds
+  constexpr int kScaleCols = 4 * kWords * (1 + kGroups);
+  constexpr int kRowsAt = kBM * kRowBytes + kScales;    // of a stage
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ Fp4Barriers sb;
+  uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  Piece* piece_s = reinterpret_cast<Piece*>(ring + p.ring_bytes);
+  int* list = reinterpret_cast<int*>(piece_s + kPieces);
+  const Tiles t{list, list + p.E, list + 2 * p.E};
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = PAIR ? static_cast<int>(cg::this_cluster().block_rank()) : 0;
+  const int who = PAIR ? blockIdx.x >> 1 : blockIdx.x;
+  volatile int* abort_v = &sb.abort_flag;
+
+  if (threadIdx.x < kFp4Stages) {
+    // a stage is full when the weights have landed and the rows have been
+    // reported (by each CTA of a pair)
+    mbar_init(&sb.full[threadIdx.x], PAIR ? 3 : 2);
+    mbar_init(&sb.landed[threadIdx.x], 32 * kLoaders);
+    mbar_init(&sb.empty[threadIdx.x], 1);
+    mbar_init_fence();
+  } else if (threadIdx.x < kFp4Stages + 2) {
+    mbar_init(&sb.acc_full[threadIdx.x - kFp4Stages], 1);
+    mbar_init(&sb.acc_empty[threadIdx.x - kFp4Stages], PAIR ? 16 : 4);
+    mbar_init_fence();
+  } else if (threadIdx.x == kFp4Stages + 2) {
+    mbar_init(&sb.drained, 1);
+    sb.abort_flag = 0;
+    mbar_init_fence();
+  } else if (threadIdx.x == kFp4Stages + 3) {
+    prefetch_map(&tmap_w);
+    prefetch_map(&tmap_s);
+  }
+  if (warp == 1) tmem_alloc<PAIR>(&sb.tmem_base, 2 * kAccCols);
+  // the trigger comes behind the wait, so that what is launched next finds this
+  // kernel's own inputs ready
+  grid_dependency_wait();
+  allow_dependent_launch();
+  const int rows_out = (SWIGLU ? 64 : 128) * (PAIR ? 2 : 1), mt = (p.n_out + rows_out - 1) / rows_out;
+  const int weight_tiles = (p.n_out + (SWIGLU ? 63 : 127)) / (SWIGLU ? 64 : 128);
+  const int walkers = static_cast<int>(PAIR ? gridDim.x >> 1 : gridDim.x);
+  list_fp4<PAIR, ONE>(p, t, mt, walkers, &sb.bn);
+  const Schedule s(p, t, mt, walkers, !PAIR);
+  {
+    const int n = s.pieces(who);
+    if (threadIdx.x == 0) sb.pieces = n;
+    for (int i = threadIdx.x; i < min(n, kPieces); i += blockDim.x) piece_s[i] = make_piece(s, t, p.E, who, i, false);
+  }
+  fence_before_sync();
+  __syncthreads();
+  if (PAIR) {  // the peer's barriers are ready before anything signals them
+    cluster_arrive_release();
+    cluster_wait_acquire();
+  }
+  fence_after_sync();
+  const uint32_t tmem = sb.tmem_base;
+  const int row_bytes = (PAIR ? kFp4PairRows / 2 : sb.bn) * kRowBytes;  // of a stage (a pair's CTA holds half of the tile's)
+  const int stage_bytes = round_up(kRowsAt + row_bytes + kGroups * kScales, 1024);
+  const int nstages = min(kFp4Stages, p.ring_bytes / stage_bytes);
+  struct Stage {
+    int st, ph;
+  };
+  auto advance = [&](Stage& x) {
+    if (++x.st == nstages) {
+      x.st = 0;
+      x.ph ^= 1;
+    }
+  };
+  const int pieces = sb.pieces;
+  // all warps walk the pieces in the same order
+  auto next = [&](int& at, Piece& w) {
+    if (at >= pieces) return false;
+    if (at < kPieces) {
+      w = piece_s[at];
+    } else {
+      Piece made;  // (a reference to w itself would keep it out of the registers)
+      make_far_piece(s, t, p.E, who, at, false, &made);
+      w = made;
+    }
+    ++at;
+    return true;
+  };
+  // barriers that the first CTA of a pair keeps for both
+  const uint32_t full0 = PAIR ? cluster_addr(&sb.full[0], 0) : smem_addr(&sb.full[0]);
+  const uint32_t acc_empty0 = PAIR ? cluster_addr(&sb.acc_empty[0], 0) : smem_addr(&sb.acc_empty[0]);
+
+  if (warp == 0) {
+    // -------------------------------------------------------------- weights
+    if (elect_one()) {  // one lane walks and copies
+      const uint64_t once = l2_evict_first_policy(), keep = l2_evict_normal_policy();
+      const int withheld = who == 0 ? p.withhold : -1;
+      constexpr uint32_t bytes = (PAIR ? 2 : 1) * kRowsAt;  // of a stage's copies, in both CTAs of a pair
+      int at = 0;
+      Piece w;
+      int n = 0;  // stages so far
+      Stage x{0, 0};
+      bool stop = false;
+      while (!stop && next(at, w)) {
+        // (a pair's second tile may lie behind the last: its codes read as zeros, its
+        // scales are the last tile's)
+        const int m = PAIR ? w.m * 2 + rank : w.m;
+        const int first = static_cast<int>((static_cast<int64_t>(w.e) * weight_tiles + min(m, weight_tiles - 1)) * s.nkb * (kScales / 1024));
+        const uint64_t pol = w.alone ? once : keep;
+        for (int kb = w.kb0; kb < w.kb1; ++kb, ++n, advance(x)) {
+          if (n >= nstages && !wait(&sb.empty[x.st], x.ph ^ 1, abort_v)) {  // its last MMAs are done
+            stop = true;
+            break;
+          }
+          if (n == withheld) continue;  // neither armed nor loaded: the MMA warp's wait runs out
+          const uint32_t a = smem_addr(ring) + static_cast<uint32_t>(x.st * stage_bytes), bar = full0 + x.st * 8;
+          if (rank == 0) mbar_arrive_expect_tx(&sb.full[x.st], bytes);
+          if (!SWIGLU) {
+            tma_load_5d<PAIR>(a, &tmap_w, kb * kBK, m * 128, 0, 0, w.e, bar, pol);
+          } else if (p.weave) {
+            tma_load_5d<PAIR>(a, &tmap_w, kb * kBK, 0, 0, m * 4, w.e, bar, pol);
+          } else {  // 16 gate rows and their 16 up rows at a time
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              tma_load_5d<PAIR>(a + i * 32 * kRowBytes, &tmap_w, kb * kBK, m * 64 + i * 16, 0, 0, w.e, bar, pol);
+          }
+          tma_load_5d<PAIR>(a + kBM * kRowBytes, &tmap_s, 0, first + kb * (kScales / 1024), 0, 0, 0, bar, pol);
+        }
+      }
+      // drain: no copy may land after this CTA exits (a pair's copies are counted
+      // by its first CTA, and neither leaves before the other)
+      if (rank == 0) {
+        const int from = n > nstages ? n - nstages : 0;
+        Stage y{from % nstages, (from / nstages) & 1};
+        for (int i = from; i < n; ++i, advance(y))
+          if (i != withheld) wait(&sb.full[y.st], y.ph, abort_v, true);
+      }
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    // ---------------------------------------------------------------- MMA
+    if (rank == 0 && elect_one()) {
+      int at = 0;
+      Piece w;
+      const uint32_t a0 = desc_low(smem_addr(ring)), step = static_cast<uint32_t>(stage_bytes) >> 4;
+      const uint32_t s0 = smem_addr(ring) >> 4;  // the same without a leading offset, for the scales
+      Stage x{0, 0}, old{0, 0};
+      int seq = 0, n = 0;
+      bool stop = false;
+      while (!stop && next(at, w)) {
+        const int acc = seq & 1, use = seq >> 1;
+        if (use > 0 && !wait(&sb.acc_empty[acc], (use - 1) & 1, abort_v)) break;
+        fence_after_sync();
+        const uint32_t d = tmem + acc * (PAIR ? kAccCols : kSoloRows);
+        const int cols = round_up(w.nr, 16);
+        for (int kb = w.kb0; kb < w.kb1; ++kb, ++n, advance(x)) {
+          const int st = x.st;
+          if (!wait(&sb.full[st], x.ph, abort_v)) {
+            stop = true;
+            break;
+          }
+          if (PAIR && n >= 2) {  // this stage's scale columns are those of the stage before the last
+            if (!wait(&sb.empty[old.st], old.ph, abort_v)) {
+              stop = true;
+              break;
+            }
+            advance(old);
+          }
+          fence_after_sync();
+          const uint32_t at16 = static_cast<uint32_t>(st) * step;
+          const uint32_t a = a0 + at16, b = a + (kRowsAt >> 4);
+          const uint32_t sf = tmem + (PAIR ? kFp4PairRows + (n & 1) * kAccCols : 2 * kSoloRows + st * kScaleCols);
+          const uint32_t sa = s0 + at16 + (kBM * kRowBytes >> 4), sr = s0 + at16 + (static_cast<uint32_t>(kRowsAt + row_bytes) >> 4);
+#pragma unroll
+          for (int i = 0; i < kWords; ++i) {
+            copy_scales<PAIR>(sf + 4 * i, sa + i * 32);
+#pragma unroll
+            for (int j = 0; j < kGroups; ++j)
+              copy_scales<PAIR>(sf + 4 * kWords + 4 * (i * kGroups + j), sr + j * (kScales >> 4) + i * 32);
+          }
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk) {
+            const int word = FORMAT == MOE_FP4_NV ? kk : kk >> 1, id = FORMAT == MOE_FP4_NV ? 0 : (kk & 1) * 2;
+            mma_fp4<PAIR, FORMAT>(d, a + kk * 2, b + kk * 2, idesc_fp4<FORMAT>(PAIR ? 2 * kBM : kBM, cols, id), sf + 4 * word,
+                                  sf + 4 * kWords + 4 * kGroups * word, kk > 0 || kb != w.kb0);
+          }
+          mma_commit<PAIR>(&sb.empty[st]);
+        }
+        if (stop) break;  // (a peer's epilogue must not take half a sum for a whole one)
+        mma_commit<PAIR>(&sb.acc_full[acc]);
+        ++seq;
+      }
+      mma_commit<PAIR>(&sb.drained);  // also after an abort: fires once the issued MMAs are done
+    }
+    __syncwarp();
+  } else if (warp < 6 || (PAIR && warp > 6 + kLoaders)) {
+    // ----------------------------------------------------------- epilogue
+    const int quarter = warp & 3;  // this warp's quarter of the tensor-memory lanes
+    int at = 0;
+    Piece w;
+    int seq = 0;
+    bool dead = false;  // a wait ran out: this and all later pieces are left as NaN
+    while (next(at, w)) {
+      const int acc = seq & 1, use = seq >> 1;
+      ++seq;
+      const float f = q.factor ? q.factor[w.e] : 1.f;
+      if (!dead) {
+        const bool ok = wait(&sb.acc_full[acc], use & 1, abort_v) && !*abort_v;
+        dead = !__all_sync(0xFFFFFFFFu, ok);
+      }
+      fence_after_sync();
+      const uint32_t d = tmem + acc * (PAIR ? kAccCols : kSoloRows) + (static_cast<uint32_t>(quarter * 32) << 16);
+      float* part = p.partial + static_cast<int64_t>(w.part) * p.slot_rows * kBM + quarter * 32 + lane;
+#pragma unroll 1
+      for (int c = PAIR && warp >= 6 ? 32 : 0; c < w.nr; c += PAIR ? 64 : 32) {  // two sets of warps take turns
+        uint32_t raw[32];
+        if (!dead) {
+          tmem_ld32(d + static_cast<uint32_t>(c), raw);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 32; ++i) raw[i] = 0x7FC00000u;
+        }
+        float v[32];
+#pragma unroll
+        for (int i = 0; i < 32; ++i) v[i] = f * __uint_as_float(raw[i]);
+        if (w.part >= 0) {  // (the factor on each piece: the join only adds)
+#pragma unroll
+          for (int i = 0; i < 32; ++i)
+            if (c + i < w.nr) part[(c + i) * kBM] = v[i];
+        } else {
+          store_cols<SWIGLU, kRows, 32>(p, w, PAIR ? w.m * 2 + rank : w.m, c, quarter, v, bad_rows(p, w, c));
+        }
+      }
+      fence_before_sync();
+      __syncwarp();
+      if (lane == 0 && !dead) {
+        if (PAIR) arrive_cluster(acc_empty0 + acc * 8);
+        else mbar_arrive(&sb.acc_empty[acc]);
+      }
+    }
+  } else if (warp < 6 + kLoaders) {
+    // ------------------------------------------------------------- gather
+    // Warp j takes rows 16 i + 4 j .. + 3 of this CTA's rows, eight lanes a
+    // row, 16 bytes a lane, at their place in the 128-byte swizzle; and of the
+    // scales of all the tile's rows, those with row % 32 = 8 j + lane / 4.
+    const int j = warp - 6, sub = lane >> 3, chunk = lane & 7;
+    const uint32_t place = static_cast<uint32_t>(kRowsAt + (4 * j + sub) * kRowBytes + ((chunk ^ ((4 * j + sub) & 7)) << 4));
+    constexpr int kPasses = PAIR ? (kFp4PairRows / 2 + 15) / 16 : kSoloRows / 16;
+    constexpr int kRowScales = 4 * kWords;  // bytes of a row's scales in a stage
+    const int in = 8 * j + (lane >> 2), of = lane & 3;  // row % 32, row % 128 / 32
+    const uint32_t scale_place = static_cast<uint32_t>(kRowsAt + row_bytes) +
+                                 (FORMAT == MOE_FP4_NV ? of * 512 + in * 16 : (of >> 1) * 512 + in * 16 + (of & 1) * 8);
+    int at = 0;
+    Piece w;
+    int n = 0;
+    Stage x{0, 0};
+    bool stop = false;
+    while (!stop && next(at, w)) {
+      const int mine = PAIR ? round_up(w.nr, 16) / 2 : w.nr;  // rows in this CTA
+      auto token = [&](int r) {  // of the tile's row r, or -1
+        if (r >= w.nr) return -1;
+        const int tok = p.row_token ? p.row_token[w.r0 + r] : w.r0 + r;
+        if (tok >= 0 && tok < p.n_x) return tok;
+        if (p.err_flag) atomicOr(p.err_flag, MOE_FLAG_BAD_INDEX);
+        return -1;
+      };
+      // Rows without a token of their own are not copied: what the stage holds
+      // there reaches only columns that are not stored, or stored as zeros.
+      const uint16_t* src[kPasses];
+      const uint8_t* scale_src[kGroups];
+      unsigned live = 0, scale_live = 0;
+#pragma unroll
+      for (int i = 0; i < kPasses; ++i) {
+        const int r = 16 * i + 4 * j + sub, tok = r < mine ? token(rank * mine + r) : -1;
+        live |= tok >= 0 ? 1u << i : 0u;
+        src[i] = p.x + static_cast<int64_t>(max(tok, 0)) * p.K + chunk * 8 + w.kb0 * kBK;
+      }
+#pragma unroll
+      for (int i = 0; i < kGroups; ++i) {
+        const int tok = token(128 * i + 32 * of + in);
+        scale_live |= tok >= 0 ? 1u << i : 0u;
+        scale_src[i] = q.x_scales + static_cast<int64_t>(max(tok, 0)) * q.row_scales + w.kb0 * kRowScales;
+      }
+      for (int kb = w.kb0; kb < w.kb1; ++kb, ++n, advance(x)) {
+        const int st = x.st;
+        if (n >= nstages && !wait(&sb.empty[st], x.ph ^ 1, abort_v)) {
+          stop = true;
+          break;
+        }
+        const uint32_t base = smem_addr(ring) + static_cast<uint32_t>(st * stage_bytes);
+        const bool inside = kb * kBK + chunk * 8 < p.K;  // zeros behind the end of K
+#pragma unroll
+        for (int i = 0; i < kPasses; ++i) {
+          if ((live >> i) & 1u) copy_async<16>(base + place + i * 16 * kRowBytes, src[i], inside ? 16 : 0);
+          src[i] += kBK;
+        }
+        const int left = q.row_scales - kb * kRowScales;  // a multiple of 4
+#pragma unroll
+        for (int i = 0; i < kGroups; ++i) {
+          const uint32_t dst = base + scale_place + i * kScales;
+          if ((scale_live >> i) & 1u) {
+            if (q.whole_scales) {
+              copy_async<kRowScales>(dst, scale_src[i], kRowScales);
+            } else {  // words: other lengths of K, or scales that start on any word
+#pragma unroll
+              for (int b = 0; b < kWords; ++b) copy_async<4>(dst + 4 * b, 4 * b < left ? scale_src[i] + 4 * b : scale_src[i], 4 * b < left ? 4 : 0);
+            }
+          }
+          scale_src[i] += kRowScales;
+        }
+        copy_arrive(&sb.landed[st]);
+      }
+    }
+    copy_drain();
+  } else {
+    // -------------------------------------------------- gathered rows are in
+    // Lane l transposes the words of rows l, l + 32, l + 64 and l + 96: row by
+    // row, as they came, to word by word.
+    int at = 0;
+    Piece w;
+    Stage x{0, 0};
+    bool stop = false;
+    while (!stop && next(at, w)) {
+      for (int kb = w.kb0; kb < w.kb1; ++kb, advance(x)) {
+        const int st = x.st;
+        const bool ok = wait(&sb.landed[st], x.ph, abort_v);
+        if (!__all_sync(0xFFFFFFFFu, ok)) {
+          stop = true;
+          break;
+        }
+        uint8_t* sc = ring + st * stage_bytes + kRowsAt + row_bytes + lane * 16;
+#pragma unroll
+        for (int i = 0; i < kGroups; ++i) {
+          uint4* const c = reinterpret_cast<uint4*>(sc + i * kScales);
+          if constexpr (FORMAT == MOE_FP4_NV) {
+            const uint4 r0 = c[0], r1 = c[32], r2 = c[64], r3 = c[96];
+            c[0] = make_uint4(r0.x, r1.x, r2.x, r3.x);
+            c[32] = make_uint4(r0.y, r1.y, r2.y, r3.y);
+            c[64] = make_uint4(r0.z, r1.z, r2.z, r3.z);
+            c[96] = make_uint4(r0.w, r1.w, r2.w, r3.w);
+          } else {
+            const uint4 r01 = c[0], r23 = c[32];
+            c[0] = make_uint4(r01.x, r01.z, r23.x, r23.z);
+            c[32] = make_uint4(r01.y, r01.w, r23.y, r23.w);
+          }
+        }
+        proxy_fence();
+        __syncwarp();
+        if (lane == 0) {
+          if (PAIR) arrive_cluster(full0 + st * 8);
+          else mbar_arrive(&sb.full[st]);
+        }
+      }
+    }
+  }
+  __syncwarp();
+  fence_before_sync();
+  __syncthreads();
+  if (threadIdx.x == 32) wait(&sb.drained, 0, abort_v, true);  // no MMA is in flight any more
+  __syncwarp();
+  if (PAIR) {  // the peer's copies and arrivals are over too
+    cluster_arrive_release();
+    cluster_wait_acquire();
+  }
+  if (threadIdx.x == 0 && p.err_flag && *abort_v) atomicOr(p.err_flag, MOE_FLAG_TIMEOUT);
+  if (warp == 1) {
+    fence_after_sync();
+    tmem_dealloc<PAIR>(tmem, 2 * kAccCols);
+  }
+}
+
+// ---------------------------------------------------------------- host side
+
+// Pairs from a mean of this many rows an expert.
+constexpr int64_t kFp4PairMeanRows = 96;
+
+// The weights' scales as rows of 1024 bytes.
+bool scale_map(CUtensorMap* map, const void* scales, int64_t bytes, int box_rows) {
+  const PFN_cuTensorMapEncodeTiled_v12000 fn = encode_fn();
+  const cuuint64_t dims[5] = {256, static_cast<cuuint64_t>(bytes / 1024), 1, 1, 1};
+  const cuuint64_t strides[4] = {1024, static_cast<cuuint64_t>(bytes), static_cast<cuuint64_t>(bytes), static_cast<cuuint64_t>(bytes)};
+  const cuuint32_t box[5] = {256, static_cast<cuuint32_t>(box_rows), 1, 1, 1}, one[5] = {1, 1, 1, 1, 1};
+  return fn && fn(map, CU_TENSOR_MAP_DATA_TYPE_INT32, 5, const_cast<void*>(scales), dims, strides, box, one,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int FORMAT, bool SWIGLU, bool PAIR, bool ONE>
+cudaError_t launch_kernels(const CUtensorMap& mw, const CUtensorMap& ms, const Fp4Params& p, cudaStream_t stream) {
+  static std::atomic<bool> done[64];
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  if (!done[dev].load()) {
+    e = cudaFuncSetAttribute(fp4_gemm_kernel<FORMAT, SWIGLU, PAIR, ONE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             static_cast<int>(gemm_smem(ONE ? 1 : MOE_MAX_E, 0, kRingBytes)));
+    if (e != cudaSuccess) return e;
+    done[dev].store(true);
+  }
+  const int G = PAIR ? gemm_ctas() / 2 * 2 : gemm_ctas();
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(G), 1, 1);
+  cfg.blockDim = dim3(kFp4Threads(PAIR), 1, 1);
+  cfg.dynamicSmemBytes = launch_smem(gemm_smem(p.g.E, 0, p.g.ring_bytes));
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2] = {pdl_attribute(), {}};
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (PAIR) {
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = 2;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.numAttrs = 2;
+  }
+  e = cudaLaunchKernelEx(&cfg, fp4_gemm_kernel<FORMAT, SWIGLU, PAIR, ONE>, mw, ms, p);
+  if constexpr (!PAIR) {
+    if (e != cudaSuccess) return e;
+    cfg.gridDim = dim3(static_cast<unsigned>(G - 1), static_cast<unsigned>((p.g.slot_rows + 15) / 16), 1);
+    cfg.blockDim = dim3(128, 1, 1);
+    cfg.dynamicSmemBytes = launch_smem(static_cast<size_t>(3 * p.g.E + 1) * sizeof(int));
+    e = cudaLaunchKernelEx(&cfg, expert_join_kernel<SWIGLU, ONE ? kParts : kRows>, p.g, G);
+  }
+  return e;
+}
+
+template <int FORMAT, bool SWIGLU>
+cudaError_t prepare_and_launch(const Fp4Gemm& g, cudaStream_t stream) {
+  Fp4Params p{};
+  p.g.x = reinterpret_cast<const uint16_t*>(g.x);
+  p.g.row_token = g.row_token;
+  p.g.offsets = g.offsets;
+  p.g.counts = g.counts;
+  p.g.out = static_cast<uint16_t*>(g.out);
+  p.g.partial = g.partial;
+  p.g.err_flag = g.err_flag;
+  p.g.n_rows = g.n_rows;
+  p.g.n_x = static_cast<int>(g.n_x);
+  p.g.E = static_cast<int>(g.E);
+  p.g.n_out = static_cast<int>(SWIGLU ? g.N / 2 : g.N);
+  p.g.K = static_cast<int>(g.K / 4);
+  p.g.slot_rows = slot_rows_of(g.n_rows);
+  p.g.ring_bytes = kRingBytes;
+  p.g.weave = SWIGLU && p.g.n_out % 16 == 0;
+  p.g.withhold = take_withheld_stage();
+  p.x_scales = g.x_scales;
+  p.factor = g.factor;
+  p.row_scales = static_cast<int>(g.K / fp4_block(FORMAT));
+  p.whole_scales = g.K % kFp4Stage == 0 && aligned(g.x_scales, fp4_stage_scales(FORMAT));
+
+  CUtensorMap mw, ms;
+  if (!weight_map(&mw, g.w, g.E, g.N, g.K / 4, SWIGLU, p.g.weave) ||
+      !scale_map(&ms, g.w_scales, fp4_weight_scales_bytes(g.E, g.N, g.K, FORMAT, SWIGLU), fp4_stage_scales(FORMAT) / 8))
+    return cudaErrorInvalidValue;
+  const bool pair = g.n_rows / g.E >= kFp4PairMeanRows, one = g.offsets == nullptr;
+  if (pair) return one ? launch_kernels<FORMAT, SWIGLU, true, true>(mw, ms, p, stream)
+                       : launch_kernels<FORMAT, SWIGLU, true, false>(mw, ms, p, stream);
+  return one ? launch_kernels<FORMAT, SWIGLU, false, true>(mw, ms, p, stream)
+             : launch_kernels<FORMAT, SWIGLU, false, false>(mw, ms, p, stream);
 }
 
 }  // namespace
 
-int64_t fp4_gemm_workspace(int64_t) { return 0; }
+int64_t fp4_gemm_workspace(int64_t n_rows) { return expert_gemm_workspace(n_rows); }
 
 cudaError_t launch_fp4_gemm(const Fp4Gemm& g, cudaStream_t stream) {
-  const int n_out = static_cast<int>(g.swiglu ? g.N / 2 : g.N);
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>((n_out + 31) / 32), static_cast<unsigned>(g.E), 1);
-  cfg.blockDim = dim3(128, 1, 1);
-  cfg.dynamicSmemBytes = launch_smem(0);
-  cfg.stream = stream;
-  cudaLaunchAttribute attr = pdl_attribute();
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
-  const int tiles = static_cast<int>(fp4_weight_tiles(g.N, g.swiglu)), stages = static_cast<int>(fp4_stages(g.K));
-  return g.format == MOE_FP4_NV ? cudaLaunchKernelEx(&cfg, fp4_plain_kernel<MOE_FP4_NV>, g, n_out, tiles, stages)
-                                : cudaLaunchKernelEx(&cfg, fp4_plain_kernel<MOE_FP4_MX>, g, n_out, tiles, stages);
+  if (g.format == MOE_FP4_NV)
+    return g.swiglu ? prepare_and_launch<MOE_FP4_NV, true>(g, stream) : prepare_and_launch<MOE_FP4_NV, false>(g, stream);
+  return g.swiglu ? prepare_and_launch<MOE_FP4_MX, true>(g, stream) : prepare_and_launch<MOE_FP4_MX, false>(g, stream);
 }
 
 }  // namespace moe

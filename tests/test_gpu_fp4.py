@@ -62,15 +62,13 @@ def check_quantize(M, bits, fmt, g=None):
 
 @pytest.mark.parametrize("fmt,T,K", [("nvfp4", 1, 64), ("nvfp4", 1, 6144), ("nvfp4", 37, 1088), ("nvfp4", 300, 2048),
                                      ("mxfp4", 1, 128), ("mxfp4", 3, 6144), ("mxfp4", 65, 1152), ("mxfp4", 257, 384)])
-@pytest.mark.parametrize("g", [None, 0.0018, 1.0, 0.125, 3.7])
-def test_quantize(M, fmt, T, K, g):
-    if fmt == "mxfp4" and g is not None:
-        pytest.skip("no global scale")
+def test_quantize(M, fmt, T, K):
     rng = np.random.default_rng([300, T, K])
     bits = draw_bf16(rng, (T, K), 1.0)
-    check_quantize(M, bits, fmt, g)
     wide = O.f64_to_bf16_bits(O.bf16_bits_to_f64(bits) * np.exp(2 * rng.standard_normal(K)))
-    check_quantize(M, wide, fmt, g)
+    for g in (None, 0.0018, 1.0, 0.125, 3.7) if fmt == "nvfp4" else (None,):
+        check_quantize(M, bits, fmt, g)
+        check_quantize(M, wide, fmt, g)
 
 
 @pytest.mark.parametrize("fmt", ["nvfp4", "mxfp4"])
@@ -219,6 +217,18 @@ def test_linear_of_words_of_scales_that_end_inside_a_stage(M):
         out, _ = run_linear(M, c, "nvfp4", None)
         want, err = O.fp4_linear(c["xv"], c["wv"], 1.0, None, rel_sum(K))
         check_rows(values(out), want, err, f"K={K}")
+
+
+def test_linear_scales_that_start_on_any_word(M):
+    for fmt, T, K in (("nvfp4", 40, 512), ("mxfp4", 40, 512), ("nvfp4", 300, 256), ("mxfp4", 300, 512)):
+        c = draw_linear(T, 144, K, fmt)
+        want, _ = run_linear(M, c, fmt, None)
+        room = torch.zeros(c["xs"].size + 16, dtype=torch.uint8, device="cuda")
+        for at in (4, 8, 12):
+            xs = room[at:at + c["xs"].size].view(c["xs"].shape)
+            xs.copy_(devn(c["xs"]))
+            got = M.moe_fp4_linear(devn(c["x"]), xs, devn(c["w"]), M.moe_fp4_weight_scales(devn(c["ws"]), format=fmt), format=fmt)
+            assert torch.equal(got, want)
 
 
 @pytest.mark.parametrize("fmt", ["nvfp4", "mxfp4"])
@@ -373,6 +383,31 @@ def test_expert_linear_same_bits_again(M, T, E, k):
     for _ in range(3):
         b, _ = run_expert(M, c, "nvfp4", "swiglu", True)
         assert torch.equal(a, b)
+
+
+def test_expert_linear_overlapping_segments_take_nothing(M):
+    for n in (60, 600):
+        c = draw_layer(8, n, 4, 2, 128, 32, "nvfp4")
+        c["counts"] = np.full(4, n, np.int32)
+        c["offsets"] = np.array([0, 5, 10, 15], np.int32)
+        out, flag = run_expert(M, c, "nvfp4", None, True)
+        assert flag == L.MOE_FLAG_BAD_INDEX and np.all(values(out) == 3.0)
+
+
+@pytest.mark.parametrize("act", [None, "swiglu"])
+@pytest.mark.parametrize("T,gather", [(2, True), (2, False), (300, True), (300, False)])  # single CTAs, pairs
+def test_expert_linear_leaves_nan_where_a_wait_ran_out(M, T, gather, act):
+    c = draw_layer(6, T, 4, 2, 2048, 4096, "nvfp4", gather=gather)
+    want, flag = run_expert(M, c, "nvfp4", act, gather)
+    assert flag == 0
+    for stage in (0, 2):
+        M.moe_debug_withhold_expert_stage(stage)
+        out, flag = run_expert(M, c, "nvfp4", act, gather)
+        assert flag & L.MOE_FLAG_TIMEOUT
+        lost = torch.isnan(out)
+        assert torch.equal(out[~lost], want[~lost]) and 0 < int(lost.sum()) < out.numel()
+    again, flag = run_expert(M, c, "nvfp4", act, gather)
+    assert flag == 0 and torch.equal(again, want)
 
 
 def test_expert_linear_without_any_token(M):
