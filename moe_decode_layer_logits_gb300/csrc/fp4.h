@@ -59,7 +59,7 @@ struct Fp4Gemm {
   int32_t* err_flag;
 };
 
-int64_t fp4_gemm_workspace(int64_t n_rows);
+int64_t fp4_gemm_workspace(int64_t n_rows, int64_t E, int64_t K);
 
 cudaError_t launch_fp4_gemm(const Fp4Gemm& g, cudaStream_t stream);
 

@@ -36,7 +36,11 @@ namespace {
 using namespace umma;
 
 constexpr int kFp4Stages = 8;      // most stages of the ring
-constexpr int kFp4PairRows = 208;  // rows of a pair's tile
+constexpr int kPairAcc = 368;      // tensor-memory columns of a pair's two accumulators
+constexpr int kPairScaleBufs = 3;  // and, behind them, of the scales of a stage each
+constexpr int kEarly = 160;        // columns read before the next tile may start, at least
+                                   // N - 112 of N <= 256 (those it can share) in pieces of 32
+constexpr int kPairSets = 3;       // sets of four warps that read a pair's accumulators
 
 struct Fp4Params {
   GemmParams g;  // x, K: in units of four elements (a BF16 number's bytes)
@@ -44,18 +48,20 @@ struct Fp4Params {
   const float* factor;
   int row_scales;   // scale bytes of a row of x
   int whole_scales; // a stage's scales of a row are one aligned piece
+  uint8_t* row_scale_tiles;  // pairs: [row tile][stage][2][word][32][4 words]
 };
 
 struct Fp4Barriers {
   uint64_t full[kFp4Stages], empty[kFp4Stages], landed[kFp4Stages];
   uint64_t acc_full[2], acc_empty[2];
+  uint64_t acc_early[2];                // pairs: the columns that the next tile may need are read
   uint64_t drained;
   uint32_t tmem_base;
   int abort_flag;
   int bn, pieces;
 };
 
-constexpr int kFp4Threads(bool pair) { return 32 * (6 + kLoaders + 1) + (pair ? 128 : 0); }
+constexpr int kFp4Threads(bool pair) { return 32 * (6 + kLoaders + 1) + (pair ? 128 * (kPairSets - 1) : 0); }
 
 // Instruction descriptor: E2M1 A and B, both K-major, FP32 D, M x N; scales E4M3
 // or E8M0, at byte `id` of each word.
@@ -113,25 +119,6 @@ __device__ __forceinline__ void copy_async(uint32_t dst, const void* src, int n)
     asm volatile("cp.async.ca.shared.global [%0], [%1], %3, %2;" ::"r"(dst), "l"(src), "r"(n), "n"(BYTES) : "memory");
 }
 
-// Row tiles of a pair that hold `count` rows.
-__device__ __forceinline__ int pair_tiles(int count) { return count / kFp4PairRows + (count % kFp4PairRows != 0 ? 1 : 0); }
-
-// Row tiles of the one segment of the plain projection in pairs: of the few numbers that hold it,
-// the one whose rounds over the pairs take the fewest rows.
-__device__ __forceinline__ int segment_tiles(int total, int mt, int G) {
-  const int least = pair_tiles(total);
-  int best = least;
-  long long cost = -1;
-  for (int n = least; n < least + 8 && n > 0; ++n) {
-    const long long c = ((static_cast<long long>(n) * mt + G - 1) / G) * round_up((total + n - 1) / n, 16);
-    if (cost < 0 || c < cost) {
-      cost = c;
-      best = n;
-    }
-  }
-  return best;
-}
-
 // The tile list; every thread calls it.  ONE: a single segment of all rows.
 template <bool PAIR, bool ONE>
 __device__ void list_fp4(const GemmParams& p, Tiles t, int mt, int walkers, int* bn_out) {
@@ -139,51 +126,152 @@ __device__ void list_fp4(const GemmParams& p, Tiles t, int mt, int walkers, int*
     list_tiles<false, ONE ? kParts : kRows>(p, t, mt, walkers, bn_out, blockIdx.x == 0);
     return;
   }
-  if (ONE) {
-    if (threadIdx.x == 0) {
-      t.start[0] = 0;
-      t.count[0] = static_cast<int>(p.n_rows);
-      t.before[0] = 0;
-      t.before[1] = segment_tiles(t.count[0], mt, walkers);
-      *bn_out = kFp4PairRows;
-    }
-    __syncthreads();
+  if (!ONE) {
+    list_tiles<true, kRows>(p, t, mt, walkers, bn_out, blockIdx.x == 0);
     return;
   }
-  // checked segments from the BF16 products' list, then tiles of this kernel's rows
-  list_tiles<true, kRows>(p, t, mt, walkers, bn_out, blockIdx.x == 0);
-  if (threadIdx.x < 32) {
-    const int lane = threadIdx.x, per = (p.E + 31) / 32, b = min(p.E, lane * per), e = min(p.E, b + per);
-    int mine = 0;
-    for (int i = b; i < e; ++i) mine += pair_tiles(t.count[i]);
-    int upto = mine;
-#pragma unroll
-    for (int off = 1; off < 32; off <<= 1) {
-      const int v = __shfl_up_sync(0xFFFFFFFFu, upto, off);
-      if (lane >= off) upto += v;
-    }
-    int at = upto - mine;
-    for (int i = b; i < e; ++i) {
-      t.before[i] = at;
-      at += pair_tiles(t.count[i]);
-    }
-    if (lane == 31) {
-      t.before[p.E] = upto;
-      *bn_out = kFp4PairRows;
-    }
+  if (threadIdx.x == 0) {
+    t.start[0] = 0;
+    t.count[0] = static_cast<int>(p.n_rows);
+    t.before[0] = 0;
+    t.before[1] = scatter_tiles(t.count[0], mt, walkers);
+    *bn_out = kPairRows;
   }
   __syncthreads();
 }
 
+// silu(g) u: the exponential as a power of two, the rounding error of its
+// exponent put back to first order, and an approximate reciprocal; within 2^-21.
+__device__ __forceinline__ float silu_mul_fast(float g, float u) {
+  constexpr float kLog2e = 1.4426950408889634f, kLow = static_cast<float>(1.4426950408889634 - static_cast<double>(kLog2e));
+  const float x = g * -kLog2e;
+  const float rest = fmaf(g, -kLow, fmaf(g, -kLog2e, -x)) * 0.6931471805599453f;
+  float e, r;
+  asm("ex2.approx.f32 %0, %1;" : "=f"(e) : "f"(x));
+  e = e < __int_as_float(0x7F800000) ? fmaf(e, rest, e) : e;
+  asm("rcp.approx.f32 %0, %1;" : "=f"(r) : "f"(1.f + e));
+  return g * r * u;
+}
+
+// 32 columns (rows r0 + c ..) of one weight tile; v[i] is this lane's weight row
+// for row i.  As store_cols of the BF16 products with fewer instructions: here a
+// tile's MMAs take a quarter of their time, and eight warps with that code took
+// longer than they (E = 64, T = 16384: 1631 us, without the epilogue 1284).
+template <bool SWIGLU>
+__device__ __forceinline__ void store_tile(const GemmParams& p, const Piece& w, int m, int c, int quarter,
+                                           const float (&v)[32], unsigned bad) {
+  const int lane = threadIdx.x & 31;
+  // lanes of a row: 0..15 hold gates and 16..31 their ups (after the swap the
+  // lower half finishes row i, the upper half row i + 1); without SwiGLU even
+  // and odd lanes share out the two rows
+  const bool second = SWIGLU ? lane >= 16 : lane & 1;
+  const int o = SWIGLU ? m * 64 + quarter * 16 + (lane & 15) : m * 128 + quarter * 32 + (lane & ~1);
+  const int left = o < p.n_out ? w.nr - c - (second ? 1 : 0) : 0;
+  const int64_t two = 2 * static_cast<int64_t>(p.n_out);
+  uint16_t* at = p.out + (static_cast<int64_t>(w.r0) + c + (second ? 1 : 0)) * p.n_out + o;
+  bad >>= second ? 1 : 0;
+#pragma unroll
+  for (int i = 0; i < 32; i += 2, at += two) {
+    const float other = __shfl_xor_sync(0xFFFFFFFFu, second ? v[i] : v[i + 1], SWIGLU ? 16 : 1);
+    const float a = second ? other : v[i], b = second ? v[i + 1] : other;
+    const bool zero = (bad >> i) & 1u;
+    if (SWIGLU) {
+      const float y = silu_mul_fast(a, b);
+      if (i < left) *at = zero ? 0 : static_cast<uint16_t>(pack_bf16x2(y, 0.f));
+    } else if (i < left) {
+      *reinterpret_cast<uint32_t*>(at) = zero ? 0u : pack_bf16x2(a, b);
+    }
+  }
+}
+
+// Place in the list of the row tile that a piece is of.
+__device__ __forceinline__ int row_tile(const Tiles& t, const Piece& w) {
+  const int ntt = t.before[w.e + 1] - t.before[w.e];
+  if (ntt == 1) return t.before[w.e];
+  // tile_begin's inverse
+  const int cnt = t.count[w.e], sixteens = cnt / 16 + (cnt % 16 != 0 ? 1 : 0), each = sixteens / ntt, more = sixteens % ntt;
+  const int at = (w.r0 - t.start[w.e]) / 16, wide = more * (each + 1);
+  return t.before[w.e] + (at < wide ? at / (each + 1) : more + (at - wide) / each);
+}
+
+// The scales of the rows as pairs read them: for each row tile and stage, two
+// groups of 128 rows in the order of fp4_weight_scales_kernel, so that a stage's
+// come by one tiled copy.  (Gathered by the warps that gather the rows, a line for
+// each row and stage, they took as long as the rows themselves.)  A block takes 128 rows and eight stages at a
+// time, reads eight pieces a row and turns them in shared memory.
+constexpr int kTurnStages = 8;
+
+template <int FORMAT, bool ONE>
+__global__ void __launch_bounds__(256) fp4_row_scales_kernel(const __grid_constant__ Fp4Params q, int mt, int walkers) {
+  const GemmParams& p = q.g;
+  constexpr int kRowScales = fp4_stage_scales(FORMAT), kScales = 128 * kRowScales;
+  using Part = typename std::conditional<FORMAT == MOE_FP4_NV, uint4, uint2>::type;  // a row's scales of a stage
+  extern __shared__ int turn_list[];
+  __shared__ int bn;
+  __shared__ __align__(16) Part turn[kTurnStages][128 + 1];
+  const Tiles t{turn_list, turn_list + p.E, turn_list + 2 * p.E};
+  grid_dependency_wait();
+  allow_dependent_launch();
+  list_fp4<true, ONE>(p, t, mt, walkers, &bn);
+  const int nkb = (p.K + kBK - 1) / kBK, parts = (nkb + kTurnStages - 1) / kTurnStages;
+  const int64_t jobs = static_cast<int64_t>(t.before[p.E]) * 2 * parts;
+  for (int64_t job = blockIdx.x; job < jobs; job += gridDim.x) {
+    const int tile = static_cast<int>(job / (2 * parts)), rest = static_cast<int>(job % (2 * parts));
+    const int group = rest / parts, kb0 = rest % parts * kTurnStages;
+    Piece w;
+    locate(t, p.E, 1, tile, w);  // (with one weight tile: the list of the row tiles)
+    if (w.nr <= 128 * group) continue;
+    __syncthreads();
+    const int st = threadIdx.x & 7, kb = kb0 + st;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int l = i * 32 + (threadIdx.x >> 3), r = 128 * group + l;
+      Part v = {};
+      if (r < w.nr && kb < nkb) {
+        const int tok = p.row_token ? p.row_token[w.r0 + r] : w.r0 + r;
+        if (tok >= 0 && tok < p.n_x) {
+          const uint8_t* src = q.x_scales + static_cast<int64_t>(tok) * q.row_scales + kb * kRowScales;
+          if (q.whole_scales) {
+            v = *reinterpret_cast<const Part*>(src);
+          } else {
+            const int left = q.row_scales - kb * kRowScales;
+#pragma unroll
+            for (int b = 0; b < kRowScales; b += 4)
+              if (b < left) reinterpret_cast<uint32_t*>(&v)[b / 4] = *reinterpret_cast<const uint32_t*>(src + b);
+          }
+        }
+      }
+      turn[st][l] = v;
+    }
+    __syncthreads();
+    const int own = kb0 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+    if (own < nkb) {
+      const Part* from = turn[threadIdx.x >> 5] + lane;
+      uint32_t words[4][kRowScales / 4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const Part v = from[32 * i];
+#pragma unroll
+        for (int b = 0; b < kRowScales / 4; ++b) words[i][b] = reinterpret_cast<const uint32_t*>(&v)[b];
+      }
+      uint8_t* to = q.row_scale_tiles + ((static_cast<int64_t>(tile) * nkb + own) * 2 + group) * kScales + lane * 16;
+#pragma unroll
+      for (int b = 0; b < kRowScales / 4; ++b)
+        *reinterpret_cast<uint4*>(to + 512 * b) = make_uint4(words[0][b], words[1][b], words[2][b], words[3][b]);
+    }
+  }
+}
+
 template <int FORMAT, bool SWIGLU, bool PAIR, bool ONE>
-__global__ void __launch_bounds__(512, 1)
+__global__ void __launch_bounds__(kFp4Threads(PAIR), 1)
 fp4_gemm_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid_constant__ CUtensorMap tmap_s,
-                const __grid_constant__ Fp4Params q) {
+                const __grid_constant__ CUtensorMap tmap_r, const __grid_constant__ Fp4Params q) {
   const GemmParams& p = q.g;
   constexpr int kWords = fp4_stage_scales(FORMAT) / 4;  // of a row and stage
   constexpr int kScales = kWords * 512;                 // bytes of 128 rows' scales
   constexpr int kGroups = PAIR ? 2 : 1;                 // of 128 rows whose scales a stage holds
-  constexpr int kScaleCols = 4 * kWords * (1 + kGroups);
+  constexpr int kBufCols = 4 * kWords * (1 + kGroups);  // scale columns of a stage
+  static_assert(kPairAcc + kPairScaleBufs * kBufCols <= 2 * kAccCols || !PAIR, "a pair's tensor memory");
   constexpr int kRowsAt = kBM * kRowBytes + kScales;    // of a stage
   extern __shared__ uint8_t smem_raw[];
   __shared__ Fp4Barriers sb;
@@ -205,7 +293,8 @@ fp4_gemm_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid_constan
     mbar_init_fence();
   } else if (threadIdx.x < kFp4Stages + 2) {
     mbar_init(&sb.acc_full[threadIdx.x - kFp4Stages], 1);
-    mbar_init(&sb.acc_empty[threadIdx.x - kFp4Stages], PAIR ? 16 : 4);
+    mbar_init(&sb.acc_empty[threadIdx.x - kFp4Stages], PAIR ? 8 * kPairSets : 4);
+    mbar_init(&sb.acc_early[threadIdx.x - kFp4Stages], 8 * kPairSets);
     mbar_init_fence();
   } else if (threadIdx.x == kFp4Stages + 2) {
     mbar_init(&sb.drained, 1);
@@ -214,6 +303,7 @@ fp4_gemm_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid_constan
   } else if (threadIdx.x == kFp4Stages + 3) {
     prefetch_map(&tmap_w);
     prefetch_map(&tmap_s);
+    if (PAIR) prefetch_map(&tmap_r);
   }
   if (warp == 1) tmem_alloc<PAIR>(&sb.tmem_base, 2 * kAccCols);
   // the trigger comes behind the wait, so that what is launched next finds this
@@ -238,7 +328,7 @@ fp4_gemm_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid_constan
   }
   fence_after_sync();
   const uint32_t tmem = sb.tmem_base;
-  const int row_bytes = (PAIR ? kFp4PairRows / 2 : sb.bn) * kRowBytes;  // of a stage (a pair's CTA holds half of the tile's)
+  const int row_bytes = (PAIR ? kPairRows / 2 : sb.bn) * kRowBytes;  // of a stage (a pair's CTA holds half of the tile's)
   const int stage_bytes = round_up(kRowsAt + row_bytes + kGroups * kScales, 1024);
   const int nstages = min(kFp4Stages, p.ring_bytes / stage_bytes);
   struct Stage {
@@ -267,13 +357,20 @@ fp4_gemm_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid_constan
   // barriers that the first CTA of a pair keeps for both
   const uint32_t full0 = PAIR ? cluster_addr(&sb.full[0], 0) : smem_addr(&sb.full[0]);
   const uint32_t acc_empty0 = PAIR ? cluster_addr(&sb.acc_empty[0], 0) : smem_addr(&sb.acc_empty[0]);
+  const uint32_t acc_early0 = PAIR ? cluster_addr(&sb.acc_early[0], 0) : 0;
+  // First column of an accumulator.  A pair's even tiles grow from the left end of
+  // its columns and the odd ones from the right end, so that two of up to 184
+  // columns are apart, and of two larger ones the next may start once the columns
+  // that it takes over, fewer than kEarly, are read.
+  auto acc_at = [&](int seq, int cols) { return (seq & 1) == 0 ? 0 : PAIR ? kPairAcc - cols : kSoloRows; };
 
   if (warp == 0) {
     // -------------------------------------------------------------- weights
     if (elect_one()) {  // one lane walks and copies
       const uint64_t once = l2_evict_first_policy(), keep = l2_evict_normal_policy();
       const int withheld = who == 0 ? p.withhold : -1;
-      constexpr uint32_t bytes = (PAIR ? 2 : 1) * kRowsAt;  // of a stage's copies, in both CTAs of a pair
+      // of a stage's copies, in both CTAs of a pair
+      constexpr uint32_t bytes = PAIR ? 2 * (kRowsAt + kGroups * kScales) : kRowsAt;
       int at = 0;
       Piece w;
       int n = 0;  // stages so far
@@ -285,6 +382,7 @@ fp4_gemm_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid_constan
         const int m = PAIR ? w.m * 2 + rank : w.m;
         const int first = static_cast<int>((static_cast<int64_t>(w.e) * weight_tiles + min(m, weight_tiles - 1)) * s.nkb * (kScales / 1024));
         const uint64_t pol = w.alone ? once : keep;
+        const int rows_first = PAIR ? row_tile(t, w) * static_cast<int>(s.nkb) * (2 * kScales / 1024) : 0;
         for (int kb = w.kb0; kb < w.kb1; ++kb, ++n, advance(x)) {
           if (n >= nstages && !wait(&sb.empty[x.st], x.ph ^ 1, abort_v)) {  // its last MMAs are done
             stop = true;
@@ -303,6 +401,7 @@ fp4_gemm_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid_constan
               tma_load_5d<PAIR>(a + i * 32 * kRowBytes, &tmap_w, kb * kBK, m * 64 + i * 16, 0, 0, w.e, bar, pol);
           }
           tma_load_5d<PAIR>(a + kBM * kRowBytes, &tmap_s, 0, first + kb * (kScales / 1024), 0, 0, 0, bar, pol);
+          if (PAIR) tma_load_5d<PAIR>(a + kRowsAt + row_bytes, &tmap_r, 0, rows_first + kb * (2 * kScales / 1024), 0, 0, 0, bar, keep);
         }
       }
       // drain: no copy may land after this CTA exits (a pair's copies are counted
@@ -322,33 +421,32 @@ fp4_gemm_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid_constan
       Piece w;
       const uint32_t a0 = desc_low(smem_addr(ring)), step = static_cast<uint32_t>(stage_bytes) >> 4;
       const uint32_t s0 = smem_addr(ring) >> 4;  // the same without a leading offset, for the scales
-      Stage x{0, 0}, old{0, 0};
-      int seq = 0, n = 0;
+      Stage x{0, 0};
+      int seq = 0, before = 0;
+      uint32_t pair_sf = 0;  // pairs: the next stage's scale columns
       bool stop = false;
       while (!stop && next(at, w)) {
-        const int acc = seq & 1, use = seq >> 1;
+        const int acc = seq & 1, use = seq >> 1, cols = round_up(w.nr, 16);
         if (use > 0 && !wait(&sb.acc_empty[acc], (use - 1) & 1, abort_v)) break;
+        if (PAIR && seq > 0 && cols + before > kPairAcc && !wait(&sb.acc_early[acc ^ 1], ((seq - 1) >> 1) & 1, abort_v)) break;
+        before = cols;
         fence_after_sync();
-        const uint32_t d = tmem + acc * (PAIR ? kAccCols : kSoloRows);
-        const int cols = round_up(w.nr, 16);
-        for (int kb = w.kb0; kb < w.kb1; ++kb, ++n, advance(x)) {
+        const uint32_t d = tmem + acc_at(seq, cols);
+        for (int kb = w.kb0; kb < w.kb1; ++kb, advance(x)) {
           const int st = x.st;
           if (!wait(&sb.full[st], x.ph, abort_v)) {
             stop = true;
             break;
           }
-          if (PAIR && n >= 2) {  // this stage's scale columns are those of the stage before the last
-            if (!wait(&sb.empty[old.st], old.ph, abort_v)) {
-              stop = true;
-              break;
-            }
-            advance(old);
-          }
           fence_after_sync();
           const uint32_t at16 = static_cast<uint32_t>(st) * step;
           const uint32_t a = a0 + at16, b = a + (kRowsAt >> 4);
-          const uint32_t sf = tmem + (PAIR ? kFp4PairRows + (n & 1) * kAccCols : 2 * kSoloRows + st * kScaleCols);
           const uint32_t sa = s0 + at16 + (kBM * kRowBytes >> 4), sr = s0 + at16 + (static_cast<uint32_t>(kRowsAt + row_bytes) >> 4);
+          uint32_t sf = tmem + 2 * kSoloRows + st * kBufCols;
+          if (PAIR) {
+            sf = tmem + kPairAcc + pair_sf;
+            pair_sf = pair_sf == (kPairScaleBufs - 1) * kBufCols ? 0 : pair_sf + kBufCols;
+          }
 #pragma unroll
           for (int i = 0; i < kWords; ++i) {
             copy_scales<PAIR>(sf + 4 * i, sa + i * 32);
@@ -387,43 +485,61 @@ fp4_gemm_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid_constan
         dead = !__all_sync(0xFFFFFFFFu, ok);
       }
       fence_after_sync();
-      const uint32_t d = tmem + acc * (PAIR ? kAccCols : kSoloRows) + (static_cast<uint32_t>(quarter * 32) << 16);
+      const uint32_t d = tmem + acc_at(seq - 1, round_up(w.nr, 16)) + (static_cast<uint32_t>(quarter * 32) << 16);
       float* part = p.partial + static_cast<int64_t>(w.part) * p.slot_rows * kBM + quarter * 32 + lane;
+      // 32 columns at a time, first those that the next tile may take over; in pairs
+      // the sets of warps take turns
+      const int chunks = (w.nr + 31) >> 5, mine = warp < 6 ? 0 : (warp - 7 - kLoaders) / 4 + 1, by = PAIR ? kPairSets : 1;
+      bool early = PAIR && !dead;
+      auto arrive = [&](uint32_t cluster_bar, uint64_t* bar) {
+        fence_before_sync();
+        __syncwarp();
+        if (lane == 0) {
+          if (PAIR) arrive_cluster(cluster_bar);
+          else mbar_arrive(bar);
+        }
+      };
+      if (early && mine >= chunks) {
+        arrive(acc_early0 + acc * 8, nullptr);
+        early = false;
+      }
+      if (!dead && mine >= chunks) arrive(acc_empty0 + acc * 8, &sb.acc_empty[acc]);
 #pragma unroll 1
-      for (int c = PAIR && warp >= 6 ? 32 : 0; c < w.nr; c += PAIR ? 64 : 32) {  // two sets of warps take turns
-        uint32_t raw[32];
+      for (int i = mine; i < chunks; i += by) {
+        const int c = 32 * (PAIR && acc == 0 ? chunks - 1 - i : i);
+        float v[32];
         if (!dead) {
+          uint32_t raw[32];
           tmem_ld32(d + static_cast<uint32_t>(c), raw);
+#pragma unroll
+          for (int k = 0; k < 32; ++k) v[k] = f * __uint_as_float(raw[k]);
+          // what is in registers need not be kept any longer
+          if (early && (32 * (i + by) >= kEarly || i + by >= chunks)) {
+            arrive(acc_early0 + acc * 8, nullptr);
+            early = false;
+          }
+          if (i + by >= chunks) arrive(acc_empty0 + acc * 8, &sb.acc_empty[acc]);
         } else {
 #pragma unroll
-          for (int i = 0; i < 32; ++i) raw[i] = 0x7FC00000u;
+          for (int k = 0; k < 32; ++k) v[k] = __uint_as_float(0x7FC00000u);
         }
-        float v[32];
-#pragma unroll
-        for (int i = 0; i < 32; ++i) v[i] = f * __uint_as_float(raw[i]);
         if (w.part >= 0) {  // (the factor on each piece: the join only adds)
 #pragma unroll
-          for (int i = 0; i < 32; ++i)
-            if (c + i < w.nr) part[(c + i) * kBM] = v[i];
+          for (int k = 0; k < 32; ++k)
+            if (c + k < w.nr) part[(c + k) * kBM] = v[k];
         } else {
-          store_cols<SWIGLU, kRows, 32>(p, w, PAIR ? w.m * 2 + rank : w.m, c, quarter, v, bad_rows(p, w, c));
+          store_tile<SWIGLU>(p, w, PAIR ? w.m * 2 + rank : w.m, c, quarter, v, bad_rows(p, w, c));
         }
-      }
-      fence_before_sync();
-      __syncwarp();
-      if (lane == 0 && !dead) {
-        if (PAIR) arrive_cluster(acc_empty0 + acc * 8);
-        else mbar_arrive(&sb.acc_empty[acc]);
       }
     }
   } else if (warp < 6 + kLoaders) {
     // ------------------------------------------------------------- gather
     // Warp j takes rows 16 i + 4 j .. + 3 of this CTA's rows, eight lanes a
-    // row, 16 bytes a lane, at their place in the 128-byte swizzle; and of the
-    // scales of all the tile's rows, those with row % 32 = 8 j + lane / 4.
+    // row, 16 bytes a lane, at their place in the 128-byte swizzle; and, in single CTAs,
+    // the scales of the rows with row % 32 = 8 j + lane / 4.
     const int j = warp - 6, sub = lane >> 3, chunk = lane & 7;
     const uint32_t place = static_cast<uint32_t>(kRowsAt + (4 * j + sub) * kRowBytes + ((chunk ^ ((4 * j + sub) & 7)) << 4));
-    constexpr int kPasses = PAIR ? (kFp4PairRows / 2 + 15) / 16 : kSoloRows / 16;
+    constexpr int kPasses = 8;  // of 16 rows
     constexpr int kRowScales = 4 * kWords;  // bytes of a row's scales in a stage
     const int in = 8 * j + (lane >> 2), of = lane & 3;  // row % 32, row % 128 / 32
     const uint32_t scale_place = static_cast<uint32_t>(kRowsAt + row_bytes) +
@@ -445,19 +561,19 @@ fp4_gemm_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid_constan
       // Rows without a token of their own are not copied: what the stage holds
       // there reaches only columns that are not stored, or stored as zeros.
       const uint16_t* src[kPasses];
-      const uint8_t* scale_src[kGroups];
-      unsigned live = 0, scale_live = 0;
+      const uint8_t* scale_src = nullptr;
+      unsigned live = 0;
+      bool scale_live = false;
 #pragma unroll
       for (int i = 0; i < kPasses; ++i) {
         const int r = 16 * i + 4 * j + sub, tok = r < mine ? token(rank * mine + r) : -1;
         live |= tok >= 0 ? 1u << i : 0u;
         src[i] = p.x + static_cast<int64_t>(max(tok, 0)) * p.K + chunk * 8 + w.kb0 * kBK;
       }
-#pragma unroll
-      for (int i = 0; i < kGroups; ++i) {
-        const int tok = token(128 * i + 32 * of + in);
-        scale_live |= tok >= 0 ? 1u << i : 0u;
-        scale_src[i] = q.x_scales + static_cast<int64_t>(max(tok, 0)) * q.row_scales + w.kb0 * kRowScales;
+      if (!PAIR) {
+        const int tok = token(32 * of + in);
+        scale_live = tok >= 0;
+        scale_src = q.x_scales + static_cast<int64_t>(max(tok, 0)) * q.row_scales + w.kb0 * kRowScales;
       }
       for (int kb = w.kb0; kb < w.kb1; ++kb, ++n, advance(x)) {
         const int st = x.st;
@@ -472,19 +588,18 @@ fp4_gemm_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid_constan
           if ((live >> i) & 1u) copy_async<16>(base + place + i * 16 * kRowBytes, src[i], inside ? 16 : 0);
           src[i] += kBK;
         }
-        const int left = q.row_scales - kb * kRowScales;  // a multiple of 4
-#pragma unroll
-        for (int i = 0; i < kGroups; ++i) {
-          const uint32_t dst = base + scale_place + i * kScales;
-          if ((scale_live >> i) & 1u) {
+        if (!PAIR) {
+          const uint32_t dst = base + scale_place;
+          if (scale_live) {
             if (q.whole_scales) {
-              copy_async<kRowScales>(dst, scale_src[i], kRowScales);
+              copy_async<kRowScales>(dst, scale_src, kRowScales);
             } else {  // words: other lengths of K, or scales that start on any word
+              const int left = q.row_scales - kb * kRowScales;  // a multiple of 4
 #pragma unroll
-              for (int b = 0; b < kWords; ++b) copy_async<4>(dst + 4 * b, 4 * b < left ? scale_src[i] + 4 * b : scale_src[i], 4 * b < left ? 4 : 0);
+              for (int b = 0; b < kRowScales; b += 4) copy_async<4>(dst + b, b < left ? scale_src + b : scale_src, b < left ? 4 : 0);
             }
           }
-          scale_src[i] += kRowScales;
+          scale_src += kRowScales;
         }
         copy_arrive(&sb.landed[st]);
       }
@@ -492,24 +607,39 @@ fp4_gemm_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid_constan
     copy_drain();
   } else {
     // -------------------------------------------------- gathered rows are in
-    // Lane l transposes the words of rows l, l + 32, l + 64 and l + 96: row by
-    // row, as they came, to word by word.
     int at = 0;
     Piece w;
     Stage x{0, 0};
     bool stop = false;
-    while (!stop && next(at, w)) {
-      for (int kb = w.kb0; kb < w.kb1; ++kb, advance(x)) {
-        const int st = x.st;
-        const bool ok = wait(&sb.landed[st], x.ph, abort_v);
-        if (!__all_sync(0xFFFFFFFFu, ok)) {
-          stop = true;
-          break;
+    if (PAIR) {
+      // What the MMA thread need not wait for itself (60 ns each time): a stage is
+      // reported once the MMAs that read its scale columns before have completed.
+      if (lane == 0) {
+        Stage old{0, 0};
+        int n = 0;
+        while (!stop && next(at, w)) {
+          for (int kb = w.kb0; kb < w.kb1; ++kb, ++n, advance(x)) {
+            if (!wait(&sb.landed[x.st], x.ph, abort_v) || (n >= kPairScaleBufs && !wait(&sb.empty[old.st], old.ph, abort_v))) {
+              stop = true;
+              break;
+            }
+            if (n >= kPairScaleBufs) advance(old);
+            proxy_fence();
+            arrive_cluster(full0 + x.st * 8);
+          }
         }
-        uint8_t* sc = ring + st * stage_bytes + kRowsAt + row_bytes + lane * 16;
-#pragma unroll
-        for (int i = 0; i < kGroups; ++i) {
-          uint4* const c = reinterpret_cast<uint4*>(sc + i * kScales);
+      }
+    } else {
+      // Lane l transposes the scale words of rows l, l + 32, l + 64 and l + 96: row
+      // by row, as they came, to word by word.
+      while (!stop && next(at, w)) {
+        for (int kb = w.kb0; kb < w.kb1; ++kb, advance(x)) {
+          const bool ok = wait(&sb.landed[x.st], x.ph, abort_v);
+          if (!__all_sync(0xFFFFFFFFu, ok)) {
+            stop = true;
+            break;
+          }
+          uint4* const c = reinterpret_cast<uint4*>(ring + x.st * stage_bytes + kRowsAt + row_bytes + lane * 16);
           if constexpr (FORMAT == MOE_FP4_NV) {
             const uint4 r0 = c[0], r1 = c[32], r2 = c[64], r3 = c[96];
             c[0] = make_uint4(r0.x, r1.x, r2.x, r3.x);
@@ -521,12 +651,9 @@ fp4_gemm_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid_constan
             c[0] = make_uint4(r01.x, r01.z, r23.x, r23.z);
             c[32] = make_uint4(r01.y, r01.w, r23.y, r23.w);
           }
-        }
-        proxy_fence();
-        __syncwarp();
-        if (lane == 0) {
-          if (PAIR) arrive_cluster(full0 + st * 8);
-          else mbar_arrive(&sb.full[st]);
+          proxy_fence();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sb.full[x.st]);
         }
       }
     }
@@ -552,7 +679,17 @@ fp4_gemm_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid_constan
 // Pairs from a mean of this many rows an expert.
 constexpr int64_t kFp4PairMeanRows = 96;
 
-// The weights' scales as rows of 1024 bytes.
+// Row tiles of pairs, at most.
+int64_t pair_tiles_most(int64_t n_rows, int64_t E) { return n_rows / kPairRows + (E < n_rows ? E : n_rows) + 8; }
+
+bool runs_in_pairs(int64_t n_rows, int64_t E) { return n_rows / E >= kFp4PairMeanRows; }
+
+// Bytes of the rows' scales as pairs read them.
+int64_t row_scale_bytes(int64_t n_rows, int64_t E, int64_t K, int format) {
+  return pair_tiles_most(n_rows, E) * fp4_stages(K) * 2 * 128 * fp4_stage_scales(format);
+}
+
+// Scales in the products' order as rows of 1024 bytes.
 bool scale_map(CUtensorMap* map, const void* scales, int64_t bytes, int box_rows) {
   const PFN_cuTensorMapEncodeTiled_v12000 fn = encode_fn();
   const cuuint64_t dims[5] = {256, static_cast<cuuint64_t>(bytes / 1024), 1, 1, 1};
@@ -564,7 +701,8 @@ bool scale_map(CUtensorMap* map, const void* scales, int64_t bytes, int box_rows
 }
 
 template <int FORMAT, bool SWIGLU, bool PAIR, bool ONE>
-cudaError_t launch_kernels(const CUtensorMap& mw, const CUtensorMap& ms, const Fp4Params& p, cudaStream_t stream) {
+cudaError_t launch_kernels(const CUtensorMap& mw, const CUtensorMap& ms, const CUtensorMap& mr, const Fp4Params& p,
+                           cudaStream_t stream) {
   static std::atomic<bool> done[64];
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -578,13 +716,21 @@ cudaError_t launch_kernels(const CUtensorMap& mw, const CUtensorMap& ms, const F
   }
   const int G = PAIR ? gemm_ctas() / 2 * 2 : gemm_ctas();
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(G), 1, 1);
-  cfg.blockDim = dim3(kFp4Threads(PAIR), 1, 1);
-  cfg.dynamicSmemBytes = launch_smem(gemm_smem(p.g.E, 0, p.g.ring_bytes));
   cfg.stream = stream;
   cudaLaunchAttribute attr[2] = {pdl_attribute(), {}};
   cfg.attrs = attr;
   cfg.numAttrs = 1;
+  if constexpr (PAIR) {
+    const int rows_out = SWIGLU ? 128 : 256;
+    cfg.gridDim = dim3(static_cast<unsigned>(4 * gemm_ctas()), 1, 1);
+    cfg.blockDim = dim3(256, 1, 1);
+    cfg.dynamicSmemBytes = launch_smem(static_cast<size_t>(3 * p.g.E + 1) * sizeof(int));
+    e = cudaLaunchKernelEx(&cfg, fp4_row_scales_kernel<FORMAT, ONE>, p, (p.g.n_out + rows_out - 1) / rows_out, G / 2);
+    if (e != cudaSuccess) return e;
+  }
+  cfg.gridDim = dim3(static_cast<unsigned>(G), 1, 1);
+  cfg.blockDim = dim3(kFp4Threads(PAIR), 1, 1);
+  cfg.dynamicSmemBytes = launch_smem(gemm_smem(p.g.E, 0, p.g.ring_bytes));
   if (PAIR) {
     attr[1].id = cudaLaunchAttributeClusterDimension;
     attr[1].val.clusterDim.x = 2;
@@ -592,7 +738,7 @@ cudaError_t launch_kernels(const CUtensorMap& mw, const CUtensorMap& ms, const F
     attr[1].val.clusterDim.z = 1;
     cfg.numAttrs = 2;
   }
-  e = cudaLaunchKernelEx(&cfg, fp4_gemm_kernel<FORMAT, SWIGLU, PAIR, ONE>, mw, ms, p);
+  e = cudaLaunchKernelEx(&cfg, fp4_gemm_kernel<FORMAT, SWIGLU, PAIR, ONE>, mw, ms, mr, p);
   if constexpr (!PAIR) {
     if (e != cudaSuccess) return e;
     cfg.gridDim = dim3(static_cast<unsigned>(G - 1), static_cast<unsigned>((p.g.slot_rows + 15) / 16), 1);
@@ -628,19 +774,28 @@ cudaError_t prepare_and_launch(const Fp4Gemm& g, cudaStream_t stream) {
   p.whole_scales = g.K % kFp4Stage == 0 && aligned(g.x_scales, fp4_stage_scales(FORMAT));
 
   CUtensorMap mw, ms;
+  const int scale_rows = fp4_stage_scales(FORMAT) / 8;  // of 1024 bytes, of a stage and 128 rows
   if (!weight_map(&mw, g.w, g.E, g.N, g.K / 4, SWIGLU, p.g.weave) ||
-      !scale_map(&ms, g.w_scales, fp4_weight_scales_bytes(g.E, g.N, g.K, FORMAT, SWIGLU), fp4_stage_scales(FORMAT) / 8))
+      !scale_map(&ms, g.w_scales, fp4_weight_scales_bytes(g.E, g.N, g.K, FORMAT, SWIGLU), scale_rows))
     return cudaErrorInvalidValue;
-  const bool pair = g.n_rows / g.E >= kFp4PairMeanRows, one = g.offsets == nullptr;
-  if (pair) return one ? launch_kernels<FORMAT, SWIGLU, true, true>(mw, ms, p, stream)
-                       : launch_kernels<FORMAT, SWIGLU, true, false>(mw, ms, p, stream);
-  return one ? launch_kernels<FORMAT, SWIGLU, false, true>(mw, ms, p, stream)
-             : launch_kernels<FORMAT, SWIGLU, false, false>(mw, ms, p, stream);
+  const bool one = g.offsets == nullptr;
+  if (runs_in_pairs(g.n_rows, g.E)) {
+    CUtensorMap mr;
+    p.row_scale_tiles = reinterpret_cast<uint8_t*>(g.partial);
+    if (!scale_map(&mr, p.row_scale_tiles, row_scale_bytes(g.n_rows, g.E, g.K, FORMAT), 2 * scale_rows)) return cudaErrorInvalidValue;
+    return one ? launch_kernels<FORMAT, SWIGLU, true, true>(mw, ms, mr, p, stream)
+               : launch_kernels<FORMAT, SWIGLU, true, false>(mw, ms, mr, p, stream);
+  }
+  return one ? launch_kernels<FORMAT, SWIGLU, false, true>(mw, ms, ms, p, stream)
+             : launch_kernels<FORMAT, SWIGLU, false, false>(mw, ms, ms, p, stream);
 }
 
 }  // namespace
 
-int64_t fp4_gemm_workspace(int64_t n_rows) { return expert_gemm_workspace(n_rows); }
+int64_t fp4_gemm_workspace(int64_t n_rows, int64_t E, int64_t K) {
+  if (n_rows <= 0) return 0;
+  return runs_in_pairs(n_rows, E) ? row_scale_bytes(n_rows, E, K, MOE_FP4_NV) : expert_gemm_workspace(n_rows);
+}
 
 cudaError_t launch_fp4_gemm(const Fp4Gemm& g, cudaStream_t stream) {
   if (g.format == MOE_FP4_NV)
