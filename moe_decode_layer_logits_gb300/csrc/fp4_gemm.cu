@@ -36,10 +36,10 @@ namespace {
 using namespace umma;
 
 constexpr int kFp4Stages = 8;      // most stages of the ring
-constexpr int kPairAcc = 368;      // tensor-memory columns of a pair's two accumulators
-constexpr int kPairScaleBufs = 3;  // and, behind them, of the scales of a stage each
-constexpr int kEarly = 160;        // columns read before the next tile may start, at least
-                                   // N - 112 of N <= 256 (those it can share) in pieces of 32
+constexpr int kPairAcc = 416;      // tensor-memory columns of a pair's two accumulators
+constexpr int kPairScaleBufs = 2;  // and, behind them, of the scales of a stage each
+constexpr int kEarly = 96;         // columns read before the next tile may start, at least
+                                   // N - 160 of N <= 256 (those it can share) in pieces of 32
 constexpr int kPairSets = 3;       // sets of four warps that read a pair's accumulators
 
 struct Fp4Params {
@@ -359,7 +359,7 @@ fp4_gemm_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid_constan
   const uint32_t acc_empty0 = PAIR ? cluster_addr(&sb.acc_empty[0], 0) : smem_addr(&sb.acc_empty[0]);
   const uint32_t acc_early0 = PAIR ? cluster_addr(&sb.acc_early[0], 0) : 0;
   // First column of an accumulator.  A pair's even tiles grow from the left end of
-  // its columns and the odd ones from the right end, so that two of up to 184
+  // its columns and the odd ones from the right end, so that two of up to 208
   // columns are apart, and of two larger ones the next may start once the columns
   // that it takes over, fewer than kEarly, are read.
   auto acc_at = [&](int seq, int cols) { return (seq & 1) == 0 ? 0 : PAIR ? kPairAcc - cols : kSoloRows; };

@@ -16,14 +16,14 @@ int done(cudaError_t e) {
   return launch_status();
 }
 
-// Threads of one launch, 16 elements each.
-constexpr int64_t kMaxThreads = static_cast<int64_t>(0x7FFFFFFF) * 256;
+// Pieces of 16 elements of one launch, two for each of a block's 128 threads.
+constexpr int64_t kMaxPieces = static_cast<int64_t>(0x7FFFFFFF) * 256;
 
 int check_rows(int64_t T, int64_t K, int32_t format) {
   if (T < 0) return MOE_ERR_INVALID_ARG;
   const int st = check_fp4(K, format);
   if (st != MOE_OK) return st;
-  return T > kMaxThreads / (K / 16) ? MOE_ERR_UNSUPPORTED : MOE_OK;
+  return T > kMaxPieces / (K / 16) ? MOE_ERR_UNSUPPORTED : MOE_OK;
 }
 
 int check_products(int64_t N, int64_t K, int32_t format, int32_t act) {
