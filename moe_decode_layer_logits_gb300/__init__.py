@@ -25,6 +25,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import functools
 
 import torch
 
@@ -174,6 +175,7 @@ def _choice(table, value, name):
 
 # the current stream's handle, without a Stream object; None in a torch built without CUDA
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
 def _enter(device, stream):
@@ -184,7 +186,7 @@ def _enter(device, stream):
     no context."""
     if device.type != "cuda":
         raise TypeError("the tensors must be CUDA tensors (there is no CPU path)")
-    if stream is None and _raw_stream is not None and device.index == torch.cuda.current_device():
+    if stream is None and _raw_stream is not None and device.index == _current_device():
         return _raw_stream(device.index), None
     with contextlib.ExitStack() as on:
         on.enter_context(torch.cuda.device(device))
@@ -377,6 +379,20 @@ def _fp4_block(K, fmt):
     return block
 
 
+@functools.lru_cache(maxsize=4096)
+def _fp4_scale_bytes(E, N, K, fmt, act):
+    nbytes = lib().moe_fp4_weight_scales_bytes(E, N, K, fmt, act)
+    if nbytes < 0:
+        raise ValueError("sizes out of range")
+    return nbytes
+
+
+@functools.lru_cache(maxsize=4096)
+def _fp4_workspace_bytes(n_rows, E, N, K, device_index):
+    """(of the current device, whose number of SMs counts)"""
+    return lib().moe_fp4_linear_workspace(n_rows, E, N, K)
+
+
 def _global_scale(t, device):
     if t is None:
         return None
@@ -440,14 +456,11 @@ def moe_fp4_weight_scales(scales, format="nvfp4", act=None, out=None, stream=Non
     K = cols * _FP4_BLOCK[fmt]
     _fp4_block(K, fmt)
     sc = _arg(scales, torch.uint8, "scales", scales.shape, device)
-    L = lib()
-    nbytes = L.moe_fp4_weight_scales_bytes(E, N, K, fmt, act)
-    if nbytes < 0:
-        raise ValueError("sizes out of range")
+    nbytes = _fp4_scale_bytes(E, N, K, fmt, act)
     handle, on = _enter(device, stream)
     try:
         out, o = _out(out, torch.uint8, "out", (nbytes,), device)
-        st = L.moe_fp4_weight_scales(sc, o, E, N, K, fmt, act, handle)
+        st = lib().moe_fp4_weight_scales(sc, o, E, N, K, fmt, act, handle)
     finally:
         if on is not None:
             on.close()
@@ -462,9 +475,7 @@ def _fp4_operands(x, x_scales, w, w_scales, format, factor, act, E):
     (n_x, half), N = x.shape, w.shape[-2]
     K = 2 * half
     block = _fp4_block(K, fmt)
-    nbytes = lib().moe_fp4_weight_scales_bytes(E, N, K, fmt, act)
-    if nbytes < 0:
-        raise ValueError("sizes out of range")
+    nbytes = _fp4_scale_bytes(E, N, K, fmt, act)
     return ((_arg(x, torch.uint8, "x", (n_x, half), device),
              _arg(x_scales, torch.uint8, "x_scales", (n_x, K // block), device),
              _arg(w, torch.uint8, "w", w.shape, device), _arg(w_scales, torch.uint8, "w_scales", (nbytes,), device),
@@ -487,7 +498,7 @@ def moe_fp4_linear(x, x_scales, w, w_scales, format="nvfp4", factor=None, act=No
     handle, on = _enter(device, stream)
     try:
         out, out_ptr = _out(out, torch.bfloat16, "out", (T, n_out), device)
-        ws, ws_ptr, nbytes = _workspace(workspace, L.moe_fp4_linear_workspace(T, 1, N, K), device)
+        ws, ws_ptr, nbytes = _workspace(workspace, _fp4_workspace_bytes(T, 1, N, K, device.index), device)
         st = L.moe_fp4_linear(*ptrs, out_ptr, T, N, K, fmt, act, ws_ptr, nbytes, _flag(err_flag, device), handle)
     finally:
         if on is not None:
@@ -516,7 +527,7 @@ def moe_fp4_expert_linear(x, x_scales, w, w_scales, offsets, counts, format="nvf
     handle, on = _enter(device, stream)
     try:
         out, out_ptr = _out(out, torch.bfloat16, "out", (n_rows, n_out), device)
-        ws, ws_ptr, nbytes = _workspace(workspace, L.moe_fp4_linear_workspace(n_rows, E, N, K), device)
+        ws, ws_ptr, nbytes = _workspace(workspace, _fp4_workspace_bytes(n_rows, E, N, K, device.index), device)
         st = L.moe_fp4_expert_linear(xp, xs, n_x, tok, wp, wsc, fac, off, cnt, out_ptr, n_rows, E, N, K, fmt, act, ws_ptr,
                                      nbytes, _flag(err_flag, device), handle)
     finally:

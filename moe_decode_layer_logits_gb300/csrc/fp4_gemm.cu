@@ -263,7 +263,8 @@ __global__ void __launch_bounds__(256) fp4_row_scales_kernel(const __grid_consta
 }
 
 template <int FORMAT, bool SWIGLU, bool PAIR, bool ONE>
-__global__ void __launch_bounds__(kFp4Threads(PAIR), 1)
+// (512 for single CTAs: registers that leave room for the join kernel beside them)
+__global__ void __launch_bounds__(PAIR ? kFp4Threads(true) : 512, 1)
 fp4_gemm_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid_constant__ CUtensorMap tmap_s,
                 const __grid_constant__ CUtensorMap tmap_r, const __grid_constant__ Fp4Params q) {
   const GemmParams& p = q.g;
@@ -679,6 +680,10 @@ fp4_gemm_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid_constan
 // Pairs from a mean of this many rows an expert.
 constexpr int64_t kFp4PairMeanRows = 96;
 
+// Rows of a partial tile's slot: no more than there are, so that the workspace of
+// a decoded token is a small allocation.
+int fp4_slot_rows(int64_t n_rows) { return static_cast<int>(n_rows < kSoloRows ? n_rows : kSoloRows); }
+
 // Row tiles of pairs, at most.
 int64_t pair_tiles_most(int64_t n_rows, int64_t E) { return n_rows / kPairRows + (E < n_rows ? E : n_rows) + 8; }
 
@@ -764,7 +769,7 @@ cudaError_t prepare_and_launch(const Fp4Gemm& g, cudaStream_t stream) {
   p.g.E = static_cast<int>(g.E);
   p.g.n_out = static_cast<int>(SWIGLU ? g.N / 2 : g.N);
   p.g.K = static_cast<int>(g.K / 4);
-  p.g.slot_rows = slot_rows_of(g.n_rows);
+  p.g.slot_rows = fp4_slot_rows(g.n_rows);
   p.g.ring_bytes = kRingBytes;
   p.g.weave = SWIGLU && p.g.n_out % 16 == 0;
   p.g.withhold = take_withheld_stage();
@@ -774,15 +779,15 @@ cudaError_t prepare_and_launch(const Fp4Gemm& g, cudaStream_t stream) {
   p.whole_scales = g.K % kFp4Stage == 0 && aligned(g.x_scales, fp4_stage_scales(FORMAT));
 
   CUtensorMap mw, ms;
-  const int scale_rows = fp4_stage_scales(FORMAT) / 8;  // of 1024 bytes, of a stage and 128 rows
+  constexpr int kMapRows = fp4_stage_scales(FORMAT) / 8;  // of 1024 bytes, of a stage and 128 rows
   if (!weight_map(&mw, g.w, g.E, g.N, g.K / 4, SWIGLU, p.g.weave) ||
-      !scale_map(&ms, g.w_scales, fp4_weight_scales_bytes(g.E, g.N, g.K, FORMAT, SWIGLU), scale_rows))
+      !scale_map(&ms, g.w_scales, fp4_weight_scales_bytes(g.E, g.N, g.K, FORMAT, SWIGLU), kMapRows))
     return cudaErrorInvalidValue;
   const bool one = g.offsets == nullptr;
   if (runs_in_pairs(g.n_rows, g.E)) {
     CUtensorMap mr;
     p.row_scale_tiles = reinterpret_cast<uint8_t*>(g.partial);
-    if (!scale_map(&mr, p.row_scale_tiles, row_scale_bytes(g.n_rows, g.E, g.K, FORMAT), 2 * scale_rows)) return cudaErrorInvalidValue;
+    if (!scale_map(&mr, p.row_scale_tiles, row_scale_bytes(g.n_rows, g.E, g.K, FORMAT), 2 * kMapRows)) return cudaErrorInvalidValue;
     return one ? launch_kernels<FORMAT, SWIGLU, true, true>(mw, ms, mr, p, stream)
                : launch_kernels<FORMAT, SWIGLU, true, false>(mw, ms, mr, p, stream);
   }
@@ -794,7 +799,8 @@ cudaError_t prepare_and_launch(const Fp4Gemm& g, cudaStream_t stream) {
 
 int64_t fp4_gemm_workspace(int64_t n_rows, int64_t E, int64_t K) {
   if (n_rows <= 0) return 0;
-  return runs_in_pairs(n_rows, E) ? row_scale_bytes(n_rows, E, K, MOE_FP4_NV) : expert_gemm_workspace(n_rows);
+  return runs_in_pairs(n_rows, E) ? row_scale_bytes(n_rows, E, K, MOE_FP4_NV)
+                               : static_cast<int64_t>(gemm_ctas()) * 2 * fp4_slot_rows(n_rows) * kBM * 4;
 }
 
 cudaError_t launch_fp4_gemm(const Fp4Gemm& g, cudaStream_t stream) {
