@@ -109,6 +109,12 @@ __device__ __forceinline__ void copy_scales(uint32_t col, uint32_t low) {
                  : "memory");
 }
 
+// Arrive on `bar` of this CTA once every MMA of the pair issued so far by this
+// thread completes.
+__device__ __forceinline__ void commit_here(uint64_t* bar) {
+  asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_addr(bar)) : "memory");
+}
+
 // BYTES (16 or 8) from global to shared memory, asynchronously; the first n of
 // them, zeros behind.
 template <int BYTES>
@@ -286,9 +292,9 @@ fp4_gemm_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid_constan
   volatile int* abort_v = &sb.abort_flag;
 
   if (threadIdx.x < kFp4Stages) {
-    // a stage is full when the weights have landed and the rows have been
-    // reported (by each CTA of a pair)
-    mbar_init(&sb.full[threadIdx.x], PAIR ? 3 : 2);
+    // a stage is full when the weights have landed, the rows have been reported (by
+    // each CTA of a pair) and, in a pair, the MMAs that used its scale columns are done
+    mbar_init(&sb.full[threadIdx.x], PAIR ? 4 : 2);
     mbar_init(&sb.landed[threadIdx.x], 32 * kLoaders);
     mbar_init(&sb.empty[threadIdx.x], 1);
     mbar_init_fence();
@@ -425,6 +431,9 @@ fp4_gemm_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid_constan
       Stage x{0, 0};
       int seq = 0, before = 0;
       uint32_t pair_sf = 0;  // pairs: the next stage's scale columns
+      int then = kPairScaleBufs;  // and the stage that comes to use them again
+      if (PAIR)
+        for (int i = 0; i < kPairScaleBufs; ++i) mbar_arrive(&sb.full[i]);  // the first ones are free
       bool stop = false;
       while (!stop && next(at, w)) {
         const int acc = seq & 1, use = seq >> 1, cols = round_up(w.nr, 16);
@@ -462,6 +471,12 @@ fp4_gemm_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid_constan
                                   sf + 4 * kWords + 4 * kGroups * word, kk > 0 || kb != w.kb0);
           }
           mma_commit<PAIR>(&sb.empty[st]);
+          if constexpr (PAIR) {
+            // (reported by the commit itself: with a wait of the MMA thread for them a
+            // stage took 60 ns longer, with one of the relay warp 20 to 100)
+            commit_here(&sb.full[then]);
+            if (++then == nstages) then = 0;
+          }
         }
         if (stop) break;  // (a peer's epilogue must not take half a sum for a whole one)
         mma_commit<PAIR>(&sb.acc_full[acc]);
@@ -613,18 +628,13 @@ fp4_gemm_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid_constan
     Stage x{0, 0};
     bool stop = false;
     if (PAIR) {
-      // What the MMA thread need not wait for itself (60 ns each time): a stage is
-      // reported once the MMAs that read its scale columns before have completed.
       if (lane == 0) {
-        Stage old{0, 0};
-        int n = 0;
         while (!stop && next(at, w)) {
-          for (int kb = w.kb0; kb < w.kb1; ++kb, ++n, advance(x)) {
-            if (!wait(&sb.landed[x.st], x.ph, abort_v) || (n >= kPairScaleBufs && !wait(&sb.empty[old.st], old.ph, abort_v))) {
+          for (int kb = w.kb0; kb < w.kb1; ++kb, advance(x)) {
+            if (!wait(&sb.landed[x.st], x.ph, abort_v)) {
               stop = true;
               break;
             }
-            if (n >= kPairScaleBufs) advance(old);
             proxy_fence();
             arrive_cluster(full0 + x.st * 8);
           }
