@@ -146,25 +146,36 @@ __device__ void list_fp4(const GemmParams& p, Tiles t, int mt, int walkers, int*
   __syncthreads();
 }
 
-// silu(g) u: the exponential as a power of two, the rounding error of its
-// exponent put back to first order, and an approximate reciprocal; within 2^-21.
-__device__ __forceinline__ float silu_mul_fast(float g, float u) {
+// silu(g) u for two outputs, the exponential as a power of two: with x = -g log2 e
+// rounded, 2^x is corrected by the rounding error of x to first order, then an
+// approximate reciprocal; within 2^-21.  The bounds keep infinite g and powers
+// beyond FP32's range from 0 * inf: above them 1 / (1 + e^-g) is 1, below 0.
+__device__ __forceinline__ float2 silu_mul2(float2 g, float2 u) {
   constexpr float kLog2e = 1.4426950408889634f, kLow = static_cast<float>(1.4426950408889634 - static_cast<double>(kLog2e));
-  const float x = g * -kLog2e;
-  const float rest = fmaf(g, -kLow, fmaf(g, -kLog2e, -x)) * 0.6931471805599453f;
-  float e, r;
-  asm("ex2.approx.f32 %0, %1;" : "=f"(e) : "f"(x));
-  e = e < __int_as_float(0x7F800000) ? fmaf(e, rest, e) : e;
-  asm("rcp.approx.f32 %0, %1;" : "=f"(r) : "f"(1.f + e));
-  return g * r * u;
+  const float2 b = make_float2(fminf(g.x, 100.f), fminf(g.y, 100.f));
+  float2 x = __fmul2_rn(b, make_float2(-kLog2e, -kLog2e));
+  x = make_float2(fminf(x.x, 127.9f), fminf(x.y, 127.9f));
+  float2 d = __ffma2_rn(b, make_float2(kLog2e, kLog2e), x);  // x less what it should be
+  d = __ffma2_rn(b, make_float2(kLow, kLow), d);
+  d = __fmul2_rn(d, make_float2(-0.6931471805599453f, -0.6931471805599453f));
+  float2 e, r;
+  asm("ex2.approx.f32 %0, %1;" : "=f"(e.x) : "f"(x.x));
+  asm("ex2.approx.f32 %0, %1;" : "=f"(e.y) : "f"(x.y));
+  e = __ffma2_rn(e, d, e);
+  e = __fadd2_rn(e, make_float2(1.f, 1.f));
+  asm("rcp.approx.f32 %0, %1;" : "=f"(r.x) : "f"(e.x));
+  asm("rcp.approx.f32 %0, %1;" : "=f"(r.y) : "f"(e.y));
+  return __fmul2_rn(__fmul2_rn(g, r), u);
 }
 
 // 32 columns (rows r0 + c ..) of one weight tile; v[i] is this lane's weight row
-// for row i.  As store_cols of the BF16 products with fewer instructions: here a
-// tile's MMAs take a quarter of their time, and eight warps with that code took
-// longer than they (E = 64, T = 16384: 1631 us, without the epilogue 1284).
-template <bool SWIGLU>
-__device__ __forceinline__ void store_tile(const GemmParams& p, const Piece& w, int m, int c, int quarter,
+// for row i, without the factor f.  As store_cols of the BF16 products with fewer
+// instructions, two rows a lane at a time: here a tile's MMAs take a quarter of
+// their time, and eight warps with that code took longer than they (E = 64, T =
+// 16384: 1631 us, without the epilogue 1284).  FULL: no row or output is left out
+// and none is bad.
+template <bool SWIGLU, bool FULL>
+__device__ __forceinline__ void store_tile(const GemmParams& p, const Piece& w, int m, int c, int quarter, float f,
                                            const float (&v)[32], unsigned bad) {
   const int lane = threadIdx.x & 31;
   // lanes of a row: 0..15 hold gates and 16..31 their ups (after the swap the
@@ -177,15 +188,26 @@ __device__ __forceinline__ void store_tile(const GemmParams& p, const Piece& w, 
   uint16_t* at = p.out + (static_cast<int64_t>(w.r0) + c + (second ? 1 : 0)) * p.n_out + o;
   bad >>= second ? 1 : 0;
 #pragma unroll
-  for (int i = 0; i < 32; i += 2, at += two) {
-    const float other = __shfl_xor_sync(0xFFFFFFFFu, second ? v[i] : v[i + 1], SWIGLU ? 16 : 1);
-    const float a = second ? other : v[i], b = second ? v[i + 1] : other;
-    const bool zero = (bad >> i) & 1u;
+  for (int i = 0; i < 32; i += 4, at += 2 * two) {
+    float2 a, b;
+    {
+      const float x = __shfl_xor_sync(0xFFFFFFFFu, second ? v[i] : v[i + 1], SWIGLU ? 16 : 1);
+      const float y = __shfl_xor_sync(0xFFFFFFFFu, second ? v[i + 2] : v[i + 3], SWIGLU ? 16 : 1);
+      a = make_float2(second ? x : v[i], second ? y : v[i + 2]);
+      b = make_float2(second ? v[i + 1] : x, second ? v[i + 3] : y);
+    }
+    a = __fmul2_rn(a, make_float2(f, f));
+    b = __fmul2_rn(b, make_float2(f, f));
+    const bool in0 = FULL || i < left, in1 = FULL || i + 2 < left;
+    const bool zero0 = !FULL && ((bad >> i) & 1u), zero1 = !FULL && ((bad >> (i + 2)) & 1u);
     if (SWIGLU) {
-      const float y = silu_mul_fast(a, b);
-      if (i < left) *at = zero ? 0 : static_cast<uint16_t>(pack_bf16x2(y, 0.f));
-    } else if (i < left) {
-      *reinterpret_cast<uint32_t*>(at) = zero ? 0u : pack_bf16x2(a, b);
+      const float2 y = silu_mul2(a, b);
+      const uint32_t u = pack_bf16x2(y.x, y.y);
+      if (in0) *at = zero0 ? 0 : static_cast<uint16_t>(u);
+      if (in1) at[two] = zero1 ? 0 : static_cast<uint16_t>(u >> 16);
+    } else {
+      if (in0) *reinterpret_cast<uint32_t*>(at) = zero0 ? 0u : pack_bf16x2(a.x, b.x);
+      if (in1) *reinterpret_cast<uint32_t*>(at + two) = zero1 ? 0u : pack_bf16x2(a.y, b.y);
     }
   }
 }
@@ -269,8 +291,8 @@ __global__ void __launch_bounds__(256) fp4_row_scales_kernel(const __grid_consta
 }
 
 template <int FORMAT, bool SWIGLU, bool PAIR, bool ONE>
-// (512 for single CTAs: registers that leave room for the join kernel beside them)
-__global__ void __launch_bounds__(PAIR ? kFp4Threads(true) : 512, 1)
+// (for single CTAs too: registers that leave room for the join kernel beside them)
+__global__ void __launch_bounds__(kFp4Threads(true), 1)
 fp4_gemm_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid_constant__ CUtensorMap tmap_s,
                 const __grid_constant__ CUtensorMap tmap_r, const __grid_constant__ Fp4Params q) {
   const GemmParams& p = q.g;
@@ -528,7 +550,7 @@ fp4_gemm_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid_constan
           uint32_t raw[32];
           tmem_ld32(d + static_cast<uint32_t>(c), raw);
 #pragma unroll
-          for (int k = 0; k < 32; ++k) v[k] = f * __uint_as_float(raw[k]);
+          for (int k = 0; k < 32; ++k) v[k] = __uint_as_float(raw[k]);
           // what is in registers need not be kept any longer
           if (early && (32 * (i + by) >= kEarly || i + by >= chunks)) {
             arrive(acc_early0 + acc * 8, nullptr);
@@ -542,9 +564,14 @@ fp4_gemm_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid_constan
         if (w.part >= 0) {  // (the factor on each piece: the join only adds)
 #pragma unroll
           for (int k = 0; k < 32; ++k)
-            if (c + k < w.nr) part[(c + k) * kBM] = v[k];
+            if (c + k < w.nr) part[(c + k) * kBM] = f * v[k];
         } else {
-          store_tile<SWIGLU>(p, w, PAIR ? w.m * 2 + rank : w.m, c, quarter, v, bad_rows(p, w, c));
+          const int m = PAIR ? w.m * 2 + rank : w.m;
+          const unsigned bad = bad_rows(p, w, c);
+          if (c + 32 <= w.nr && (m + 1) * (SWIGLU ? 64 : 128) <= p.n_out && bad == 0)
+            store_tile<SWIGLU, true>(p, w, m, c, quarter, f, v, 0);
+          else
+            store_tile<SWIGLU, false>(p, w, m, c, quarter, f, v, bad);
         }
       }
     }
