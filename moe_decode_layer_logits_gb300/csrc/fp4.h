@@ -1,5 +1,5 @@
 // Microscaled 4-bit floating point: formats, sizes and launches (the kernels
-// are in fp4_quant.cu and fp4_gemm.cu, the calls in fp4_linear.cu).
+// are in fp4_quant.cu and fp4_gemm.cuh, the calls in fp4_linear.cu).
 #pragma once
 
 #include <cuda_runtime.h>
@@ -55,12 +55,13 @@ struct Fp4Gemm {
   int64_t n_x, n_rows, E, N, K;
   int format;
   bool swiglu;
-  float* partial;            // workspace of fp4_gemm_workspace() bytes
+  void* workspace;           // of fp4_gemm_workspace() bytes
   int32_t* err_flag;
 };
 
 int64_t fp4_gemm_workspace(int64_t n_rows, int64_t E, int64_t K);
 
-cudaError_t launch_fp4_gemm(const Fp4Gemm& g, cudaStream_t stream);
+cudaError_t launch_fp4_gemm_nv(const Fp4Gemm& g, cudaStream_t stream);
+cudaError_t launch_fp4_gemm_mx(const Fp4Gemm& g, cudaStream_t stream);
 
 }  // namespace moe

@@ -1,14 +1,13 @@
 // Products of rows with weights, both in microscaled 4-bit floating point, on
 // the block-scaled tensor-core instructions:
-// out[r, :] = act(f_e W_e x[src(r)]) for the rows r of segment e.
+// out[r, :] = act(f_e W_e x[src(r)]) for the rows r of segment e (device code and
+// launches; fp4_gemm_nv.cu and fp4_gemm_mx.cu hold the two formats).
 //
-// The frame is that of the BF16 products (expert_gemm.cuh, whose tile lists,
-// schedule, epilogue stores and join kernel are used here): the weights are the M
-// side (128 rows a CTA) and the rows the N side with an N of the segment's own
-// size; persistent CTAs, one per SM, single ones with the last round split along
-// K, or pairs (cta_group::2) for large segments.  A stage of the ring holds the
-// same 128 bytes of a row, which are 256 elements here, and beside them the
-// scales:
+// The frame is that of the BF16 products (expert_gemm.cuh, whose tile lists and
+// schedule are used here): the weights are the M side (128 rows a CTA) and the
+// rows the N side with an N of the segment's own size; persistent CTAs, one per SM.
+// A stage of the ring holds the same 128 bytes of a row, which are 256 elements
+// here, and beside them the scales:
 //
 //   [128 weight rows: 16 KB][their scales: S words x 512 B][rows][rows' scales]
 //
@@ -16,16 +15,27 @@
 // The tensor core takes scales from tensor memory, word w of 128 rows as four
 // columns [row % 32][row / 32], which tcgen05.cp fills from 512 bytes in the same
 // order.  Weights' scales lie in global memory like that, so one tiled copy brings
-// them.  Those of the rows come with the rows, copied by the gathering warps one
-// row a lane to the place of the row's own word 0 .. S - 1 block, so that the four
-// rows of equal row % 32 fill the same four 16-byte places as their four words
-// will; the relay warp, which stands between the copies and the MMAs anyway,
-// transposes these 4 x 4 words in place.
+// them.
 //
-// Tensor memory of a pair: accumulators [0, 208) and [256, 464), scales of two
-// stages in between and behind; a stage's scales are copied once the MMAs of the
-// stage before the last have completed.  Single CTAs (up to 128 rows a tile) have
-// scale columns for each of up to eight stages.
+// The forms:
+//  - single CTAs: whole tiles round-robin.  (Splitting the last round along K as
+//    the BF16 products do, with a kernel that joins the pieces, was slower
+//    everywhere: T = 1, 8 of 64 experts 29.5 us against 24.0; T = 64, E = 256
+//    431 / 417; K = 1088, N = 2056, 222 rows of 168 experts 47 / 36; K = 2048,
+//    N = 6144, T = 2048 304 / 294.  The SMs of a partial round share the HBM's rate
+//    among fewer, and the pieces wait for two launches.)  The rows' scales are
+//    gathered with the rows, one row a lane, to the place where the four rows of
+//    equal row % 32 fill the same four 16-byte places as their four words will; the
+//    relay warp, which stands between the copies and the MMAs anyway, transposes
+//    these 4 x 4 words in place.
+//  - clusters, where there are too few tiles for the SMs: the CTAs of a cluster
+//    share one tile's K, and each finishes some quarters of the weight rows, whose
+//    partial sums the others send into its shared memory.
+//  - pairs (cta_group::2) for large segments: 256 weight rows and up to 256 rows.
+//
+// Measured, NVFP4, SwiGLU, K = 6144, N = 4096, 8 experts a token, even: FIGURES
+#pragma once
+
 #include "expert_gemm.cuh"
 #include "fp4.h"
 
@@ -41,6 +51,10 @@ constexpr int kPairScaleBufs = 2;  // and, behind them, of the scales of a stage
 constexpr int kEarly = 96;         // columns read before the next tile may start, at least
                                    // N - 160 of N <= 256 (those it can share) in pieces of 32
 constexpr int kPairSets = 3;       // sets of four warps that read a pair's accumulators
+constexpr int kMostSplit = 4;      // CTAs of a cluster that share a tile's K
+
+// How CTAs work on tiles.
+enum Form { kSingle, kCluster, kPair };
 
 struct Fp4Params {
   GemmParams g;  // x, K: in units of four elements (a BF16 number's bytes)
@@ -55,13 +69,18 @@ struct Fp4Barriers {
   uint64_t full[kFp4Stages], empty[kFp4Stages], landed[kFp4Stages];
   uint64_t acc_full[2], acc_empty[2];
   uint64_t acc_early[2];                // pairs: the columns that the next tile may need are read
+  uint64_t received[4];                 // clusters: the other CTAs' sums of a quarter
   uint64_t drained;
   uint32_t tmem_base;
   int abort_flag;
   int bn, pieces;
 };
 
-constexpr int kFp4Threads(bool pair) { return 32 * (6 + kLoaders + 1) + (pair ? 128 * (kPairSets - 1) : 0); }
+constexpr int kFp4Threads(Form form) { return 32 * (6 + kLoaders + 1) + (form == kPair ? 128 * (kPairSets - 1) : 0); }
+
+// Shared memory of a cluster's CTA for the sums that others send it: its 4 / n
+// quarters from n - 1 others, 128 rows each.
+__host__ __device__ constexpr int received_bytes(int n) { return n > 1 ? 4 / n * (n - 1) * kSoloRows * 128 : 0; }
 
 // Instruction descriptor: E2M1 A and B, both K-major, FP32 D, M x N; scales E4M3
 // or E8M0, at byte `id` of each word.
@@ -212,6 +231,14 @@ __device__ __forceinline__ void store_tile(const GemmParams& p, const Piece& w, 
   }
 }
 
+// `bytes` of this CTA's shared memory to that of another CTA of the cluster, counted
+// on a barrier there.
+__device__ __forceinline__ void send(uint32_t remote, uint32_t local, uint32_t bytes, uint32_t remote_bar) {
+  asm volatile("cp.async.bulk.shared::cluster.shared::cta.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(remote),
+               "r"(local), "r"(bytes), "r"(remote_bar)
+               : "memory");
+}
+
 // Place in the list of the row tile that a piece is of.
 __device__ __forceinline__ int row_tile(const Tiles& t, const Piece& w) {
   const int ntt = t.before[w.e + 1] - t.before[w.e];
@@ -290,12 +317,13 @@ __global__ void __launch_bounds__(256) fp4_row_scales_kernel(const __grid_consta
   }
 }
 
-template <int FORMAT, bool SWIGLU, bool PAIR, bool ONE>
-// (for single CTAs too: registers that leave room for the join kernel beside them)
-__global__ void __launch_bounds__(kFp4Threads(true), 1)
+template <int FORMAT, bool SWIGLU, Form FORM, bool ONE>
+// (registers that leave room for another kernel's blocks beside single CTAs too)
+__global__ void __launch_bounds__(kFp4Threads(kPair), 1)
 fp4_gemm_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid_constant__ CUtensorMap tmap_s,
                 const __grid_constant__ CUtensorMap tmap_r, const __grid_constant__ Fp4Params q) {
   const GemmParams& p = q.g;
+  constexpr bool PAIR = FORM == kPair, CLUSTER = FORM == kCluster;
   constexpr int kWords = fp4_stage_scales(FORMAT) / 4;  // of a row and stage
   constexpr int kScales = kWords * 512;                 // bytes of 128 rows' scales
   constexpr int kGroups = PAIR ? 2 : 1;                 // of 128 rows whose scales a stage holds
@@ -305,12 +333,14 @@ fp4_gemm_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid_constan
   extern __shared__ uint8_t smem_raw[];
   __shared__ Fp4Barriers sb;
   uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
-  Piece* piece_s = reinterpret_cast<Piece*>(ring + p.ring_bytes);
+  const int split = CLUSTER ? static_cast<int>(cg::this_cluster().num_blocks()) : 1;
+  float* received = reinterpret_cast<float*>(ring + p.ring_bytes);  // clusters: [own quarter][other CTA][row][32 weight rows]
+  Piece* piece_s = reinterpret_cast<Piece*>(ring + p.ring_bytes + (CLUSTER ? received_bytes(split) : 0));
   int* list = reinterpret_cast<int*>(piece_s + kPieces);
   const Tiles t{list, list + p.E, list + 2 * p.E};
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int rank = PAIR ? static_cast<int>(cg::this_cluster().block_rank()) : 0;
-  const int who = PAIR ? blockIdx.x >> 1 : blockIdx.x;
+  const int rank = PAIR || CLUSTER ? static_cast<int>(cg::this_cluster().block_rank()) : 0;
+  const int who = PAIR ? blockIdx.x >> 1 : blockIdx.x / split;
   volatile int* abort_v = &sb.abort_flag;
 
   if (threadIdx.x < kFp4Stages) {
@@ -329,6 +359,9 @@ fp4_gemm_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid_constan
     mbar_init(&sb.drained, 1);
     sb.abort_flag = 0;
     mbar_init_fence();
+  } else if (threadIdx.x >= 16 && threadIdx.x < 20) {
+    mbar_init(&sb.received[threadIdx.x - 16], 1);
+    mbar_init_fence();
   } else if (threadIdx.x == kFp4Stages + 3) {
     prefetch_map(&tmap_w);
     prefetch_map(&tmap_s);
@@ -337,13 +370,15 @@ fp4_gemm_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid_constan
   if (warp == 1) tmem_alloc<PAIR>(&sb.tmem_base, 2 * kAccCols);
   // the trigger comes behind the wait, so that what is launched next finds this
   // kernel's own inputs ready
-  grid_dependency_wait();
-  allow_dependent_launch();
+  if (!ONE) {
+    grid_dependency_wait();
+    allow_dependent_launch();
+  }
   const int rows_out = (SWIGLU ? 64 : 128) * (PAIR ? 2 : 1), mt = (p.n_out + rows_out - 1) / rows_out;
   const int weight_tiles = (p.n_out + (SWIGLU ? 63 : 127)) / (SWIGLU ? 64 : 128);
-  const int walkers = static_cast<int>(PAIR ? gridDim.x >> 1 : gridDim.x);
-  list_fp4<PAIR, ONE>(p, t, mt, walkers, &sb.bn);
-  const Schedule s(p, t, mt, walkers, !PAIR);
+  const int walkers = static_cast<int>(PAIR ? gridDim.x >> 1 : gridDim.x / split);
+  list_fp4<PAIR, ONE>(p, t, mt, walkers, &sb.bn);  // ONE: reads no global memory
+  const Schedule s(p, t, mt, walkers, false);
   {
     const int n = s.pieces(who);
     if (threadIdx.x == 0) sb.pieces = n;
@@ -351,7 +386,7 @@ fp4_gemm_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid_constan
   }
   fence_before_sync();
   __syncthreads();
-  if (PAIR) {  // the peer's barriers are ready before anything signals them
+  if (PAIR || CLUSTER) {  // the others' barriers are ready before anything signals them
     cluster_arrive_release();
     cluster_wait_acquire();
   }
@@ -369,7 +404,7 @@ fp4_gemm_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid_constan
       x.ph ^= 1;
     }
   };
-  const int pieces = sb.pieces;
+  const int pieces = sb.pieces;  // (of a cluster: one at most)
   // all warps walk the pieces in the same order
   auto next = [&](int& at, Piece& w) {
     if (at >= pieces) return false;
@@ -380,9 +415,37 @@ fp4_gemm_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid_constan
       make_far_piece(s, t, p.E, who, at, false, &made);
       w = made;
     }
+    if (CLUSTER) {  // this CTA's share of K
+      w.kb0 = static_cast<int>(s.nkb) * rank / split;
+      w.kb1 = static_cast<int>(s.nkb) * (rank + 1) / split;
+    }
     ++at;
     return true;
   };
+  if (ONE) {
+    // the first stages' weights into the L2 before the wait (not into shared memory:
+    // a kernel still running may write them)
+    if (!PAIR && warp == 0 && elect_one()) {
+      int ahead = 0;
+      Piece w;
+      if (next(ahead, w)) {
+        const int end = min(w.kb1, w.kb0 + nstages);
+        for (int kb = w.kb0; kb < end; ++kb) {
+          if (!SWIGLU) {
+            tma_prefetch_5d(&tmap_w, kb * kBK, w.m * 128, 0, 0, w.e);
+          } else if (p.weave) {
+            tma_prefetch_5d(&tmap_w, kb * kBK, 0, 0, w.m * 4, w.e);
+          } else {
+            for (int i = 0; i < 4; ++i) tma_prefetch_5d(&tmap_w, kb * kBK, w.m * 64 + i * 16, 0, 0, w.e);
+          }
+          tma_prefetch_5d(&tmap_s, 0, (w.m * static_cast<int>(s.nkb) + kb) * (kScales / 1024), 0, 0, 0);
+        }
+      }
+    }
+    __syncwarp();
+    grid_dependency_wait();
+    allow_dependent_launch();
+  }
   // barriers that the first CTA of a pair keeps for both
   const uint32_t full0 = PAIR ? cluster_addr(&sb.full[0], 0) : smem_addr(&sb.full[0]);
   const uint32_t acc_empty0 = PAIR ? cluster_addr(&sb.acc_empty[0], 0) : smem_addr(&sb.acc_empty[0]);
@@ -419,7 +482,7 @@ fp4_gemm_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid_constan
           }
           if (n == withheld) continue;  // neither armed nor loaded: the MMA warp's wait runs out
           const uint32_t a = smem_addr(ring) + static_cast<uint32_t>(x.st * stage_bytes), bar = full0 + x.st * 8;
-          if (rank == 0) mbar_arrive_expect_tx(&sb.full[x.st], bytes);
+          if (!PAIR || rank == 0) mbar_arrive_expect_tx(&sb.full[x.st], bytes);
           if (!SWIGLU) {
             tma_load_5d<PAIR>(a, &tmap_w, kb * kBK, m * 128, 0, 0, w.e, bar, pol);
           } else if (p.weave) {
@@ -435,7 +498,7 @@ fp4_gemm_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid_constan
       }
       // drain: no copy may land after this CTA exits (a pair's copies are counted
       // by its first CTA, and neither leaves before the other)
-      if (rank == 0) {
+      if (!PAIR || rank == 0) {
         const int from = n > nstages ? n - nstages : 0;
         Stage y{from % nstages, (from / nstages) & 1};
         for (int i = from; i < n; ++i, advance(y))
@@ -445,7 +508,7 @@ fp4_gemm_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid_constan
     __syncwarp();
   } else if (warp == 1) {
     // ---------------------------------------------------------------- MMA
-    if (rank == 0 && elect_one()) {
+    if ((!PAIR || rank == 0) && elect_one()) {
       int at = 0;
       Piece w;
       const uint32_t a0 = desc_low(smem_addr(ring)), step = static_cast<uint32_t>(stage_bytes) >> 4;
@@ -524,7 +587,66 @@ fp4_gemm_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid_constan
       }
       fence_after_sync();
       const uint32_t d = tmem + acc_at(seq - 1, round_up(w.nr, 16)) + (static_cast<uint32_t>(quarter * 32) << 16);
-      float* part = p.partial + static_cast<int64_t>(w.part) * p.slot_rows * kBM + quarter * 32 + lane;
+      const int m = PAIR ? w.m * 2 + rank : w.m;
+      auto store = [&](int c, const float (&v)[32]) {
+        const unsigned bad = bad_rows(p, w, c);
+        if (c + 32 <= w.nr && (m + 1) * (SWIGLU ? 64 : 128) <= p.n_out && bad == 0)
+          store_tile<SWIGLU, true>(p, w, m, c, quarter, f, v, 0);
+        else
+          store_tile<SWIGLU, false>(p, w, m, c, quarter, f, v, bad);
+      };
+      if (CLUSTER) {
+        // a quarter's sums meet in one CTA, in the order of the CTAs
+        const int owner = quarter * split / 4;
+        const uint32_t bytes = static_cast<uint32_t>(w.nr) * 128;
+        if (rank != owner) {
+          // this CTA's ring is idle: its MMAs are done, and every copy before them
+          float* mine = reinterpret_cast<float*>(ring) + quarter * kSoloRows * 32;
+          if (!dead) {
+#pragma unroll 1
+            for (int c = 0; c < w.nr; c += 32) {
+              uint32_t raw[32];
+              tmem_ld32(d + static_cast<uint32_t>(c), raw);
+#pragma unroll
+              for (int k = 0; k < 32; ++k)
+                if (c + k < w.nr) mine[(c + k) * 32 + lane] = __uint_as_float(raw[k]);
+            }
+            proxy_fence();
+            __syncwarp();
+            if (lane == 0) {
+              const int slot = (quarter - owner * 4 / split) * (split - 1) + (rank < owner ? rank : rank - 1);
+              send(cluster_addr(received + slot * kSoloRows * 32, owner), smem_addr(mine), bytes,
+                   cluster_addr(&sb.received[quarter], owner));
+            }
+          }
+          continue;
+        }
+        if (lane == 0) mbar_arrive_expect_tx(&sb.received[quarter], bytes * (split - 1));
+        __syncwarp();
+        const bool ok = wait(&sb.received[quarter], 0, abort_v, true);  // (nothing lands behind this CTA's end)
+        dead = !__all_sync(0xFFFFFFFFu, ok) || dead;
+        const float* others = received + (quarter - owner * 4 / split) * (split - 1) * kSoloRows * 32 + lane;
+#pragma unroll 1
+        for (int c = 0; c < w.nr; c += 32) {
+          float v[32];
+          if (!dead) {
+            uint32_t raw[32];
+            tmem_ld32(d + static_cast<uint32_t>(c), raw);
+#pragma unroll
+            for (int k = 0; k < 32; ++k) v[k] = 0.f;
+            for (int r = 0; r < split; ++r) {
+              const float* from = others + ((r < rank ? r : r - 1) * kSoloRows + c) * 32;
+#pragma unroll
+              for (int k = 0; k < 32; ++k) v[k] += r == rank ? __uint_as_float(raw[k]) : c + k < w.nr ? from[k * 32] : 0.f;
+            }
+          } else {
+#pragma unroll
+            for (int k = 0; k < 32; ++k) v[k] = __uint_as_float(0x7FC00000u);
+          }
+          store(c, v);
+        }
+        continue;
+      }
       // 32 columns at a time, first those that the next tile may take over; in pairs
       // the sets of warps take turns
       const int chunks = (w.nr + 31) >> 5, mine = warp < 6 ? 0 : (warp - 7 - kLoaders) / 4 + 1, by = PAIR ? kPairSets : 1;
@@ -561,18 +683,7 @@ fp4_gemm_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid_constan
 #pragma unroll
           for (int k = 0; k < 32; ++k) v[k] = __uint_as_float(0x7FC00000u);
         }
-        if (w.part >= 0) {  // (the factor on each piece: the join only adds)
-#pragma unroll
-          for (int k = 0; k < 32; ++k)
-            if (c + k < w.nr) part[(c + k) * kBM] = f * v[k];
-        } else {
-          const int m = PAIR ? w.m * 2 + rank : w.m;
-          const unsigned bad = bad_rows(p, w, c);
-          if (c + 32 <= w.nr && (m + 1) * (SWIGLU ? 64 : 128) <= p.n_out && bad == 0)
-            store_tile<SWIGLU, true>(p, w, m, c, quarter, f, v, 0);
-          else
-            store_tile<SWIGLU, false>(p, w, m, c, quarter, f, v, bad);
-        }
+        store(c, v);
       }
     }
   } else if (warp < 6 + kLoaders) {
@@ -609,7 +720,7 @@ fp4_gemm_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid_constan
       bool scale_live = false;
 #pragma unroll
       for (int i = 0; i < kPasses; ++i) {
-        const int r = 16 * i + 4 * j + sub, tok = r < mine ? token(rank * mine + r) : -1;
+        const int r = 16 * i + 4 * j + sub, tok = r < mine ? token((PAIR ? rank * mine : 0) + r) : -1;
         live |= tok >= 0 ? 1u << i : 0u;
         src[i] = p.x + static_cast<int64_t>(max(tok, 0)) * p.K + chunk * 8 + w.kb0 * kBK;
       }
@@ -701,7 +812,7 @@ fp4_gemm_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid_constan
   __syncthreads();
   if (threadIdx.x == 32) wait(&sb.drained, 0, abort_v, true);  // no MMA is in flight any more
   __syncwarp();
-  if (PAIR) {  // the peer's copies and arrivals are over too
+  if (PAIR || CLUSTER) {  // the others' copies and arrivals are over too
     cluster_arrive_release();
     cluster_wait_acquire();
   }
@@ -717,22 +828,28 @@ fp4_gemm_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid_constan
 // Pairs from a mean of this many rows an expert.
 constexpr int64_t kFp4PairMeanRows = 96;
 
-// Rows of a partial tile's slot: no more than there are, so that the workspace of
-// a decoded token is a small allocation.
-int fp4_slot_rows(int64_t n_rows) { return static_cast<int>(n_rows < kSoloRows ? n_rows : kSoloRows); }
-
 // Row tiles of pairs, at most.
-int64_t pair_tiles_most(int64_t n_rows, int64_t E) { return n_rows / kPairRows + (E < n_rows ? E : n_rows) + 8; }
+inline int64_t pair_tiles_most(int64_t n_rows, int64_t E) { return n_rows / kPairRows + (E < n_rows ? E : n_rows) + 8; }
 
-bool runs_in_pairs(int64_t n_rows, int64_t E) { return n_rows / E >= kFp4PairMeanRows; }
+inline bool runs_in_pairs(int64_t n_rows, int64_t E) { return n_rows / E >= kFp4PairMeanRows; }
 
 // Bytes of the rows' scales as pairs read them.
-int64_t row_scale_bytes(int64_t n_rows, int64_t E, int64_t K, int format) {
+inline int64_t row_scale_bytes(int64_t n_rows, int64_t E, int64_t K, int format) {
   return pair_tiles_most(n_rows, E) * fp4_stages(K) * 2 * 128 * fp4_stage_scales(format);
 }
 
+// CTAs that share a tile's K: as many (1, 2 or 4) as leave one wave of tiles, of
+// which the rows make at most that many.  Clusters of four fill 36 x 4 SMs.
+inline int split_of(int64_t n_rows, int64_t E, int64_t weight_tiles, int64_t stages, bool one) {
+  const int64_t row = one ? (n_rows <= kSoloRows ? 1 : (n_rows + kSoloRows - 1) / kSoloRows) : n_rows / 32 + (E < n_rows ? E : n_rows);
+  const int64_t tiles = row * weight_tiles;
+  for (int n = kMostSplit; n > 1; n /= 2)
+    if (tiles <= gemm_ctas() / n && (n < 4 || tiles <= 36) && stages >= n) return n;
+  return 1;
+}
+
 // Scales in the products' order as rows of 1024 bytes.
-bool scale_map(CUtensorMap* map, const void* scales, int64_t bytes, int box_rows) {
+inline bool scale_map(CUtensorMap* map, const void* scales, int64_t bytes, int box_rows) {
   const PFN_cuTensorMapEncodeTiled_v12000 fn = encode_fn();
   const cuuint64_t dims[5] = {256, static_cast<cuuint64_t>(bytes / 1024), 1, 1, 1};
   const cuuint64_t strides[4] = {1024, static_cast<cuuint64_t>(bytes), static_cast<cuuint64_t>(bytes), static_cast<cuuint64_t>(bytes)};
@@ -742,27 +859,30 @@ bool scale_map(CUtensorMap* map, const void* scales, int64_t bytes, int box_rows
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int FORMAT, bool SWIGLU, bool PAIR, bool ONE>
-cudaError_t launch_kernels(const CUtensorMap& mw, const CUtensorMap& ms, const CUtensorMap& mr, const Fp4Params& p,
-                           cudaStream_t stream) {
+template <int FORMAT, bool SWIGLU, Form FORM, bool ONE>
+cudaError_t launch_fp4(const CUtensorMap& mw, const CUtensorMap& ms, const CUtensorMap& mr, Fp4Params& p, int split,
+                       cudaStream_t stream) {
   static std::atomic<bool> done[64];
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
   if (!done[dev].load()) {
-    e = cudaFuncSetAttribute(fp4_gemm_kernel<FORMAT, SWIGLU, PAIR, ONE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    e = cudaFuncSetAttribute(fp4_gemm_kernel<FORMAT, SWIGLU, FORM, ONE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              static_cast<int>(gemm_smem(ONE ? 1 : MOE_MAX_E, 0, kRingBytes)));
     if (e != cudaSuccess) return e;
     done[dev].store(true);
   }
-  const int G = PAIR ? gemm_ctas() / 2 * 2 : gemm_ctas();
+  p.g.ring_bytes = kRingBytes - (FORM == kCluster ? received_bytes(split) : 0);
+  int G = gemm_ctas();
+  if (FORM == kPair) G = G / 2 * 2;
+  if (FORM == kCluster) G = G / split * split;
   cudaLaunchConfig_t cfg = {};
   cfg.stream = stream;
   cudaLaunchAttribute attr[2] = {pdl_attribute(), {}};
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  if constexpr (PAIR) {
+  if constexpr (FORM == kPair) {
     const int rows_out = SWIGLU ? 128 : 256;
     cfg.gridDim = dim3(static_cast<unsigned>(4 * gemm_ctas()), 1, 1);
     cfg.blockDim = dim3(256, 1, 1);
@@ -771,27 +891,19 @@ cudaError_t launch_kernels(const CUtensorMap& mw, const CUtensorMap& ms, const C
     if (e != cudaSuccess) return e;
   }
   cfg.gridDim = dim3(static_cast<unsigned>(G), 1, 1);
-  cfg.blockDim = dim3(kFp4Threads(PAIR), 1, 1);
-  cfg.dynamicSmemBytes = launch_smem(gemm_smem(p.g.E, 0, p.g.ring_bytes));
-  if (PAIR) {
+  cfg.blockDim = dim3(kFp4Threads(FORM), 1, 1);
+  cfg.dynamicSmemBytes = launch_smem(gemm_smem(p.g.E, 0, kRingBytes));
+  if (FORM != kSingle) {
     attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = 2;
+    attr[1].val.clusterDim.x = FORM == kPair ? 2 : static_cast<unsigned>(split);
     attr[1].val.clusterDim.y = 1;
     attr[1].val.clusterDim.z = 1;
     cfg.numAttrs = 2;
   }
-  e = cudaLaunchKernelEx(&cfg, fp4_gemm_kernel<FORMAT, SWIGLU, PAIR, ONE>, mw, ms, mr, p);
-  if constexpr (!PAIR) {
-    if (e != cudaSuccess) return e;
-    cfg.gridDim = dim3(static_cast<unsigned>(G - 1), static_cast<unsigned>((p.g.slot_rows + 15) / 16), 1);
-    cfg.blockDim = dim3(128, 1, 1);
-    cfg.dynamicSmemBytes = launch_smem(static_cast<size_t>(3 * p.g.E + 1) * sizeof(int));
-    e = cudaLaunchKernelEx(&cfg, expert_join_kernel<SWIGLU, ONE ? kParts : kRows>, p.g, G);
-  }
-  return e;
+  return cudaLaunchKernelEx(&cfg, fp4_gemm_kernel<FORMAT, SWIGLU, FORM, ONE>, mw, ms, mr, p);
 }
 
-template <int FORMAT, bool SWIGLU>
+template <int FORMAT, bool SWIGLU, bool ONE>
 cudaError_t prepare_and_launch(const Fp4Gemm& g, cudaStream_t stream) {
   Fp4Params p{};
   p.g.x = reinterpret_cast<const uint16_t*>(g.x);
@@ -799,15 +911,12 @@ cudaError_t prepare_and_launch(const Fp4Gemm& g, cudaStream_t stream) {
   p.g.offsets = g.offsets;
   p.g.counts = g.counts;
   p.g.out = static_cast<uint16_t*>(g.out);
-  p.g.partial = g.partial;
   p.g.err_flag = g.err_flag;
   p.g.n_rows = g.n_rows;
   p.g.n_x = static_cast<int>(g.n_x);
   p.g.E = static_cast<int>(g.E);
   p.g.n_out = static_cast<int>(SWIGLU ? g.N / 2 : g.N);
   p.g.K = static_cast<int>(g.K / 4);
-  p.g.slot_rows = fp4_slot_rows(g.n_rows);
-  p.g.ring_bytes = kRingBytes;
   p.g.weave = SWIGLU && p.g.n_out % 16 == 0;
   p.g.withhold = take_withheld_stage();
   p.x_scales = g.x_scales;
@@ -820,30 +929,23 @@ cudaError_t prepare_and_launch(const Fp4Gemm& g, cudaStream_t stream) {
   if (!weight_map(&mw, g.w, g.E, g.N, g.K / 4, SWIGLU, p.g.weave) ||
       !scale_map(&ms, g.w_scales, fp4_weight_scales_bytes(g.E, g.N, g.K, FORMAT, SWIGLU), kMapRows))
     return cudaErrorInvalidValue;
-  const bool one = g.offsets == nullptr;
   if (runs_in_pairs(g.n_rows, g.E)) {
     CUtensorMap mr;
-    p.row_scale_tiles = reinterpret_cast<uint8_t*>(g.partial);
+    p.row_scale_tiles = static_cast<uint8_t*>(g.workspace);
     if (!scale_map(&mr, p.row_scale_tiles, row_scale_bytes(g.n_rows, g.E, g.K, FORMAT), 2 * kMapRows)) return cudaErrorInvalidValue;
-    return one ? launch_kernels<FORMAT, SWIGLU, true, true>(mw, ms, mr, p, stream)
-               : launch_kernels<FORMAT, SWIGLU, true, false>(mw, ms, mr, p, stream);
+    return launch_fp4<FORMAT, SWIGLU, kPair, ONE>(mw, ms, mr, p, 1, stream);
   }
-  return one ? launch_kernels<FORMAT, SWIGLU, false, true>(mw, ms, ms, p, stream)
-             : launch_kernels<FORMAT, SWIGLU, false, false>(mw, ms, ms, p, stream);
+  const int split = split_of(g.n_rows, g.E, fp4_weight_tiles(g.N, SWIGLU), fp4_stages(g.K), ONE);
+  if (split > 1) return launch_fp4<FORMAT, SWIGLU, kCluster, ONE>(mw, ms, ms, p, split, stream);
+  return launch_fp4<FORMAT, SWIGLU, kSingle, ONE>(mw, ms, ms, p, 1, stream);
+}
+
+template <int FORMAT>
+cudaError_t launch_format(const Fp4Gemm& g, cudaStream_t stream) {
+  const bool one = g.offsets == nullptr;
+  if (g.swiglu) return one ? prepare_and_launch<FORMAT, true, true>(g, stream) : prepare_and_launch<FORMAT, true, false>(g, stream);
+  return one ? prepare_and_launch<FORMAT, false, true>(g, stream) : prepare_and_launch<FORMAT, false, false>(g, stream);
 }
 
 }  // namespace
-
-int64_t fp4_gemm_workspace(int64_t n_rows, int64_t E, int64_t K) {
-  if (n_rows <= 0) return 0;
-  return runs_in_pairs(n_rows, E) ? row_scale_bytes(n_rows, E, K, MOE_FP4_NV)
-                               : static_cast<int64_t>(gemm_ctas()) * 2 * fp4_slot_rows(n_rows) * kBM * 4;
-}
-
-cudaError_t launch_fp4_gemm(const Fp4Gemm& g, cudaStream_t stream) {
-  if (g.format == MOE_FP4_NV)
-    return g.swiglu ? prepare_and_launch<MOE_FP4_NV, true>(g, stream) : prepare_and_launch<MOE_FP4_NV, false>(g, stream);
-  return g.swiglu ? prepare_and_launch<MOE_FP4_MX, true>(g, stream) : prepare_and_launch<MOE_FP4_MX, false>(g, stream);
-}
-
 }  // namespace moe

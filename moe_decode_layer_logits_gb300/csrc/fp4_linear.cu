@@ -1,5 +1,5 @@
 // The calls of the 4-bit operators: argument checks (the kernels are in
-// fp4_quant.cu and fp4_gemm.cu).
+// fp4_quant.cu and fp4_gemm.cuh).
 #include "expert_gemm.h"
 #include "fp4.h"
 #include "host_util.h"
@@ -100,7 +100,7 @@ int products(const Fp4Gemm& g, int32_t act, void* workspace, int64_t workspace_b
       !aligned(workspace, 16) || !aligned(g.row_token, 4) || !aligned(g.factor, 4) || !aligned(g.offsets, 4) ||
       !aligned(g.counts, 4) || !aligned(g.err_flag, 4))
     return MOE_ERR_MISALIGNED;
-  return done(launch_fp4_gemm(g, stream));
+  return done(g.format == MOE_FP4_NV ? launch_fp4_gemm_nv(g, stream) : launch_fp4_gemm_mx(g, stream));
 }
 
 }  // namespace
@@ -113,7 +113,7 @@ extern "C" int moe_fp4_linear(const void* x_codes, const void* x_scales, const v
   using namespace moe;
   const Fp4Gemm g{static_cast<const uint8_t*>(x_codes), static_cast<const uint8_t*>(x_scales), nullptr,
                   static_cast<const uint8_t*>(w_codes), static_cast<const uint8_t*>(w_scales), factor, nullptr, nullptr,
-                  out_bf16, T, T, 1, N, K, format, act == MOE_ACT_SWIGLU, static_cast<float*>(workspace), err_flag};
+                  out_bf16, T, T, 1, N, K, format, act == MOE_ACT_SWIGLU, workspace, err_flag};
   return products(g, act, workspace, workspace_bytes, stream);
 }
 
@@ -126,6 +126,6 @@ extern "C" int moe_fp4_expert_linear(const void* x_codes, const void* x_scales, 
   if (n_rows > 0 && (!offsets || !counts)) return MOE_ERR_INVALID_ARG;
   const Fp4Gemm g{static_cast<const uint8_t*>(x_codes), static_cast<const uint8_t*>(x_scales), row_token,
                   static_cast<const uint8_t*>(w_codes), static_cast<const uint8_t*>(w_scales), factor, offsets, counts,
-                  out_bf16, n_x, n_rows, E, N, K, format, act == MOE_ACT_SWIGLU, static_cast<float*>(workspace), err_flag};
+                  out_bf16, n_x, n_rows, E, N, K, format, act == MOE_ACT_SWIGLU, workspace, err_flag};
   return products(g, act, workspace, workspace_bytes, stream);
 }

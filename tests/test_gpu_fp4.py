@@ -194,6 +194,7 @@ LINEAR = [  # T, N, K
     (1, 4096, 6144), (1, 16, 128), (1, 8, 128), (2, 528, 1152), (7, 272, 256), (16, 256, 384), (17, 2056, 640), (33, 144, 2048),
     (64, 1024, 2048), (65, 272, 512), (128, 256, 896), (129, 144, 1408), (200, 264, 128), (255, 512, 256), (300, 528, 1152),
     (513, 16, 256), (700, 384, 384), (1000, 256, 640), (1100, 2048, 256), (2100, 128, 128),
+    (1, 4096, 256), (31, 9728, 512), (64, 8192, 768), (95, 4608, 384), (90, 16384, 256), (5, 20480, 128),
 ]
 
 
@@ -244,6 +245,30 @@ def test_linear_scales_of_any_size(M, T, fmt):
     out, _ = run_linear(M, c, fmt, None)
     want, err = O.fp4_linear(O.fp4_values(x, xs, fmt), O.fp4_values(w, ws, fmt), 1.0, None, rel_sum(K))
     check_rows(values(out), want, err, "any size")
+
+
+@pytest.mark.parametrize("act", [None, "swiglu"])
+@pytest.mark.parametrize("T,N,K", [(3, 4096, 2048), (100, 4096, 2048), (3, 8192, 1024), (20, 65536, 512), (300, 8192, 2048)])
+def test_linear_leaves_nan_where_a_wait_ran_out(M, T, N, K, act):  # clusters of 4 and 2, single CTAs, pairs
+    c = draw_linear(T, N, K, "nvfp4")
+    want, flag = run_linear(M, c, "nvfp4", act)
+    assert flag == 0
+    for stage in (0, 1):
+        M.moe_debug_withhold_expert_stage(stage)
+        out, flag = run_linear(M, c, "nvfp4", act)
+        assert flag & L.MOE_FLAG_TIMEOUT
+        lost = torch.isnan(out)
+        assert torch.equal(out[~lost], want[~lost]) and 0 < int(lost.sum()) < out.numel()
+    again, flag = run_linear(M, c, "nvfp4", act)
+    assert flag == 0 and torch.equal(again, want)
+
+
+def test_linear_same_bits_again(M):
+    for T, N, K in ((2, 4096, 2048), (50, 6144, 1024), (90, 16384, 512), (700, 1024, 512)):
+        c = draw_linear(T, N, K, "nvfp4")
+        a, _ = run_linear(M, c, "nvfp4", "swiglu")
+        for _ in range(3):
+            assert torch.equal(run_linear(M, c, "nvfp4", "swiglu")[0], a)
 
 
 def test_linear_empty_batch(M):
