@@ -59,7 +59,7 @@ struct Fp4Gemm {
   int32_t* err_flag;
 };
 
-int64_t fp4_gemm_workspace(int64_t n_rows, int64_t E, int64_t K);
+int64_t fp4_gemm_workspace(int64_t n_rows, int64_t E, int64_t N, int64_t K);
 
 cudaError_t launch_fp4_gemm_nv(const Fp4Gemm& g, cudaStream_t stream);
 cudaError_t launch_fp4_gemm_mx(const Fp4Gemm& g, cudaStream_t stream);

@@ -28,9 +28,6 @@
 //    equal row % 32 fill the same four 16-byte places as their four words will; the
 //    relay warp, which stands between the copies and the MMAs anyway, transposes
 //    these 4 x 4 words in place.
-//  - clusters, where there are too few tiles for the SMs: the CTAs of a cluster
-//    share one tile's K, and each finishes some quarters of the weight rows, whose
-//    partial sums the others send into its shared memory.
 //  - pairs (cta_group::2) for large segments: 256 weight rows and up to 256 rows.
 //
 // Measured, NVFP4, SwiGLU, K = 6144, N = 4096, 8 experts a token, even: FIGURES
@@ -51,10 +48,6 @@ constexpr int kPairScaleBufs = 2;  // and, behind them, of the scales of a stage
 constexpr int kEarly = 96;         // columns read before the next tile may start, at least
                                    // N - 160 of N <= 256 (those it can share) in pieces of 32
 constexpr int kPairSets = 3;       // sets of four warps that read a pair's accumulators
-constexpr int kMostSplit = 4;      // CTAs of a cluster that share a tile's K
-
-// How CTAs work on tiles.
-enum Form { kSingle, kCluster, kPair };
 
 struct Fp4Params {
   GemmParams g;  // x, K: in units of four elements (a BF16 number's bytes)
@@ -69,18 +62,13 @@ struct Fp4Barriers {
   uint64_t full[kFp4Stages], empty[kFp4Stages], landed[kFp4Stages];
   uint64_t acc_full[2], acc_empty[2];
   uint64_t acc_early[2];                // pairs: the columns that the next tile may need are read
-  uint64_t received[4];                 // clusters: the other CTAs' sums of a quarter
   uint64_t drained;
   uint32_t tmem_base;
   int abort_flag;
   int bn, pieces;
 };
 
-constexpr int kFp4Threads(Form form) { return 32 * (6 + kLoaders + 1) + (form == kPair ? 128 * (kPairSets - 1) : 0); }
-
-// Shared memory of a cluster's CTA for the sums that others send it: its 4 / n
-// quarters from n - 1 others, 128 rows each.
-__host__ __device__ constexpr int received_bytes(int n) { return n > 1 ? 4 / n * (n - 1) * kSoloRows * 128 : 0; }
+constexpr int kFp4Threads(bool pair) { return 32 * (6 + kLoaders + 1) + (pair ? 128 * (kPairSets - 1) : 0); }
 
 // Instruction descriptor: E2M1 A and B, both K-major, FP32 D, M x N; scales E4M3
 // or E8M0, at byte `id` of each word.
@@ -231,14 +219,6 @@ __device__ __forceinline__ void store_tile(const GemmParams& p, const Piece& w, 
   }
 }
 
-// `bytes` of this CTA's shared memory to that of another CTA of the cluster, counted
-// on a barrier there.
-__device__ __forceinline__ void send(uint32_t remote, uint32_t local, uint32_t bytes, uint32_t remote_bar) {
-  asm volatile("cp.async.bulk.shared::cluster.shared::cta.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(remote),
-               "r"(local), "r"(bytes), "r"(remote_bar)
-               : "memory");
-}
-
 // Place in the list of the row tile that a piece is of.
 __device__ __forceinline__ int row_tile(const Tiles& t, const Piece& w) {
   const int ntt = t.before[w.e + 1] - t.before[w.e];
@@ -317,13 +297,12 @@ __global__ void __launch_bounds__(256) fp4_row_scales_kernel(const __grid_consta
   }
 }
 
-template <int FORMAT, bool SWIGLU, Form FORM, bool ONE>
+template <int FORMAT, bool SWIGLU, bool PAIR, bool ONE>
 // (registers that leave room for another kernel's blocks beside single CTAs too)
-__global__ void __launch_bounds__(kFp4Threads(kPair), 1)
+__global__ void __launch_bounds__(kFp4Threads(true), 1)
 fp4_gemm_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid_constant__ CUtensorMap tmap_s,
                 const __grid_constant__ CUtensorMap tmap_r, const __grid_constant__ Fp4Params q) {
   const GemmParams& p = q.g;
-  constexpr bool PAIR = FORM == kPair, CLUSTER = FORM == kCluster;
   constexpr int kWords = fp4_stage_scales(FORMAT) / 4;  // of a row and stage
   constexpr int kScales = kWords * 512;                 // bytes of 128 rows' scales
   constexpr int kGroups = PAIR ? 2 : 1;                 // of 128 rows whose scales a stage holds
@@ -333,14 +312,12 @@ fp4_gemm_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid_constan
   extern __shared__ uint8_t smem_raw[];
   __shared__ Fp4Barriers sb;
   uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
-  const int split = CLUSTER ? static_cast<int>(cg::this_cluster().num_blocks()) : 1;
-  float* received = reinterpret_cast<float*>(ring + p.ring_bytes);  // clusters: [own quarter][other CTA][row][32 weight rows]
-  Piece* piece_s = reinterpret_cast<Piece*>(ring + p.ring_bytes + (CLUSTER ? received_bytes(split) : 0));
+  Piece* piece_s = reinterpret_cast<Piece*>(ring + p.ring_bytes);
   int* list = reinterpret_cast<int*>(piece_s + kPieces);
   const Tiles t{list, list + p.E, list + 2 * p.E};
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int rank = PAIR || CLUSTER ? static_cast<int>(cg::this_cluster().block_rank()) : 0;
-  const int who = PAIR ? blockIdx.x >> 1 : blockIdx.x / split;
+  const int rank = PAIR ? static_cast<int>(cg::this_cluster().block_rank()) : 0;
+  const int who = PAIR ? blockIdx.x >> 1 : blockIdx.x;
   volatile int* abort_v = &sb.abort_flag;
 
   if (threadIdx.x < kFp4Stages) {
@@ -359,9 +336,6 @@ fp4_gemm_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid_constan
     mbar_init(&sb.drained, 1);
     sb.abort_flag = 0;
     mbar_init_fence();
-  } else if (threadIdx.x >= 16 && threadIdx.x < 20) {
-    mbar_init(&sb.received[threadIdx.x - 16], 1);
-    mbar_init_fence();
   } else if (threadIdx.x == kFp4Stages + 3) {
     prefetch_map(&tmap_w);
     prefetch_map(&tmap_s);
@@ -376,7 +350,7 @@ fp4_gemm_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid_constan
   }
   const int rows_out = (SWIGLU ? 64 : 128) * (PAIR ? 2 : 1), mt = (p.n_out + rows_out - 1) / rows_out;
   const int weight_tiles = (p.n_out + (SWIGLU ? 63 : 127)) / (SWIGLU ? 64 : 128);
-  const int walkers = static_cast<int>(PAIR ? gridDim.x >> 1 : gridDim.x / split);
+  const int walkers = static_cast<int>(PAIR ? gridDim.x >> 1 : gridDim.x);
   list_fp4<PAIR, ONE>(p, t, mt, walkers, &sb.bn);  // ONE: reads no global memory
   const Schedule s(p, t, mt, walkers, false);
   {
@@ -386,7 +360,7 @@ fp4_gemm_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid_constan
   }
   fence_before_sync();
   __syncthreads();
-  if (PAIR || CLUSTER) {  // the others' barriers are ready before anything signals them
+  if (PAIR) {  // the peer's barriers are ready before anything signals them
     cluster_arrive_release();
     cluster_wait_acquire();
   }
@@ -404,7 +378,7 @@ fp4_gemm_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid_constan
       x.ph ^= 1;
     }
   };
-  const int pieces = sb.pieces;  // (of a cluster: one at most)
+  const int pieces = sb.pieces;
   // all warps walk the pieces in the same order
   auto next = [&](int& at, Piece& w) {
     if (at >= pieces) return false;
@@ -414,10 +388,6 @@ fp4_gemm_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid_constan
       Piece made;  // (a reference to w itself would keep it out of the registers)
       make_far_piece(s, t, p.E, who, at, false, &made);
       w = made;
-    }
-    if (CLUSTER) {  // this CTA's share of K
-      w.kb0 = static_cast<int>(s.nkb) * rank / split;
-      w.kb1 = static_cast<int>(s.nkb) * (rank + 1) / split;
     }
     ++at;
     return true;
@@ -595,58 +565,6 @@ fp4_gemm_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid_constan
         else
           store_tile<SWIGLU, false>(p, w, m, c, quarter, f, v, bad);
       };
-      if (CLUSTER) {
-        // a quarter's sums meet in one CTA, in the order of the CTAs
-        const int owner = quarter * split / 4;
-        const uint32_t bytes = static_cast<uint32_t>(w.nr) * 128;
-        if (rank != owner) {
-          // this CTA's ring is idle: its MMAs are done, and every copy before them
-          float* mine = reinterpret_cast<float*>(ring) + quarter * kSoloRows * 32;
-          if (!dead) {
-#pragma unroll 1
-            for (int c = 0; c < w.nr; c += 32) {
-              uint32_t raw[32];
-              tmem_ld32(d + static_cast<uint32_t>(c), raw);
-#pragma unroll
-              for (int k = 0; k < 32; ++k)
-                if (c + k < w.nr) mine[(c + k) * 32 + lane] = __uint_as_float(raw[k]);
-            }
-            proxy_fence();
-            __syncwarp();
-            if (lane == 0) {
-              const int slot = (quarter - owner * 4 / split) * (split - 1) + (rank < owner ? rank : rank - 1);
-              send(cluster_addr(received + slot * kSoloRows * 32, owner), smem_addr(mine), bytes,
-                   cluster_addr(&sb.received[quarter], owner));
-            }
-          }
-          continue;
-        }
-        if (lane == 0) mbar_arrive_expect_tx(&sb.received[quarter], bytes * (split - 1));
-        __syncwarp();
-        const bool ok = wait(&sb.received[quarter], 0, abort_v, true);  // (nothing lands behind this CTA's end)
-        dead = !__all_sync(0xFFFFFFFFu, ok) || dead;
-        const float* others = received + (quarter - owner * 4 / split) * (split - 1) * kSoloRows * 32 + lane;
-#pragma unroll 1
-        for (int c = 0; c < w.nr; c += 32) {
-          float v[32];
-          if (!dead) {
-            uint32_t raw[32];
-            tmem_ld32(d + static_cast<uint32_t>(c), raw);
-#pragma unroll
-            for (int k = 0; k < 32; ++k) v[k] = 0.f;
-            for (int r = 0; r < split; ++r) {
-              const float* from = others + ((r < rank ? r : r - 1) * kSoloRows + c) * 32;
-#pragma unroll
-              for (int k = 0; k < 32; ++k) v[k] += r == rank ? __uint_as_float(raw[k]) : c + k < w.nr ? from[k * 32] : 0.f;
-            }
-          } else {
-#pragma unroll
-            for (int k = 0; k < 32; ++k) v[k] = __uint_as_float(0x7FC00000u);
-          }
-          store(c, v);
-        }
-        continue;
-      }
       // 32 columns at a time, first those that the next tile may take over; in pairs
       // the sets of warps take turns
       const int chunks = (w.nr + 31) >> 5, mine = warp < 6 ? 0 : (warp - 7 - kLoaders) / 4 + 1, by = PAIR ? kPairSets : 1;
@@ -812,7 +730,7 @@ fp4_gemm_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid_constan
   __syncthreads();
   if (threadIdx.x == 32) wait(&sb.drained, 0, abort_v, true);  // no MMA is in flight any more
   __syncwarp();
-  if (PAIR || CLUSTER) {  // the others' copies and arrivals are over too
+  if (PAIR) {  // the peer's copies and arrivals are over too
     cluster_arrive_release();
     cluster_wait_acquire();
   }
@@ -825,27 +743,24 @@ fp4_gemm_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid_constan
 
 // ---------------------------------------------------------------- host side
 
-// Pairs from a mean of this many rows an expert.
-constexpr int64_t kFp4PairMeanRows = 96;
+// Pairs from a mean of this many rows an expert, as in the BF16 products (mean 64,
+// E = 256, K = 6144, N = 4096: single CTAs 559 us, pairs 571; 128: 729 and 590), if
+// there are so many stages of 128 weight rows and 128 rows that the kernel before
+// them, which lays out the rows' scales, is made up for: one segment, K = 6144, N =
+// 4096, T = 512 (3 * 1024 stages) single CTAs 14.8 us, pairs 19.6; T = 1024 23.5
+// and 22.6; T = 2048 40.7 and 32.0; K = 2048, N = 6144, T = 1024 14.4 and 19.2.
+constexpr int64_t kFp4PairMeanRows = 96, kFp4PairStages = 8 * 1024;
 
 // Row tiles of pairs, at most.
 inline int64_t pair_tiles_most(int64_t n_rows, int64_t E) { return n_rows / kPairRows + (E < n_rows ? E : n_rows) + 8; }
 
-inline bool runs_in_pairs(int64_t n_rows, int64_t E) { return n_rows / E >= kFp4PairMeanRows; }
+inline bool runs_in_pairs(int64_t n_rows, int64_t E, int64_t N, int64_t K) {
+  return n_rows / E >= kFp4PairMeanRows && n_rows / 128 * ((N + 127) / 128) * fp4_stages(K) >= kFp4PairStages;
+}
 
 // Bytes of the rows' scales as pairs read them.
 inline int64_t row_scale_bytes(int64_t n_rows, int64_t E, int64_t K, int format) {
   return pair_tiles_most(n_rows, E) * fp4_stages(K) * 2 * 128 * fp4_stage_scales(format);
-}
-
-// CTAs that share a tile's K: as many (1, 2 or 4) as leave one wave of tiles, of
-// which the rows make at most that many.  Clusters of four fill 36 x 4 SMs.
-inline int split_of(int64_t n_rows, int64_t E, int64_t weight_tiles, int64_t stages, bool one) {
-  const int64_t row = one ? (n_rows <= kSoloRows ? 1 : (n_rows + kSoloRows - 1) / kSoloRows) : n_rows / 32 + (E < n_rows ? E : n_rows);
-  const int64_t tiles = row * weight_tiles;
-  for (int n = kMostSplit; n > 1; n /= 2)
-    if (tiles <= gemm_ctas() / n && (n < 4 || tiles <= 36) && stages >= n) return n;
-  return 1;
 }
 
 // Scales in the products' order as rows of 1024 bytes.
@@ -859,8 +774,8 @@ inline bool scale_map(CUtensorMap* map, const void* scales, int64_t bytes, int b
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int FORMAT, bool SWIGLU, Form FORM, bool ONE>
-cudaError_t launch_fp4(const CUtensorMap& mw, const CUtensorMap& ms, const CUtensorMap& mr, Fp4Params& p, int split,
+template <int FORMAT, bool SWIGLU, bool PAIR, bool ONE>
+cudaError_t launch_fp4(const CUtensorMap& mw, const CUtensorMap& ms, const CUtensorMap& mr, const Fp4Params& p,
                        cudaStream_t stream) {
   static std::atomic<bool> done[64];
   int dev = 0;
@@ -868,21 +783,18 @@ cudaError_t launch_fp4(const CUtensorMap& mw, const CUtensorMap& ms, const CUten
   if (e != cudaSuccess) return e;
   if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
   if (!done[dev].load()) {
-    e = cudaFuncSetAttribute(fp4_gemm_kernel<FORMAT, SWIGLU, FORM, ONE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    e = cudaFuncSetAttribute(fp4_gemm_kernel<FORMAT, SWIGLU, PAIR, ONE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              static_cast<int>(gemm_smem(ONE ? 1 : MOE_MAX_E, 0, kRingBytes)));
     if (e != cudaSuccess) return e;
     done[dev].store(true);
   }
-  p.g.ring_bytes = kRingBytes - (FORM == kCluster ? received_bytes(split) : 0);
-  int G = gemm_ctas();
-  if (FORM == kPair) G = G / 2 * 2;
-  if (FORM == kCluster) G = G / split * split;
+  const int G = PAIR ? gemm_ctas() / 2 * 2 : gemm_ctas();
   cudaLaunchConfig_t cfg = {};
   cfg.stream = stream;
   cudaLaunchAttribute attr[2] = {pdl_attribute(), {}};
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  if constexpr (FORM == kPair) {
+  if constexpr (PAIR) {
     const int rows_out = SWIGLU ? 128 : 256;
     cfg.gridDim = dim3(static_cast<unsigned>(4 * gemm_ctas()), 1, 1);
     cfg.blockDim = dim3(256, 1, 1);
@@ -891,16 +803,16 @@ cudaError_t launch_fp4(const CUtensorMap& mw, const CUtensorMap& ms, const CUten
     if (e != cudaSuccess) return e;
   }
   cfg.gridDim = dim3(static_cast<unsigned>(G), 1, 1);
-  cfg.blockDim = dim3(kFp4Threads(FORM), 1, 1);
-  cfg.dynamicSmemBytes = launch_smem(gemm_smem(p.g.E, 0, kRingBytes));
-  if (FORM != kSingle) {
+  cfg.blockDim = dim3(kFp4Threads(PAIR), 1, 1);
+  cfg.dynamicSmemBytes = launch_smem(gemm_smem(p.g.E, 0, p.g.ring_bytes));
+  if (PAIR) {
     attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = FORM == kPair ? 2 : static_cast<unsigned>(split);
+    attr[1].val.clusterDim.x = 2;
     attr[1].val.clusterDim.y = 1;
     attr[1].val.clusterDim.z = 1;
     cfg.numAttrs = 2;
   }
-  return cudaLaunchKernelEx(&cfg, fp4_gemm_kernel<FORMAT, SWIGLU, FORM, ONE>, mw, ms, mr, p);
+  return cudaLaunchKernelEx(&cfg, fp4_gemm_kernel<FORMAT, SWIGLU, PAIR, ONE>, mw, ms, mr, p);
 }
 
 template <int FORMAT, bool SWIGLU, bool ONE>
@@ -917,6 +829,7 @@ cudaError_t prepare_and_launch(const Fp4Gemm& g, cudaStream_t stream) {
   p.g.E = static_cast<int>(g.E);
   p.g.n_out = static_cast<int>(SWIGLU ? g.N / 2 : g.N);
   p.g.K = static_cast<int>(g.K / 4);
+  p.g.ring_bytes = kRingBytes;
   p.g.weave = SWIGLU && p.g.n_out % 16 == 0;
   p.g.withhold = take_withheld_stage();
   p.x_scales = g.x_scales;
@@ -929,15 +842,13 @@ cudaError_t prepare_and_launch(const Fp4Gemm& g, cudaStream_t stream) {
   if (!weight_map(&mw, g.w, g.E, g.N, g.K / 4, SWIGLU, p.g.weave) ||
       !scale_map(&ms, g.w_scales, fp4_weight_scales_bytes(g.E, g.N, g.K, FORMAT, SWIGLU), kMapRows))
     return cudaErrorInvalidValue;
-  if (runs_in_pairs(g.n_rows, g.E)) {
+  if (runs_in_pairs(g.n_rows, g.E, g.N, g.K)) {
     CUtensorMap mr;
     p.row_scale_tiles = static_cast<uint8_t*>(g.workspace);
     if (!scale_map(&mr, p.row_scale_tiles, row_scale_bytes(g.n_rows, g.E, g.K, FORMAT), 2 * kMapRows)) return cudaErrorInvalidValue;
-    return launch_fp4<FORMAT, SWIGLU, kPair, ONE>(mw, ms, mr, p, 1, stream);
+    return launch_fp4<FORMAT, SWIGLU, true, ONE>(mw, ms, mr, p, stream);
   }
-  const int split = split_of(g.n_rows, g.E, fp4_weight_tiles(g.N, SWIGLU), fp4_stages(g.K), ONE);
-  if (split > 1) return launch_fp4<FORMAT, SWIGLU, kCluster, ONE>(mw, ms, ms, p, split, stream);
-  return launch_fp4<FORMAT, SWIGLU, kSingle, ONE>(mw, ms, ms, p, 1, stream);
+  return launch_fp4<FORMAT, SWIGLU, false, ONE>(mw, ms, ms, p, stream);
 }
 
 template <int FORMAT>

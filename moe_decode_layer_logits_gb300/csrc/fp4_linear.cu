@@ -77,8 +77,8 @@ extern "C" int moe_fp4_weight_scales(const void* scales, void* tiled, int64_t E,
 }
 
 extern "C" int64_t moe_fp4_linear_workspace(int64_t n_rows, int64_t E, int64_t N, int64_t K) {
-  if (n_rows < 0 || n_rows > 0x7FFFFFFFll || E < 1 || N < 1 || K < 1 || K > MOE_MAX_DIM) return -1;
-  return moe::fp4_gemm_workspace(n_rows, E, K);
+  if (n_rows < 0 || n_rows > 0x7FFFFFFFll || E < 1 || N < 1 || K < 1 || N > MOE_MAX_DIM || K > MOE_MAX_DIM) return -1;
+  return moe::fp4_gemm_workspace(n_rows, E, N, K);
 }
 
 namespace moe {
@@ -95,7 +95,7 @@ int products(const Fp4Gemm& g, int32_t act, void* workspace, int64_t workspace_b
   if (!g.row_token && g.n_x < g.n_rows) return MOE_ERR_INVALID_ARG;
   if (g.n_rows == 0) return MOE_OK;
   if ((g.n_x > 0 && (!g.x || !g.x_scales)) || !g.w || !g.w_scales || !g.out) return MOE_ERR_INVALID_ARG;
-  if (workspace_bytes < fp4_gemm_workspace(g.n_rows, g.E, g.K) || (workspace_bytes > 0 && !workspace)) return MOE_ERR_INVALID_ARG;
+  if (workspace_bytes < fp4_gemm_workspace(g.n_rows, g.E, g.N, g.K) || (workspace_bytes > 0 && !workspace)) return MOE_ERR_INVALID_ARG;
   if (!aligned(g.x, 16) || !aligned(g.x_scales, 4) || !aligned(g.w, 16) || !aligned(g.w_scales, 16) || !aligned(g.out, 16) ||
       !aligned(workspace, 16) || !aligned(g.row_token, 4) || !aligned(g.factor, 4) || !aligned(g.offsets, 4) ||
       !aligned(g.counts, 4) || !aligned(g.err_flag, 4))

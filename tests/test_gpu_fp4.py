@@ -248,8 +248,8 @@ def test_linear_scales_of_any_size(M, T, fmt):
 
 
 @pytest.mark.parametrize("act", [None, "swiglu"])
-@pytest.mark.parametrize("T,N,K", [(3, 4096, 2048), (100, 4096, 2048), (3, 8192, 1024), (20, 65536, 512), (300, 8192, 2048)])
-def test_linear_leaves_nan_where_a_wait_ran_out(M, T, N, K, act):  # clusters of 4 and 2, single CTAs, pairs
+@pytest.mark.parametrize("T,N,K", [(3, 4096, 2048), (100, 4096, 2048), (3, 8192, 1024), (20, 65536, 512), (300, 8192, 2048), (1200, 8192, 4096)])
+def test_linear_leaves_nan_where_a_wait_ran_out(M, T, N, K, act):  # single CTAs, pairs
     c = draw_linear(T, N, K, "nvfp4")
     want, flag = run_linear(M, c, "nvfp4", act)
     assert flag == 0
