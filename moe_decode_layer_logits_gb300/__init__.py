@@ -379,6 +379,7 @@ def _fp4_block(K, fmt):
     return block
 
 
+# sizes, which depend on their arguments alone (each call of the library costs a microsecond)
 @functools.lru_cache(maxsize=4096)
 def _fp4_scale_bytes(E, N, K, fmt, act):
     nbytes = lib().moe_fp4_weight_scales_bytes(E, N, K, fmt, act)
@@ -388,8 +389,7 @@ def _fp4_scale_bytes(E, N, K, fmt, act):
 
 
 @functools.lru_cache(maxsize=4096)
-def _fp4_workspace_bytes(n_rows, E, N, K, device_index):
-    """(of the current device, whose number of SMs counts)"""
+def _fp4_workspace_bytes(n_rows, E, N, K):
     return lib().moe_fp4_linear_workspace(n_rows, E, N, K)
 
 
@@ -498,7 +498,7 @@ def moe_fp4_linear(x, x_scales, w, w_scales, format="nvfp4", factor=None, act=No
     handle, on = _enter(device, stream)
     try:
         out, out_ptr = _out(out, torch.bfloat16, "out", (T, n_out), device)
-        ws, ws_ptr, nbytes = _workspace(workspace, _fp4_workspace_bytes(T, 1, N, K, device.index), device)
+        ws, ws_ptr, nbytes = _workspace(workspace, _fp4_workspace_bytes(T, 1, N, K), device)
         st = L.moe_fp4_linear(*ptrs, out_ptr, T, N, K, fmt, act, ws_ptr, nbytes, _flag(err_flag, device), handle)
     finally:
         if on is not None:
@@ -527,7 +527,7 @@ def moe_fp4_expert_linear(x, x_scales, w, w_scales, offsets, counts, format="nvf
     handle, on = _enter(device, stream)
     try:
         out, out_ptr = _out(out, torch.bfloat16, "out", (n_rows, n_out), device)
-        ws, ws_ptr, nbytes = _workspace(workspace, _fp4_workspace_bytes(n_rows, E, N, K, device.index), device)
+        ws, ws_ptr, nbytes = _workspace(workspace, _fp4_workspace_bytes(n_rows, E, N, K), device)
         st = L.moe_fp4_expert_linear(xp, xs, n_x, tok, wp, wsc, fac, off, cnt, out_ptr, n_rows, E, N, K, fmt, act, ws_ptr,
                                      nbytes, _flag(err_flag, device), handle)
     finally:

@@ -444,6 +444,106 @@ def test_expert_linear_without_any_token(M):
     assert not out.any() and flag == L.MOE_FLAG_BAD_INDEX
 
 
+def halves(seed, *shape):
+    """Codes and, as FP32, their values, for scales of 1: products are multiples
+    of a quarter, and sums of some hundred of them are exact in FP32."""
+    g = torch.Generator(device="cuda")
+    g.manual_seed(seed)
+    codes = torch.randint(0, 256, (*shape[:-1], shape[-1] // 2), generator=g, device="cuda", dtype=torch.uint8)
+    table = torch.tensor(O.fp4_e2m1, dtype=torch.float32, device="cuda")
+    return codes, lambda c: table[torch.stack([c & 15, c >> 4], dim=-1).long()].flatten(-2)
+
+
+def ones(*shape):
+    return torch.full(shape, 0x38, dtype=torch.uint8, device="cuda")      # E4M3 1.0
+
+
+@pytest.mark.parametrize("E,rows", [(80, 1), (80, 96)])
+def test_expert_linear_more_pieces_than_a_walker_keeps(M, E, rows):
+    # 512 (pairs: 256) weight tiles an expert: over 256 tiles a CTA or pair
+    N, K = 65536, 64
+    x, val = halves(1, E * rows, K)
+    w, _ = halves(2, E, N, K)
+    off = torch.arange(E + 1, device="cuda", dtype=torch.int32) * rows
+    out = M.moe_fp4_expert_linear(x, ones(E * rows, 4), w, M.moe_fp4_weight_scales(ones(E, N, 4)), off,
+                                  torch.full((E,), rows, device="cuda", dtype=torch.int32))
+    for e in range(E):
+        want = (val(x[e * rows:(e + 1) * rows]) @ val(w[e]).T).to(torch.bfloat16)
+        assert torch.equal(out[e * rows:(e + 1) * rows], want), e
+
+
+def test_products_with_offsets_beyond_31_bits(M):
+    # outputs, then rows of x, whose offsets in elements pass 2^31 and 2^32
+    n, N, K = 70000, 65536, 64
+    x, val = halves(3, n, K)
+    w, _ = halves(4, N, K)
+    t = M.moe_fp4_weight_scales(ones(N, 4))
+    out = M.moe_fp4_linear(x, ones(n, 4), w, t)
+    at = torch.tensor([0, 1, 32767, 32768, 65535, 65536, n - 1], device="cuda")
+    assert torch.equal(out[at], (val(x[at]) @ val(w).T).to(torch.bfloat16))
+    del out
+    n, K, N = 140000, 65536, 16
+    x = torch.zeros(n, K // 2, dtype=torch.uint8, device="cuda")
+    some, _ = halves(5, n, 64)
+    x[:, 20000:20032] = some
+    xs = ones(n, K // 16)
+    w, _ = halves(6, 1, N, K)
+    t = M.moe_fp4_weight_scales(ones(1, N, K // 16))
+    want = (val(some) @ val(w[0, :, 20000:20032]).T).to(torch.bfloat16)
+    seg = torch.tensor([0, n], device="cuda", dtype=torch.int32)
+    back = torch.arange(n - 1, -1, -1, device="cuda", dtype=torch.int32)
+    for tok, ref in ((None, want), (back, want.flip(0))):
+        assert torch.equal(M.moe_fp4_expert_linear(x, xs, w, t, seg, seg[1:], row_token=tok), ref)
+    few = torch.tensor([n - 1, 0, 65536, 131072], device="cuda", dtype=torch.int32)
+    four = torch.tensor([0, 4], device="cuda", dtype=torch.int32)
+    assert torch.equal(M.moe_fp4_expert_linear(x, xs, w, t, four, four[1:], row_token=few), want[few.long()])
+
+
+@pytest.mark.parametrize("T,N,K", [(3, 512, 256), (1200, 8192, 1024)])
+def test_linear_behind_a_kernel_that_runs_long(M, T, N, K):
+    # An expert map of 2^30 slots lets its dependents start at once and runs for
+    # longer than the probes of one bounded wait last: the call behind it must not
+    # give up, nor read its inputs, which the kernel between them writes, too early.
+    c = draw_linear(T, N, K, "nvfp4")
+    want, _ = run_linear(M, c, "nvfp4", "swiglu")
+    ids = torch.randint(0, 1024, (1 << 25, 32), dtype=torch.int32, device="cuda")
+    x, xs = devn(c["x"]), devn(c["xs"])
+    late, late_s = torch.zeros_like(x), torch.zeros_like(xs)
+    w, t = devn(c["w"]), M.moe_fp4_weight_scales(devn(c["ws"]), act="swiglu")
+    flag = torch.zeros(1, dtype=torch.int32, device="cuda")
+    torch.cuda.synchronize()
+    M.moe_expert_map(ids, 1024)
+    late.copy_(x)
+    late_s.copy_(xs)
+    out = M.moe_fp4_linear(late, late_s, w, t, act="swiglu", err_flag=flag)
+    torch.cuda.synchronize()
+    assert int(flag.item()) == 0 and torch.equal(out, want)
+    M.moe_expert_map(ids, 1024)
+    out = M.moe_fp4_linear(x, xs, w, t, act="swiglu", err_flag=flag)
+    assert int(flag.item()) == 0 and torch.equal(out, want)
+
+
+@pytest.mark.parametrize("T", [2, 1200])
+def test_quantised_rows_are_read_behind_the_kernel_that_writes_them(M, T):
+    # quantisation and product back to back, over and over, on new rows each time
+    N, K = 4096, 2048
+    g = torch.Generator(device="cuda")
+    g.manual_seed(7)
+    rows = torch.randn(6, T, K, generator=g, device="cuda", dtype=torch.bfloat16)
+    w, ws = M.moe_fp4_quantize(torch.randn(N, K, generator=g, device="cuda", dtype=torch.bfloat16))
+    t = M.moe_fp4_weight_scales(ws)
+    codes, scales = torch.empty(T, K // 2, dtype=torch.uint8, device="cuda"), torch.empty(T, K // 16, dtype=torch.uint8, device="cuda")
+    want = []
+    for r in rows:
+        q = M.moe_fp4_quantize(r)
+        torch.cuda.synchronize()
+        want.append(M.moe_fp4_linear(*q, w, t))
+        torch.cuda.synchronize()
+    got = [M.moe_fp4_linear(*M.moe_fp4_quantize(r, codes=codes, scales=scales), w, t) for r in rows]
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)
+
+
 # ---------------------------------------------------------------------------
 # together: a layer whose experts work in 4 bits
 # ---------------------------------------------------------------------------
