@@ -58,7 +58,7 @@ def parse_args():
     ap.add_argument("--no-cpu-baseline", action="store_true")
     ap.add_argument("--min-timed-s", type=float, default=1.0,
                     help="repeat the K-step timed region until this much time is covered")
-    ap.add_argument("--ncu-case", choices=["decode", "decode1", "prefill", "router", "routing", "experts", "adapters"], default=None,
+    ap.add_argument("--ncu-case", choices=["decode", "decode1", "prefill", "router", "routing", "experts", "adapters", "fp4"], default=None,
                     help="run a small fixed case for an ncu capture and exit (no timing, no JSON)")
     return ap.parse_args()
 
@@ -857,7 +857,9 @@ def run_ncu_case(case):
     inputs at T=8192 (x 100 MB each), twice; routing -- grouped routing and
     expert map at T=8192, experts -- products of 64 experts at T=64 and of 48
     at T=1600 (3.2 GB of weights), adapters -- the adapter projection at T=64
-    and T=4096, each twice with another 256 MB written in between."""
+    and T=4096, fp4 -- NVFP4 quantisation of 8192 rows and back, and the
+    products of "experts" in 4 bits (0.9 GB of weights), each twice with
+    another 256 MB written in between."""
     import torch
     import moe_decode_layer_logits_gb300 as M
     from moe_decode_layer_logits_gb300.inputs import device_layer
@@ -871,7 +873,7 @@ def run_ncu_case(case):
                 M.moe_router_logits_fp32(d["x"], d["w_gate"], logits_out=d["logits"])
         torch.cuda.synchronize()
         return
-    if case in ("routing", "experts", "adapters"):
+    if case in ("routing", "experts", "adapters", "fp4"):
         run_expert_ncu_case(torch, M, case)
         return
     if case == "decode":
@@ -919,6 +921,21 @@ def run_expert_ncu_case(torch, M, case):
             _, row_token, offsets, counts = M.moe_expert_map(ids, E)
             calls.append(lambda x=x, w=w[:E], o=offsets, c=counts, t=row_token:
                          M.moe_expert_linear(x, w, o, c, row_token=t, act="swiglu"))
+    elif case == "fp4":
+        rows = randn(1.0, 8192, 6144)
+        one = torch.full((1,), 0.002, device="cuda")
+        codes, scales = (torch.empty(8192, n, dtype=torch.uint8, device="cuda") for n in (6144 // 2, 6144 // 16))
+        calls += [lambda: M.moe_fp4_quantize(rows, global_scale=one, codes=codes, scales=scales),
+                  lambda: M.moe_fp4_dequantize(codes, scales, global_scale=one)]
+        w = torch.randint(0, 256, (64, 4096, 6144 // 2), generator=g, device="cuda", dtype=torch.uint8)
+        ws = torch.randint(40, 80, (64, 4096, 6144 // 16), generator=g, device="cuda", dtype=torch.uint8)
+        f = torch.full((64,), 1e-5, device="cuda")
+        for T, E in ((64, 64), (1600, 48)):
+            x, xs = M.moe_fp4_quantize(randn(1.0, T, 6144))
+            ids = torch.rand(T, E, generator=g, device="cuda").topk(8, dim=1).indices.to(torch.int32)
+            _, row_token, offsets, counts = M.moe_expert_map(ids, E)
+            calls.append(lambda x=x, xs=xs, w=w[:E], t=M.moe_fp4_weight_scales(ws[:E], act="swiglu"), o=offsets, c=counts,
+                         r=row_token, f=f[:E]: M.moe_fp4_expert_linear(x, xs, w, t, o, c, factor=f, row_token=r, act="swiglu"))
     else:
         for T, K, N, R, n, act in ((64, 2048, 6144, 16, 64, None), (4096, 6144, 4096, 64, 8, "swiglu")):
             a = (randn(1.0, T, K), randn(0.02, N, K), randn(K ** -0.5, n, R, K), randn(0.05, n, N, R),

@@ -371,21 +371,26 @@ _FP4 = {"nvfp4": _lib.MOE_FP4_NV, "mxfp4": _lib.MOE_FP4_MX}
 _FP4_BLOCK = {_lib.MOE_FP4_NV: 16, _lib.MOE_FP4_MX: 32}
 
 
-def _fp4_block(K, fmt):
-    """Elements that share a scale; K in whole words of scales, as the library takes it."""
-    block = _FP4_BLOCK[fmt]
-    if K % (4 * block):
-        raise ValueError(f"K must be a multiple of {4 * block}, got {K}")
-    return block
-
-
-# sizes, which depend on their arguments alone (each call of the library costs a microsecond)
+# What follows from names and sizes alone is worked out once for each of them: a
+# call with new tensors of the same sizes finds it (1.5 us of 14).
 @functools.lru_cache(maxsize=4096)
-def _fp4_scale_bytes(E, N, K, fmt, act):
+def _fp4_rows(format, K):
+    """(format, scales of a row) of rows of K elements."""
+    fmt = _choice(_FP4, format, "format")
+    block = _FP4_BLOCK[fmt]
+    if K % (4 * block):  # whole words of scales
+        raise ValueError(f"K must be a multiple of {4 * block}, got {K}")
+    return fmt, K // block
+
+
+@functools.lru_cache(maxsize=4096)
+def _fp4_products(format, act, E, N, K):
+    """(format, act, scales of a row, bytes of the weights' scales, outputs)."""
+    (fmt, cols), act = _fp4_rows(format, K), _choice(_ACTS, act, "act")
     nbytes = lib().moe_fp4_weight_scales_bytes(E, N, K, fmt, act)
     if nbytes < 0:
         raise ValueError("sizes out of range")
-    return nbytes
+    return fmt, act, cols, nbytes, N // 2 if act == _lib.MOE_ACT_SWIGLU else N
 
 
 @functools.lru_cache(maxsize=4096)
@@ -409,13 +414,13 @@ def moe_fp4_quantize(x, format="nvfp4", global_scale=None, codes=None, scales=No
     element; nvfp4 only)."""
     if x.dim() != 2:
         raise ValueError("x must have 2 dimensions")
-    (T, K), device, fmt = x.shape, x.device, _choice(_FP4, format, "format")
-    block = _fp4_block(K, fmt)
+    (T, K), device = x.shape, x.device
+    fmt, cols = _fp4_rows(format, K)
     args = _arg(x, torch.bfloat16, "x", (T, K), device), _global_scale(global_scale, device)
     handle, on = _enter(device, stream)
     try:
         codes, c = _out(codes, torch.uint8, "codes", (T, K // 2), device)
-        scales, s = _out(scales, torch.uint8, "scales", (T, K // block), device)
+        scales, s = _out(scales, torch.uint8, "scales", (T, cols), device)
         st = lib().moe_fp4_quantize(*args, c, s, T, K, fmt, handle)
     finally:
         if on is not None:
@@ -429,10 +434,10 @@ def moe_fp4_dequantize(codes, scales, format="nvfp4", global_scale=None, out=Non
     global_scale, as BF16 [T, K]."""
     if codes.dim() != 2:
         raise ValueError("codes must have 2 dimensions")
-    (T, half), device, fmt = codes.shape, codes.device, _choice(_FP4, format, "format")
+    (T, half), device = codes.shape, codes.device
     K = 2 * half
-    block = _fp4_block(K, fmt)
-    args = (_arg(codes, torch.uint8, "codes", (T, half), device), _arg(scales, torch.uint8, "scales", (T, K // block), device),
+    fmt, cols = _fp4_rows(format, K)
+    args = (_arg(codes, torch.uint8, "codes", (T, half), device), _arg(scales, torch.uint8, "scales", (T, cols), device),
             _global_scale(global_scale, device))
     handle, on = _enter(device, stream)
     try:
@@ -451,12 +456,11 @@ def moe_fp4_weight_scales(scales, format="nvfp4", act=None, out=None, stream=Non
     when called with this act.  Made once, when weights are loaded."""
     if scales.dim() not in (2, 3):
         raise ValueError("scales must be [N, K/block] or [E, N, K/block]")
-    device, fmt, act = scales.device, _choice(_FP4, format, "format"), _choice(_ACTS, act, "act")
+    device = scales.device
     E, (N, cols) = (scales.shape[0] if scales.dim() == 3 else 1), scales.shape[-2:]
-    K = cols * _FP4_BLOCK[fmt]
-    _fp4_block(K, fmt)
+    K = cols * _FP4_BLOCK[_choice(_FP4, format, "format")]
+    fmt, act, _, nbytes, _ = _fp4_products(format, act, E, N, K)
     sc = _arg(scales, torch.uint8, "scales", scales.shape, device)
-    nbytes = _fp4_scale_bytes(E, N, K, fmt, act)
     handle, on = _enter(device, stream)
     try:
         out, o = _out(out, torch.uint8, "out", (nbytes,), device)
@@ -468,20 +472,6 @@ def moe_fp4_weight_scales(scales, format="nvfp4", act=None, out=None, stream=Non
     return out
 
 
-def _fp4_operands(x, x_scales, w, w_scales, format, factor, act, E):
-    """Checks common to both 4-bit products: (pointers of x, x_scales, w,
-    w_scales and factor, sizes (n_x, N, K), format, act)."""
-    device, fmt, act = x.device, _choice(_FP4, format, "format"), _choice(_ACTS, act, "act")
-    (n_x, half), N = x.shape, w.shape[-2]
-    K = 2 * half
-    block = _fp4_block(K, fmt)
-    nbytes = _fp4_scale_bytes(E, N, K, fmt, act)
-    return ((_arg(x, torch.uint8, "x", (n_x, half), device),
-             _arg(x_scales, torch.uint8, "x_scales", (n_x, K // block), device),
-             _arg(w, torch.uint8, "w", w.shape, device), _arg(w_scales, torch.uint8, "w_scales", (nbytes,), device),
-             _opt(factor, torch.float32, "factor", (E,), device)), (n_x, N, K), fmt, act)
-
-
 def moe_fp4_linear(x, x_scales, w, w_scales, format="nvfp4", factor=None, act=None, out=None, workspace=None,
                    err_flag=None, stream=None):
     """One projection of all rows, both operands in 4 bits: act(factor * (w @
@@ -489,17 +479,20 @@ def moe_fp4_linear(x, x_scales, w, w_scales, format="nvfp4", factor=None, act=No
     [N, K/2] uint8, w_scales as moe_fp4_weight_scales gives them for this act,
     factor [1] FP32 (the global scales of x and w multiplied); workspace as
     in moe_expert_linear."""
-    if x.dim() != 2 or w.dim() != 2 or x.shape[1] != w.shape[1]:
+    xs, wshape = x.shape, w.shape
+    if len(xs) != 2 or len(wshape) != 2 or xs[1] != wshape[1]:
         raise ValueError("x must be [T, K/2] and w [N, K/2]")
-    device = x.device
-    ptrs, (T, N, K), fmt, act = _fp4_operands(x, x_scales, w, w_scales, format, factor, act, 1)
-    n_out = N // 2 if act == _lib.MOE_ACT_SWIGLU else N
-    L = lib()
+    (T, half), N, device = xs, wshape[0], x.device
+    K = 2 * half
+    fmt, act, cols, nbytes, n_out = _fp4_products(format, act, 1, N, K)
+    args = (_arg(x, torch.uint8, "x", xs, device), _arg(x_scales, torch.uint8, "x_scales", (T, cols), device),
+            _arg(w, torch.uint8, "w", wshape, device), _arg(w_scales, torch.uint8, "w_scales", (nbytes,), device),
+            _opt(factor, torch.float32, "factor", (1,), device))
     handle, on = _enter(device, stream)
     try:
         out, out_ptr = _out(out, torch.bfloat16, "out", (T, n_out), device)
         ws, ws_ptr, nbytes = _workspace(workspace, _fp4_workspace_bytes(T, 1, N, K), device)
-        st = L.moe_fp4_linear(*ptrs, out_ptr, T, N, K, fmt, act, ws_ptr, nbytes, _flag(err_flag, device), handle)
+        st = lib().moe_fp4_linear(*args, out_ptr, T, N, K, fmt, act, ws_ptr, nbytes, _flag(err_flag, device), handle)
     finally:
         if on is not None:
             on.close()
@@ -513,23 +506,26 @@ def moe_fp4_expert_linear(x, x_scales, w, w_scales, offsets, counts, format="nvf
     (w[e] @ x[src])) for the rows r of each expert's segment.  x [n, K/2],
     w [E, N, K/2] uint8, x_scales and w_scales as in moe_fp4_linear, factor [E]
     FP32; the rest as in moe_expert_linear."""
-    if x.dim() != 2 or w.dim() != 3 or x.shape[1] != w.shape[2]:
+    xs, wshape = x.shape, w.shape
+    if len(xs) != 2 or len(wshape) != 3 or xs[1] != wshape[2]:
         raise ValueError("x must be [n, K/2] and w [E, N, K/2]")
-    E, device = w.shape[0], x.device
+    (n_x, half), (E, N, _), device = xs, wshape, x.device
+    K = 2 * half
     if offsets.dim() != 1 or offsets.shape[0] not in (E, E + 1):
         raise ValueError("offsets must have E or E + 1 entries")
-    (xp, xs, wp, wsc, fac), (n_x, N, K), fmt, act = _fp4_operands(x, x_scales, w, w_scales, format, factor, act, E)
+    fmt, act, cols, nbytes, n_out = _fp4_products(format, act, E, N, K)
     n_rows = n_x if row_token is None else row_token.numel()
-    n_out = N // 2 if act == _lib.MOE_ACT_SWIGLU else N
-    tok = _opt(row_token, torch.int32, "row_token", (n_rows,), device)
-    off, cnt = _arg(offsets, torch.int32, "offsets", offsets.shape, device), _arg(counts, torch.int32, "counts", (E,), device)
-    L = lib()
+    args = (_arg(x, torch.uint8, "x", xs, device), _arg(x_scales, torch.uint8, "x_scales", (n_x, cols), device), n_x,
+            _opt(row_token, torch.int32, "row_token", (n_rows,), device), _arg(w, torch.uint8, "w", wshape, device),
+            _arg(w_scales, torch.uint8, "w_scales", (nbytes,), device), _opt(factor, torch.float32, "factor", (E,), device),
+            _arg(offsets, torch.int32, "offsets", offsets.shape, device),
+            _arg(counts, torch.int32, "counts", (E,), device))
     handle, on = _enter(device, stream)
     try:
         out, out_ptr = _out(out, torch.bfloat16, "out", (n_rows, n_out), device)
         ws, ws_ptr, nbytes = _workspace(workspace, _fp4_workspace_bytes(n_rows, E, N, K), device)
-        st = L.moe_fp4_expert_linear(xp, xs, n_x, tok, wp, wsc, fac, off, cnt, out_ptr, n_rows, E, N, K, fmt, act, ws_ptr,
-                                     nbytes, _flag(err_flag, device), handle)
+        st = lib().moe_fp4_expert_linear(*args, out_ptr, n_rows, E, N, K, fmt, act, ws_ptr, nbytes,
+                                         _flag(err_flag, device), handle)
     finally:
         if on is not None:
             on.close()

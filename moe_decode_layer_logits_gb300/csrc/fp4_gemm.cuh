@@ -30,7 +30,17 @@
 //    these 4 x 4 words in place.
 //  - pairs (cta_group::2) for large segments: 256 weight rows and up to 256 rows.
 //
-// Measured, NVFP4, SwiGLU, K = 6144, N = 4096, 8 experts a token, even: FIGURES
+// Measured, NVFP4, SwiGLU, K = 6144, N = 4096, 8 experts a token, cold weights: of
+// 256 experts T = 64 416 us (6.9 TB/s: reads alone are faster than a copy), T = 512
+// 556, T = 2048 559 (6.6 TB/s), T = 4096 590, T = 6144 612 (6.3 TB/s, 4.0 PFLOP/s),
+// T = 8192 760 to 780 (4.3 PFLOP/s; half of the experts then have more than 256 rows
+// and two row tiles); of 64 experts T = 1 23.5 us (113 MB: 4.8 TB/s; launch, first
+// stages and a partial round), T = 16384 1.03 to 1.08 ms (6.1 to 6.4 PFLOP/s).  The
+// weights' bytes bound it up to about 200 rows an expert.  Behind that a pair's feed
+// does: a stage of 256 rows brings 38 KB into each CTA's shared memory, which the
+// MMAs read once, and takes 400 ns where its MMAs take 270; without the rows'
+// copies it is 9 to 12% faster, without the weights' 11%, without the epilogue 9 to
+// 11%, and with zeros as scales (less power) 14%.
 #pragma once
 
 #include "expert_gemm.cuh"
@@ -796,7 +806,7 @@ cudaError_t launch_fp4(const CUtensorMap& mw, const CUtensorMap& ms, const CUten
   cfg.numAttrs = 1;
   if constexpr (PAIR) {
     const int rows_out = SWIGLU ? 128 : 256;
-    cfg.gridDim = dim3(static_cast<unsigned>(4 * gemm_ctas()), 1, 1);
+    cfg.gridDim = dim3(static_cast<unsigned>(8 * gemm_ctas()), 1, 1);
     cfg.blockDim = dim3(256, 1, 1);
     cfg.dynamicSmemBytes = launch_smem(static_cast<size_t>(3 * p.g.E + 1) * sizeof(int));
     e = cudaLaunchKernelEx(&cfg, fp4_row_scales_kernel<FORMAT, ONE>, p, (p.g.n_out + rows_out - 1) / rows_out, G / 2);
