@@ -65,6 +65,7 @@ struct Fp4Params {
   const float* factor;
   int row_scales;   // scale bytes of a row of x
   int whole_scales; // a stage's scales of a row are one aligned piece
+  int box_rows;     // pairs of one segment: rows of a CTA that one tiled copy brings
   uint8_t* row_scale_tiles;  // pairs: [row tile][stage][2][word][32][4 words]
 };
 
@@ -142,6 +143,22 @@ __device__ __forceinline__ void copy_async(uint32_t dst, const void* src, int n)
     asm volatile("cp.async.ca.shared.global [%0], [%1], %3, %2;" ::"r"(dst), "l"(src), "r"(n), "n"(BYTES) : "memory");
 }
 
+// Row tiles of the one segment of a projection in pairs: of the few numbers that
+// hold it, the one whose rounds over the pairs take the fewest rows.
+__host__ __device__ inline int segment_tiles(int total, int mt, int pairs) {
+  const int least = row_tiles(total, 8);
+  int best = least;
+  long long cost = -1;
+  for (int n = least; n < least + 8 && n > 0; ++n) {
+    const long long c = ((static_cast<long long>(n) * mt + pairs - 1) / pairs) * round_up((total + n - 1) / n, 16);
+    if (cost < 0 || c < cost) {
+      cost = c;
+      best = n;
+    }
+  }
+  return best;
+}
+
 // The tile list; every thread calls it.  ONE: a single segment of all rows.
 template <bool PAIR, bool ONE>
 __device__ void list_fp4(const GemmParams& p, Tiles t, int mt, int walkers, int* bn_out) {
@@ -157,7 +174,7 @@ __device__ void list_fp4(const GemmParams& p, Tiles t, int mt, int walkers, int*
     t.start[0] = 0;
     t.count[0] = static_cast<int>(p.n_rows);
     t.before[0] = 0;
-    t.before[1] = scatter_tiles(t.count[0], mt, walkers);
+    t.before[1] = segment_tiles(t.count[0], mt, walkers);
     *bn_out = kPairRows;
   }
   __syncthreads();
@@ -311,7 +328,8 @@ template <int FORMAT, bool SWIGLU, bool PAIR, bool ONE>
 // (registers that leave room for another kernel's blocks beside single CTAs too)
 __global__ void __launch_bounds__(kFp4Threads(true), 1)
 fp4_gemm_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid_constant__ CUtensorMap tmap_s,
-                const __grid_constant__ CUtensorMap tmap_r, const __grid_constant__ Fp4Params q) {
+                const __grid_constant__ CUtensorMap tmap_r, const __grid_constant__ CUtensorMap tmap_x,
+                const __grid_constant__ Fp4Params q) {
   const GemmParams& p = q.g;
   constexpr int kWords = fp4_stage_scales(FORMAT) / 4;  // of a row and stage
   constexpr int kScales = kWords * 512;                 // bytes of 128 rows' scales
@@ -333,7 +351,7 @@ fp4_gemm_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid_constan
   if (threadIdx.x < kFp4Stages) {
     // a stage is full when the weights have landed, the rows have been reported (by
     // each CTA of a pair) and, in a pair, the MMAs that used its scale columns are done
-    mbar_init(&sb.full[threadIdx.x], PAIR ? 4 : 2);
+    mbar_init(&sb.full[threadIdx.x], PAIR ? (ONE ? 2 : 4) : 2);
     mbar_init(&sb.landed[threadIdx.x], 32 * kLoaders);
     mbar_init(&sb.empty[threadIdx.x], 1);
     mbar_init_fence();
@@ -350,6 +368,7 @@ fp4_gemm_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid_constan
     prefetch_map(&tmap_w);
     prefetch_map(&tmap_s);
     if (PAIR) prefetch_map(&tmap_r);
+    if (PAIR && ONE) prefetch_map(&tmap_x);
   }
   if (warp == 1) tmem_alloc<PAIR>(&sb.tmem_base, 2 * kAccCols);
   // the trigger comes behind the wait, so that what is launched next finds this
@@ -442,7 +461,7 @@ fp4_gemm_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid_constan
       const uint64_t once = l2_evict_first_policy(), keep = l2_evict_normal_policy();
       const int withheld = who == 0 ? p.withhold : -1;
       // of a stage's copies, in both CTAs of a pair
-      constexpr uint32_t bytes = PAIR ? 2 * (kRowsAt + kGroups * kScales) : kRowsAt;
+      const uint32_t bytes = PAIR ? 2 * (kRowsAt + kGroups * kScales + (ONE ? q.box_rows * kRowBytes : 0)) : kRowsAt;
       int at = 0;
       Piece w;
       int n = 0;  // stages so far
@@ -473,6 +492,7 @@ fp4_gemm_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid_constan
               tma_load_5d<PAIR>(a + i * 32 * kRowBytes, &tmap_w, kb * kBK, m * 64 + i * 16, 0, 0, w.e, bar, pol);
           }
           tma_load_5d<PAIR>(a + kBM * kRowBytes, &tmap_s, 0, first + kb * (kScales / 1024), 0, 0, 0, bar, pol);
+          if (PAIR && ONE) tma_load_5d<PAIR>(a + kRowsAt, &tmap_x, kb * kBK, w.r0 + rank * (round_up(w.nr, 16) / 2), 0, 0, 0, bar, keep);
           if (PAIR) tma_load_5d<PAIR>(a + kRowsAt + row_bytes, &tmap_r, 0, rows_first + kb * (2 * kScales / 1024), 0, 0, 0, bar, keep);
         }
       }
@@ -614,6 +634,8 @@ fp4_gemm_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid_constan
         store(c, v);
       }
     }
+  } else if (PAIR && ONE) {
+    // (the rows come by tiled copies)
   } else if (warp < 6 + kLoaders) {
     // ------------------------------------------------------------- gather
     // Warp j takes rows 16 i + 4 j .. + 3 of this CTA's rows, eight lanes a
@@ -784,9 +806,18 @@ inline bool scale_map(CUtensorMap* map, const void* scales, int64_t bytes, int b
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// Rows of codes, `cols` BF16 numbers' bytes each, in boxes of a stage and `rows`.
+inline bool rows_map(CUtensorMap* map, const void* x, int64_t n, int64_t cols, int rows) {
+  const cuuint64_t row = static_cast<cuuint64_t>(cols) * 2, all = row * static_cast<cuuint64_t>(n);
+  const cuuint64_t dims[5] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(n), 1, 1, 1};
+  const cuuint64_t strides[4] = {row, all, all, all};
+  const cuuint32_t box[5] = {kBK, static_cast<cuuint32_t>(rows), 1, 1, 1};
+  return make_map(map, x, 5, dims, strides, box);
+}
+
 template <int FORMAT, bool SWIGLU, bool PAIR, bool ONE>
-cudaError_t launch_fp4(const CUtensorMap& mw, const CUtensorMap& ms, const CUtensorMap& mr, const Fp4Params& p,
-                       cudaStream_t stream) {
+cudaError_t launch_fp4(const CUtensorMap& mw, const CUtensorMap& ms, const CUtensorMap& mr, const CUtensorMap& mx,
+                       const Fp4Params& p, cudaStream_t stream) {
   static std::atomic<bool> done[64];
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -822,7 +853,7 @@ cudaError_t launch_fp4(const CUtensorMap& mw, const CUtensorMap& ms, const CUten
     attr[1].val.clusterDim.z = 1;
     cfg.numAttrs = 2;
   }
-  return cudaLaunchKernelEx(&cfg, fp4_gemm_kernel<FORMAT, SWIGLU, PAIR, ONE>, mw, ms, mr, p);
+  return cudaLaunchKernelEx(&cfg, fp4_gemm_kernel<FORMAT, SWIGLU, PAIR, ONE>, mw, ms, mr, mx, p);
 }
 
 template <int FORMAT, bool SWIGLU, bool ONE>
@@ -856,9 +887,18 @@ cudaError_t prepare_and_launch(const Fp4Gemm& g, cudaStream_t stream) {
     CUtensorMap mr;
     p.row_scale_tiles = static_cast<uint8_t*>(g.workspace);
     if (!scale_map(&mr, p.row_scale_tiles, row_scale_bytes(g.n_rows, g.E, g.K, FORMAT), 2 * kMapRows)) return cudaErrorInvalidValue;
-    return launch_fp4<FORMAT, SWIGLU, true, ONE>(mw, ms, mr, p, stream);
+    if (ONE) {
+      CUtensorMap mx;
+      const int rows_out = SWIGLU ? 128 : 256, total = static_cast<int>(g.n_rows);
+      const int tiles = segment_tiles(total, (p.g.n_out + rows_out - 1) / rows_out, gemm_ctas() / 2);
+      const int sixteens = total / 16 + (total % 16 != 0 ? 1 : 0);
+      p.box_rows = (sixteens + tiles - 1) / tiles * 8;  // half of the widest tile
+      if (!rows_map(&mx, g.x, g.n_x, g.K / 4, p.box_rows)) return cudaErrorInvalidValue;
+      return launch_fp4<FORMAT, SWIGLU, true, ONE>(mw, ms, mr, mx, p, stream);
+    }
+    return launch_fp4<FORMAT, SWIGLU, true, ONE>(mw, ms, mr, mr, p, stream);
   }
-  return launch_fp4<FORMAT, SWIGLU, false, ONE>(mw, ms, ms, p, stream);
+  return launch_fp4<FORMAT, SWIGLU, false, ONE>(mw, ms, ms, ms, p, stream);
 }
 
 template <int FORMAT>
