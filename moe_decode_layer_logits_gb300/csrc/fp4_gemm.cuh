@@ -28,13 +28,22 @@
 //    equal row % 32 fill the same four 16-byte places as their four words will; the
 //    relay warp, which stands between the copies and the MMAs anyway, transposes
 //    these 4 x 4 words in place.
+//    Two or four CTAs for a tile of a small projection, each with a part of K and
+//    the sums sent into one CTA's shared memory, were no better: T = 1, K = 6144 9.7
+//    and 10.5 us against 10.8, K = 2048, N = 6144 7.8 against 5.7.
 //  - pairs (cta_group::2) for large segments: 256 weight rows and up to 256 rows.
+//    The rows' scales are laid out by a kernel before (fp4_row_scales_kernel).  The
+//    rows are gathered by warps, or come by one tiled copy where there is one
+//    segment (T = 4096 49.2 -> 46.1 us).  Tensor memory: two accumulators at the ends
+//    of 416 columns, which share up to 96, and scales of two stages behind them.
+//    More buffers of scales and fewer columns of accumulators were slower (three:
+//    E = 64, T = 16384 1.18 ms against 1.12).
 //
 // Measured, NVFP4, SwiGLU, K = 6144, N = 4096, 8 experts a token, cold weights: of
 // 256 experts T = 64 416 us (6.9 TB/s: reads alone are faster than a copy), T = 512
 // 556, T = 2048 559 (6.6 TB/s), T = 4096 590, T = 6144 612 (6.3 TB/s, 4.0 PFLOP/s),
 // T = 8192 760 to 780 (4.3 PFLOP/s; half of the experts then have more than 256 rows
-// and two row tiles); of 64 experts T = 1 23.5 us (113 MB: 4.8 TB/s; launch, first
+// and two row tiles of some 136, each of which has the weights brought again); of 64 experts T = 1 23.5 us (113 MB: 4.8 TB/s; launch, first
 // stages and a partial round), T = 16384 1.03 to 1.08 ms (6.1 to 6.4 PFLOP/s).  The
 // weights' bytes bound it up to about 200 rows an expert.  Behind that a pair's feed
 // does: a stage of 256 rows brings 38 KB into each CTA's shared memory, which the
@@ -182,8 +191,9 @@ __device__ void list_fp4(const GemmParams& p, Tiles t, int mt, int walkers, int*
 
 // silu(g) u for two outputs, the exponential as a power of two: with x = -g log2 e
 // rounded, 2^x is corrected by the rounding error of x to first order, then an
-// approximate reciprocal; within 2^-21.  The bounds keep infinite g and powers
-// beyond FP32's range from 0 * inf: above them 1 / (1 + e^-g) is 1, below 0.
+// approximate reciprocal; within 2^-20 (the two approximations 2^-22 and 2^-23, six
+// roundings of 2^-24).  The bounds keep infinite g and powers beyond FP32's range
+// from 0 * inf; where e^-g is beyond it (g < -88.7), the result is 0.
 __device__ __forceinline__ float2 silu_mul2(float2 g, float2 u) {
   constexpr float kLog2e = 1.4426950408889634f, kLow = static_cast<float>(1.4426950408889634 - static_cast<double>(kLog2e));
   const float2 b = make_float2(fminf(g.x, 100.f), fminf(g.y, 100.f));
@@ -259,8 +269,10 @@ __device__ __forceinline__ int row_tile(const Tiles& t, const Piece& w) {
 // The scales of the rows as pairs read them: for each row tile and stage, two
 // groups of 128 rows in the order of fp4_weight_scales_kernel, so that a stage's
 // come by one tiled copy.  (Gathered by the warps that gather the rows, a line for
-// each row and stage, they took as long as the rows themselves.)  A block takes 128 rows and eight stages at a
-// time, reads eight pieces a row and turns them in shared memory.
+// each row and stage, they took longer than the rows themselves: E = 64, T = 16384
+// without the epilogue 1286 us, without them 1100, without the rows 1151.)  A block
+// takes 128 rows and eight stages at a time, reads eight pieces a row and turns them
+// in shared memory.  Latency bounds it: T = 4096 of one segment 4 us.
 constexpr int kTurnStages = 8;
 
 template <int FORMAT, bool ONE>

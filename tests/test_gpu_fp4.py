@@ -271,6 +271,30 @@ def test_linear_same_bits_again(M):
             assert torch.equal(run_linear(M, c, "nvfp4", "swiglu")[0], a)
 
 
+def test_linear_swiglu_over_the_range_of_its_gate(M):
+    # y = the weight itself (one element of x is 1): gates from -150 to 150 and beyond, ups of 1
+    rng = np.random.default_rng(312)
+    n_out, K = 2048, 64
+    w, ws = np.zeros((2 * n_out, K // 2), np.uint8), np.full((2 * n_out, K // 16), 0x38, np.uint8)
+    w[:n_out, 0], ws[:n_out, 0] = rng.integers(1, 16, n_out), rng.integers(0x18, 0x60, n_out)
+    w[n_out:, 0] = 2                                       # 1.0
+    x, xs = np.zeros((1, K // 2), np.uint8), np.full((1, K // 16), 0x38, np.uint8)
+    x[0, 0] = 2
+    gate = O.fp4_values(w, ws, "nvfp4")[:n_out, 0]
+    assert gate.min() < -90 and gate.max() > 90 and (np.abs(gate) < 0.1).any()
+    with np.errstate(over="ignore"):
+        want = gate / (1 + np.exp(-gate))
+    for T in (1, 1200):                                    # (1200: pairs)
+        rep = {"x": np.repeat(x, T, 0), "xs": np.repeat(xs, T, 0), "w": w, "ws": ws}
+        got = values(run_linear(M, rep, "nvfp4", "swiglu")[0])
+        # FP32's exponential ends at e^88.7: below, the result is 0 instead of some 1e-37
+        err = (2.0 ** -8 + 2.0 ** -20) * np.abs(want) + np.where(gate < -88, 1e-36, 2.0 ** -133)
+        check_rows(got, np.repeat(want[None], T, 0), np.repeat(err[None], T, 0), "range of the gate")
+    big = run_linear(M, {"x": x, "xs": xs, "w": w, "ws": ws}, "nvfp4", "swiglu", 3e38)[0]
+    got = values(big)[0]
+    assert np.all(np.isposinf(got[gate * 3e38 > 3.4e38])) and not np.isnan(got[gate > 0]).any()
+
+
 def test_linear_empty_batch(M):
     c = draw_linear(1, 64, 128, "nvfp4")
     assert run_linear(M, {**c, "x": c["x"][:0], "xs": c["xs"][:0]}, "nvfp4", None)[0].shape == (0, 64)
