@@ -455,11 +455,11 @@ int moe_debug_withhold_stream_stage(int32_t stage);
 int moe_debug_withhold_router_stage(int32_t kb);
 
 /*
- * Test hook of the bounded waits of the expert and adapter products; no
+ * Test hook of the bounded waits of the expert, adapter and 4-bit products; no
  * counterpart on the pages.  The product launches of the next
- * moe_expert_linear or moe_adapter_linear call issue no loads for K block
- * `stage` (counted over all tiles of that thread block) in their first thread
- * block, so that block gives up after its bounded wait: what it had left to
+ * moe_expert_linear, moe_adapter_linear, moe_fp4_linear or moe_fp4_expert_linear
+ * call issue no loads for K block `stage` (counted over all tiles of that thread
+ * block) in their first thread block, so that block gives up after its bounded wait: what it had left to
  * compute is written as NaN, MOE_FLAG_TIMEOUT is set, the launch completes,
  * and the next call is unaffected.  stage -1 cancels the request.  Returns MOE_OK, or
  * MOE_ERR_INVALID_ARG for stage < -1.  Not for production use.

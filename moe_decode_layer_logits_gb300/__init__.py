@@ -550,7 +550,7 @@ def moe_debug_withhold_router_stage(kb):
 
 def moe_debug_withhold_expert_stage(stage):
     """Test hook of the bounded waits: the product launches of the next
-    moe_expert_linear or moe_adapter_linear call issue no loads for K block
+    moe_expert_linear, moe_adapter_linear or 4-bit product call issue no loads for K block
     `stage` of their first thread block, so that its wait runs out, what it
     had left to compute is NaN and MOE_FLAG_TIMEOUT is set; -1 cancels the
     request."""
