@@ -18,6 +18,7 @@ import numpy as np
 import pytest
 import torch
 
+import moe_decode_layer_logits_gb300 as M_
 import oracle as O
 from _guard import Guarded, check_all
 from moe_decode_layer_logits_gb300 import _lib as L
@@ -444,7 +445,7 @@ def test_expert_linear_overlapping_segments_take_nothing(M):
 
 
 @pytest.mark.parametrize("act", [None, "swiglu"])
-@pytest.mark.parametrize("T,gather", [(2, True), (2, False), (300, True), (300, False)])  # single CTAs, pairs
+@pytest.mark.parametrize("T,gather", [(2, True), (2, False), (300, True), (300, False)])
 def test_expert_linear_leaves_nan_where_a_wait_ran_out(M, T, gather, act):
     c = draw_layer(6, T, 4, 2, 2048, 4096, "nvfp4", gather=gather)
     want, flag = run_expert(M, c, "nvfp4", act, gather)
@@ -523,7 +524,7 @@ def test_products_with_offsets_beyond_31_bits(M):
     assert torch.equal(M.moe_fp4_expert_linear(x, xs, w, t, four, four[1:], row_token=few), want[few.long()])
 
 
-@pytest.mark.parametrize("T,N,K", [(3, 512, 256), (1200, 8192, 1024)])
+@pytest.mark.parametrize("T,N,K", [(3, 512, 256), (1200, 8192, 4096)])
 def test_linear_behind_a_kernel_that_runs_long(M, T, N, K):
     # An expert map of 2^30 slots lets its dependents start at once and runs for
     # longer than the probes of one bounded wait last: the call behind it must not
@@ -550,7 +551,7 @@ def test_linear_behind_a_kernel_that_runs_long(M, T, N, K):
 @pytest.mark.parametrize("T", [2, 1200])
 def test_quantised_rows_are_read_behind_the_kernel_that_writes_them(M, T):
     # quantisation and product back to back, over and over, on new rows each time
-    N, K = 4096, 2048
+    N, K = 8192, 4096
     g = torch.Generator(device="cuda")
     g.manual_seed(7)
     rows = torch.randn(6, T, K, generator=g, device="cuda", dtype=torch.bfloat16)
@@ -566,6 +567,180 @@ def test_quantised_rows_are_read_behind_the_kernel_that_writes_them(M, T):
     got = [M.moe_fp4_linear(*M.moe_fp4_quantize(r, codes=codes, scales=scales), w, t) for r in rows]
     for a, b in zip(got, want):
         assert torch.equal(a, b)
+
+
+# ---------------------------------------------------------------------------
+# products large enough for pairs of CTAs (against 64-bit products on the GPU)
+# ---------------------------------------------------------------------------
+
+def in_pairs(n_rows, E, N, K):
+    """Whether a call of these sizes runs in pairs: it has a workspace then."""
+    return L.lib().moe_fp4_linear_workspace(n_rows, E, N, K) > 0
+
+
+def bytes_of(seed, lo, hi, *shape):
+    g = torch.Generator(device="cuda")
+    g.manual_seed(seed)
+    return torch.randint(lo, hi, shape, generator=g, device="cuda", dtype=torch.uint8)
+
+
+def decoded(codes, scales, fmt):
+    e2m1 = torch.tensor(O.fp4_e2m1, device="cuda")
+    scale = torch.tensor(O.fp4_scale_values(fmt), device="cuda")
+    two = torch.stack([codes & 15, codes >> 4], dim=-1).flatten(-2)
+    return e2m1[two.long()] * scale[scales.long()].repeat_interleave(O.FP4_BLOCK[fmt], dim=-1)
+
+
+def reference(x, w, factor, act):
+    """O.fp4_linear on the GPU."""
+    rel = rel_sum(x.shape[1])
+    y, dy = factor * (x @ w.T), (x.abs() @ w.abs().T) * abs(factor) * rel
+    dy += 2.0 ** -24 * y.abs()
+    if act:
+        h = y.shape[1] // 2
+        gate, up, dg, du = y[:, :h], y[:, h:], dy[:, :h], dy[:, h:]
+        s = gate / (1 + torch.exp(-gate))
+        y, dy = s * up, 1.1 * dg * (up.abs() + du) + s.abs() * du
+        dy = dy + 2.0 ** -20 * y.abs()
+    return y, dy + 2.0 ** -8 * (y.abs() + dy) + 2.0 ** -133
+
+
+LENGTHS = [1, 15, 0, 16, 17, 128, 129, 192, 207, 208, 209, 224, 225, 240, 241, 255, 256, 257, 0, 272, 415, 416, 417, 511, 512, 513, 700]
+
+
+def large_case(fmt, act, N, K, gather, lengths=LENGTHS, seed=0):
+    counts = torch.tensor(lengths, dtype=torch.int32)
+    offsets = torch.cat([torch.zeros(1, dtype=torch.int32), torch.cumsum(counts, 0, dtype=torch.int32)])
+    E, n = len(lengths), int(offsets[-1])
+    n_x = 500 if gather else n
+    B = O.FP4_BLOCK[fmt]
+    lo, hi = (40, 70) if fmt == "nvfp4" else (120, 130)
+    assert in_pairs(n, E, N, K)
+    g = torch.Generator(device="cuda")
+    g.manual_seed(seed)
+    c = dict(x=bytes_of(seed + 1, 0, 256, n_x, K // 2), xs=bytes_of(seed + 2, lo, hi, n_x, K // B),
+             w=bytes_of(seed + 3, 0, 256, E, N, K // 2), ws=bytes_of(seed + 4, lo, hi, E, N, K // B), offsets=offsets.cuda(),
+             counts=counts.cuda(), factor=torch.rand(E, generator=g, device="cuda") * 0.01,
+             token=torch.randint(0, n_x, (n,), generator=g, device="cuda", dtype=torch.int32) if gather else None)
+    c["t"] = M_.moe_fp4_weight_scales(c["ws"], format=fmt, act=act)
+    return c, n
+
+
+def run_large(c, n, fmt, act):
+    N = c["w"].shape[1]
+    out, flag = Guarded((n, N // 2 if act else N), torch.bfloat16, fill=3.0), Guarded((1,), torch.int32, fill=0)
+    M_.moe_fp4_expert_linear(c["x"], c["xs"], c["w"], c["t"], c["offsets"], c["counts"], format=fmt, factor=c["factor"],
+                             row_token=c["token"], act=act, out=out.t, err_flag=flag.t)
+    check_all(out=out, flag=flag)
+    return out.t, int(flag.t.item())
+
+
+def check_large(c, n, fmt, act, out, skip=None):
+    x = decoded(c["x"], c["xs"], fmt)
+    for e, (off, cnt) in enumerate(zip(c["offsets"].tolist(), c["counts"].tolist())):
+        rows = torch.arange(off, off + cnt, device="cuda")
+        if skip is not None:
+            rows = rows[~skip[rows]]
+        want, err = reference(x[c["token"][rows].long()] if c["token"] is not None else x[rows], decoded(c["w"][e], c["ws"][e], fmt),
+                              float(c["factor"][e]), act)
+        d = (out[rows].double() - want).abs()
+        assert bool((d <= err).all()), (e, cnt, float((d / err).max()))
+
+
+@pytest.mark.parametrize("fmt", ["nvfp4", "mxfp4"])
+@pytest.mark.parametrize("act", [None, "swiglu"])
+@pytest.mark.parametrize("N,K,gather", [(4112, 1408, True), (4112, 1536, False), (8208, 640, False), (8240, 768, True), (2064, 2816, True)])
+def test_pairs_segment_lengths(M, N, K, gather, act, fmt):
+    c, n = large_case(fmt, act, N, K, gather)
+    out, flag = run_large(c, n, fmt, act)
+    assert flag == 0
+    check_large(c, n, fmt, act, out)
+
+
+@pytest.mark.parametrize("act", [None, "swiglu"])
+def test_pairs_word_long_scales(M, act):
+    # rows' scales that start and end on any word
+    c, n = large_case("nvfp4", act, 4112, 1344, True)
+    check_large(c, n, "nvfp4", act, run_large(c, n, "nvfp4", act)[0])
+    c, n = large_case("nvfp4", act, 4112, 1536, True)
+    want, _ = run_large(c, n, "nvfp4", act)
+    room = torch.zeros(c["xs"].numel() + 16, dtype=torch.uint8, device="cuda")
+    c["xs"] = room[4:4 + c["xs"].numel()].view(c["xs"].shape).copy_(c["xs"])
+    assert torch.equal(run_large(c, n, "nvfp4", act)[0], want)
+
+
+@pytest.mark.parametrize("fmt", ["nvfp4", "mxfp4"])
+@pytest.mark.parametrize("act", [None, "swiglu"])
+@pytest.mark.parametrize("T,N,K", [(1024, 8192, 4096), (1111, 8208, 4224), (1800, 16400, 1152), (2305, 4112, 3712), (9000, 2064, 2048)])
+def test_pairs_of_one_segment(M, T, N, K, act, fmt):
+    assert in_pairs(T, 1, N, K)
+    B = O.FP4_BLOCK[fmt]
+    lo, hi = (40, 70) if fmt == "nvfp4" else (120, 130)
+    x, xs, w, ws = bytes_of(1, 0, 256, T, K // 2), bytes_of(2, lo, hi, T, K // B), bytes_of(3, 0, 256, N, K // 2), bytes_of(4, lo, hi, N, K // B)
+    f = torch.tensor([0.003], device="cuda")
+    out, flag = Guarded((T, N // 2 if act else N), torch.bfloat16, fill=3.0), Guarded((1,), torch.int32, fill=0)
+    M.moe_fp4_linear(x, xs, w, M.moe_fp4_weight_scales(ws, format=fmt, act=act), format=fmt, factor=f, act=act, out=out.t, err_flag=flag.t)
+    check_all(out=out, flag=flag)
+    assert int(flag.t.item()) == 0
+    wv = decoded(w, ws, fmt)
+    for a in range(0, T, 2048):
+        want, err = reference(decoded(x[a:a + 2048], xs[a:a + 2048], fmt), wv, float(f), act)
+        d = (out.t[a:a + 2048].double() - want).abs()
+        assert bool((d <= err).all()), float((d / err).max())
+
+
+def test_pairs_bad_tokens_and_nan_scales_stay_in_their_rows(M):
+    c, n = large_case("nvfp4", "swiglu", 4112, 1536, True)
+    clean, _ = run_large(c, n, "nvfp4", "swiglu")
+    bad = torch.zeros(n, dtype=torch.bool, device="cuda")
+    bad[torch.tensor([0, 31, 400, 4000, n - 1], device="cuda")] = True
+    token = c["token"].clone()
+    token[bad] = torch.tensor([-1, 500, 2 ** 31 - 1, -7, 501], dtype=torch.int32, device="cuda")
+    out, flag = run_large({**c, "token": token}, n, "nvfp4", "swiglu")
+    assert flag == L.MOE_FLAG_BAD_INDEX and not out[bad].any() and torch.equal(out[~bad], clean[~bad])
+    xs = c["xs"].clone()
+    xs[77, 90] = 0x7F
+    out, flag = run_large({**c, "xs": xs}, n, "nvfp4", "swiglu")
+    hit = c["token"] == 77
+    assert flag == 0 and hit.any() and torch.isnan(out[hit]).all() and torch.equal(out[~hit], clean[~hit])
+    again, _ = run_large(c, n, "nvfp4", "swiglu")
+    assert torch.equal(again, clean)
+
+
+@pytest.mark.parametrize("gather", [True, False])
+def test_pairs_leave_nan_where_a_wait_ran_out(M, gather):
+    c, n = large_case("nvfp4", "swiglu", 4112, 1536, gather)
+    want, _ = run_large(c, n, "nvfp4", "swiglu")
+    for stage in (0, 2, 40):
+        M.moe_debug_withhold_expert_stage(stage)
+        out, flag = run_large(c, n, "nvfp4", "swiglu")
+        assert flag & L.MOE_FLAG_TIMEOUT
+        lost = torch.isnan(out)
+        assert torch.equal(out[~lost], want[~lost]) and 0 < int(lost.sum()) < out.numel()
+    again, flag = run_large(c, n, "nvfp4", "swiglu")
+    assert flag == 0 and torch.equal(again, want)
+
+
+def test_pairs_captured_on_two_streams(M):
+    """Two graphs of large products, whose workspaces are their own, replayed at once."""
+    cases = [large_case("nvfp4", "swiglu", 4112, 1536, True, seed=s) for s in (0, 50)]
+    want = [run_large(c, n, "nvfp4", "swiglu")[0].clone() for c, n in cases]
+    graphs, outs = [], []
+    call = lambda c: M.moe_fp4_expert_linear(c["x"], c["xs"], c["w"], c["t"], c["offsets"], c["counts"], factor=c["factor"],
+                                             row_token=c["token"], act="swiglu")
+    for c, _ in cases:
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            outs.append(call(c))
+        graphs.append(graph)
+    streams = [torch.cuda.Stream() for _ in graphs]
+    for _ in range(4):
+        for graph, s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                graph.replay()
+    torch.cuda.synchronize()
+    for out, ref in zip(outs, want):
+        assert torch.equal(out, ref)
 
 
 # ---------------------------------------------------------------------------
