@@ -8,13 +8,19 @@
 //    6 m g - amax, m the midpoint to the neighbour on the product's side, keeps or
 //    moves it; 6 m has at most 7 bits, so one fused multiply-add has that sign
 //    exactly;
-//  - the codes: |x| against the seven midpoints times scale times global scale.
-//    m s is exact in FP32 (at most 7 bits); times g it is rounded down, and cut to
-//    BF16, for the midpoints that go to the lower code, and rounded up for the
-//    others, which leaves every comparison with a BF16 number as it was.
-// So no quotient is formed, and two elements are compared at once.  The values of
+//  - the codes: where no midpoint times scale times global scale lies next to a
+//    BF16 number, an FP32 quotient with its few roundings is on the right side of
+//    every midpoint, and the conversion instruction finds the code.  That depends on
+//    the mantissa of the global scale alone, so a warp asks it once.  (MXFP4's
+//    quotients are exact.)
+//  - else, as without a global scale, |x| is compared with the seven midpoints times
+//    scale times global scale.  m s is exact in FP32 (at most 7 bits); times g it is
+//    rounded down, and cut to BF16, for the midpoints that go to the lower code, and
+//    rounded up for the others, which leaves every comparison with a BF16 number as
+//    it was.  Two elements are compared at once.  The values of
 // the eight codes of a block, rounded to BF16 once, are a table of 16 bytes on the
 // way back, from which byte permutations pick four at a time.
+#include <cuda_fp4.h>
 #include <cuda_fp8.h>
 
 #include "common.cuh"
@@ -78,7 +84,7 @@ __device__ __forceinline__ uint32_t pick(uint32_t mask, uint32_t yes, uint32_t n
 // 4 [b2] + 2 [b1] + [b0] in each half, from masks of 0xFFFF.  As numbers the masks
 // with bits h and l are 2^16 (l - h) - l, so their weighted sum times -(2^16 + 1)
 // is 2^16 of the high code plus the low one.  (Multiply-adds, as the logic pipe
-// bounds this kernel: T = 8192 33.3 -> 30.4 us.)
+// bounds this way: T = 8192 33.3 -> 30.4 us.)
 __device__ __forceinline__ uint32_t bits_of(uint32_t b2, uint32_t b1, uint32_t b0) {
   uint32_t s;
   asm("mad.lo.u32 %0, %1, 2, %2;" : "=r"(s) : "r"(b1), "r"(b0));
@@ -86,9 +92,21 @@ __device__ __forceinline__ uint32_t bits_of(uint32_t b2, uint32_t b1, uint32_t b
   return s * 0xFFFEFFFFu;
 }
 
+// Whether an FP32 quotient x / (s g) may lie on the other side of a midpoint than
+// the real one, or on it: some m s g within 32 units of FP32's last place from a
+// BF16 number, over all mantissas of m (1, 1.25, 1.5, 1.75) and s (1 to 1.875), one
+// product a lane.  (The quotient's roundings are some 2^-22, 2 to 4 units; a code
+// needs x next to the midpoint, and x is a BF16 number.)
+__device__ __forceinline__ bool near_midpoints(float g) {
+  const int lane = threadIdx.x & 31;
+  const float ms = (1.f + 0.25f * static_cast<float>(lane & 3)) * (1.f + 0.125f * static_cast<float>(lane >> 2));
+  const uint32_t low = __float_as_uint(ms * g) & 0xFFFFu;
+  return __any_sync(0xFFFFFFFFu, low <= 32u || low >= 0x10000u - 32u);
+}
+
 // One piece: 16 BF16 numbers to 8 bytes of codes; `scale` of its block.
 template <int FORMAT>
-__device__ __forceinline__ uint2 quantize_piece(const uint4 (&v)[2], float g, float about, bool usable_g, int& scale) {
+__device__ __forceinline__ uint2 quantize_piece(const uint4 (&v)[2], float g, float about, bool usable_g, bool near, int& scale) {
   const uint32_t w[8] = {v[0].x, v[0].y, v[0].z, v[0].w, v[1].x, v[1].y, v[1].z, v[1].w};
   uint32_t top = 0;
 #pragma unroll
@@ -108,6 +126,16 @@ __device__ __forceinline__ uint2 quantize_piece(const uint4 (&v)[2], float g, fl
     s = e8m0_value(scale);
   }
   if (!codes) return make_uint2(0u, 0u);
+  if (FORMAT == MOE_FP4_MX || !near) {
+    const float inverse = FORMAT == MOE_FP4_MX ? __uint_as_float(static_cast<uint32_t>(254 - scale) << 23) : __frcp_rn(s * g);
+    uint32_t out[2] = {0u, 0u};
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const float2 q = make_float2(bf16lo(w[j]) * inverse, bf16hi(w[j]) * inverse);
+      out[j >> 2] |= static_cast<uint32_t>(__nv_cvt_float2_to_fp4x2(q, __NV_E2M1, cudaRoundNearest)) << (8 * (j & 3));
+    }
+    return make_uint2(out[0], out[1]);
+  }
   const uint32_t t0 = threshold<true>(0.25f * s, g), t1 = threshold<false>(0.75f * s, g), t2 = threshold<true>(1.25f * s, g),
                  t3 = threshold<false>(1.75f * s, g), t4 = threshold<true>(2.5f * s, g), t5 = threshold<false>(3.5f * s, g),
                  t6 = threshold<true>(5.f * s, g);
@@ -131,8 +159,9 @@ __device__ __forceinline__ uint2 quantize_piece(const uint4 (&v)[2], float g, fl
   return make_uint2(out[0], out[1]);
 }
 
-// Measured, T = 8192, K = 6144: NVFP4 29.5 us (129 MB: 4.4 TB/s, 65% of the copy
-// rate), MXFP4 28 us; without any of the arithmetic 21.6.  The logic pipe bounds it.
+// Measured, T = 8192, K = 6144 (129 MB): NVFP4 21.7 us (5.9 TB/s, 89% of the copy
+// rate), MXFP4 20.7, HBM; by comparisons, as without a global scale or next to
+// midpoints, 28.5 to 30.6 (the logic pipe).
 template <int FORMAT>
 __global__ void __launch_bounds__(kThreads)
 fp4_quantize_kernel(const uint4* x, const float* global_scale, uint2* codes, uint8_t* scales, int64_t pieces) {
@@ -151,11 +180,12 @@ fp4_quantize_kernel(const uint4* x, const float* global_scale, uint2* codes, uin
   const float g = FORMAT == MOE_FP4_NV && global_scale ? __ldg(global_scale) : 1.f;
   const bool usable_g = usable(g);
   const float about = 1.f / (6.f * g);
+  const bool near = FORMAT == MOE_FP4_NV && near_midpoints(g);
 #pragma unroll
   for (int k = 0; k < kPieces; ++k) {
     const int64_t i = first + k * kThreads;
     int scale;
-    const uint2 c = quantize_piece<FORMAT>(v[k], g, about, usable_g, scale);
+    const uint2 c = quantize_piece<FORMAT>(v[k], g, about, usable_g, near, scale);
     if (i < pieces) {  // (no thread leaves before the others' shuffles)
       codes[i] = c;
       if (FORMAT == MOE_FP4_NV) scales[i] = static_cast<uint8_t>(scale);

@@ -87,6 +87,22 @@ def test_quantize_ties_zeros_and_the_ends_of_the_range(M, fmt):
             check_quantize(M, bits, fmt, g)
 
 
+def test_quantize_global_scales_that_bring_midpoints_next_to_bf16_numbers(M):
+    # g such that midpoint * scale * g is a BF16 number, or a few, 30 and 40 units of FP32's last place beside one
+    rng = np.random.default_rng(305)
+    bits = draw_bf16(rng, (64, 256), 1.0)
+    for ms in (1.0, 1.25 * 1.375, 1.75 * 1.875, 1.5 * 1.125):
+        for off in (0, 1, -1, 3, -30, 30, 40, -40):
+            near = np.float32(1.0078125 / 256) / np.float32(ms)
+            g = (near.view(np.int32) + np.int32(off)).view(np.float32)
+            x = bits.copy()
+            # elements that sit at such midpoints: x = m s g for many m and s, rounded to BF16
+            at = np.outer(np.array([0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5.0]), 2.0 ** np.arange(-6, 8) * ms).reshape(-1)[:64] * float(g)
+            x[:, 3::16] = O.f64_to_bf16_bits(np.resize(at, (64, 16)))
+            check_quantize(M, x, "nvfp4", float(g))
+            check_quantize(M, O.f64_to_bf16_bits(O.bf16_bits_to_f64(x) * 2.0 ** -9), "nvfp4", float(g))
+
+
 def test_quantize_every_bf16_as_the_largest_of_its_block(M):
     # 2^15 blocks: the largest takes every value, the others lie below it
     rng = np.random.default_rng(302)
