@@ -8,16 +8,18 @@
 //    6 m g - amax, m the midpoint to the neighbour on the product's side, keeps or
 //    moves it; 6 m has at most 7 bits, so one fused multiply-add has that sign
 //    exactly;
-//  - the codes: where no midpoint times scale times global scale lies next to a
-//    BF16 number, an FP32 quotient with its few roundings is on the right side of
-//    every midpoint, and the conversion instruction finds the code.  That depends on
-//    the mantissa of the global scale alone, so a warp asks it once.  (MXFP4's
-//    quotients are exact.)
-//  - else, as without a global scale, |x| is compared with the seven midpoints times
-//    scale times global scale.  m s is exact in FP32 (at most 7 bits); times g it is
-//    rounded down, and cut to BF16, for the midpoints that go to the lower code, and
-//    rounded up for the others, which leaves every comparison with a BF16 number as
-//    it was.  Two elements are compared at once.  The values of
+//  - the codes, by the conversion instruction from an FP32 quotient: where a midpoint
+//    times scale times global scale lies beside every BF16 number, the quotient's few
+//    roundings leave it on the right side.  Where one lies next to a BF16 number, or
+//    on it, the quotient is moved by 2^-20 to the side on which the real one is (or
+//    on which a tie ends).  Both depend on mantissas alone, 4 of midpoints times 8 of
+//    scales, so a warp asks once.  (MXFP4's quotients are exact.)
+//  - where the midpoints of a block's scale want both sides, as without a global
+//    scale, |x| is compared with the seven midpoints times scale times global scale.
+//    m s is exact in FP32 (at most 7 bits); times g it is rounded down, and cut to
+//    BF16, for the midpoints that go to the lower code, and rounded up for the
+//    others, which leaves every comparison with a BF16 number as it was.  Two
+//    elements are compared at once.  The values of
 // the eight codes of a block, rounded to BF16 once, are a table of 16 bytes on the
 // way back, from which byte permutations pick four at a time.
 #include <cuda_fp4.h>
@@ -92,21 +94,27 @@ __device__ __forceinline__ uint32_t bits_of(uint32_t b2, uint32_t b1, uint32_t b
   return s * 0xFFFEFFFFu;
 }
 
-// Whether an FP32 quotient x / (s g) may lie on the other side of a midpoint than
-// the real one, or on it: some m s g within 32 units of FP32's last place from a
-// BF16 number, over all mantissas of m (1, 1.25, 1.5, 1.75) and s (1 to 1.875), one
-// product a lane.  (The quotient's roundings are some 2^-22, 2 to 4 units; a code
-// needs x next to the midpoint, and x is a BF16 number.)
-__device__ __forceinline__ bool near_midpoints(float g) {
+// Which of the 32 pairs of mantissas, of m (1, 1.25, 1.5, 1.75: bits 0, 1) and s (1 to
+// 1.875: bits 2 to 4), have an m s g within 32 units of FP32's last place of a BF16
+// number, where an FP32 quotient x / (s g) (whose roundings are some 2^-22, 2 to 4
+// units) may lie on the other side of m than the real one: `up` if the real one is
+// above it, or on it and the code above is even, `down` otherwise.
+struct Sides {
+  uint32_t up, down;
+};
+__device__ __forceinline__ Sides sides_of(float g) {
   const int lane = threadIdx.x & 31;
   const float ms = (1.f + 0.25f * static_cast<float>(lane & 3)) * (1.f + 0.125f * static_cast<float>(lane >> 2));
-  const uint32_t low = __float_as_uint(ms * g) & 0xFFFFu;
-  return __any_sync(0xFFFFFFFFu, low <= 32u || low >= 0x10000u - 32u);
+  const uint32_t bits = __float_as_uint(ms * g), low = bits & 0xFFFFu;
+  const bool near = low <= 32u || low >= 0x10000u - 32u;
+  const float d = fmaf(ms, g, -__uint_as_float((bits + 0x8000u) & 0xFFFF0000u));  // m s g less that number
+  const bool above = d < 0.f || (d == 0.f && (lane & 3) >= 2);
+  return {__ballot_sync(0xFFFFFFFFu, near && above), __ballot_sync(0xFFFFFFFFu, near && !above)};
 }
 
 // One piece: 16 BF16 numbers to 8 bytes of codes; `scale` of its block.
 template <int FORMAT>
-__device__ __forceinline__ uint2 quantize_piece(const uint4 (&v)[2], float g, float about, bool usable_g, bool near, int& scale) {
+__device__ __forceinline__ uint2 quantize_piece(const uint4 (&v)[2], float g, float about, bool usable_g, Sides sides, int& scale) {
   const uint32_t w[8] = {v[0].x, v[0].y, v[0].z, v[0].w, v[1].x, v[1].y, v[1].z, v[1].w};
   uint32_t top = 0;
 #pragma unroll
@@ -126,8 +134,13 @@ __device__ __forceinline__ uint2 quantize_piece(const uint4 (&v)[2], float g, fl
     s = e8m0_value(scale);
   }
   if (!codes) return make_uint2(0u, 0u);
-  if (FORMAT == MOE_FP4_MX || !near) {
-    const float inverse = FORMAT == MOE_FP4_MX ? __uint_as_float(static_cast<uint32_t>(254 - scale) << 23) : __frcp_rn(s * g);
+  // the mantissa's three bits (of a scale below 2^-6: those behind its first one)
+  const int at = 4 * (scale >= 8 ? scale & 7 : static_cast<int>(0x64204000u >> (4 * scale) & 7u));
+  const bool up = FORMAT == MOE_FP4_NV && (sides.up >> at & 15u) != 0u, down = FORMAT == MOE_FP4_NV && (sides.down >> at & 15u) != 0u;
+  if (!(up && down)) {
+    float inverse;
+    if (FORMAT == MOE_FP4_MX) inverse = __uint_as_float(static_cast<uint32_t>(254 - scale) << 23);
+    else inverse = __frcp_rn(s * g) * (up ? 1.f + 0x1p-20f : down ? 1.f - 0x1p-20f : 1.f);
     uint32_t out[2] = {0u, 0u};
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
@@ -160,8 +173,8 @@ __device__ __forceinline__ uint2 quantize_piece(const uint4 (&v)[2], float g, fl
 }
 
 // Measured, T = 8192, K = 6144 (129 MB): NVFP4 21.7 us (5.9 TB/s, 89% of the copy
-// rate), MXFP4 20.7, HBM; by comparisons, as without a global scale or next to
-// midpoints, 28.5 to 30.6 (the logic pipe).
+// rate), MXFP4 20.7, HBM; by comparisons, as without a global scale, 30.6 (the logic
+// pipe).
 template <int FORMAT>
 __global__ void __launch_bounds__(kThreads)
 fp4_quantize_kernel(const uint4* x, const float* global_scale, uint2* codes, uint8_t* scales, int64_t pieces) {
@@ -180,12 +193,12 @@ fp4_quantize_kernel(const uint4* x, const float* global_scale, uint2* codes, uin
   const float g = FORMAT == MOE_FP4_NV && global_scale ? __ldg(global_scale) : 1.f;
   const bool usable_g = usable(g);
   const float about = 1.f / (6.f * g);
-  const bool near = FORMAT == MOE_FP4_NV && near_midpoints(g);
+  const Sides sides = FORMAT == MOE_FP4_NV ? sides_of(g) : Sides{0u, 0u};
 #pragma unroll
   for (int k = 0; k < kPieces; ++k) {
     const int64_t i = first + k * kThreads;
     int scale;
-    const uint2 c = quantize_piece<FORMAT>(v[k], g, about, usable_g, near, scale);
+    const uint2 c = quantize_piece<FORMAT>(v[k], g, about, usable_g, sides, scale);
     if (i < pieces) {  // (no thread leaves before the others' shuffles)
       codes[i] = c;
       if (FORMAT == MOE_FP4_NV) scales[i] = static_cast<uint8_t>(scale);

@@ -103,6 +103,23 @@ def test_quantize_global_scales_that_bring_midpoints_next_to_bf16_numbers(M):
             check_quantize(M, O.f64_to_bf16_bits(O.bf16_bits_to_f64(x) * 2.0 ** -9), "nvfp4", float(g))
 
 
+def test_quantize_global_scales_from_the_largest_element(M):
+    # g = amax / (448 * 6), as calibration sets it: 0.75 * 448 * g and 0.875 * 384 * g are then next to BF16 numbers
+    rng = np.random.default_rng(306)
+    for mantissa in range(128):
+        top = float(np.float32(2.0 ** (mantissa % 9 - 3) * (1 + mantissa / 128)))
+        x = O.bf16_bits_to_f64(draw_bf16(rng, (16, 512), 1.0)) * rng.choice([0.05, 0.3, 1.0], (16, 32)).repeat(16, axis=1) * top
+        # elements on and beside midpoints of the blocks' scales
+        g = np.float32(top) / np.float32(448 * 6)
+        _, s = O.fp4_quantize(np.clip(x, -top, top), "nvfp4", float(g))
+        s = O.fp4_scale_values("nvfp4")[s] * float(g)
+        m = np.array([0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5.0])
+        for i in range(7):
+            x[:, i + 2::16] = m[i] * s * (1 + rng.integers(-1, 2, s.shape) * 2.0 ** -8)
+        bits = O.f64_to_bf16_bits(np.clip(x, -top, top) * rng.choice([-1, 1], x.shape))
+        check_quantize(M, bits, "nvfp4", g)
+
+
 def test_quantize_every_bf16_as_the_largest_of_its_block(M):
     # 2^15 blocks: the largest takes every value, the others lie below it
     rng = np.random.default_rng(302)
