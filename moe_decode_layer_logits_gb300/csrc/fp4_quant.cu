@@ -14,14 +14,10 @@
 //    on it, the quotient is moved by 2^-20 to the side on which the real one is (or
 //    on which a tie ends).  Both depend on mantissas alone, 4 of midpoints times 8 of
 //    scales, so a warp asks once.  (MXFP4's quotients are exact.)
-//  - where the midpoints of a block's scale want both sides, as without a global
-//    scale, |x| is compared with the seven midpoints times scale times global scale.
-//    m s is exact in FP32 (at most 7 bits); times g it is rounded down, and cut to
-//    BF16, for the midpoints that go to the lower code, and rounded up for the
-//    others, which leaves every comparison with a BF16 number as it was.  Two
-//    elements are compared at once.  The values of
-// the eight codes of a block, rounded to BF16 once, are a table of 16 bytes on the
-// way back, from which byte permutations pick four at a time.
+//    Ties that end on different sides (so of a global scale of few bits, or none) want
+//    the nearest quotient instead, which is a midpoint only if the real one is.
+// On the way back the values of a block's eight codes, rounded to BF16 once, are a
+// table of 16 bytes, from which byte permutations pick four at a time.
 #include <cuda_fp4.h>
 #include <cuda_fp8.h>
 
@@ -69,29 +65,24 @@ __device__ __forceinline__ int e4m3_scale(float amax, float g, float about) {
   return up ? c + (d < 0.f || tie ? 1 : 0) : c - (d > 0.f || tie ? 1 : 0);
 }
 
-// The same BF16 number twice: x > it if and only if x > m s g (EVEN_BELOW: a tie
-// goes to the lower code), or x >= m s g.
-template <bool EVEN_BELOW>
-__device__ __forceinline__ uint32_t threshold(float ms, float g) {
-  if (EVEN_BELOW) return __byte_perm(__float_as_uint(__fmul_rd(ms, g)), 0, 0x3232);
-  return __byte_perm(__float_as_uint(__fmul_ru(ms, g)) - 1u, 0, 0x3232);
-}
-
-__device__ __forceinline__ uint32_t greater2(uint32_t a, uint32_t b) {  // 0xFFFF in each half where a > b
-  return __hgt2_mask(*reinterpret_cast<__nv_bfloat162*>(&a), *reinterpret_cast<__nv_bfloat162*>(&b));
-}
-
-__device__ __forceinline__ uint32_t pick(uint32_t mask, uint32_t yes, uint32_t no) { return (yes & mask) | (no & ~mask); }
-
-// 4 [b2] + 2 [b1] + [b0] in each half, from masks of 0xFFFF.  As numbers the masks
-// with bits h and l are 2^16 (l - h) - l, so their weighted sum times -(2^16 + 1)
-// is 2^16 of the high code plus the low one.  (Multiply-adds, as the logic pipe
-// bounds this way: T = 8192 33.3 -> 30.4 us.)
-__device__ __forceinline__ uint32_t bits_of(uint32_t b2, uint32_t b1, uint32_t b0) {
-  uint32_t s;
-  asm("mad.lo.u32 %0, %1, 2, %2;" : "=r"(s) : "r"(b1), "r"(b0));
-  asm("mad.lo.u32 %0, %1, 4, %2;" : "=r"(s) : "r"(b2), "r"(s));
-  return s * 0xFFFEFFFFu;
+// 8 numbers (four words of two) times f to codes, nearest even; REFINED: divided by
+// p, whose reciprocal f is: one step of Newton's makes the quotient the nearest to the
+// real one.  (CUT: of x cut off at 8 p, as quotients of a scale that stopped at 448 have
+// no bound, and infinite ones no next step.)
+template <bool REFINED = false, bool CUT = false>
+__device__ __forceinline__ uint32_t codes_of(const uint32_t* w, float f, float p = 1.f) {
+  const auto quotient = [=](float x) {
+    if (CUT) x = fminf(fmaxf(x, -8.f * p), 8.f * p);
+    const float q = x * f;
+    return REFINED ? fmaf(fmaf(q, p, -x), -f, q) : q;  // (signs that keep -0)
+  };
+  uint32_t out = 0u;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const float2 q = make_float2(quotient(bf16lo(w[j])), quotient(bf16hi(w[j])));
+    out |= static_cast<uint32_t>(__nv_cvt_float2_to_fp4x2(q, __NV_E2M1, cudaRoundNearest)) << (8 * j);
+  }
+  return out;
 }
 
 // Which of the 32 pairs of mantissas, of m (1, 1.25, 1.5, 1.75: bits 0, 1) and s (1 to
@@ -99,6 +90,10 @@ __device__ __forceinline__ uint32_t bits_of(uint32_t b2, uint32_t b1, uint32_t b
 // number, where an FP32 quotient x / (s g) (whose roundings are some 2^-22, 2 to 4
 // units) may lie on the other side of m than the real one: `up` if the real one is
 // above it, or on it and the code above is even, `down` otherwise.
+// One global scale's products beside BF16 numbers, of the same s, are m1 s g = b1 (1 +
+// d1) and m2 s g = b2 (1 + d2): then b1 m2 and b2 m1, numbers of 11 bits, differ by a
+// few 2^-19 at most, so not at all, and d1 = d2.  So a scale's midpoints want both
+// sides only where all such products are on BF16 numbers: ties.
 struct Sides {
   uint32_t up, down;
 };
@@ -121,60 +116,37 @@ __device__ __forceinline__ uint2 quantize_piece(const uint4 (&v)[2], float g, fl
   for (int j = 0; j < 8; ++j) top = __vmaxu2(top, w[j] & 0x7FFF7FFFu);
   top = max(top & 0xFFFFu, top >> 16);  // the largest |x|, as BF16 bits
   if (FORMAT == MOE_FP4_MX) top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
-  float s;
   bool codes;  // (a block that is not finite has none, nor one whose scale is zero)
   if (FORMAT == MOE_FP4_NV) {
     const bool finite = top < 0x7F80u && usable_g;
     scale = finite ? e4m3_scale(__uint_as_float(top << 16), g, about) : kNanE4m3;
     codes = finite && scale > 0;
-    s = e4m3_value(scale);
   } else {
     codes = top < 0x7F80u;
     scale = codes ? max(static_cast<int>(top >> 7) - 2, 0) : kNanE8m0;  // floor(log2) - 2, biased
-    s = e8m0_value(scale);
   }
   if (!codes) return make_uint2(0u, 0u);
+  if (FORMAT == MOE_FP4_MX) {
+    const float inverse = __uint_as_float(static_cast<uint32_t>(254 - scale) << 23);
+    return make_uint2(codes_of(w, inverse), codes_of(w + 4, inverse));
+  }
   // the mantissa's three bits (of a scale below 2^-6: those behind its first one)
   const int at = 4 * (scale >= 8 ? scale & 7 : static_cast<int>(0x64204000u >> (4 * scale) & 7u));
-  const bool up = FORMAT == MOE_FP4_NV && (sides.up >> at & 15u) != 0u, down = FORMAT == MOE_FP4_NV && (sides.down >> at & 15u) != 0u;
+  const bool up = (sides.up >> at & 15u) != 0u, down = (sides.down >> at & 15u) != 0u;
+  const float p = e4m3_value(scale) * g, inverse = __frcp_rn(p);
   if (!(up && down)) {
-    float inverse;
-    if (FORMAT == MOE_FP4_MX) inverse = __uint_as_float(static_cast<uint32_t>(254 - scale) << 23);
-    else inverse = __frcp_rn(s * g) * (up ? 1.f + 0x1p-20f : down ? 1.f - 0x1p-20f : 1.f);
-    uint32_t out[2] = {0u, 0u};
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const float2 q = make_float2(bf16lo(w[j]) * inverse, bf16hi(w[j]) * inverse);
-      out[j >> 2] |= static_cast<uint32_t>(__nv_cvt_float2_to_fp4x2(q, __NV_E2M1, cudaRoundNearest)) << (8 * (j & 3));
-    }
-    return make_uint2(out[0], out[1]);
+    const float f = up ? inverse * (1.f + 0x1p-20f) : down ? inverse * (1.f - 0x1p-20f) : inverse;
+    return make_uint2(codes_of(w, f), codes_of(w + 4, f));
   }
-  const uint32_t t0 = threshold<true>(0.25f * s, g), t1 = threshold<false>(0.75f * s, g), t2 = threshold<true>(1.25f * s, g),
-                 t3 = threshold<false>(1.75f * s, g), t4 = threshold<true>(2.5f * s, g), t5 = threshold<false>(3.5f * s, g),
-                 t6 = threshold<true>(5.f * s, g);
-  uint32_t c[8];  // each: code of the even element, and of the odd one 16 bits above
-#pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    const uint32_t a = w[j] & 0x7FFF7FFFu;
-    const uint32_t b2 = greater2(a, t3);
-    const uint32_t b1 = greater2(a, pick(b2, t5, t1));
-    const uint32_t b0 = greater2(a, pick(b1, pick(b2, t6, t2), pick(b2, t4, t0)));
-    c[j] = (w[j] >> 12 & 0x00080008u) | bits_of(b2, b1, b0);
-  }
-  uint32_t out[2];
-#pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    const uint32_t* k = c + 4 * h;
-    const uint32_t even = __byte_perm(k[0], k[2], 0x5410) + (__byte_perm(k[1], k[3], 0x5410) << 8);
-    const uint32_t odd = __byte_perm(k[0], k[2], 0x7632) + (__byte_perm(k[1], k[3], 0x7632) << 8);
-    out[h] = even + (odd << 4);
-  }
-  return make_uint2(out[0], out[1]);
+  // Ties: m s g is a BF16 number, so g has 8 bits at most and p is exact; m p has 15,
+  // and another number than x is at least 2^-14 away.
+  if (__uint_as_float(top << 16) * inverse < 16.f) return make_uint2(codes_of<true>(w, inverse, p), codes_of<true>(w + 4, inverse, p));
+  return make_uint2(codes_of<true, true>(w, inverse, p), codes_of<true, true>(w + 4, inverse, p));
 }
 
-// Measured, T = 8192, K = 6144 (129 MB): NVFP4 21.7 us (5.9 TB/s, 89% of the copy
-// rate), MXFP4 20.7, HBM; by comparisons, as without a global scale, 30.6 (the logic
-// pipe).
+// Measured, T = 8192, K = 6144 (129 MB): NVFP4 22.5 us (5.7 TB/s, 86% of the copy
+// rate), MXFP4 20.6, HBM; quotients refined, as without a global scale, 26.5 (two more
+// multiply-adds an element; comparisons with the midpoints instead: 30.6).
 template <int FORMAT>
 __global__ void __launch_bounds__(kThreads)
 fp4_quantize_kernel(const uint4* x, const float* global_scale, uint2* codes, uint8_t* scales, int64_t pieces) {

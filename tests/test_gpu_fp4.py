@@ -103,6 +103,25 @@ def test_quantize_global_scales_that_bring_midpoints_next_to_bf16_numbers(M):
             check_quantize(M, O.f64_to_bf16_bits(O.bf16_bits_to_f64(x) * 2.0 ** -9), "nvfp4", float(g))
 
 
+def test_quantize_ties_of_global_scales_of_few_bits(M):
+    # all with 8 bits, and some of 9: elements on midpoints of blocks' scales, beside them, and far above the largest
+    rng = np.random.default_rng(307)
+    m = np.array([0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5.0])
+    for mantissa in [*range(128, 256), *(k + 0.5 for k in range(128, 256, 9))]:
+        g = float(np.float32(mantissa * 2.0 ** (-8 - mantissa % 5)))
+        x = rng.standard_normal((18, 256)) * 2.0 ** rng.integers(-6, 4, (18, 16)).repeat(16, axis=1) * g * 6
+        x[16] *= 2.0 ** 20  # scales that stop at 448
+        x[17, ::16] = 3e38
+        _, s = O.fp4_quantize(O.bf16_bits_to_f64(O.f64_to_bf16_bits(x)), "nvfp4", g)
+        s = O.fp4_scale_values("nvfp4")[s] * g
+        for i in range(7):
+            x[:, i + 2::16] = m[i] * s * (1 + rng.integers(-1, 2, s.shape) * 2.0 ** -8)
+        x[:, 10::16], x[:, 11::16] = 0.0, -0.0
+        bits = O.f64_to_bf16_bits(x * rng.choice([-1, 1], x.shape))
+        check_quantize(M, bits, "nvfp4", g)
+        check_quantize(M, O.f64_to_bf16_bits(O.bf16_bits_to_f64(bits) * 2.0 ** -100), "nvfp4", g * 2.0 ** -94)
+
+
 def test_quantize_global_scales_from_the_largest_element(M):
     # g = amax / (448 * 6), as calibration sets it: 0.75 * 448 * g and 0.875 * 384 * g are then next to BF16 numbers
     rng = np.random.default_rng(306)
