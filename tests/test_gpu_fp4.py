@@ -164,6 +164,28 @@ def test_quantize_what_is_not_finite(M, fmt):
 
 
 @pytest.mark.parametrize("fmt", ["nvfp4", "mxfp4"])
+@pytest.mark.parametrize("T,K", [(1, 64), (37, 1088), (300, 2048)])
+def test_tensors_that_begin_between_sectors(M, fmt, T, K):
+    # 16 bytes behind a multiple of 32: the same values, and nothing written beside them
+    K = K if fmt == "nvfp4" else K * 2
+    x = dev(draw_bf16(np.random.default_rng([308, T, K]), (T, K), 1.0))
+    codes, scales = M.moe_fp4_quantize(x, format=fmt)
+    at = torch.empty(T * K + 16, dtype=torch.bfloat16, device="cuda")
+    at = at[8 if at.data_ptr() % 32 == 0 else 0:][:T * K].view(T, K)
+    assert at.data_ptr() % 32 == 16
+    at.copy_(x)
+    for got, want in zip(M.moe_fp4_quantize(at, format=fmt), (codes, scales)):
+        assert torch.equal(got, want)
+    whole = torch.full((T * K + 32,), 7.0, dtype=torch.bfloat16, device="cuda")
+    first = 8 if whole.data_ptr() % 32 == 0 else 16
+    out = whole[first:first + T * K].view(T, K)
+    assert out.data_ptr() % 32 == 16
+    M.moe_fp4_dequantize(codes, scales, format=fmt, out=out)
+    assert torch.equal(out, M.moe_fp4_dequantize(codes, scales, format=fmt))
+    assert bool((whole[:first] == 7).all()) and bool((whole[first + T * K:] == 7).all())
+
+
+@pytest.mark.parametrize("fmt", ["nvfp4", "mxfp4"])
 def test_dequantize_every_code_with_every_scale(M, fmt):
     B = O.FP4_BLOCK[fmt]
     codes = np.tile(np.arange(256, dtype=np.uint8).reshape(-1, B // 2), (1, 1)).reshape(1, -1)   # 512 elements
